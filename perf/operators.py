@@ -217,8 +217,6 @@ def _prepare_adamw(case, seed):
         s["opt"] = q.AdamW(cut(s["master"] if p32 else s["param"]), cut(s["grad"]), masters=None if p32 else cut(s["master"]),
                            m=cut(s["m"]), v=cut(s["v"]), m_scale=cutb(s.get("ms")), v_scale=cutb(s.get("vs")), betas=(BETA1, BETA2), eps=EPS,
                            weight_decay=0.01, lr_scale=[1.0, 4.0] * (len(sizes) // 2))
-        if case["state"] == 8:
-            s["m_cut"], s["v_cut"] = cut(s["m_out"]), cut(s["v_out"])
     return s
 
 
@@ -331,7 +329,7 @@ def _run_adamw(s):
             s["opt"].step(LR, STEP, seed=s["seed"])
         m, v = s["m"], s["v"]
         if c["state"] == 8:
-            s["opt"].read_state(s["m_cut"], s["v_cut"])
+            s["opt"].read_state(s["m_out"], s["v_out"])
             m, v = s["m_out"], s["v_out"]
         return {"param": s["param"], "master": s["master"], "m": m, "v": v, "norm": s["norm"]}
     per_tensor = lambda t: torch.repeat_interleave(t, s["blocks_t"])[:, None]  # noqa: E731
