@@ -55,7 +55,8 @@ typedef enum {
     QERL_ERR_TIMEOUT = 6,            /* a bounded device-side wait ran out (latched) */
     QERL_ERR_UNSUPPORTED_DEVICE = 7, /* current device is not compute capability 10.3 */
     QERL_ERR_WORKSPACE = 8,          /* workspace missing or smaller than required */
-    QERL_ERR_TOO_LARGE = 9           /* needs more scratch than the fixed no-allocation buffer */
+    QERL_ERR_TOO_LARGE = 9,          /* needs more scratch than the fixed no-allocation buffer */
+    QERL_ERR_HOST_MEMORY = 10        /* no host memory for a plan */
 } qerl_status;
 
 /* Size of the fixed device scratch buffer behind qerl_nvfp4_lora_linear_fwd_noalloc. */
@@ -75,8 +76,12 @@ enum {
     QERL_OP_LINEAR_BWD = 2,
     QERL_OP_AQN_RMSNORM = 3,
     QERL_OP_MXFP4_FWD = 4,        /* qerl_mxfp4_lora_linear_fwd */
-    QERL_OP_LINEAR_FWD_F32AB = 5  /* qerl_nvfp4_lora_linear_fwd_f32ab */
+    QERL_OP_LINEAR_FWD_F32AB = 5, /* qerl_nvfp4_lora_linear_fwd_f32ab */
+    QERL_OP_POLICY_LOSS = 6       /* qerl_policy_loss: M = tokens; N, K, r unused */
 };
+
+/* Element types of the calls that take more than one. */
+enum { QERL_DTYPE_F32 = 0, QERL_DTYPE_BF16 = 1 };
 
 /* Linear algorithm selection (qerl_set_linear_algo); AUTO is the default.
  * AUTO: a single-token forward on a weight of at most 24M values runs the
@@ -472,6 +477,160 @@ void qerl_decoder_chain_destroy(qerl_chain *plan);
  */
 qerl_status qerl_residual_add(const void *h, const void *y, int64_t n, void *out, qerl_stream_t stream);
 qerl_status qerl_swiglu(const void *g, const void *u, int64_t n, void *out, qerl_stream_t stream);
+
+/*
+ * The rest of an RL step around the linears: attention of the rollout batch,
+ * the policy loss with its gradient, and the adapters' optimizer ("QeRL: Beyond
+ * Efficiency", summary: GRPO and DAPO; bitsofall, "Workflow: Rollout, Update,
+ * Quantization": several answers are sampled for each prompt and only the LoRA
+ * matrices are updated).
+ *
+ * Attention of a batch whose sequences share long prefixes (one decode step, or
+ * a few new tokens of every sequence).  Sequence b of B belongs to prefix
+ * g = b / (B / n_prefix); token l of its Lq new ones, query head h (kv head
+ * h / (Hq / Hkv)) sees all P_g keys of the prefix and the suffix keys 0 ..
+ * n_b - Lq + l, where n_b counts the sequence's own tokens, the new ones among
+ * them (their keys and values are in the suffix cache already):
+ *     a_k = scale q . k_k,   lse = ln sum_k e^a_k,   out = sum_k e^(a_k - lse) v_k
+ * A row that sees no key gets out = 0 and lse = -inf.
+ *   q, out  (device) bf16 [B, Lq, Hq, D]; strides of B, Lq, Hq in elements
+ *   k_prefix, v_prefix (device) bf16 [n_prefix, P, Hkv, D], prefix_lens (device)
+ *           int32 [n_prefix] or NULL (P for every prefix)
+ *   k_suffix, v_suffix (device) bf16 [B, S, Hkv, D], suffix_lens (device) int32 [B]
+ *   lse     (device) optional float [B, Lq, Hq]
+ *   P and S are capacities (either may be 0, its pointers NULL); the lengths are
+ *   read on the device and taken into [0, P] and [0, S].  What lies beyond them
+ *   is never used, whatever it holds.
+ *   D is 64 or 128, Hq % Hkv == 0, B % n_prefix == 0 (QERL_ERR_SHAPE); scale
+ *   finite and > 0; the last dimension is contiguous, strides are multiples of
+ *   8 elements and >= 0, pointers 16-byte aligned (QERL_ERR_ALIGN).
+ *   ws (device) >= qerl_prefix_attention_ws_bytes(dims), contents on entry
+ *   ignored; calls that may overlap need a workspace each.
+ * Products of bf16 operands accumulate in FP32; the probabilities are rounded
+ * to bf16 for the second product, their sum is not.  Results are the same on
+ * every run.
+ */
+typedef struct {
+    int64_t B, Lq, Hq, Hkv, D, n_prefix, P, S;
+    int64_t q_stride[3], out_stride[3];                /* B, Lq, Hq */
+    int64_t k_prefix_stride[3], v_prefix_stride[3];    /* n_prefix, P, Hkv */
+    int64_t k_suffix_stride[3], v_suffix_stride[3];    /* B, S, Hkv */
+} qerl_prefix_attn_dims;
+
+/* Workspace bytes (0 if the sizes are not covered). */
+size_t qerl_prefix_attention_ws_bytes(const qerl_prefix_attn_dims *dims);
+qerl_status qerl_prefix_attention(const qerl_prefix_attn_dims *dims, const void *q, const void *k_prefix, const void *v_prefix,
+                                  const int32_t *prefix_lens, const void *k_suffix, const void *v_suffix,
+                                  const int32_t *suffix_lens, float scale, void *out, float *lse, void *ws, size_t ws_bytes,
+                                  qerl_stream_t stream);
+
+/*
+ * Log-probability of each row's chosen token and the entropy of its
+ * distribution p = softmax(x / temperature):
+ *     logp[t] = ln p[ids[t]],   entropy[t] = -sum_j p_j ln p_j
+ *   logits (device) [T, V] of `dtype`, row stride ld elements; any alignment of
+ *   the element.  ids (device) int32 or int64 [T] (ids_bits 32 or 64).
+ *   weight (device) optional float [T]; entropy (device) optional float [T].
+ * A row takes no part where its weight is 0 or its id lies outside [0, V): its
+ * logits are not read and its results are 0.  A row whose logits are all -inf
+ * has logp -inf and entropy 0.  Inf or NaN in a row that takes part shows in its
+ * results.  temperature finite and > 0.
+ */
+qerl_status qerl_token_logp(const void *logits, int dtype, int64_t T, int64_t V, int64_t ld, const void *ids, int ids_bits,
+                            const float *weight, float temperature, float *logp, float *entropy, qerl_stream_t stream);
+
+/*
+ * Clipped policy loss with a KL term (GRPO; DAPO with clip_high > clip_low), and
+ * the gradient of the logits in the same pass over them:
+ *     rho = e^(logp - old),  d = ref - logp
+ *     l_t = -min(rho A, clip(rho, 1 - clip_low, 1 + clip_high) A) + beta (e^d - d - 1)
+ *     sums = { sum w l, sum w (policy term), sum w (e^d - d - 1), sum of w over clipped tokens }
+ *     dlogits = grad_scale dL/dlogits
+ *   logits, ids, logp, entropy as in qerl_token_logp; old_logp, adv (device)
+ *   float [T]; ref_logp (device) float [T], NULL only with beta = 0; weight
+ *   (device) float [T] or NULL (1): the mask and the normalisation, e.g. 1 / (all
+ *   tokens) for DAPO, 1 / (answers x tokens of the answer) for GRPO; 0 leaves a
+ *   token out (its row of dlogits is 0).
+ *   sums (device) float [4]; dlogits (device) optional [T, V] of `dtype`, row
+ *   stride ldd; it may be logits itself (with ldd == ld); any other overlap is
+ *   QERL_ERR_INVALID_ARG.  ws (device) >= qerl_workspace_bytes(
+ *   QERL_OP_POLICY_LOSS, T, V, 0, 0).
+ * At rho = 1 + clip_high (1 - clip_low) the gradient is the unclipped one.  An
+ * all -inf row adds nothing and gets a zero gradient.  The sums are taken in a
+ * fixed order (the same on every run).  T = 0 sets sums to 0.
+ */
+typedef struct {
+    float clip_low, clip_high; /* in [0, 1] and >= 0 */
+    float beta;                /* KL weight, >= 0 */
+    float temperature;         /* finite, > 0 */
+    float grad_scale;          /* factor of dlogits, e.g. of a scaled loss */
+} qerl_policy_opts;
+qerl_status qerl_policy_loss(const void *logits, int dtype, int64_t T, int64_t V, int64_t ld, const void *ids, int ids_bits,
+                             const float *old_logp, const float *ref_logp, const float *adv, const float *weight,
+                             const qerl_policy_opts *opts, float *sums, float *logp, float *entropy, void *dlogits, int64_t ldd,
+                             void *ws, size_t ws_bytes, qerl_stream_t stream);
+
+/*
+ * AdamW over many tensors in one launch (two with the clip), states in FP32 or 8
+ * bits:
+ *     g = c grad (c = min(1, max_grad_norm / |grad|) over all tensors, or 1)
+ *     m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2,   lr = hyper.lr * lr_scale
+ *     p = p (1 - lr weight_decay) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+ * A plan holds the table of tensors (in ws, caller owned; built with blocking
+ * copies, outside stream capture); the buffers must stay valid while it is used,
+ * and steps of one plan must not overlap.
+ *   param: FP32, or bf16 beside an FP32 master, which is updated and then
+ *   rounded into param (updates of a bf16 weight alone would be lost below half
+ *   a unit).  master is NULL for FP32 params.  grad: FP32 or bf16.
+ *   State bits 32: m, v float [n].  8: m, v uint8 [n], m_scale, v_scale float
+ *   [ceil(n / 256)], one scale per block of 256 elements.  All zero at first.
+ *   Pointers 16-byte aligned (scales 4).  n = 0 is allowed.
+ * 8-bit codes: m is a sign bit (7), sqrt(v) unsigned; the other bits are 3
+ * exponent and 4 (m) or 5 (sqrt v) mantissa bits, value = 2^(e-7) (1 + f) or
+ * 2^-6 f at e = 0, times the block's scale = (largest magnitude) / (2 - 2^-4 or
+ * 2 - 2^-5).  They are rounded stochastically: up with the probability of the
+ * part dropped, from 16 random bits of Philox4x32-10 (Salmon et al., SC'11) with
+ * counter (element / 4 low, high, tensor, step), key seed, word element % 4 (low
+ * half for m, high half for sqrt v).  A nonzero sqrt(v) keeps a code of at least
+ * 1; a block whose largest magnitude is below 2^-100 is stored as zero.
+ * step counts from 1 and is a host value: a captured graph repeats its step.
+ * With max_grad_norm > 0 the norm of all gradients goes to grad_norm (device,
+ * optional), and a norm that is not finite leaves everything unchanged.  Without
+ * it Inf and NaN enter the tensors they are in.  Results are the same on every
+ * run, clip included.
+ */
+typedef struct {
+    int64_t n;
+    void *param;
+    float *master;
+    const void *grad;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    double lr_scale, weight_decay;
+} qerl_adamw_tensor;
+typedef struct {
+    int param_dtype, grad_dtype; /* QERL_DTYPE_* */
+    int state_bits;              /* 32 or 8 */
+} qerl_adamw_format;
+typedef struct {
+    double lr, beta1, beta2, eps;
+    double max_grad_norm; /* 0: no clip */
+    int64_t step;         /* 1, 2, ... */
+    uint64_t seed;        /* of the stochastic rounding */
+} qerl_adamw_hyper;
+typedef struct qerl_adamw qerl_adamw;
+
+/* Workspace bytes of a plan (0 for invalid arguments). */
+size_t qerl_adamw_ws_bytes(const qerl_adamw_tensor *tensors, int64_t n_tensors);
+qerl_status qerl_adamw_plan(const qerl_adamw_tensor *tensors, int64_t n_tensors, const qerl_adamw_format *format, void *ws,
+                            size_t ws_bytes, qerl_adamw **plan);
+qerl_status qerl_adamw_step(const qerl_adamw *plan, const qerl_adamw_hyper *hyper, float *grad_norm, qerl_stream_t stream);
+/* The values the 8-bit states stand for, for a checkpoint: m_out, v_out (device,
+ * 16-byte aligned) of out_dtype hold the tensors in order, each from a multiple
+ * of 256 elements on (what lies between is not written). */
+qerl_status qerl_adamw_read_state(const qerl_adamw *plan, void *m_out, void *v_out, int out_dtype, qerl_stream_t stream);
+/* Frees the host handle (the workspace stays the caller's). */
+void qerl_adamw_destroy(qerl_adamw *plan);
 
 /* Scratch bytes an operation needs (0 if none).  Sizes as in the calls. */
 size_t qerl_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int r);

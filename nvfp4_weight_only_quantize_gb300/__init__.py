@@ -21,10 +21,13 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libqerl.so")
 QERL_OK = 0
 STATUS_NAMES = {0: "QERL_OK", 1: "QERL_ERR_INVALID_ARG", 2: "QERL_ERR_SHAPE", 3: "QERL_ERR_ALIGN",
                 4: "QERL_ERR_NONFINITE", 5: "QERL_ERR_CUDA", 6: "QERL_ERR_TIMEOUT",
-                7: "QERL_ERR_UNSUPPORTED_DEVICE", 8: "QERL_ERR_WORKSPACE", 9: "QERL_ERR_TOO_LARGE"}
+                7: "QERL_ERR_UNSUPPORTED_DEVICE", 8: "QERL_ERR_WORKSPACE", 9: "QERL_ERR_TOO_LARGE",
+                10: "QERL_ERR_HOST_MEMORY"}
 NOALLOC_SCRATCH_BYTES = 8 << 20  # QERL_NOALLOC_SCRATCH_BYTES
 SCALE_ROUND_UP, SCALE_ROUND_NEAREST_EVEN = 0, 1
 OP_QUANTIZE, OP_LINEAR_FWD, OP_LINEAR_BWD, OP_AQN_RMSNORM, OP_MXFP4_FWD, OP_LINEAR_FWD_F32AB = 0, 1, 2, 3, 4, 5
+OP_POLICY_LOSS = 6
+DTYPE_F32, DTYPE_BF16 = 0, 1
 ALGO_AUTO, ALGO_SIMT, ALGO_TCGEN05, ALGO_GEMV = 0, 1, 2, 3
 AQN_NOISE_ADD, AQN_NOISE_MUL = 0, 1
 
@@ -39,7 +42,9 @@ EXPORTED = ["qerl_nvfp4_quantize", "qerl_nvfp4_dequantize", "qerl_nvfp4_lora_lin
             "qerl_nvfp4_lora_linear_fwd_grouped",
             "qerl_launch_count", "qerl_decoder_chain_ws_bytes", "qerl_decoder_chain_plan",
             "qerl_decoder_chain_run", "qerl_decoder_chain_destroy", "qerl_mxfp4_quantize",
-            "qerl_mxfp4_lora_linear_fwd", "qerl_nvfp4_lora_linear_fwd_f32ab", "qerl_residual_add", "qerl_swiglu"]
+            "qerl_mxfp4_lora_linear_fwd", "qerl_nvfp4_lora_linear_fwd_f32ab", "qerl_residual_add", "qerl_swiglu",
+            "qerl_prefix_attention_ws_bytes", "qerl_prefix_attention", "qerl_token_logp", "qerl_policy_loss",
+            "qerl_adamw_ws_bytes", "qerl_adamw_plan", "qerl_adamw_step", "qerl_adamw_read_state", "qerl_adamw_destroy"]
 
 
 class QerlError(RuntimeError):
@@ -57,7 +62,9 @@ _lock = threading.Lock()
 
 
 def build(force: bool = False) -> str:
+    this = build
     from .build import build as _build
+    globals()["build"] = this  # importing the submodule has put the module under this name
     return _build(force=force)
 
 
@@ -106,6 +113,16 @@ def lib() -> C.CDLL:
             sig["qerl_decoder_chain_destroy"] = ([vp], None)
             sig["qerl_residual_add"] = ([vp, vp, i64, vp, vp], i32)
             sig["qerl_swiglu"] = ([vp, vp, i64, vp, vp], i32)
+            sig["qerl_prefix_attention_ws_bytes"] = ([vp], sz)
+            sig["qerl_prefix_attention"] = ([vp, vp, vp, vp, vp, vp, vp, vp, f32, vp, vp, vp, sz, vp], i32)
+            sig["qerl_token_logp"] = ([vp, i32, i64, i64, i64, vp, i32, vp, f32, vp, vp, vp], i32)
+            sig["qerl_policy_loss"] = ([vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp,
+                                        sz, vp], i32)
+            sig["qerl_adamw_ws_bytes"] = ([vp, i64], sz)
+            sig["qerl_adamw_plan"] = ([vp, i64, vp, vp, sz, vp], i32)
+            sig["qerl_adamw_step"] = ([vp, vp, vp, vp], i32)
+            sig["qerl_adamw_read_state"] = ([vp, vp, vp, i32, vp], i32)
+            sig["qerl_adamw_destroy"] = ([vp], None)
             sig["qerl_nvfp4_lora_linear_fwd_packed"] = sig["qerl_nvfp4_lora_linear_fwd"]
             sig["qerl_nvfp4_lora_linear_bwd_packed"] = sig["qerl_nvfp4_lora_linear_bwd"]
             for name, (args, res) in sig.items():
@@ -453,6 +470,226 @@ class DecoderChain:
     def close(self):
         if self._h:
             lib().qerl_decoder_chain_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ---------------------------------------------------------------- attention over shared prefixes
+class _AttnDims(C.Structure):
+    _fields_ = [(n, C.c_int64) for n in ("B", "Lq", "Hq", "Hkv", "D", "n_prefix", "P", "S")] + [
+        (n, C.c_int64 * 3) for n in ("q_stride", "out_stride", "k_prefix_stride", "v_prefix_stride", "k_suffix_stride",
+                                     "v_suffix_stride")]
+
+
+class PrefixAttention:
+    """Attention of a rollout batch over shared prefixes and per-sequence suffixes
+    (qerl_prefix_attention), for caches that stay in place from step to step.
+
+    k_prefix, v_prefix: bf16 [n_prefix, P, Hkv, D]; k_suffix, v_suffix: bf16
+    [B, S, Hkv, D] (any strides that are multiples of 8, last dimension
+    contiguous); sequence b reads prefix b // (B // n_prefix).  q_heads: query
+    heads; q_len: new tokens per sequence and call; scale: 1 / sqrt(D) if None.
+    The tensors are kept referenced; the workspace is this object's (calls that
+    may overlap need an object each)."""
+
+    def __init__(self, k_prefix, v_prefix, k_suffix, v_suffix, q_heads: int, q_len: int = 1, scale: float = None, ws=None):
+        n, P, Hkv, D = k_prefix.shape
+        B, S = k_suffix.shape[:2]
+        for t in (k_prefix, v_prefix, k_suffix, v_suffix):
+            assert t.dtype == torch.bfloat16 and t.dim() == 4 and (t.stride(3) == 1 or t.numel() == 0)
+        assert v_prefix.shape == k_prefix.shape and v_suffix.shape == k_suffix.shape and k_suffix.shape[2:] == (Hkv, D)
+        self._keep = (k_prefix, v_prefix, k_suffix, v_suffix)
+        st = lambda t: (C.c_int64 * 3)(*t.stride()[:3])  # noqa: E731
+        self._d = _AttnDims(B, q_len, q_heads, Hkv, D, n, P, S)
+        self._d.k_prefix_stride, self._d.v_prefix_stride = st(k_prefix), st(v_prefix)
+        self._d.k_suffix_stride, self._d.v_suffix_stride = st(k_suffix), st(v_suffix)
+        nbytes = lib().qerl_prefix_attention_ws_bytes(C.byref(self._d))
+        if nbytes == 0:
+            raise QerlError(2, "qerl_prefix_attention_ws_bytes")
+        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=k_suffix.device) if ws is None else ws
+        self._q_shape = (B, q_len, q_heads, D)
+        self._scale = D ** -0.5 if scale is None else float(scale)
+        self._p = [_p(t) for t in self._keep]
+
+    def run(self, q, suffix_lens, prefix_lens=None, out=None, lse=None, stream=None):
+        """q bf16 [B, Lq, Hq, D], suffix_lens int32 [B] (new tokens included),
+        prefix_lens int32 [n_prefix] or None (P) -> out bf16 like q; lse f32 [B, Lq, Hq] is filled if given."""
+        d = self._d
+        assert q.shape == self._q_shape and q.dtype == torch.bfloat16 and q.stride(3) == 1
+        assert suffix_lens.dtype == torch.int32 and suffix_lens.is_contiguous() and suffix_lens.numel() == d.B
+        if prefix_lens is not None:
+            assert prefix_lens.dtype == torch.int32 and prefix_lens.is_contiguous() and prefix_lens.numel() == d.n_prefix
+        if out is None:
+            out = torch.empty(self._q_shape, dtype=torch.bfloat16, device=q.device)
+        assert out.shape == self._q_shape and out.dtype == torch.bfloat16 and out.stride(3) == 1
+        if lse is not None:
+            assert lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == self._q_shape[:3]
+        d.q_stride[:] = q.stride()[:3]
+        d.out_stride[:] = out.stride()[:3]
+        kp, vp, ks, vs = self._p
+        _check(lib().qerl_prefix_attention(C.byref(d), q.data_ptr(), kp, vp, _p(prefix_lens), ks, vs, suffix_lens.data_ptr(),
+                                           self._scale, out.data_ptr(), _p(lse), self.ws.data_ptr(), self.ws.numel(),
+                                           _stream(stream)), "qerl_prefix_attention")
+        return out
+
+
+def qerl_prefix_attention(q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_lens, prefix_lens=None, scale: float = None,
+                          out=None, lse=None, ws=None, stream=None):
+    """One call of PrefixAttention: out bf16 [B, Lq, Hq, D]."""
+    plan = PrefixAttention(k_prefix, v_prefix, k_suffix, v_suffix, q.shape[2], q.shape[1], scale, ws)
+    return plan.run(q, suffix_lens, prefix_lens, out, lse, stream)
+
+
+# ---------------------------------------------------------------- policy loss
+class _PolicyOpts(C.Structure):
+    _fields_ = [(n, C.c_float) for n in ("clip_low", "clip_high", "beta", "temperature", "grad_scale")]
+
+
+_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
+def _logits_args(logits, ids, vectors):
+    """(pointer, dtype, T, V, ld, ids pointer, ids bits) of a logits matrix, after the checks of its companions."""
+    T, V = logits.shape
+    assert logits.dtype in _DTYPES and (logits.stride(1) == 1 or V == 1)
+    assert ids.dtype in (torch.int32, torch.int64) and ids.shape == (T,) and ids.is_contiguous()
+    for t in vectors:
+        assert t is None or (t.dtype == torch.float32 and t.shape == (T,) and t.is_contiguous())
+    return (logits.data_ptr(), _DTYPES[logits.dtype], T, V, logits.stride(0) if T > 1 else V, ids.data_ptr(),
+            32 if ids.dtype == torch.int32 else 64)
+
+
+def qerl_token_logp(logits, ids, weights=None, temperature: float = 1.0, logp=None, entropy=None, stream=None):
+    """logits bf16/f32 [T, V], ids int32/int64 [T] -> (logp, entropy) f32 [T]; rows of weight 0 are not read."""
+    T = logits.shape[0]
+    logp = torch.empty(T, dtype=torch.float32, device=logits.device) if logp is None else logp
+    entropy = torch.empty(T, dtype=torch.float32, device=logits.device) if entropy is None else entropy
+    args = _logits_args(logits, ids, (weights, logp, entropy))
+    _check(lib().qerl_token_logp(*args, _p(weights), float(temperature), _p(logp), _p(entropy), _stream(stream)),
+           "qerl_token_logp")
+    return logp, entropy
+
+
+def qerl_policy_loss(logits, ids, old_logp, advantages, weights=None, ref_logp=None, clip_low: float = 0.2,
+                     clip_high: float = 0.2, beta: float = 0.0, temperature: float = 1.0, grad_scale: float = 1.0,
+                     want_grad: bool = True, dlogits=None, logp=None, entropy=None, sums=None, ws=None, stream=None):
+    """Clipped policy loss with a KL term and the gradient of the logits:
+    (sums f32 [4] = loss, policy term, KL term, clipped weight; logp f32 [T]; entropy f32 [T]; dlogits like logits,
+    or None without want_grad).  dlogits may be logits."""
+    T, V = logits.shape
+    dev = logits.device
+    logp = torch.empty(T, dtype=torch.float32, device=dev) if logp is None else logp
+    entropy = torch.empty(T, dtype=torch.float32, device=dev) if entropy is None else entropy
+    sums = torch.empty(4, dtype=torch.float32, device=dev) if sums is None else sums
+    if dlogits is None and want_grad:
+        dlogits = torch.empty(T, V, dtype=logits.dtype, device=dev)
+    ws = workspace(OP_POLICY_LOSS, T, V, 0, 0, dev) if ws is None else ws
+    args = _logits_args(logits, ids, (old_logp, ref_logp, advantages, weights, logp, entropy))
+    assert sums.dtype == torch.float32 and sums.numel() == 4 and sums.is_contiguous()
+    ldd = V
+    if dlogits is not None:
+        assert dlogits.shape == (T, V) and dlogits.dtype == logits.dtype and (dlogits.stride(1) == 1 or V == 1)
+        ldd = dlogits.stride(0) if T > 1 else V
+    opts = _PolicyOpts(clip_low, clip_high, beta, temperature, grad_scale)
+    _check(lib().qerl_policy_loss(*args, _p(old_logp), _p(ref_logp), _p(advantages), _p(weights), C.byref(opts), _p(sums),
+                                  _p(logp), _p(entropy), _p(dlogits), ldd, _p(ws), ws.numel(), _stream(stream)),
+           "qerl_policy_loss")
+    return sums, logp, entropy, dlogits
+
+
+# ---------------------------------------------------------------- AdamW
+class _AdamTensor(C.Structure):
+    _fields_ = [("n", C.c_int64)] + [(n, C.c_void_p) for n in ("param", "master", "grad", "m", "v", "m_scale", "v_scale")] + [
+        ("lr_scale", C.c_double), ("weight_decay", C.c_double)]
+
+
+class _AdamFormat(C.Structure):
+    _fields_ = [("param_dtype", C.c_int), ("grad_dtype", C.c_int), ("state_bits", C.c_int)]
+
+
+class _AdamHyper(C.Structure):
+    _fields_ = [(n, C.c_double) for n in ("lr", "beta1", "beta2", "eps", "max_grad_norm")] + [
+        ("step", C.c_int64), ("seed", C.c_uint64)]
+
+
+class AdamW:
+    """AdamW over many tensors at once (qerl_adamw_plan / _step).
+
+    params: contiguous f32 tensors, or bf16 ones with f32 `masters`; grads: f32 or
+    bf16 of the same shapes.  State: state_bits 32 or 8 allocates zeros (in m, v,
+    m_scale, v_scale: lists of tensors); given lists are used as they are, and
+    their type (float32 or uint8) sets the bits.  lr_scale and weight_decay: one
+    number, or one per tensor.  The tensors are kept referenced."""
+
+    BLOCK = 256
+
+    def __init__(self, params, grads, masters=None, state_bits: int = 32, m=None, v=None, m_scale=None, v_scale=None,
+                 betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01, lr_scale=1.0, ws=None):
+        self._h = None
+        n = len(params)
+        assert n > 0 and len(grads) == n and (masters is None or len(masters) == n)
+        if m is not None:
+            state_bits = 8 if m[0].dtype == torch.uint8 else 32
+        sdt = torch.uint8 if state_bits == 8 else torch.float32
+        new = lambda: [torch.zeros(p.numel(), dtype=sdt, device=p.device) for p in params]  # noqa: E731
+        news = lambda: [torch.zeros(-(-p.numel() // self.BLOCK), dtype=torch.float32, device=p.device) for p in params]  # noqa: E731
+        self.params, self.grads, self.masters = list(params), list(grads), masters
+        self.m = new() if m is None else list(m)
+        self.v = new() if v is None else list(v)
+        self.m_scale = self.v_scale = [None] * n
+        if state_bits == 8:
+            self.m_scale = news() if m_scale is None else list(m_scale)
+            self.v_scale = news() if v_scale is None else list(v_scale)
+        per = lambda x: [float(x)] * n if isinstance(x, (int, float)) else [float(k) for k in x]  # noqa: E731
+        lrs, wds = per(lr_scale), per(weight_decay)
+        assert len(lrs) == n and len(wds) == n
+        table = (_AdamTensor * n)()
+        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        for i in range(n):
+            p, g, w, c = params[i], grads[i], None if masters is None else masters[i], params[i].numel()
+            assert p.dtype == params[0].dtype and g.dtype == grads[0].dtype and p.dtype in _DTYPES and g.dtype in _DTYPES
+            assert (w is None) == (p.dtype == torch.float32) and (w is None or w.dtype == torch.float32)
+            blocks = -(-c // self.BLOCK)
+            for t, size, dt in ((p, c, p.dtype), (g, c, g.dtype), (w, c, torch.float32), (self.m[i], c, sdt), (self.v[i], c, sdt),
+                                (self.m_scale[i], blocks, torch.float32), (self.v_scale[i], blocks, torch.float32)):
+                assert t is None or (t.numel() == size and t.dtype == dt and t.is_contiguous())
+            table[i] = _AdamTensor(c, ptr(p), ptr(w), ptr(g), ptr(self.m[i]), ptr(self.v[i]), ptr(self.m_scale[i]),
+                                   ptr(self.v_scale[i]), lrs[i], wds[i])
+        nbytes = lib().qerl_adamw_ws_bytes(C.cast(table, C.c_void_p), n)
+        if nbytes == 0:
+            raise QerlError(1, "qerl_adamw_ws_bytes")
+        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=params[0].device) if ws is None else ws
+        fmt = _AdamFormat(_DTYPES[params[0].dtype], _DTYPES[grads[0].dtype], state_bits)
+        h = C.c_void_p()
+        _check(lib().qerl_adamw_plan(C.cast(table, C.c_void_p), n, C.byref(fmt), _p(self.ws), self.ws.numel(), C.byref(h)),
+               "qerl_adamw_plan")
+        self._h = h
+        self._flat = sum(-(-p.numel() // self.BLOCK) for p in params[:-1]) * self.BLOCK + params[-1].numel()
+        self._hyper = _AdamHyper(0.0, betas[0], betas[1], eps, 0.0, 1, 0)
+
+    def step(self, lr: float, step: int, seed: int = 0, max_grad_norm: float = 0.0, grad_norm=None, stream=None):
+        """Step number `step` (1, 2, ...) with the gradients in place; max_grad_norm > 0 clips by the norm of all of
+        them, which goes to grad_norm (f32 [1]) if given."""
+        hy = self._hyper
+        hy.lr, hy.step, hy.seed, hy.max_grad_norm = lr, step, seed, max_grad_norm
+        _check(lib().qerl_adamw_step(self._h, C.byref(hy), _p(grad_norm), _stream(stream)), "qerl_adamw_step")
+
+    def read_state(self, m_out, v_out, stream=None):
+        """The values of the 8-bit states, f32 or bf16: the tensors in order, each from a multiple of 256 elements on."""
+        size = self._flat
+        assert m_out.dtype == v_out.dtype and m_out.dtype in _DTYPES and m_out.is_contiguous() and v_out.is_contiguous()
+        assert m_out.numel() >= size and v_out.numel() >= size
+        _check(lib().qerl_adamw_read_state(self._h, _p(m_out), _p(v_out), _DTYPES[m_out.dtype], _stream(stream)),
+               "qerl_adamw_read_state")
+
+    def close(self):
+        if self._h:
+            lib().qerl_adamw_destroy(self._h)
             self._h = None
 
     def __del__(self):

@@ -1,0 +1,554 @@
+// One AdamW step over many tensors (the LoRA adapters), FP32 or 8-bit states.
+//
+//   g = c grad                      c = min(1, max_norm / |grad|) over all tensors, or 1
+//   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
+//   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// Elementwise and bound by HBM: with a bf16 parameter beside its FP32 master an
+// element moves 30 bytes with FP32 states and 18 with 8-bit ones (plus 8/256 of
+// scales), for some 70 instructions.  A warp owns one block of 256 elements,
+// eight per lane, so every access is a 16-byte vector and a block's largest
+// magnitude is one warp reduction; a CTA takes 32 blocks of one tensor.
+//
+// 8-bit states, per block of 256 with an FP32 scale: m as sign, 3 exponent and 4
+// mantissa bits; sqrt(v) (half of v's exponent range) as 3 exponent and 5
+// mantissa bits, both with subnormals, and scale = (block's largest) / (largest
+// code value).  A code's bits placed at the FP32 mantissa's top are the value
+// times 2^-120, subnormals included, so both directions are a shift and two
+// multiplies.  Rounding is stochastic: b2 = 0.999 moves sqrt(v) by about 0.0005
+// of itself a step, far below half a code step (1/128), so rounding to nearest
+// would freeze v within a few steps.  The random bits are Philox4x32-10
+// (Salmon et al., SC'11) of (element / 4, tensor, step) under the key `seed`.
+// A nonzero sqrt(v) keeps a code of at least 1: zero would leave only eps below m.
+//
+// Every product, sum, division and root that reaches a code is rounded by itself
+// (no contraction), so the codes do not depend on the compiler's choices.
+#include <math.h>
+
+#include <new>
+
+#include "common.cuh"
+
+namespace qerl {
+namespace {
+
+constexpr int kBlk = 256;             // elements that share a scale
+constexpr int kThreads = 256;         // 8 warps
+constexpr int kChunkBlks = 32;        // blocks per CTA: 4 per warp
+constexpr int kNormThreads = 512;
+constexpr int kNormCtasMax = 1024;    // partial sums of the global norm
+constexpr float kTopM = 1.9375f, kTopV = 1.96875f;  // largest code values: 2 - 2^-4, 2 - 2^-5
+constexpr float kTiny = 7.888609052210118e-31f;     // 2^-100: smaller blocks are stored as zero
+
+// One tensor as the kernels see it.
+struct Rec {
+    int64_t n;
+    void *param;
+    float *master;
+    const void *grad;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    double lr_scale, weight_decay;
+    int64_t first_blk;  // blocks of the tensors before it
+};
+struct Chunk {
+    uint32_t tensor, blk;  // blocks [blk, blk + kChunkBlks) of the tensor
+};
+
+// Per-step values, rounded once to FP32 from the doubles of the call.
+struct Step {
+    double lr, bc1;  // lr and 1 - b1^t
+    float b1, c1, b2, c2, rs2, eps;
+    uint32_t key0, key1, t;
+};
+
+__device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint32_t k0, uint32_t k1)
+{
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint32_t h0 = __umulhi(0xD2511F53u, c.x), l0 = 0xD2511F53u * c.x;
+        const uint32_t h1 = __umulhi(0xCD9E8D57u, c.z), l1 = 0xCD9E8D57u * c.z;
+        c = make_uint4(h1 ^ c.y ^ k0, l1, h0 ^ c.w ^ k1, l0);
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return c;
+}
+
+constexpr float kUp = 1.329227995784916e+36f;    // 2^120
+constexpr float kDown = 7.52316384526264e-37f;   // 2^-120
+
+// Value of a code with 3 exponent and BITS mantissa bits, in [0, 2).
+template <int BITS>
+__device__ __forceinline__ float code_value(uint32_t code)
+{
+    return __fmul_rn(__uint_as_float(code << (23 - BITS)), kUp);
+}
+// Code of x in [0, top], rounded up with the probability of the part it drops.
+template <int BITS>
+__device__ __forceinline__ uint32_t to_code(float y, uint32_t rnd16)
+{
+    constexpr int DROP = 23 - BITS;
+    const uint32_t u = __float_as_uint(__fmul_rn(y, kDown)) + (rnd16 << (DROP - 16)) + (1u << (DROP - 17));
+    return min(u >> DROP, (8u << BITS) - 1u);
+}
+
+// Eight consecutive elements of a lane, in FP32.
+template <bool BF16>
+__device__ __forceinline__ void load8(const void *p, int64_t i, int64_t n, bool full, float (&o)[8])
+{
+    if (full) {
+        if (BF16) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + i);
+            o[0] = bf16lo(a.x), o[1] = bf16hi(a.x), o[2] = bf16lo(a.y), o[3] = bf16hi(a.y);
+            o[4] = bf16lo(a.z), o[5] = bf16hi(a.z), o[6] = bf16lo(a.w), o[7] = bf16hi(a.w);
+        } else {
+            const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+            const float4 b = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + 4);
+            o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            o[j] = i + j < n ? (BF16 ? bf16f(static_cast<const __nv_bfloat16 *>(p)[i + j]) : static_cast<const float *>(p)[i + j])
+                             : 0.0f;
+    }
+}
+template <bool BF16>
+__device__ __forceinline__ void store8(void *p, int64_t i, int64_t n, bool full, const float (&o)[8])
+{
+    if (full) {
+        if (BF16) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * j], o[2 * j + 1]);
+                w[j] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = make_float4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<float4 *>(static_cast<float *>(p) + i + 4) = make_float4(o[4], o[5], o[6], o[7]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (i + j < n) {
+                if (BF16)
+                    static_cast<__nv_bfloat16 *>(p)[i + j] = __float2bfloat16_rn(o[j]);
+                else
+                    static_cast<float *>(p)[i + j] = o[j];
+            }
+    }
+}
+__device__ __forceinline__ uint2 load_codes(const void *p, int64_t i, int64_t n, bool full)
+{
+    const uint8_t *c = static_cast<const uint8_t *>(p);
+    if (full) return *reinterpret_cast<const uint2 *>(c + i);
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (i + j < n) w[j / 4] |= (uint32_t)c[i + j] << (8 * (j % 4));
+    return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void store_codes(void *p, int64_t i, int64_t n, bool full, const uint32_t (&w)[2])
+{
+    uint8_t *c = static_cast<uint8_t *>(p);
+    if (full) {
+        *reinterpret_cast<uint2 *>(c + i) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (i + j < n) c[i + j] = (uint8_t)(w[j / 4] >> (8 * (j % 4)));
+    }
+}
+__device__ __forceinline__ uint32_t code_byte(const uint2 w, int j) { return ((j < 4 ? w.x : w.y) >> (8 * (j % 4))) & 255u; }
+
+// Largest FP32 bit pattern of non-negative values over a warp (a NaN is the largest).
+__device__ __forceinline__ float warp_top(float x) { return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x))); }
+
+// Scale of a block and its inverse (both 0 for a block below 2^-100).
+__device__ __forceinline__ float block_scale(float amax, float top, float &inv)
+{
+    const bool tiny = amax < kTiny;
+    inv = tiny ? 0.0f : __fdiv_rn(top, amax);
+    return tiny ? 0.0f : __fdiv_rn(amax, top);
+}
+
+// clip: nullptr, or {c, skip flag} from norm_kernel.
+template <bool PB, bool GB, bool S8>
+__global__ void __launch_bounds__(kThreads) step_kernel(const Rec *recs, const Chunk *chunks, Step st, const float *clip)
+{
+    __shared__ float s_lr, s_decay;
+    pdl_trigger();
+    const Chunk ch = chunks[gridDim.x - 1 - blockIdx.x];  // from the end: what the norm's pass read last is in L2
+    const Rec &R = recs[ch.tensor];
+    if (threadIdx.x == 0) {
+        const double lr = __dmul_rn(st.lr, R.lr_scale);
+        s_lr = (float)__ddiv_rn(lr, st.bc1);
+        s_decay = (float)__dadd_rn(1.0, -__dmul_rn(lr, R.weight_decay));
+    }
+    __syncthreads();
+    const float step_size = s_lr, decay = s_decay;
+    pdl_wait();
+    float coef = 1.0f;
+    if (clip) {
+        if (clip[1] != 0.0f) return;  // the norm is not finite: the step is skipped
+        coef = clip[0];
+    }
+    const int64_t n = R.n;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    float *const p32 = PB ? R.master : static_cast<float *>(R.param);
+    for (int b = warp; b < kChunkBlks; b += kThreads / 32) {
+        const int64_t blk = (int64_t)ch.blk + b;
+        if (blk * kBlk >= n) break;
+        const int64_t i = blk * kBlk + lane * 8;
+        const bool full = i + 8 <= n;
+        float g[8], p[8], m[8], v[8];
+        load8<GB>(R.grad, i, n, full, g);
+        load8<false>(p32, i, n, full, p);
+        if (S8) {
+            const uint2 cm = load_codes(R.m, i, n, full), cv = load_codes(R.v, i, n, full);
+            const float ms = R.m_scale[blk], vs = R.v_scale[blk];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t a = code_byte(cm, j);
+                const float x = __fmul_rn(code_value<4>(a & 127u), ms);
+                m[j] = a & 128u ? -x : x;
+                const float s = __fmul_rn(code_value<5>(code_byte(cv, j)), vs);
+                v[j] = __fmul_rn(s, s);
+            }
+        } else {
+            load8<false>(R.m, i, n, full, m);
+            load8<false>(R.v, i, n, full, v);
+        }
+        float root[8], mtop = 0.0f, vtop = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float gc = clip ? __fmul_rn(g[j], coef) : g[j];
+            m[j] = __fadd_rn(__fmul_rn(m[j], st.b1), __fmul_rn(gc, st.c1));
+            v[j] = __fadd_rn(__fmul_rn(v[j], st.b2), __fmul_rn(__fmul_rn(gc, gc), st.c2));
+            root[j] = __fsqrt_rn(v[j]);
+            const float den = __fadd_rn(__fmul_rn(root[j], st.rs2), st.eps);
+            p[j] = __fsub_rn(__fmul_rn(p[j], decay), __fmul_rn(step_size, __fdividef(m[j], den)));
+            if (S8) {
+                mtop = __uint_as_float(max(__float_as_uint(mtop), __float_as_uint(fabsf(m[j]))));
+                vtop = __uint_as_float(max(__float_as_uint(vtop), __float_as_uint(root[j])));
+            }
+        }
+        store8<false>(p32, i, n, full, p);
+        if (PB) store8<true>(R.param, i, n, full, p);
+        if (S8) {
+            float im, iv;
+            const float sm = block_scale(warp_top(mtop), kTopM, im), sv = block_scale(warp_top(vtop), kTopV, iv);
+            uint32_t wm[2] = {0, 0}, wv[2] = {0, 0};
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const uint64_t grp = (uint64_t)(i / 4) + q;
+                const uint4 r4 = philox4x32_10(make_uint4((uint32_t)grp, (uint32_t)(grp >> 32), ch.tensor, st.t), st.key0, st.key1);
+                const uint32_t r[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = 4 * q + k;
+                    uint32_t a = to_code<4>(__fmul_rn(fabsf(m[j]), im), r[k] & 0xFFFFu);
+                    if (m[j] < 0.0f && a) a |= 128u;
+                    uint32_t c = to_code<5>(__fmul_rn(root[j], iv), r[k] >> 16);
+                    if (iv != 0.0f && root[j] > 0.0f && c == 0) c = 1;
+                    wm[q] |= a << (8 * k);
+                    wv[q] |= c << (8 * k);
+                }
+            }
+            store_codes(R.m, i, n, full, wm);
+            store_codes(R.v, i, n, full, wv);
+            if (lane == 0) {
+                R.m_scale[blk] = sm;
+                R.v_scale[blk] = sv;
+            }
+        } else {
+            store8<false>(R.m, i, n, full, m);
+            store8<false>(R.v, i, n, full, v);
+        }
+    }
+}
+
+// Global norm of the gradients: sum of squares as an unevaluated pair of floats
+// per thread (the product's and the sum's rounding errors are kept: Dekker's and
+// Knuth's exact transformations), joined in double in a fixed order, so that the
+// norm is the same on every run and right to FP32's last bit.  The last CTA to
+// arrive joins the partial sums and resets the counter.
+// out: {c, 1 if the norm is not finite}; norm_out may be null.
+template <bool GB>
+__global__ void __launch_bounds__(kNormThreads)
+    norm_kernel(const Rec *recs, const Chunk *chunks, uint32_t n_chunks, double max_norm, double *partial, unsigned int *arrived,
+                float *out, float *norm_out)
+{
+    __shared__ double s_sum[kNormThreads / 32];
+    __shared__ bool s_last;
+    pdl_trigger();
+    pdl_wait();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    float s = 0.0f, e = 0.0f;
+    for (uint32_t k = blockIdx.x; k < n_chunks; k += gridDim.x) {
+        const Chunk ch = chunks[k];
+        const Rec &R = recs[ch.tensor];
+        const int64_t n = R.n;
+        for (int b = warp; b < kChunkBlks; b += kNormThreads / 32) {
+            const int64_t i = ((int64_t)ch.blk + b) * kBlk + lane * 8;
+            if (i >= n) break;
+            float g[8];
+            load8<GB>(R.grad, i, n, i + 8 <= n, g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float p = __fmul_rn(g[j], g[j]);
+                const float pe = __fmaf_rn(g[j], g[j], -p);
+                const float t = __fadd_rn(s, p);
+                const float bb = __fsub_rn(t, s);
+                const float se = __fadd_rn(__fsub_rn(s, __fsub_rn(t, bb)), __fsub_rn(p, bb));
+                s = t;
+                e = __fadd_rn(e, __fadd_rn(pe, se));
+            }
+        }
+    }
+    // An overflowed sum leaves NaN in its error term; the sum itself tells.
+    double d = isfinite(s) ? (double)s + (double)e : (double)s;
+    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
+    if (lane == 0) s_sum[warp] = d;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double t = 0.0;
+        for (int w = 0; w < kNormThreads / 32; ++w) t += s_sum[w];
+        partial[blockIdx.x] = t;
+        __threadfence();
+        s_last = atomicAdd(arrived, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    double t = 0.0;
+    for (unsigned int k = threadIdx.x; k < gridDim.x; k += kNormThreads) t += __ldcg(partial + k);
+    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    if (lane == 0) s_sum[warp] = t;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double total = 0.0;
+        for (int w = 0; w < kNormThreads / 32; ++w) total += s_sum[w];
+        const double norm = sqrt(total);
+        out[0] = (float)(norm > max_norm ? max_norm / norm : 1.0);
+        out[1] = isfinite(norm) ? 0.0f : 1.0f;
+        if (norm_out) *norm_out = (float)norm;
+        *arrived = 0;
+    }
+}
+
+// The values the 8-bit codes stand for, every tensor from a multiple of 256 on.
+template <bool OB>
+__global__ void __launch_bounds__(kThreads) read_kernel(const Rec *recs, const Chunk *chunks, void *m_out, void *v_out)
+{
+    pdl_trigger();
+    pdl_wait();
+    const Chunk ch = chunks[blockIdx.x];
+    const Rec &R = recs[ch.tensor];
+    const int64_t n = R.n;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    for (int b = warp; b < kChunkBlks; b += kThreads / 32) {
+        const int64_t blk = (int64_t)ch.blk + b;
+        if (blk * kBlk >= n) break;
+        const int64_t i = blk * kBlk + lane * 8, to = (R.first_blk + blk) * kBlk + lane * 8;
+        const bool full = i + 8 <= n;
+        const uint2 cm = load_codes(R.m, i, n, full), cv = load_codes(R.v, i, n, full);
+        const float ms = R.m_scale[blk], vs = R.v_scale[blk];
+        float m[8], v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t a = code_byte(cm, j);
+            const float x = __fmul_rn(code_value<4>(a & 127u), ms);
+            m[j] = a & 128u ? -x : x;
+            const float s = __fmul_rn(code_value<5>(code_byte(cv, j)), vs);
+            v[j] = __fmul_rn(s, s);
+        }
+        store8<OB>(m_out, to, to + n - i, full, m);
+        store8<OB>(v_out, to, to + n - i, full, v);
+    }
+}
+
+size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
+
+struct Layout {
+    size_t recs, chunks, partial, clip, counter, total;
+    int64_t n_chunks;
+};
+
+// false: a negative or too large size.
+bool layout(const qerl_adamw_tensor *t, int64_t n, Layout &lo)
+{
+    int64_t chunks = 0;
+    for (int64_t k = 0; k < n; ++k) {
+        if (t[k].n < 0 || t[k].n > (int64_t(1) << 38)) return false;
+        chunks += (t[k].n + int64_t(kBlk) * kChunkBlks - 1) / (int64_t(kBlk) * kChunkBlks);
+    }
+    if (chunks > 0x7FFFFFFF) return false;
+    lo.n_chunks = chunks;
+    lo.recs = 0;
+    lo.chunks = round256(sizeof(Rec) * (size_t)n);
+    lo.partial = lo.chunks + round256(sizeof(Chunk) * (size_t)chunks);
+    lo.clip = lo.partial + sizeof(double) * kNormCtasMax;
+    lo.counter = lo.clip + 256;
+    lo.total = lo.counter + 256;
+    return true;
+}
+
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+}  // namespace
+}  // namespace qerl
+
+using namespace qerl;
+
+struct qerl_adamw {
+    Rec *recs;
+    Chunk *chunks;
+    double *partial;
+    float *clip;
+    unsigned int *counter;
+    uint32_t n_chunks;
+    qerl_adamw_format fmt;
+    int device;
+};
+
+extern "C" size_t qerl_adamw_ws_bytes(const qerl_adamw_tensor *tensors, int64_t n_tensors)
+{
+    Layout lo;
+    if (!tensors || n_tensors < 1 || n_tensors > (1 << 24) || !layout(tensors, n_tensors, lo)) return 0;
+    return lo.total;
+}
+
+extern "C" qerl_status qerl_adamw_plan(const qerl_adamw_tensor *tensors, int64_t n_tensors, const qerl_adamw_format *format,
+                                       void *ws, size_t ws_bytes, qerl_adamw **plan)
+{
+    if (!plan) return QERL_ERR_INVALID_ARG;
+    *plan = nullptr;
+    if (!tensors || !format || n_tensors < 1 || n_tensors > (1 << 24)) return QERL_ERR_INVALID_ARG;
+    const auto dtype_ok = [](int d) { return d == QERL_DTYPE_F32 || d == QERL_DTYPE_BF16; };
+    if (!dtype_ok(format->param_dtype) || !dtype_ok(format->grad_dtype) || (format->state_bits != 8 && format->state_bits != 32))
+        return QERL_ERR_INVALID_ARG;
+    const bool pb = format->param_dtype == QERL_DTYPE_BF16, s8 = format->state_bits == 8;
+    Layout lo;
+    if (!layout(tensors, n_tensors, lo)) return QERL_ERR_SHAPE;
+    for (int64_t k = 0; k < n_tensors; ++k) {
+        const qerl_adamw_tensor &t = tensors[k];
+        if (!isfinite(t.lr_scale) || !isfinite(t.weight_decay)) return QERL_ERR_INVALID_ARG;
+        if (t.n == 0) continue;
+        if (!t.param || !t.grad || !t.m || !t.v || pb != (t.master != nullptr) || (s8 && (!t.m_scale || !t.v_scale)))
+            return QERL_ERR_INVALID_ARG;
+        if (!aligned16(t.param) || !aligned16(t.master) || !aligned16(t.grad) || !aligned16(t.m) || !aligned16(t.v) ||
+            (s8 && (!aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))))
+            return QERL_ERR_ALIGN;
+    }
+    if (!ws || ws_bytes < lo.total) return QERL_ERR_WORKSPACE;
+    if (!aligned16(ws)) return QERL_ERR_ALIGN;
+    QERL_TRY(check_device());
+
+    Rec *recs = new (std::nothrow) Rec[n_tensors];
+    Chunk *chunks = new (std::nothrow) Chunk[lo.n_chunks ? lo.n_chunks : 1];
+    qerl_adamw *h = new (std::nothrow) qerl_adamw;
+    qerl_status st = recs && chunks && h ? QERL_OK : QERL_ERR_HOST_MEMORY;
+    if (st == QERL_OK) {
+        int64_t c = 0, blk = 0;
+        for (int64_t k = 0; k < n_tensors; ++k) {
+            const qerl_adamw_tensor &t = tensors[k];
+            recs[k] = Rec{t.n, t.param, t.master, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.lr_scale, t.weight_decay, blk};
+            const int64_t nb = (t.n + kBlk - 1) / kBlk;
+            for (int64_t b = 0; b < nb; b += kChunkBlks) chunks[c++] = Chunk{(uint32_t)k, (uint32_t)b};
+            blk += nb;
+        }
+        char *W = static_cast<char *>(ws);
+        h->recs = reinterpret_cast<Rec *>(W + lo.recs);
+        h->chunks = reinterpret_cast<Chunk *>(W + lo.chunks);
+        h->partial = reinterpret_cast<double *>(W + lo.partial);
+        h->clip = reinterpret_cast<float *>(W + lo.clip);
+        h->counter = reinterpret_cast<unsigned int *>(W + lo.counter);
+        h->n_chunks = (uint32_t)lo.n_chunks;
+        h->fmt = *format;
+        cudaGetDevice(&h->device);
+        if (cudaMemcpy(h->recs, recs, sizeof(Rec) * n_tensors, cudaMemcpyHostToDevice) != cudaSuccess ||
+            (lo.n_chunks &&
+             cudaMemcpy(h->chunks, chunks, sizeof(Chunk) * lo.n_chunks, cudaMemcpyHostToDevice) != cudaSuccess) ||
+            cudaMemset(h->counter, 0, 256) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)
+            st = QERL_ERR_CUDA;
+    }
+    delete[] recs;
+    delete[] chunks;
+    if (st != QERL_OK) {
+        delete h;
+        return st;
+    }
+    *plan = h;
+    return QERL_OK;
+}
+
+namespace {
+using StepFn = void (*)(const Rec *, const Chunk *, Step, const float *);
+StepFn step_fn(bool pb, bool gb, bool s8)
+{
+    static const StepFn fns[8] = {step_kernel<false, false, false>, step_kernel<false, false, true>, step_kernel<false, true, false>,
+                                  step_kernel<false, true, true>,   step_kernel<true, false, false>, step_kernel<true, false, true>,
+                                  step_kernel<true, true, false>,   step_kernel<true, true, true>};
+    return fns[(pb ? 4 : 0) + (gb ? 2 : 0) + (s8 ? 1 : 0)];
+}
+}  // namespace
+
+extern "C" qerl_status qerl_adamw_step(const qerl_adamw *h, const qerl_adamw_hyper *hy, float *grad_norm, qerl_stream_t stream)
+{
+    if (!h || !hy) return QERL_ERR_INVALID_ARG;
+    if (hy->step < 1 || hy->step > 0xFFFFFFFFll || !isfinite(hy->lr) || !(hy->beta1 >= 0.0 && hy->beta1 < 1.0) ||
+        !(hy->beta2 >= 0.0 && hy->beta2 < 1.0) || !(hy->eps >= 0.0) || !isfinite(hy->eps) || !(hy->max_grad_norm >= 0.0) ||
+        (grad_norm && hy->max_grad_norm == 0.0))
+        return QERL_ERR_INVALID_ARG;
+    if (!aligned(grad_norm, 4)) return QERL_ERR_ALIGN;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return QERL_ERR_CUDA;
+    if (dev != h->device) return QERL_ERR_INVALID_ARG;
+    if (h->n_chunks == 0 && hy->max_grad_norm == 0.0) return QERL_OK;
+    Step st;
+    st.lr = hy->lr;
+    st.bc1 = 1.0 - pow(hy->beta1, (double)hy->step);
+    st.b1 = (float)hy->beta1;
+    st.c1 = (float)(1.0 - hy->beta1);
+    st.b2 = (float)hy->beta2;
+    st.c2 = (float)(1.0 - hy->beta2);
+    st.rs2 = (float)(1.0 / sqrt(1.0 - pow(hy->beta2, (double)hy->step)));
+    st.eps = (float)hy->eps;
+    st.key0 = (uint32_t)hy->seed;
+    st.key1 = (uint32_t)(hy->seed >> 32);
+    st.t = (uint32_t)hy->step;
+    const bool gb = h->fmt.grad_dtype == QERL_DTYPE_BF16, chain = g_chain.load() != 0, clip = hy->max_grad_norm > 0.0;
+    if (clip) {
+        int64_t grid = h->n_chunks ? h->n_chunks : 1;
+        if (grid > 4 * num_sms()) grid = 4 * num_sms();
+        if (grid > kNormCtasMax) grid = kNormCtasMax;
+        auto *fn = gb ? norm_kernel<true> : norm_kernel<false>;
+        QERL_TRY(launched(launch_k(fn, dim3((unsigned)grid), dim3(kNormThreads), 0, as_cuda(stream), chain, (const Rec *)h->recs,
+                                   (const Chunk *)h->chunks, h->n_chunks, hy->max_grad_norm, h->partial, h->counter, h->clip,
+                                   grad_norm)));
+    }
+    if (h->n_chunks == 0) return QERL_OK;
+    return launched(launch_k(step_fn(h->fmt.param_dtype == QERL_DTYPE_BF16, gb, h->fmt.state_bits == 8), dim3(h->n_chunks),
+                             dim3(kThreads), 0, as_cuda(stream), chain, (const Rec *)h->recs, (const Chunk *)h->chunks, st,
+                             clip ? (const float *)h->clip : (const float *)nullptr));
+}
+
+extern "C" qerl_status qerl_adamw_read_state(const qerl_adamw *h, void *m_out, void *v_out, int out_dtype, qerl_stream_t stream)
+{
+    if (!h || !m_out || !v_out || (out_dtype != QERL_DTYPE_F32 && out_dtype != QERL_DTYPE_BF16) || h->fmt.state_bits != 8)
+        return QERL_ERR_INVALID_ARG;
+    if (!aligned16(m_out) || !aligned16(v_out)) return QERL_ERR_ALIGN;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return QERL_ERR_CUDA;
+    if (dev != h->device) return QERL_ERR_INVALID_ARG;
+    if (h->n_chunks == 0) return QERL_OK;
+    auto *fn = out_dtype == QERL_DTYPE_BF16 ? read_kernel<true> : read_kernel<false>;
+    return launched(launch_k(fn, dim3(h->n_chunks), dim3(kThreads), 0, as_cuda(stream), g_chain.load() != 0, (const Rec *)h->recs,
+                             (const Chunk *)h->chunks, m_out, v_out));
+}
+
+extern "C" void qerl_adamw_destroy(qerl_adamw *h) { delete h; }

@@ -85,6 +85,7 @@ extern "C" const char *qerl_status_string(qerl_status s)
     case QERL_ERR_TIMEOUT: return "bounded device wait timed out";
     case QERL_ERR_UNSUPPORTED_DEVICE: return "device is not compute capability 10.3 (GB300)";
     case QERL_ERR_WORKSPACE: return "workspace missing or too small";
+    case QERL_ERR_HOST_MEMORY: return "no host memory for a plan";
     case QERL_ERR_TOO_LARGE: return "problem needs more scratch than the fixed no-allocation buffer holds";
     }
     return "unknown status";
@@ -98,6 +99,7 @@ extern "C" size_t qerl_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, 
     case QERL_OP_QUANTIZE: return 4096;  // per-CTA amax partials (<= 1024 words)
     case QERL_OP_AQN_RMSNORM: return round256(size_t(K) * sizeof(float));  // K = H: noisy scale
     case QERL_OP_LINEAR_FWD: return linear_fwd_ws_bytes(M, N, K, r);
+    case QERL_OP_POLICY_LOSS: return round256(size_t(M) * 3 * sizeof(float)) + 256;  // M = tokens: their loss terms
     case QERL_OP_LINEAR_BWD: return linear_bwd_ws_bytes(M, N, K, r);
     case QERL_OP_MXFP4_FWD:
     case QERL_OP_LINEAR_FWD_F32AB: return variant_fwd_ws_bytes(op, M, N, K, r);

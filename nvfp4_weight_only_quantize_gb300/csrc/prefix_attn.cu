@@ -1,0 +1,384 @@
+// Attention of a batch whose sequences share long prefixes (the prompt of a
+// group of sampled answers): every query row sees its group's prefix and, causally,
+// its own sequence's suffix, in one softmax.
+//
+//   a_k = scale q . k_k,  lse = log sum_k e^(a_k),  out = sum_k e^(a_k - lse) v_k
+//
+// The prefix's keys and values are read once for all the group's sequences: their
+// query rows share its tiles.  Segments are cut along the keys into chunks that
+// run side by side; each leaves (o, m, l) in the workspace and a second kernel
+// joins a row's parts.
+#include <float.h>
+#include <math.h>
+
+#include "prefix_attn.cuh"
+#include "sm100_ptx.cuh"
+
+namespace qerl {
+namespace attn {
+namespace {
+
+// ------------------------------------------------------------------ chunks of up to 16 rows
+constexpr int kWarps = 4;    // a warp takes every fourth 16-key tile of the chunk
+constexpr int kStages = 3;   // tiles in flight per warp
+constexpr int kTile = 16;
+
+template <int D>
+constexpr int smem_bytes()
+{
+    return kWarps * kStages * kTile * D * 2 * 2;
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool take)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// One CTA: up to 16 query rows that share a kv head, one chunk of a segment's
+// keys.  Each warp streams its own 16-key tiles through a ring of cp.async
+// stages (no barrier between warps until the end) and keeps its own softmax
+// statistics; the warps' results are joined in shared memory.
+// Probabilities are rounded to bf16 for the second product, as its operands are
+// bf16; their sum l stays in FP32.
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32) rows16_kernel(const Args a, int prefix_items)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    pdl_trigger();
+    pdl_wait();
+    // which rows, which keys
+    int item = blockIdx.x;
+    const bool pre = item < prefix_items;
+    if (!pre) item -= prefix_items;
+    const int n_parts = pre ? a.n_pp : a.n_sp, tiles = pre ? a.p_tiles : a.s_tiles;
+    const int part = item % n_parts;
+    int rest = item / n_parts;
+    const int tile = rest % tiles;
+    rest /= tiles;
+    const int hk = rest % a.Hkv, seg = rest / a.Hkv;  // seg: group or sequence
+    const int len = pre ? prefix_len(a, seg) : suffix_len(a, seg);
+    const int k_lo = part * (pre ? a.p_chunk : a.s_chunk);
+    if (k_lo >= len) return;
+    const int k_hi = min(len, k_lo + (pre ? a.p_chunk : a.s_chunk));
+    const int n_rows = (pre ? a.G : 1) * a.Lq * a.gs;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t tk = pre ? a.kp_t : a.ks_t, tv = pre ? a.vp_t : a.vs_t;
+    const __nv_bfloat16 *K = pre ? a.kp + seg * a.kp_g + hk * a.kp_h : a.ks + seg * a.ks_b + hk * a.ks_h;
+    const __nv_bfloat16 *V = pre ? a.vp + seg * a.vp_g + hk * a.vp_h : a.vs + seg * a.vs_b + hk * a.vs_h;
+
+    constexpr int CH = D / 8;                 // 16-byte chunks per key row
+    constexpr int STAGE = kTile * D * 2 * 2;  // K tile, V tile
+    const uint32_t ring = ptx::smem_u32(smem) + warp * kStages * STAGE;
+    const int n_tiles = (k_hi - k_lo + kTile - 1) / kTile;
+    const int mine = n_tiles > warp ? (n_tiles - warp + kWarps - 1) / kWarps : 0;
+    auto fetch = [&](int j) {
+        if (j < mine) {
+            const int k0 = k_lo + (j * kWarps + warp) * kTile;
+            const uint32_t to = ring + (j % kStages) * STAGE;
+#pragma unroll
+            for (int c = 0; c < kTile * CH / 32; ++c) {
+                const int idx = c * 32 + lane, r = idx / CH, ch = idx % CH;
+                const bool in = k0 + r < k_hi;
+                const int64_t tok = in ? k0 + r : k_lo;
+                const uint32_t at = to + r * D * 2 + ((ch ^ (r & 7)) * 16);
+                cp16(at, K + tok * tk + ch * 8, in);
+                cp16(at + kTile * D * 2, V + tok * tv + ch * 8, in);
+            }
+        }
+        cp_commit();
+    };
+#pragma unroll
+    for (int j = 0; j < kStages - 1; ++j) fetch(j);
+
+    // query rows lane / 4 and lane / 4 + 8 of the tile
+    auto row_of = [&](int r, int &b, int &l, int &h) {
+        const int rr = tile * 16 + r;
+        const int bi = rr / (a.Lq * a.gs), in = rr % (a.Lq * a.gs);
+        b = pre ? seg * a.G + bi : seg;
+        l = in / a.gs;
+        h = hk * a.gs + in % a.gs;
+        return rr < n_rows;
+    };
+    uint32_t qf[D / 16][4];
+    int limit[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        int b, l, h;
+        const bool ok = row_of(lane / 4 + 8 * half, b, l, h);
+        limit[half] = pre ? len : len - a.Lq + 1 + l;
+        const __nv_bfloat16 *q = a.q + b * a.q_b + l * a.q_l + h * a.q_h + (lane % 4) * 2;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+            qf[s][half] = ok ? *reinterpret_cast<const uint32_t *>(q + s * 16) : 0u;
+            qf[s][half + 2] = ok ? *reinterpret_cast<const uint32_t *>(q + s * 16 + 8) : 0u;
+        }
+    }
+
+    float o[D / 8][4];
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
+    float m[2] = {kNone, kNone}, l[2] = {0.0f, 0.0f};
+    for (int j = 0; j < mine; ++j) {
+        cp_wait<kStages - 2>();
+        __syncwarp();
+        const uint32_t kt = ring + (j % kStages) * STAGE, vt = kt + kTile * D * 2;
+        float s[2][4] = {};
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+            const int key = (lane / 16) * 8 + lane % 8, ch = d * 2 + ((lane / 8) & 1);
+            uint32_t b[4];
+            ldsm4(kt + key * D * 2 + ((ch ^ (key & 7)) * 16), b);
+            mma(s[0], qf[d], b[0], b[1]);
+            mma(s[1], qf[d], b[2], b[3]);
+        }
+        const int k0 = k_lo + (j * kWarps + warp) * kTile + (lane % 4) * 2;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float x[4], top = kNone;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int k = k0 + (c / 2) * 8 + c % 2;
+                x[c] = k < min(limit[half], k_hi) ? s[c / 2][half * 2 + c % 2] * a.scale_log2 : -INFINITY;
+                top = fmaxf(top, x[c]);
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            const float to = fmaxf(m[half], top), f = ex2(m[half] - to);
+            m[half] = to;
+            l[half] *= f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                x[c] = ex2(x[c] - to);
+                l[half] += x[c];
+                s[c / 2][half * 2 + c % 2] = x[c];
+            }
+            if (__any_sync(0xFFFFFFFFu, f != 1.0f)) {
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) o[n][half * 2] *= f, o[n][half * 2 + 1] *= f;
+            }
+        }
+        const uint32_t p[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]), pack2(s[1][0], s[1][1]), pack2(s[1][2], s[1][3])};
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+            const int key = ((lane / 8) & 1) * 8 + lane % 8, ch = n * 2 + lane / 16;
+            uint32_t b[4];
+            ldsm4_t(vt + key * D * 2 + ((ch ^ (key & 7)) * 16), b);
+            mma(o[2 * n], p, b[0], b[1]);
+            mma(o[2 * n + 1], p, b[2], b[3]);
+        }
+        __syncwarp();
+        fetch(j + kStages - 1);
+    }
+    cp_wait<0>();
+    __syncthreads();
+
+    // join the warps: [warp][row][D] and [warp][row] (m, l) in the ring's memory
+    float *so = reinterpret_cast<float *>(smem);
+    float2 *sml = reinterpret_cast<float2 *>(smem + kWarps * 16 * D * 4);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        l[half] += __shfl_xor_sync(0xFFFFFFFFu, l[half], 1);
+        l[half] += __shfl_xor_sync(0xFFFFFFFFu, l[half], 2);
+        const int r = lane / 4 + 8 * half;
+        if (lane % 4 == 0) sml[warp * 16 + r] = make_float2(m[half], l[half]);
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+            *reinterpret_cast<float2 *>(so + (warp * 16 + r) * D + n * 8 + (lane % 4) * 2) =
+                make_float2(o[n][half * 2], o[n][half * 2 + 1]);
+    }
+    __syncthreads();
+    const int parts = a.n_pp + a.n_sp;
+    for (int r = warp; r < 16; r += kWarps) {
+        int b, li, h;
+        if (!row_of(r, b, li, h)) break;
+        float M = kNone, w[kWarps], L = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) M = fmaxf(M, sml[k * 16 + r].x);
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            w[k] = ex2(sml[k * 16 + r].x - M);
+            L = fmaf(w[k], sml[k * 16 + r].y, L);
+        }
+        const int64_t at = (((int64_t)b * a.Lq + li) * a.Hq + h) * parts + (pre ? 0 : a.n_pp) + part;
+        for (int d = lane; d < D; d += 32) {
+            float t = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) t = fmaf(w[k], so[(k * 16 + r) * D + d], t);
+            a.part_o[at * D + d] = t;
+        }
+        if (lane == 0) a.part_ml[at] = make_float2(M, L);
+    }
+}
+
+// ------------------------------------------------------------------ joining a row's parts
+// One warp per query row; the parts that exist follow from the lengths.
+template <int D>
+__global__ void __launch_bounds__(128) join_kernel(const Args a)
+{
+    pdl_trigger();
+    pdl_wait();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t row = (int64_t)blockIdx.x * 4 + warp;
+    if (row >= (int64_t)a.B * a.Lq * a.Hq) return;
+    const int h = (int)(row % a.Hq);
+    const int64_t bl = row / a.Hq;
+    const int l = (int)(bl % a.Lq), b = (int)(bl / a.Lq);
+    const int np = a.n_pp ? (prefix_len(a, b / a.G) + a.p_chunk - 1) / a.p_chunk : 0;
+    const int ns = a.n_sp ? (suffix_len(a, b) + a.s_chunk - 1) / a.s_chunk : 0;
+    const int64_t base = row * (a.n_pp + a.n_sp);
+    const auto at = [&](int k) { return base + (k < np ? k : a.n_pp + k - np); };
+    float M = kNone;
+    for (int k = lane; k < np + ns; k += 32) M = fmaxf(M, a.part_ml[at(k)].x);
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+    float L = 0.0f;
+    constexpr int E = D / 32;
+    float acc[E] = {};
+#pragma unroll 4
+    for (int k = 0; k < np + ns; ++k) {
+        const float2 ml = a.part_ml[at(k)];
+        const float w = ex2(ml.x - M);
+        L = fmaf(w, ml.y, L);
+        const float *p = a.part_o + at(k) * D + lane * E;
+        if (E == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(p);
+            acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
+            acc[E - 2] = fmaf(w, v.z, acc[E - 2]), acc[E - 1] = fmaf(w, v.w, acc[E - 1]);
+        } else {
+            const float2 v = *reinterpret_cast<const float2 *>(p);
+            acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
+        }
+    }
+    const float inv = L == 0.0f ? 0.0f : __fdividef(1.0f, L);  // a row that sees no key: zeros, lse -inf
+    uint32_t *out = reinterpret_cast<uint32_t *>(a.out + b * a.o_b + l * a.o_l + h * a.o_h + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) out[e / 2] = pack2(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0 && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : (float)((double)M * 0.6931471805599453 + (double)logf(L));
+}
+
+int ceil_div(int64_t x, int64_t y) { return (int)((x + y - 1) / y); }
+
+// Chunk lengths, tiles and parts of a call; false where a size is not covered.
+// Chunks: about four CTAs per SM over all rows and keys, 64 to 2048 keys each.
+bool shape(const qerl_prefix_attn_dims *d, Args &a)
+{
+    if (d->B < 1 || d->Lq < 1 || d->Hq < 1 || d->Hkv < 1 || d->n_prefix < 1 || d->P < 0 || d->S < 0) return false;
+    if ((d->D != 64 && d->D != 128) || d->Hq % d->Hkv || d->B % d->n_prefix) return false;
+    const int64_t big = 1 << 30;
+    if (d->B > big || d->Lq > big || d->Hq > 65536 || d->P > big || d->S > big || d->B * d->Lq > big / d->Hq) return false;
+    a.B = (int)d->B, a.Lq = (int)d->Lq, a.Hq = (int)d->Hq, a.Hkv = (int)d->Hkv, a.n_prefix = (int)d->n_prefix;
+    a.G = a.B / a.n_prefix, a.gs = a.Hq / a.Hkv, a.P = (int)d->P, a.S = (int)d->S;
+    a.p_tiles = ceil_div((int64_t)a.G * a.Lq * a.gs, 16);
+    a.s_tiles = ceil_div((int64_t)a.Lq * a.gs, 16);
+    const int64_t up = (int64_t)a.n_prefix * a.Hkv * a.p_tiles, us = (int64_t)a.B * a.Hkv * a.s_tiles;
+    const int64_t want = (up * a.P + us * a.S) / (4 * num_sms());
+    int64_t chunk = (want + 63) / 64 * 64;
+    chunk = chunk < 64 ? 64 : chunk > 2048 ? 2048 : chunk;
+    a.p_chunk = a.s_chunk = (int)chunk;
+    a.n_pp = ceil_div(a.P, chunk), a.n_sp = ceil_div(a.S, chunk);
+    return up * a.n_pp + us * a.n_sp < 0x7FFFFFFF;
+}
+size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
+size_t ml_bytes(const Args &a) { return round256((size_t)a.B * a.Lq * a.Hq * (a.n_pp + a.n_sp) * sizeof(float2)); }
+size_t ws_total(const Args &a, int64_t D)
+{
+    return ml_bytes(a) + (size_t)a.B * a.Lq * a.Hq * (a.n_pp + a.n_sp) * D * sizeof(float);
+}
+
+template <int D>
+qerl_status run(const Args &a, cudaStream_t s)
+{
+    const bool chain = g_chain.load() != 0;
+    const int64_t pi = (int64_t)a.n_prefix * a.Hkv * a.p_tiles * a.n_pp, si = (int64_t)a.B * a.Hkv * a.s_tiles * a.n_sp;
+    if (pi + si > 0) {
+        static const cudaError_t attr =
+            cudaFuncSetAttribute(rows16_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
+        if (attr != cudaSuccess) return QERL_ERR_CUDA;
+        QERL_TRY(launched(launch_k(rows16_kernel<D>, dim3((unsigned)(pi + si)), dim3(kWarps * 32), smem_bytes<D>(), s, chain, a, (int)pi)));
+    }
+    const int64_t rows = (int64_t)a.B * a.Lq * a.Hq;
+    return launched(launch_k(join_kernel<D>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, chain, a));
+}
+
+}  // namespace
+}  // namespace attn
+}  // namespace qerl
+
+using namespace qerl;
+
+extern "C" size_t qerl_prefix_attention_ws_bytes(const qerl_prefix_attn_dims *dims)
+{
+    attn::Args a = {};
+    if (!dims || !attn::shape(dims, a)) return 0;
+    const size_t n = attn::ws_total(a, dims->D);
+    return n ? n : 256;
+}
+
+extern "C" qerl_status qerl_prefix_attention(const qerl_prefix_attn_dims *d, const void *q, const void *k_prefix, const void *v_prefix,
+                                             const int32_t *prefix_lens, const void *k_suffix, const void *v_suffix,
+                                             const int32_t *suffix_lens, float scale, void *out, float *lse, void *ws, size_t ws_bytes,
+                                             qerl_stream_t stream)
+{
+    if (!d || !q || !out || !(scale > 0.0f) || !(scale <= FLT_MAX)) return QERL_ERR_INVALID_ARG;
+    attn::Args a = {};
+    if (!attn::shape(d, a)) return QERL_ERR_SHAPE;
+    if ((a.P && (!k_prefix || !v_prefix)) || (a.S && (!k_suffix || !v_suffix || !suffix_lens))) return QERL_ERR_INVALID_ARG;
+    const int64_t *const strides[] = {d->q_stride, d->out_stride, d->k_prefix_stride, d->v_prefix_stride, d->k_suffix_stride, d->v_suffix_stride};
+    for (int t = 0; t < 6; ++t)
+        for (int k = 0; k < 3; ++k) {
+            if (strides[t][k] < 0 || strides[t][k] > (int64_t(1) << 40)) return QERL_ERR_SHAPE;
+            if (strides[t][k] % 8) return QERL_ERR_ALIGN;
+        }
+    if (!aligned16(q) || !aligned16(out) || !aligned16(k_prefix) || !aligned16(v_prefix) || !aligned16(k_suffix) || !aligned16(v_suffix) ||
+        (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(prefix_lens) & 3u) ||
+        (reinterpret_cast<uintptr_t>(suffix_lens) & 3u))
+        return QERL_ERR_ALIGN;
+    if (!ws || ws_bytes < qerl_prefix_attention_ws_bytes(d)) return QERL_ERR_WORKSPACE;
+    if (!aligned16(ws)) return QERL_ERR_ALIGN;
+    QERL_TRY(check_device());
+    const auto bf = [](const void *p) { return static_cast<const __nv_bfloat16 *>(p); };
+    a.q = bf(q), a.kp = bf(k_prefix), a.vp = bf(v_prefix), a.ks = bf(k_suffix), a.vs = bf(v_suffix);
+    a.plen = prefix_lens, a.slen = suffix_lens;
+    a.out = static_cast<__nv_bfloat16 *>(out), a.lse = lse;
+    a.part_ml = static_cast<float2 *>(ws);
+    a.part_o = reinterpret_cast<float *>(static_cast<char *>(ws) + attn::ml_bytes(a));
+    a.q_b = d->q_stride[0], a.q_l = d->q_stride[1], a.q_h = d->q_stride[2];
+    a.o_b = d->out_stride[0], a.o_l = d->out_stride[1], a.o_h = d->out_stride[2];
+    a.kp_g = d->k_prefix_stride[0], a.kp_t = d->k_prefix_stride[1], a.kp_h = d->k_prefix_stride[2];
+    a.vp_g = d->v_prefix_stride[0], a.vp_t = d->v_prefix_stride[1], a.vp_h = d->v_prefix_stride[2];
+    a.ks_b = d->k_suffix_stride[0], a.ks_t = d->k_suffix_stride[1], a.ks_h = d->k_suffix_stride[2];
+    a.vs_b = d->v_suffix_stride[0], a.vs_t = d->v_suffix_stride[1], a.vs_h = d->v_suffix_stride[2];
+    a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    return d->D == 128 ? attn::run<128>(a, as_cuda(stream)) : attn::run<64>(a, as_cuda(stream));
+}
