@@ -49,6 +49,41 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Two FP32 lanes in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+// Logits below kLow count as kLow; a row whose maximum lies beyond +-kFar is left to the second attempt.  kLow is the
+// lower by far, so that a thread without values (all kLow, its maximum taken as -kFar) adds e^(kLow + kFar) = 0.
+constexpr float kLow = -1e30f, kFar = 1e29f;
+
 __device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -88,6 +123,16 @@ struct Vec<true> {
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
+    // every value at least kLow; NaN stays
+    static __device__ __forceinline__ uint4 raised(const uint4 &v)
+    {
+        const __nv_bfloat162 low = __float2bfloat162_rn(kLow);
+        const auto up = [&](uint32_t w) {
+            const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&w), low);
+            return *reinterpret_cast<const uint32_t *>(&m);
+        };
+        return make_uint4(up(v.x), up(v.y), up(v.z), up(v.w));
+    }
     static __device__ __forceinline__ float get(const void *p, int64_t i) { return bf16f(static_cast<const __nv_bfloat16 *>(p)[i]); }
     static __device__ __forceinline__ void put(void *p, int64_t i, float v) { static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v); }
 };
@@ -106,6 +151,15 @@ struct Vec<false> {
     static __device__ __forceinline__ uint4 pack(const float (&f)[4])
     {
         return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+    static __device__ __forceinline__ uint4 raised(const uint4 &v)
+    {
+        const auto up = [](uint32_t w) {
+            uint32_t m;
+            asm("max.NaN.f32 %0, %1, %2;" : "=r"(m) : "r"(w), "r"(__float_as_uint(kLow)));
+            return m;
+        };
+        return make_uint4(up(v.x), up(v.y), up(v.z), up(v.w));
     }
     static __device__ __forceinline__ float get(const void *p, int64_t i) { return static_cast<const float *>(p)[i]; }
     static __device__ __forceinline__ void put(void *p, int64_t i, float v) { static_cast<float *>(p)[i] = v; }
@@ -146,9 +200,14 @@ struct Row {
     int off, n, nvec, full0, full1;  // vectors [full0, full1) lie inside the row
     bool dx_vec;
     __device__ __forceinline__ Row(const LossArgs &a, int64_t row)
+        : Row(a, static_cast<const char *>(a.x) + row * a.ld * S,
+              a.dx ? static_cast<char *>(a.dx) + row * a.ldd * S : nullptr)
     {
-        x = static_cast<const char *>(a.x) + row * a.ld * S;
-        dx = a.dx ? static_cast<char *>(a.dx) + row * a.ldd * S : nullptr;
+    }
+    __device__ __forceinline__ Row(const LossArgs &a, const char *x_row, char *dx_row)
+    {
+        x = x_row;
+        dx = dx_row;
         off = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / S);
         n = (int)a.V;
         nvec = (off + n + E - 1) / E;
@@ -248,21 +307,41 @@ __device__ __forceinline__ void no_part(const LossArgs &a, int64_t row)
     if (a.terms) a.terms[3 * row] = a.terms[3 * row + 1] = a.terms[3 * row + 2] = 0.0f;
 }
 
-// One vector's part of the statistics, relative to a maximum: y = x c + shift in
-// one rounding with shift = -max c.  Where a maximum lies beyond +-1e30 (a row of
-// the type's lowest values) that may overflow and leave z = 0; such a row, or
-// one that is all -inf, is taken again as (x - max) c (`plain`).
+// A thread's sums in pairs of lanes: y = x c + shift in one rounding with shift =
+// -max c, and logits no lower than kLow, so that 0 * -inf never enters s.  Where
+// a row's maximum lies beyond +-kFar (a row of the type's lowest values, or all
+// -inf) the row is taken again as (x - max) c (`plain`).
+struct Sums {
+    float2 z, s;
+};
 template <bool BF16>
-__device__ __forceinline__ void add(Stat &st, const uint4 &q, float c, float shift)
+__device__ __forceinline__ void add(Sums &t, const uint4 &q, float c, float shift)
 {
-    float f[Vec<BF16>::E];
-    Vec<BF16>::unpack(q, f);
+    constexpr int E = Vec<BF16>::E;
+    float f[E];
+    Vec<BF16>::unpack(Vec<BF16>::raised(q), f);
 #pragma unroll
-    for (int j = 0; j < Vec<BF16>::E; ++j) {
-        const float y = fmaf(f[j], c, shift), e = ex2(y);
-        st.z += e;
-        st.s = fmaf(e, fmaxf(y, -1e4f), st.s);
+    for (int j = 0; j < E; j += 2) {
+        const float2 y = fma2(make_float2(f[j], f[j + 1]), make_float2(c, c), make_float2(shift, shift));
+        const float2 e = make_float2(ex2(y.x), ex2(y.y));
+        t.z = add2(t.z, e);
+        t.s = fma2(e, y, t.s);
     }
+}
+// The statistics and N vectors more.
+template <bool BF16, int N>
+__device__ __forceinline__ void add_block(Stat &st, const uint4 (&q)[N], float c)
+{
+    float m = st.m;
+#pragma unroll
+    for (int k = 0; k < N; ++k) m = fmaxf(m, Vec<BF16>::top(q[k]));
+    st = moved(st, m, c);
+    const float shift = -fmaxf(m, -kFar) * c;
+    Sums t = {make_float2(st.z, 0.0f), make_float2(st.s, 0.0f)};
+#pragma unroll
+    for (int k = 0; k < N; ++k) add<BF16>(t, q[k], c, shift);
+    st.z = t.z.x + t.z.y;
+    st.s = t.s.x + t.s.y;
 }
 template <bool BF16>
 __device__ __forceinline__ void add_plain(Stat &st, const uint4 &q, float c)
@@ -277,7 +356,7 @@ __device__ __forceinline__ void add_plain(Stat &st, const uint4 &q, float c)
         st.s = fmaf(e, fmaxf(y, -1e4f), st.s);
     }
 }
-__device__ __forceinline__ float shift_of(float m, float c) { return -fmaxf(m, -1e30f) * c; }
+__device__ __forceinline__ bool far_off(const Stat &t) { return !(fabsf(t.m) < kFar); }
 
 // The gradient of one vector, k = -factor / z.
 template <bool BF16>
@@ -292,7 +371,11 @@ __device__ __forceinline__ void grad(const Row<BF16> &r, int i, const uint4 &q, 
     } else {
         const float shift = -all.m * c;
 #pragma unroll
-        for (int j = 0; j < E; ++j) f[j] = ex2(fmaf(f[j], c, shift)) * k;
+        for (int j = 0; j < E; j += 2) {
+            const float2 y = fma2(make_float2(f[j], f[j + 1]), make_float2(c, c), make_float2(shift, shift));
+            const float2 g = mul2(make_float2(ex2(y.x), ex2(y.y)), make_float2(k, k));
+            f[j] = g.x, f[j + 1] = g.y;
+        }
     }
     r.store(i, f);
 }
@@ -346,29 +429,18 @@ __global__ void __launch_bounds__(NT, (NV > 4 ? 512 : 1024) / NT) policy_kernel(
                 if (i < v1 && !r.inside(i)) hold[k] = r.load_end(i);
             }
         }
-#pragma unroll
-        for (int k = 0; k < NV; ++k) st.m = fmaxf(st.m, V::top(hold[k]));
-        const float shift = shift_of(st.m, a.c);
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (v0 + k * NT < v1) add<BF16>(st, hold[k], a.c, shift);
+        add_block<BF16, NV>(st, hold, a.c);
     } else {
         for (int i = v0 + tid; i < v1; i += NV * NT) {
-            float m = st.m;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 hold[k] = nothing;
                 if (i + k * NT < v1 && r.inside(i + k * NT)) hold[k] = xv[i + k * NT];
             }
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
+            for (int k = 0; k < NV; ++k)
                 if (i + k * NT < v1 && !r.inside(i + k * NT)) hold[k] = r.load_end(i + k * NT);
-                m = fmaxf(m, V::top(hold[k]));
-            }
-            st = moved(st, m, a.c);
-            const float shift = shift_of(m, a.c);
-#pragma unroll
-            for (int k = 0; k < NV; ++k) add<BF16>(st, hold[k], a.c, shift);
+            add_block<BF16, NV>(st, hold, a.c);
         }
     }
     // the row's statistics from every thread's, in all threads
@@ -399,7 +471,7 @@ __global__ void __launch_bounds__(NT, (NV > 4 ? 512 : 1024) / NT) policy_kernel(
         return over_warp(Stat{q.x, q.y, q.z}, a.c, 4);
     };
     all = join(st, 0);
-    const bool plain = all.z == 0.0f;
+    const bool plain = far_off(all);
     if (plain) {
         if (cs > 1) cluster_arrive();
         st = Stat{-FLT_MAX, 0.0f, 0.0f};
@@ -424,15 +496,17 @@ __global__ void __launch_bounds__(NT, (NV > 4 ? 512 : 1024) / NT) policy_kernel(
 }
 
 // ------------------------------------------------------------------ many long rows: a ring of row slices in shared memory
-// Persistent clusters; a CTA's slice of a row is one bulk copy into a stage of
-// its ring, issued by a producer warp that runs ahead of the eight warps that
-// compute, so that reading goes on through the exchanges and the writing.  Two
-// CTAs share an SM: one computes while the other waits for its cluster.  The
-// exchange is a 16-byte asynchronous store to every CTA of the cluster, which
-// counts on the receiver's barrier.
-constexpr int kRingWarps = 8, kRingThreads = (kRingWarps + 1) * 32, kMaxStages = 3;
-static_assert(kRingWarps <= kMaxCluster, "the warps' statistics are joined in eight lanes");
-constexpr size_t kRingBytes = 108 << 10;  // of one of two CTAs on an SM
+// Persistent clusters, one CTA per SM; a CTA's slice of a row is one bulk copy
+// into a stage of its ring.  Three roles run apart, joined by barriers only:
+//   - sixteen warps compute: the statistics of row n + 1, then the gradient of row
+//     n, so that no one waits for a row's exchange;
+//   - one warp joins the warps' statistics, exchanges them with the cluster (a
+//     16-byte asynchronous store to every CTA, counted by the receiver's barrier)
+//     and forms the row's factor;
+//   - one warp runs ahead with the copies and the tokens' inputs.
+// Every wait is bounded: past two seconds the error is latched and the CTA winds up.
+constexpr int kRingWarps = 16, kRingThreads = (kRingWarps + 2) * 32, kMaxStages = 6;
+constexpr size_t kRingBytes = 216 << 10;
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
 {
@@ -450,30 +524,46 @@ __device__ __forceinline__ void st_async_v4(void *addr, uint64_t *bar, int rank,
                  : "memory");
 }
 
+// A walk over the ring's stages.
+struct Stage {
+    int st, parity;
+    __device__ __forceinline__ void next(int stages)
+    {
+        if (++st == stages) st = 0, parity ^= 1;
+    }
+};
+
 template <bool BF16>
-__global__ void __launch_bounds__(kRingThreads, 2)
-    policy_ring_kernel(LossArgs a, int cs, int stages, uint32_t stage_bytes, unsigned int *err)
+__global__ void __launch_bounds__(kRingThreads, 1)
+    policy_ring_kernel(LossArgs a, int log_cs, int stages, uint32_t stage_bytes, unsigned int *err)
 {
     using V = Vec<BF16>;
     constexpr int E = V::E, NT = kRingWarps * 32;
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_met[2];
+    // a stage's data is there / its row is done; row n's statistics: every warp's are there, the cluster's are, the
+    // row's are (buffers n & 1); the same for the second attempt
+    __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_part[2], s_met[2], s_ready[2], s_part2, s_ready2;
     __shared__ alignas(16) float4 s_cta[2][kMaxCluster];
-    __shared__ float4 s_warp[kRingWarps];
+    __shared__ float4 s_warp[2][kRingWarps];
     __shared__ Token s_tok[kMaxStages];
-    __shared__ float2 s_factor;
-    __shared__ Stat s_all;
+    __shared__ Stat s_all[2];
+    __shared__ float2 s_factor[2];
     __shared__ int s_stop;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int rank = blockIdx.x % cs;
-    const int64_t first = blockIdx.x / cs, step = gridDim.x / cs;
+    const int cs = 1 << log_cs, rank = blockIdx.x & (cs - 1);
+    const int64_t first = blockIdx.x >> log_cs, step = gridDim.x >> log_cs;
     if (tid == 0) {
         for (int k = 0; k < stages; ++k) {
             ptx::mbar_init(&s_full[k], 1);
             ptx::mbar_init(&s_empty[k], kRingWarps);
         }
-        ptx::mbar_init(&s_met[0], 1);
-        ptx::mbar_init(&s_met[1], 1);
+        for (int k = 0; k < 2; ++k) {
+            ptx::mbar_init(&s_part[k], kRingWarps);
+            ptx::mbar_init(&s_met[k], 1);
+            ptx::mbar_init(&s_ready[k], 1);
+        }
+        ptx::mbar_init(&s_part2, kRingWarps);
+        ptx::mbar_init(&s_ready2, 1);
         s_stop = 0;
         ptx::fence_mbar_init();
     }
@@ -485,129 +575,210 @@ __global__ void __launch_bounds__(kRingThreads, 2)
     }
     pdl_wait();
 
-    // Every wait is bounded: past two seconds the error is latched and the CTA winds up.
-    const uint64_t deadline_ns = 2000000000ull;
-    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        if (ptx::mbar_try_wait(bar, parity)) return true;
-        const uint64_t until = ptx::globaltimer_ns() + deadline_ns;
-        for (;;) {
-            if (ptx::mbar_try_wait_sleep(bar, parity, 20000u)) return true;
-            if (*reinterpret_cast<volatile int *>(&s_stop)) return false;
-            if (ptx::globaltimer_ns() > until) {
-                *reinterpret_cast<volatile int *>(&s_stop) = 1;
-                latch_error(err, QERL_ERR_TIMEOUT);
-                return false;
+    const uint64_t limit_ns = 2000000000ull;
+    // true for the whole warp, or false for it
+    auto wait = [&](uint64_t *bar, int parity) -> bool {
+        bool ok = ptx::mbar_try_wait(bar, (uint32_t)parity);
+        if (!ok) {
+            const uint64_t until = ptx::globaltimer_ns() + limit_ns;
+            while (!(ok = ptx::mbar_try_wait_sleep(bar, (uint32_t)parity, 20000u))) {
+                if (*reinterpret_cast<volatile int *>(&s_stop)) break;
+                if (ptx::globaltimer_ns() > until) {
+                    *reinterpret_cast<volatile int *>(&s_stop) = 1;
+                    latch_error(err, QERL_ERR_TIMEOUT);
+                    break;
+                }
             }
         }
+        return __all_sync(0xFFFFFFFFu, ok);
+    };
+    const auto slice = [&](const Row<BF16> &r, int &v0, int &len) {
+        const int per = (r.nvec + cs - 1) >> log_cs;
+        v0 = rank * per;
+        len = max(0, min(per, r.nvec - v0));
     };
 
-    if (warp == kRingWarps) {
+    if (warp == kRingWarps) {  // copies
         int n = 0;
-        for (int64_t row = first; row < a.T; row += step, ++n) {
-            const int st = n % stages;
-            Token tok = token<BF16>(a, row);
-            if (tok.takes) token_inputs<BF16>(a, row, tok);
-            if (n >= stages && !__all_sync(0xFFFFFFFFu, wait(&s_empty[st], (n / stages - 1) & 1))) break;
-            const Row<BF16> r(a, row);
-            const int per = (r.nvec + cs - 1) / cs, v0 = rank * per, v1 = min(v0 + per, r.nvec);
-            uint8_t *to = ring + st * stage_bytes;
-            const int b0 = max(v0, r.full0), b1 = min(v1, r.full1), last = r.nvec - 1;
-            if (tok.takes) {  // the row's ends by element
-                if (lane == 0 && v0 == 0 && r.full0) *reinterpret_cast<uint4 *>(to) = r.load_end(0);
-                if (lane == 1 && last >= max(v0, r.full1) && last < v1 && (last > 0 || !r.full0))
-                    *reinterpret_cast<uint4 *>(to + (last - v0) * 16) = r.load_end(last);
+        Token tok = {};
+        Stage at = {0, 0};
+        for (int64_t row = first; row < a.T; row += step, ++n, at.next(stages)) {
+            const int st = at.st;
+            if (n % 32 == 0 && row + lane * step < a.T) {  // the next 32 rows' tokens, one per lane
+                tok = token<BF16>(a, row + lane * step);
+                if (tok.takes) token_inputs<BF16>(a, row + lane * step, tok);
             }
-            if (lane == 0) s_tok[st] = tok;
             __syncwarp();
-            if (lane == 0) {
-                const uint32_t bytes = tok.takes && b1 > b0 ? (uint32_t)(b1 - b0) * 16u : 0u;
-                ptx::mbar_arrive_expect_tx(&s_full[st], bytes);
-                if (bytes) bulk_load(to + (b0 - v0) * 16, r.vec() + b0, bytes, &s_full[st]);
-            }
+            const bool takes = __shfl_sync(0xFFFFFFFFu, tok.takes, n % 32) != 0;
+            const Row<BF16> r(a, row);
+            int v0, len;
+            slice(r, v0, len);
+            // the row's ends by element: lane 0 the first vector, lane 1 the last
+            const int last = r.nvec - 1;
+            const bool end = takes && (lane == 0 ? v0 == 0 && r.full0 : lane == 1 && last >= max(v0, r.full1) && last < v0 + len && (last > 0 || !r.full0));
+            uint4 e = make_uint4(0, 0, 0, 0);
+            if (end) e = r.load_end(lane == 0 ? 0 : last);
+            __syncwarp();
+            if (n >= stages && !wait(&s_empty[st], at.parity ^ 1)) break;
+            uint8_t *to = ring + st * stage_bytes;
+            const int b0 = max(v0, r.full0), b1 = min(v0 + len, r.full1);
+            const uint32_t bytes = takes && b1 > b0 ? (uint32_t)(b1 - b0) * 16u : 0u;
+            if (lane == 0 && bytes) bulk_load(to + (b0 - v0) * 16, r.vec() + b0, bytes, &s_full[st]);
+            if (end) *reinterpret_cast<uint4 *>(to + (lane == 0 ? 0 : last - v0) * 16) = e;
+            if (lane == n % 32) s_tok[st] = tok;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&s_full[st], bytes);
+            __syncwarp();
         }
         // no copy may be in flight when the CTA ends
         if (lane == 0 && *reinterpret_cast<volatile int *>(&s_stop)) {
-            const uint64_t until = ptx::globaltimer_ns() + deadline_ns;
+            const uint64_t until = ptx::globaltimer_ns() + limit_ns;
             for (int k = max(0, n - stages); k < n; ++k)
                 while (!ptx::mbar_try_wait(&s_full[k % stages], (k / stages) & 1) && ptx::globaltimer_ns() < until) {
                 }
         }
-        __syncwarp();
-    } else {
-        int n = 0, met = 0;
-        for (int64_t row = first; row < a.T; row += step, ++n) {
-            const int st = n % stages;
-            // warps leave the loop together: the barriers below count all of them
-            if (!ptx::named_bar_and(2, NT, wait(&s_full[st], (n / stages) & 1))) break;
-            const Row<BF16> r(a, row);
-            const int per = (r.nvec + cs - 1) / cs, v0 = rank * per, v1 = min(v0 + per, r.nvec), len = max(0, v1 - v0);
-            const uint4 *sl = reinterpret_cast<const uint4 *>(ring + st * stage_bytes);
-            const int id = s_tok[st].id;
+    } else if (warp == kRingWarps + 1) {  // exchanges
+        int n = 0, met = 0, again = 0;
+        // the cluster's statistics from every warp's, in all lanes; false where a wait ran out
+        auto join = [&](const float4 *from, Stat &t) -> bool {
+            float4 q = lane < kRingWarps ? from[lane] : make_float4(-FLT_MAX, 0.0f, 0.0f, 0.0f);
+            t = over_warp(Stat{q.x, q.y, q.z}, a.c, 16);
+            if (cs == 1) return true;  // launched without a cluster: nothing to exchange, no access to a peer
+            const int buf = met & 1;
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&s_met[buf], (uint32_t)cs * 16u);
+            __syncwarp();
+            if (lane < cs) st_async_v4(&s_cta[buf][rank], &s_met[buf], lane, make_float4(t.m, t.z, t.s, 0.0f));
+            __syncwarp();
+            if (!wait(&s_met[buf], (met / 2) & 1)) return false;
+            ++met;
+            q = (lane & 7) < cs ? s_cta[buf][lane & 7] : make_float4(-FLT_MAX, 0.0f, 0.0f, 0.0f);
+            t = over_warp(Stat{q.x, q.y, q.z}, a.c, 4);
+            return true;
+        };
+        Stage at = {0, 0};
+        for (int64_t row = first; row < a.T; row += step, ++n, at.next(stages)) {
+            const int st = at.st, buf = n & 1;
+            if (!wait(&s_part[buf], (n / 2) & 1)) break;
             if (!s_tok[st].takes) {
-                const float zero[E] = {};
-                if (r.dx)
-                    for (int i = tid; i < len; i += NT) r.store(v0 + i, zero);
-                if (rank == 0 && tid == 0) no_part(a, row);
-            } else {
-                Stat mine = {-FLT_MAX, 0.0f, 0.0f};
-                const uint4 nothing = make_uint4(V::kFill, V::kFill, V::kFill, V::kFill);
-                for (int i = tid; i < len; i += 4 * NT) {
-                    uint4 q[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) q[k] = i + k * NT < len ? sl[i + k * NT] : nothing;
-                    const float m = fmaxf(fmaxf(fmaxf(mine.m, V::top(q[0])), V::top(q[1])), fmaxf(V::top(q[2]), V::top(q[3])));
-                    mine = moved(mine, m, a.c);
-                    const float shift = shift_of(m, a.c);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) add<BF16>(mine, q[k], a.c, shift);
+                if (lane == 0) {
+                    if (rank == 0) no_part(a, row);
+                    ptx::mbar_arrive(&s_ready[buf]);
                 }
-                // Joins every thread's statistics into the row's; its factor follows in the same warp.  False where the
-                // cluster's others did not answer in time.
-                auto join = [&](Stat t, bool plain) -> bool {
-                    const int buf = met & 1;
-                    t = over_warp(t, a.c, 16);
-                    if (lane == 0) s_warp[warp] = make_float4(t.m, t.z, t.s, 0.0f);
-                    ptx::named_bar_sync(1, NT);
-                    bool ok = true;
-                    if (warp == 0) {
-                        float4 q = lane < kRingWarps ? s_warp[lane] : make_float4(-FLT_MAX, 0.0f, 0.0f, 0.0f);
-                        t = over_warp(Stat{q.x, q.y, q.z}, a.c, 4);  // in lanes 0 to 7, which send it
-                        if (lane == 0) ptx::mbar_arrive_expect_tx(&s_met[buf], (uint32_t)cs * 16u);
-                        __syncwarp();
-                        if (lane < cs) st_async_v4(&s_cta[buf][rank], &s_met[buf], lane, make_float4(t.m, t.z, t.s, 0.0f));
-                        ok = __all_sync(0xFFFFFFFFu, wait(&s_met[buf], (met / 2) & 1));
-                        q = ok && (lane & 7) < cs ? s_cta[buf][lane & 7] : make_float4(-FLT_MAX, 0.0f, 0.0f, 0.0f);
-                        t = over_warp(Stat{q.x, q.y, q.z}, a.c, 4);
-                        if (lane == 0) {
-                            s_all = t;
-                            if (ok && (t.z != 0.0f || plain)) s_factor = factor(a, row, s_tok[st], t, plain, rank == 0);
-                        }
-                    }
-                    ++met;
-                    return ptx::named_bar_and(1, NT, ok);
-                };
-                bool ok = join(mine, false);
-                const bool plain = ok && s_all.z == 0.0f;
-                if (plain) {
-                    mine = Stat{-FLT_MAX, 0.0f, 0.0f};
-                    for (int i = tid; i < len; i += NT) add_plain<BF16>(mine, sl[i], a.c);
-                    ok = join(mine, true);
-                }
-                if (!ok) break;
-                if (r.dx) {
-                    const Stat all = s_all;
-                    const float coef = s_factor.x, one_p = s_factor.y, k = all.z == 0.0f ? 0.0f : -coef / all.z;
-#pragma unroll 2
-                    for (int i = tid; i < len; i += NT) grad<BF16>(r, v0 + i, sl[i], all, a.c, k, plain);
-                    const int own = (id + r.off) / E - v0;  // the vector that holds the chosen token
-                    if (own >= 0 && own < len && own % NT == tid) V::put(r.dx, id, coef * one_p);
-                }
+                __syncwarp();
+                continue;
+            }
+            Stat t;
+            if (!join(s_warp[buf], t)) break;
+            const bool plain = far_off(t);
+            if (lane == 0) {
+                s_all[buf] = t;
+                if (!plain) s_factor[buf] = factor(a, row, s_tok[st], t, false, rank == 0);
+                ptx::mbar_arrive(&s_ready[buf]);
             }
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&s_empty[st]);
+            if (plain) {
+                if (!wait(&s_part2, again & 1) || !join(s_warp[buf], t)) break;
+                if (lane == 0) {
+                    s_all[buf] = t;
+                    s_factor[buf] = factor(a, row, s_tok[st], t, true, rank == 0);
+                    ptx::mbar_arrive(&s_ready2);
+                }
+                __syncwarp();
+                ++again;
+            }
         }
-        __syncwarp();
+    } else {
+        int again = 0;
+        auto give = [&](Stat t, int buf, uint64_t *bar) {
+            t = over_warp(t, a.c, 16);
+            if (lane == 0) {
+                s_warp[buf][warp] = make_float4(t.m, t.z, t.s, 0.0f);
+                ptx::mbar_arrive(bar);
+            }
+            __syncwarp();
+        };
+        const int64_t x_step = step * a.ld * (16 / E), dx_step = step * a.ldd * (16 / E);
+        const char *x_in = static_cast<const char *>(a.x) + first * a.ld * (16 / E), *x_out = x_in;
+        char *dx = a.dx ? static_cast<char *>(a.dx) + first * a.ldd * (16 / E) : nullptr;
+        Stage in = {0, 0}, out = {0, 0};
+        // row n's statistics
+        auto measure = [&](int n) -> bool {
+            if (!wait(&s_full[in.st], in.parity)) return false;
+            Stat mine = {-FLT_MAX, 0.0f, 0.0f};
+            if (s_tok[in.st].takes) {
+                const Row<BF16> r(a, x_in, nullptr);
+                int v0, len;
+                slice(r, v0, len);
+                const uint4 *sl = reinterpret_cast<const uint4 *>(ring + in.st * stage_bytes);
+                int i = tid;
+                for (; i + 3 * NT < len; i += 4 * NT) {
+                    const uint4 q[4] = {sl[i], sl[i + NT], sl[i + 2 * NT], sl[i + 3 * NT]};
+                    add_block<BF16, 4>(mine, q, a.c);
+                }
+                for (; i < len; i += NT) {
+                    const uint4 q[1] = {sl[i]};
+                    add_block<BF16, 1>(mine, q, a.c);
+                }
+            }
+            give(mine, n & 1, &s_part[n & 1]);
+            x_in += x_step;
+            in.next(stages);
+            return true;
+        };
+        // row n's gradient
+        auto finish = [&](int n) -> bool {
+            const int buf = n & 1, st = out.st;
+            if (!wait(&s_ready[buf], (n / 2) & 1)) return false;
+            const bool takes = s_tok[st].takes != 0;
+            if (dx || (takes && far_off(s_all[buf]))) {
+                const Row<BF16> r(a, x_out, dx);
+                int v0, len;
+                slice(r, v0, len);
+                if (!takes) {
+                    const float zero[E] = {};
+                    for (int i = tid; i < len; i += NT) r.store(v0 + i, zero);
+                } else {
+                    const uint4 *sl = reinterpret_cast<const uint4 *>(ring + st * stage_bytes);
+                    Stat all = s_all[buf];
+                    const bool plain = far_off(all);
+                    if (plain) {
+                        Stat mine = {-FLT_MAX, 0.0f, 0.0f};
+                        for (int i = tid; i < len; i += NT) add_plain<BF16>(mine, sl[i], a.c);
+                        give(mine, buf, &s_part2);
+                        if (!wait(&s_ready2, again & 1)) return false;
+                        ++again;
+                        all = s_all[buf];
+                    }
+                    if (dx) {
+                        const float coef = s_factor[buf].x, one_p = s_factor[buf].y, k = all.z == 0.0f ? 0.0f : -coef / all.z;
+                        int i = tid;
+                        if (!plain)
+                            for (; i + NT < len; i += 2 * NT) {
+                                const uint4 q0 = sl[i], q1 = sl[i + NT];
+                                grad<BF16>(r, v0 + i, q0, all, a.c, k, false);
+                                grad<BF16>(r, v0 + i + NT, q1, all, a.c, k, false);
+                            }
+                        for (; i < len; i += NT) grad<BF16>(r, v0 + i, sl[i], all, a.c, k, plain);
+                        const int own = (s_tok[st].id + r.off) / E - v0;  // the vector that holds the chosen token
+                        if (own >= 0 && own < len && own % NT == tid) V::put(dx, s_tok[st].id, coef * one_p);
+                    }
+                }
+                __syncwarp();
+            }
+            if (lane == 0) ptx::mbar_arrive(&s_empty[st]);
+            x_out += x_step;
+            if (dx) dx += dx_step;
+            out.next(stages);
+            return true;
+        };
+        bool ok = first < a.T && measure(0);
+        int n = 0;
+        for (int64_t row = first; ok && row < a.T; row += step, ++n) {
+            if (row + step < a.T) ok = measure(n + 1);
+            ok = ok && finish(n);
+        }
     }
+    __syncwarp();
     if (cs > 1) {  // no CTA ends while another may still write to it
         cluster_arrive();
         cluster_wait();
@@ -677,15 +848,14 @@ cudaError_t launch_nv(const LossArgs &a, int cs, int64_t nv, cudaStream_t s)
 }
 
 template <bool BF16>
-cudaError_t launch_ring(const LossArgs &a, int cs, int stages, size_t slice, int per_sm, cudaStream_t s)
+cudaError_t launch_ring(const LossArgs &a, int cs, int stages, size_t slice, cudaStream_t s)
 {
-    const size_t smem = stages * slice;
     static const cudaError_t attr =
-        cudaFuncSetAttribute(policy_ring_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(2 * kRingBytes));
+        cudaFuncSetAttribute(policy_ring_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
     if (attr != cudaSuccess) return attr;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kRingThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = kRingBytes;  // whatever the slices take: one CTA per SM
     cfg.stream = s;
     cudaLaunchAttribute attrs[2];
     int n = 0;
@@ -698,19 +868,18 @@ cudaError_t launch_ring(const LossArgs &a, int cs, int stages, size_t slice, int
     cfg.attrs = attrs;
     cfg.numAttrs = n;
     // clusters that fit at once (fewer than the SMs would hold: a cluster stays within a GPC)
-    static std::atomic<int> fit[2][4];
-    std::atomic<int> &known = fit[per_sm - 1][cs == 1 ? 0 : cs == 2 ? 1 : cs == 4 ? 2 : 3];
+    static std::atomic<int> fit[4];
+    const int log_cs = cs == 1 ? 0 : cs == 2 ? 1 : cs == 4 ? 2 : 3;
+    std::atomic<int> &known = fit[log_cs];
     int64_t clusters = known.load();
     if (clusters == 0) {
-        clusters = (int64_t)per_sm * num_sms();
+        clusters = num_sms();
         if (cs > 1) {
             int most = 0;
             cfg.gridDim = dim3((unsigned)(clusters / cs * cs));
-            cfg.dynamicSmemBytes = (3 - per_sm) * kRingBytes;
             const cudaError_t e = cudaOccupancyMaxActiveClusters(&most, policy_ring_kernel<BF16>, &cfg);
             if (e != cudaSuccess) return e;
             clusters = most > 0 ? most : 1;
-            cfg.dynamicSmemBytes = smem;
         }
         known.store((int)clusters);
     }
@@ -721,18 +890,17 @@ cudaError_t launch_ring(const LossArgs &a, int cs, int stages, size_t slice, int
         attrs[n].val.programmaticStreamSerializationAllowed = 1;
         ++n;
     }
-    cfg.attrs = attrs;
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, policy_ring_kernel<BF16>, a, cs, stages, (uint32_t)slice, error_word());
+    return cudaLaunchKernelEx(&cfg, policy_ring_kernel<BF16>, a, log_cs, stages, (uint32_t)slice, error_word());
 }
 
 // Which kernel, and its cluster.  The ring: rows of 16 KB and more, when there
 // are more of them than clusters that fit at once; the smallest cluster whose
-// slices leave three stages to each of two CTAs on an SM, else two stages, else
-// two stages of one CTA.  Otherwise one cluster per row: 128 threads where eight
-// vectors each hold a row, else 256; the smallest cluster whose registers hold
-// a row (eight vectors a thread), then larger ones while the launch would leave
-// SMs idle and every CTA keeps a vector for half its threads.
+// slices leave three stages, else two.  Otherwise one cluster per row: 128
+// threads where eight vectors each hold a row, else 256; the smallest cluster
+// whose registers hold a row (eight vectors a thread), then larger ones while
+// the launch would leave SMs idle and every CTA keeps a vector for half its
+// threads.
 template <bool BF16>
 cudaError_t launch_any(const LossArgs &a, cudaStream_t s)
 {
@@ -740,13 +908,13 @@ cudaError_t launch_any(const LossArgs &a, cudaStream_t s)
     const bool even = aligned16(a.x) && a.ld % E == 0;  // every row starts with a vector
     const int64_t nvec = (a.V + (even ? 0 : E - 1) + E - 1) / E;
     if (nvec >= 1024) {
-        for (int per_sm = 2; per_sm >= 1; --per_sm)
-            for (int stages = 3; stages >= 2; --stages)
-                for (int cs = 1; cs <= kMaxCluster; cs *= 2) {
-                    const size_t slice = ((size_t)((nvec + cs - 1) / cs) * 16 + 127) & ~size_t(127);
-                    if (stages * slice <= (3 - per_sm) * kRingBytes && a.T * cs > (int64_t)per_sm * num_sms())
-                        return launch_ring<BF16>(a, cs, stages, slice, per_sm, s);
-                }
+        for (int least = 3; least >= 2; --least)
+            for (int cs = 1; cs <= kMaxCluster; cs *= 2) {
+                const size_t slice = ((size_t)((nvec + cs - 1) / cs) * 16 + 127) & ~size_t(127);
+                const int64_t stages = kRingBytes / slice;
+                if (stages >= least && a.T * cs > num_sms())
+                    return launch_ring<BF16>(a, cs, stages > kMaxStages ? kMaxStages : (int)stages, slice, s);
+            }
     }
     const int nt = nvec <= 128 * 8 ? 128 : 256;
     int cs = 1;
