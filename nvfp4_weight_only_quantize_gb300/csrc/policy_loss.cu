@@ -358,6 +358,22 @@ __device__ __forceinline__ void add_plain(Stat &st, const uint4 &q, float c)
 }
 __device__ __forceinline__ bool far_off(const Stat &t) { return !(fabsf(t.m) < kFar); }
 
+// k e^(x c + shift) of one vector's elements.
+template <bool BF16>
+__device__ __forceinline__ uint4 scaled(const uint4 &q, float c, float shift, float k)
+{
+    constexpr int E = Vec<BF16>::E;
+    float f[E];
+    Vec<BF16>::unpack(q, f);
+#pragma unroll
+    for (int j = 0; j < E; j += 2) {
+        const float2 y = fma2(make_float2(f[j], f[j + 1]), make_float2(c, c), make_float2(shift, shift));
+        const float2 g = mul2(make_float2(ex2(y.x), ex2(y.y)), make_float2(k, k));
+        f[j] = g.x, f[j + 1] = g.y;
+    }
+    return Vec<BF16>::pack(f);
+}
+
 // The gradient of one vector, k = -factor / z.
 template <bool BF16>
 __device__ __forceinline__ void grad(const Row<BF16> &r, int i, const uint4 &q, const Stat &all, float c, float k, bool plain)
@@ -496,17 +512,27 @@ __global__ void __launch_bounds__(NT, (NV > 4 ? 512 : 1024) / NT) policy_kernel(
 }
 
 // ------------------------------------------------------------------ many long rows: a ring of row slices in shared memory
+// The statistics are taken relative to the chosen token's logit, which the copies bring along: no maximum, and sums that
+// only add.  Where they overflow (a token some 88 nats below the maximum) or are not finite, the row is taken again with
+// its maximum.
 // Persistent clusters, one CTA per SM; a CTA's slice of a row is one bulk copy
 // into a stage of its ring.  Three roles run apart, joined by barriers only:
-//   - sixteen warps compute: the statistics of row n + 1, then the gradient of row
-//     n, so that no one waits for a row's exchange;
-//   - one warp joins the warps' statistics, exchanges them with the cluster (a
-//     16-byte asynchronous store to every CTA, counted by the receiver's barrier)
-//     and forms the row's factor;
+//   - sixteen warps compute: the statistics of row n + depth, then the gradient of
+//     row n, so that no one waits for a row's exchange;
+//   - one warp joins the warps' statistics and sends them to the cluster's CTAs (a
+//     16-byte asynchronous store to each, counted by the receiver's barrier);
+//   - one warp receives them and forms the row's factor;
 //   - one warp runs ahead with the copies and the tokens' inputs.
 // Every wait is bounded: past two seconds the error is latched and the CTA winds up.
-constexpr int kRingWarps = 16, kRingThreads = (kRingWarps + 2) * 32, kMaxStages = 6;
-constexpr size_t kRingBytes = 216 << 10;
+constexpr int kRingWarps = 16, kRingThreads = (kRingWarps + 3) * 32, kMaxStages = 6;
+constexpr size_t kRingBytes = 204 << 10;
+// Rows between a row's statistics and its gradient: at most kRows - 1.  Rows whose tokens are in flight: those, the
+// stages that the copies may run ahead, and one.
+constexpr int kRows = 4, kTokens = 16;
+// Buffers of received statistics.  A CTA sends row n + 8 after its own warps took row n + 8 - kRows to its end, so after
+// every other CTA sent that row, so after that CTA had received row n + 8 - 2 kRows = n.
+constexpr int kMet = 2 * kRows;
+static_assert(kTokens >= kRows + kMaxStages + 1, "a token outlives its stage");
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
 {
@@ -535,19 +561,22 @@ struct Stage {
 
 template <bool BF16>
 __global__ void __launch_bounds__(kRingThreads, 1)
-    policy_ring_kernel(LossArgs a, int log_cs, int stages, uint32_t stage_bytes, unsigned int *err)
+    policy_ring_kernel(LossArgs a, int log_cs, int stages, int depth, uint32_t stage_bytes, unsigned int *err)
 {
     using V = Vec<BF16>;
     constexpr int E = V::E, NT = kRingWarps * 32;
     extern __shared__ __align__(128) uint8_t ring[];
-    // a stage's data is there / its row is done; row n's statistics: every warp's are there, the cluster's are, the
-    // row's are (buffers n & 1); the same for the second attempt
-    __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_part[2], s_met[2], s_ready[2], s_part2, s_ready2;
-    __shared__ alignas(16) float4 s_cta[2][kMaxCluster];
-    __shared__ float4 s_warp[2][kRingWarps];
-    __shared__ Token s_tok[kMaxStages];
-    __shared__ Stat s_all[2];
-    __shared__ float2 s_factor[2];
+    // a stage's data is there / it may be filled again; row n's statistics (buffers n % kRows): every warp's are there,
+    // the row's are; the cluster's; the same for the second attempt
+    __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages], s_part[kRows], s_met[kMet], s_ready[kRows], s_part2, s_met2[2],
+        s_ready2;
+    __shared__ alignas(16) float4 s_cta[kMet][kMaxCluster], s_cta2[2][kMaxCluster];
+    __shared__ alignas(16) float2 s_sum[kRows][NT];  // every thread's (z, s)
+    __shared__ float4 s_warp[kRingWarps];           // every warp's statistics, second attempt
+    __shared__ bool s_plain[kRows];
+    __shared__ Token s_tok[kTokens];
+    __shared__ Stat s_all[kRows];
+    __shared__ float2 s_factor[kRows];
     __shared__ int s_stop;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int cs = 1 << log_cs, rank = blockIdx.x & (cs - 1);
@@ -557,11 +586,12 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             ptx::mbar_init(&s_full[k], 1);
             ptx::mbar_init(&s_empty[k], kRingWarps);
         }
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < kRows; ++k) {
             ptx::mbar_init(&s_part[k], kRingWarps);
-            ptx::mbar_init(&s_met[k], 1);
-            ptx::mbar_init(&s_ready[k], 1);
+            ptx::mbar_init(&s_ready[k], 2);  // sent, and received
         }
+        for (int k = 0; k < kMet; ++k) ptx::mbar_init(&s_met[k], 1);
+        for (int k = 0; k < 2; ++k) ptx::mbar_init(&s_met2[k], 1);
         ptx::mbar_init(&s_part2, kRingWarps);
         ptx::mbar_init(&s_ready2, 1);
         s_stop = 0;
@@ -598,6 +628,22 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         len = max(0, min(per, r.nvec - v0));
     };
 
+    // (z, s) over the CTA's threads, in all lanes
+    auto of_threads = [&](int buf) {
+        const float4 *p = reinterpret_cast<const float4 *>(s_sum[buf]);
+        float2 t = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < NT / 64; ++k) {
+            const float4 q = p[k * 32 + lane];
+            t = add2(t, add2(make_float2(q.x, q.y), make_float2(q.z, q.w)));
+        }
+        for (int o = 16; o; o >>= 1) {
+            t.x += __shfl_xor_sync(0xFFFFFFFFu, t.x, o);
+            t.y += __shfl_xor_sync(0xFFFFFFFFu, t.y, o);
+        }
+        return t;
+    };
+
     if (warp == kRingWarps) {  // copies
         int n = 0;
         Token tok = {};
@@ -625,7 +671,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             const uint32_t bytes = takes && b1 > b0 ? (uint32_t)(b1 - b0) * 16u : 0u;
             if (lane == 0 && bytes) bulk_load(to + (b0 - v0) * 16, r.vec() + b0, bytes, &s_full[st]);
             if (end) *reinterpret_cast<uint4 *>(to + (lane == 0 ? 0 : last - v0) * 16) = e;
-            if (lane == n % 32) s_tok[st] = tok;
+            if (lane == n % 32) s_tok[n % kTokens] = tok;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive_expect_tx(&s_full[st], bytes);
             __syncwarp();
@@ -637,29 +683,36 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 while (!ptx::mbar_try_wait(&s_full[k % stages], (k / stages) & 1) && ptx::globaltimer_ns() < until) {
                 }
         }
-    } else if (warp == kRingWarps + 1) {  // exchanges
+    } else if (warp == kRingWarps + 1) {  // sends
+        int met = 0;
+        const int rows = (int)((a.T - first + step - 1) / step);
+        for (int n = 0; n < rows; ++n) {
+            const int buf = n % kRows;
+            if (!wait(&s_part[buf], (n / kRows) & 1)) break;
+            if (cs > 1 && s_tok[n % kTokens].takes) {
+                const float2 t = of_threads(buf);
+                if (lane < cs) st_async_v4(&s_cta[met % kMet][rank], &s_met[met % kMet], lane, make_float4(t.x, t.y, 0.0f, 0.0f));
+                ++met;
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&s_ready[buf]);
+            __syncwarp();
+        }
+    } else if (warp == kRingWarps + 2) {  // receives
         int n = 0, met = 0, again = 0;
-        // the cluster's statistics from every warp's, in all lanes; false where a wait ran out
-        auto join = [&](const float4 *from, Stat &t) -> bool {
-            float4 q = lane < kRingWarps ? from[lane] : make_float4(-FLT_MAX, 0.0f, 0.0f, 0.0f);
-            t = over_warp(Stat{q.x, q.y, q.z}, a.c, 16);
-            if (cs == 1) return true;  // launched without a cluster: nothing to exchange, no access to a peer
-            const int buf = met & 1;
-            if (lane == 0) ptx::mbar_arrive_expect_tx(&s_met[buf], (uint32_t)cs * 16u);
+        // what CTA lane % 8 sent; false where the wait ran out
+        auto receive = [&](const float4 *from, uint64_t *bar, int parity, float4 &q) -> bool {
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, (uint32_t)cs * 16u);
             __syncwarp();
-            if (lane < cs) st_async_v4(&s_cta[buf][rank], &s_met[buf], lane, make_float4(t.m, t.z, t.s, 0.0f));
-            __syncwarp();
-            if (!wait(&s_met[buf], (met / 2) & 1)) return false;
-            ++met;
-            q = (lane & 7) < cs ? s_cta[buf][lane & 7] : make_float4(-FLT_MAX, 0.0f, 0.0f, 0.0f);
-            t = over_warp(Stat{q.x, q.y, q.z}, a.c, 4);
+            if (!wait(bar, parity)) return false;
+            if ((lane & 7) < cs) q = from[lane & 7];
             return true;
         };
-        Stage at = {0, 0};
-        for (int64_t row = first; row < a.T; row += step, ++n, at.next(stages)) {
-            const int st = at.st, buf = n & 1;
-            if (!wait(&s_part[buf], (n / 2) & 1)) break;
-            if (!s_tok[st].takes) {
+        for (int64_t row = first; row < a.T; row += step, ++n) {
+            const int buf = n % kRows;
+            const Token &tok = s_tok[n % kTokens];
+            if (!wait(&s_part[buf], (n / kRows) & 1)) break;
+            if (!tok.takes) {
                 if (lane == 0) {
                     if (rank == 0) no_part(a, row);
                     ptx::mbar_arrive(&s_ready[buf]);
@@ -667,20 +720,43 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 __syncwarp();
                 continue;
             }
-            Stat t;
-            if (!join(s_warp[buf], t)) break;
-            const bool plain = far_off(t);
+            float2 z;
+            if (cs == 1) {  // launched without a cluster: nothing to exchange, no access to a peer
+                z = of_threads(buf);
+            } else {
+                float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (!receive(s_cta[met % kMet], &s_met[met % kMet], (met / kMet) & 1, q)) break;
+                z = make_float2(q.x, q.y);
+                for (int o = 4; o; o >>= 1) {
+                    z.x += __shfl_xor_sync(0xFFFFFFFFu, z.x, o);
+                    z.y += __shfl_xor_sync(0xFFFFFFFFu, z.y, o);
+                }
+            }
+            Stat t = {tok.x_id, z.x, z.y};
+            ++met;
+            const bool plain = far_off(t) || !isfinite(t.z) || !isfinite(t.s);
             if (lane == 0) {
                 s_all[buf] = t;
-                if (!plain) s_factor[buf] = factor(a, row, s_tok[st], t, false, rank == 0);
+                s_plain[buf] = plain;
+                if (!plain) s_factor[buf] = factor(a, row, tok, t, false, rank == 0);
                 ptx::mbar_arrive(&s_ready[buf]);
             }
             __syncwarp();
             if (plain) {
-                if (!wait(&s_part2, again & 1) || !join(s_warp[buf], t)) break;
+                if (!wait(&s_part2, again & 1)) break;
+                float4 q = lane < kRingWarps ? s_warp[lane] : make_float4(-FLT_MAX, 0.0f, 0.0f, 0.0f);
+                t = over_warp(Stat{q.x, q.y, q.z}, a.c, 16);
+                if (cs > 1) {
+                    const int k = again & 1;
+                    if (lane < cs) st_async_v4(&s_cta2[k][rank], &s_met2[k], lane, make_float4(t.m, t.z, t.s, 0.0f));
+                    __syncwarp();
+                    q = make_float4(-FLT_MAX, 0.0f, 0.0f, 0.0f);
+                    if (!receive(s_cta2[k], &s_met2[k], (again / 2) & 1, q)) break;
+                    t = over_warp(Stat{q.x, q.y, q.z}, a.c, 4);
+                }
                 if (lane == 0) {
                     s_all[buf] = t;
-                    s_factor[buf] = factor(a, row, s_tok[st], t, true, rank == 0);
+                    s_factor[buf] = factor(a, row, tok, t, true, rank == 0);
                     ptx::mbar_arrive(&s_ready2);
                 }
                 __syncwarp();
@@ -689,14 +765,6 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         }
     } else {
         int again = 0;
-        auto give = [&](Stat t, int buf, uint64_t *bar) {
-            t = over_warp(t, a.c, 16);
-            if (lane == 0) {
-                s_warp[buf][warp] = make_float4(t.m, t.z, t.s, 0.0f);
-                ptx::mbar_arrive(bar);
-            }
-            __syncwarp();
-        };
         const int64_t x_step = step * a.ld * (16 / E), dx_step = step * a.ldd * (16 / E);
         const char *x_in = static_cast<const char *>(a.x) + first * a.ld * (16 / E), *x_out = x_in;
         char *dx = a.dx ? static_cast<char *>(a.dx) + first * a.ldd * (16 / E) : nullptr;
@@ -704,33 +772,38 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         // row n's statistics
         auto measure = [&](int n) -> bool {
             if (!wait(&s_full[in.st], in.parity)) return false;
-            Stat mine = {-FLT_MAX, 0.0f, 0.0f};
-            if (s_tok[in.st].takes) {
+            Sums t = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            const Token &tok = s_tok[n % kTokens];
+            if (tok.takes) {
                 const Row<BF16> r(a, x_in, nullptr);
                 int v0, len;
                 slice(r, v0, len);
                 const uint4 *sl = reinterpret_cast<const uint4 *>(ring + in.st * stage_bytes);
+                const float shift = -tok.x_id * a.c;
                 int i = tid;
                 for (; i + 3 * NT < len; i += 4 * NT) {
                     const uint4 q[4] = {sl[i], sl[i + NT], sl[i + 2 * NT], sl[i + 3 * NT]};
-                    add_block<BF16, 4>(mine, q, a.c);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) add<BF16>(t, q[k], a.c, shift);
                 }
-                for (; i < len; i += NT) {
-                    const uint4 q[1] = {sl[i]};
-                    add_block<BF16, 1>(mine, q, a.c);
-                }
+                for (; i < len; i += NT) add<BF16>(t, sl[i], a.c, shift);
+                s_sum[n % kRows][tid] = make_float2(t.z.x + t.z.y, t.s.x + t.s.y);
             }
-            give(mine, n & 1, &s_part[n & 1]);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&s_part[n % kRows]);
+            if (!dx && lane == 0) ptx::mbar_arrive(&s_empty[in.st]);  // the gradient alone reads the slice again
             x_in += x_step;
             in.next(stages);
             return true;
         };
         // row n's gradient
         auto finish = [&](int n) -> bool {
-            const int buf = n & 1, st = out.st;
-            if (!wait(&s_ready[buf], (n / 2) & 1)) return false;
-            const bool takes = s_tok[st].takes != 0;
-            if (dx || (takes && far_off(s_all[buf]))) {
+            const int buf = n % kRows;
+            const Token &tok = s_tok[n % kTokens];
+            if (!wait(&s_ready[buf], (n / kRows) & 1)) return false;
+            const bool takes = tok.takes != 0;
+            const bool plain = takes && s_plain[buf];
+            if (dx || plain) {
                 const Row<BF16> r(a, x_out, dx);
                 int v0, len;
                 slice(r, v0, len);
@@ -738,44 +811,62 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                     const float zero[E] = {};
                     for (int i = tid; i < len; i += NT) r.store(v0 + i, zero);
                 } else {
-                    const uint4 *sl = reinterpret_cast<const uint4 *>(ring + st * stage_bytes);
-                    Stat all = s_all[buf];
-                    const bool plain = far_off(all);
                     if (plain) {
                         Stat mine = {-FLT_MAX, 0.0f, 0.0f};
-                        for (int i = tid; i < len; i += NT) add_plain<BF16>(mine, sl[i], a.c);
-                        give(mine, buf, &s_part2);
+                        const uint4 *xv = r.vec();
+                        for (int i = v0 + tid; i < v0 + len; i += NT) add_plain<BF16>(mine, r.inside(i) ? xv[i] : r.load_end(i), a.c);
+                        mine = over_warp(mine, a.c, 16);
+                        if (lane == 0) {
+                            s_warp[warp] = make_float4(mine.m, mine.z, mine.s, 0.0f);
+                            ptx::mbar_arrive(&s_part2);
+                        }
+                        __syncwarp();
                         if (!wait(&s_ready2, again & 1)) return false;
                         ++again;
-                        all = s_all[buf];
                     }
                     if (dx) {
-                        const float coef = s_factor[buf].x, one_p = s_factor[buf].y, k = all.z == 0.0f ? 0.0f : -coef / all.z;
+                        const uint4 *sl = reinterpret_cast<const uint4 *>(ring + out.st * stage_bytes);
+                        const Stat all = s_all[buf];
+                        const float coef = s_factor[buf].x, k = all.z == 0.0f ? 0.0f : -coef / all.z;
                         int i = tid;
-                        if (!plain)
-                            for (; i + NT < len; i += 2 * NT) {
+                        if (!plain && r.dx_vec) {  // whole vectors, but for the row's ends
+                            const int in0 = max(r.full0 - v0, 0), in1 = min(r.full1 - v0, len);
+                            uint4 *to = reinterpret_cast<uint4 *>(dx - r.off * (16 / E)) + v0;
+                            const float shift = -all.m * a.c;
+                            for (i += in0; i + NT < in1; i += 2 * NT) {
                                 const uint4 q0 = sl[i], q1 = sl[i + NT];
-                                grad<BF16>(r, v0 + i, q0, all, a.c, k, false);
-                                grad<BF16>(r, v0 + i + NT, q1, all, a.c, k, false);
+                                to[i] = scaled<BF16>(q0, a.c, shift, k);
+                                to[i + NT] = scaled<BF16>(q1, a.c, shift, k);
                             }
+                            if (i < in1) to[i] = scaled<BF16>(sl[i], a.c, shift, k);
+                            if (tid < in0) grad<BF16>(r, v0 + tid, sl[tid], all, a.c, k, false);
+                            i = in1 + tid;
+                        }
                         for (; i < len; i += NT) grad<BF16>(r, v0 + i, sl[i], all, a.c, k, plain);
-                        const int own = (s_tok[st].id + r.off) / E - v0;  // the vector that holds the chosen token
-                        if (own >= 0 && own < len && own % NT == tid) V::put(dx, s_tok[st].id, coef * one_p);
+                        // the chosen token, by the thread that wrote its vector: which one follows from the loops above
+                        const int own = (tok.id + r.off) / E - v0;
+                        if (own >= 0 && own < len) {
+                            const int in0 = max(r.full0 - v0, 0), in1 = min(r.full1 - v0, len);
+                            const int by = plain || !r.dx_vec ? own : own < in0 ? own : own < in1 ? own - in0 : own - in1;
+                            if (by % NT == tid) V::put(dx, tok.id, coef * s_factor[buf].y);
+                        }
                     }
                 }
                 __syncwarp();
             }
-            if (lane == 0) ptx::mbar_arrive(&s_empty[st]);
+            if (dx) {
+                if (lane == 0) ptx::mbar_arrive(&s_empty[out.st]);
+                dx += dx_step;
+            }
             x_out += x_step;
-            if (dx) dx += dx_step;
             out.next(stages);
             return true;
         };
-        bool ok = first < a.T && measure(0);
-        int n = 0;
-        for (int64_t row = first; ok && row < a.T; row += step, ++n) {
-            if (row + step < a.T) ok = measure(n + 1);
-            ok = ok && finish(n);
+        bool ok = true;
+        const int rows = (int)((a.T - first + step - 1) / step);
+        for (int n = 0; ok && n < rows + depth; ++n) {
+            if (n < rows) ok = measure(n);
+            if (ok && n >= depth) ok = finish(n - depth);
         }
     }
     __syncwarp();
@@ -891,7 +982,9 @@ cudaError_t launch_ring(const LossArgs &a, int cs, int stages, size_t slice, cud
         ++n;
     }
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, policy_ring_kernel<BF16>, a, log_cs, stages, (uint32_t)slice, error_word());
+    // without a gradient a slice is free after its statistics; with one, half the stages are left to the copies
+    const int depth = !a.dx ? kRows - 1 : stages >= 5 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, policy_ring_kernel<BF16>, a, log_cs, stages, depth, (uint32_t)slice, error_word());
 }
 
 // Which kernel, and its cluster.  The ring: rows of 16 KB and more, when there
