@@ -72,11 +72,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 // Probabilities are rounded to bf16 for the second product, as its operands are
 // bf16; their sum l stays in FP32.
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) rows16_kernel(const Args a, int prefix_items)
+__global__ void __launch_bounds__(kWarps * 32) rows16_kernel(const Args a, int prefix_items, int beside_tc)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     pdl_trigger();
-    pdl_wait();
+    // Beside the tcgen05 kernel, whose CTAs let this one start once all work before both has finished, there is nothing to
+    // wait for here; the kernel that joins the parts waits for both, because this one waits at its end.
+    if (!beside_tc) pdl_wait();
     // which rows, which keys
     int item = blockIdx.x;
     const bool pre = item < prefix_items;
@@ -89,7 +91,10 @@ __global__ void __launch_bounds__(kWarps * 32) rows16_kernel(const Args a, int p
     const int hk = rest % a.Hkv, seg = rest / a.Hkv;  // seg: group or sequence
     const int len = pre ? prefix_len(a, seg) : suffix_len(a, seg);
     const int k_lo = part * (pre ? a.p_chunk : a.s_chunk);
-    if (k_lo >= len) return;
+    if (k_lo >= len) {
+        if (beside_tc) pdl_wait();
+        return;
+    }
     const int k_hi = min(len, k_lo + (pre ? a.p_chunk : a.s_chunk));
     const int n_rows = (pre ? a.G : 1) * a.Lq * a.gs;
 
@@ -240,9 +245,25 @@ __global__ void __launch_bounds__(kWarps * 32) rows16_kernel(const Args a, int p
         }
         if (lane == 0) a.part_ml[at] = make_float2(M, L);
     }
+    if (beside_tc) pdl_wait();
 }
 
 // ------------------------------------------------------------------ joining a row's parts
+// Parts that the tcgen05 kernel left for row r of a segment and kv head.
+__device__ __forceinline__ int tc_parts(const Args &a, bool pre, int seg, int hk, int r, int len)
+{
+    const int T = key_tiles(len);
+    if (T == 0) return 0;
+    const Units u((pre ? a.G : 1) * a.Lq * a.gs);
+    int64_t before, total;
+    steps_before(a, pre, seg, before, total);
+    const int64_t per_cta = steps_per_cta(a, total);
+    const int pair = r / 256;
+    const bool single = pair == u.full;
+    const int64_t first = before + hk * u.steps(T) + (int64_t)pair * T, n = single ? (T + 1) / 2 : T;
+    return (int)((first + n - 1) / per_cta - first / per_cta + 1) * (single ? 2 : 1);
+}
+
 // One warp per query row; the parts that exist follow from the lengths.
 template <int D>
 __global__ void __launch_bounds__(128) join_kernel(const Args a)
@@ -255,8 +276,12 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a)
     const int h = (int)(row % a.Hq);
     const int64_t bl = row / a.Hq;
     const int l = (int)(bl % a.Lq), b = (int)(bl / a.Lq);
-    const int np = a.n_pp ? (prefix_len(a, b / a.G) + a.p_chunk - 1) / a.p_chunk : 0;
-    const int ns = a.n_sp ? (suffix_len(a, b) + a.s_chunk - 1) / a.s_chunk : 0;
+    const int plen = a.n_pp ? prefix_len(a, b / a.G) : 0, slen = a.n_sp ? suffix_len(a, b) : 0;
+    const int hk = h / a.gs, hi = h - hk * a.gs;
+    int np = a.n_pp ? (plen + a.p_chunk - 1) / a.p_chunk : 0;
+    int ns = a.n_sp ? (slen + a.s_chunk - 1) / a.s_chunk : 0;
+    if (a.p_tc) np = tc_parts(a, true, b / a.G, hk, ((b % a.G) * a.Lq + l) * a.gs + hi, plen);
+    if (a.s_tc) ns = tc_parts(a, false, b, hk, l * a.gs + hi, slen);
     const int64_t base = row * (a.n_pp + a.n_sp);
     const auto at = [&](int k) { return base + (k < np ? k : a.n_pp + k - np); };
     float M = kNone;
@@ -268,6 +293,7 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a)
 #pragma unroll 4
     for (int k = 0; k < np + ns; ++k) {
         const float2 ml = a.part_ml[at(k)];
+        if (ml.y == 0.0f && ml.x == kNone) continue;  // saw no key, and may have left no o
         const float w = ex2(ml.x - M);
         L = fmaf(w, ml.y, L);
         const float *p = a.part_o + at(k) * D + lane * E;
@@ -289,9 +315,21 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a)
 
 int ceil_div(int64_t x, int64_t y) { return (int)((x + y - 1) / y); }
 
-// Chunk lengths, tiles and parts of a call; false where a size is not covered.
-// Chunks: about four CTAs per SM over all rows and keys, 64 to 2048 keys each.
-bool shape(const qerl_prefix_attn_dims *d, Args &a)
+// Most parts of a row that the tcgen05 kernel leaves: a unit's steps over a CTA's, which are at least the line's length
+// over the CTAs; of a left-over tile two each.
+int tc_parts_most(int64_t rows, int64_t len, int64_t Hkv, int64_t ctas)
+{
+    const int64_t t = (rows + 127) / 128, full = t / 2, T = (len + 127) / 128, half = (T + 1) / 2;
+    const auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
+    const int64_t pairs = full ? least(T, ctas / (Hkv * full) + 3) : 0;
+    const int64_t single = t & 1 ? 2 * least(half, ctas / (Hkv * (full ? full + 1 : 1)) + 3) : 0;
+    return (int)(pairs > single ? pairs : single);
+}
+
+// Kernels, chunk lengths, tiles and parts of a call; false where a size is not covered.
+// tcgen05 takes a segment whose rows fill more than two tiles of 16.
+// Chunks of the other kernel: about four CTAs per SM over all rows and keys, 64 to 2048 keys each.
+bool shape(const qerl_prefix_attn_dims *d, Args &a, bool tc)
 {
     if (d->B < 1 || d->Lq < 1 || d->Hq < 1 || d->Hkv < 1 || d->n_prefix < 1 || d->P < 0 || d->S < 0) return false;
     if ((d->D != 64 && d->D != 128) || d->Hq % d->Hkv || d->B % d->n_prefix) return false;
@@ -299,14 +337,18 @@ bool shape(const qerl_prefix_attn_dims *d, Args &a)
     if (d->B > big || d->Lq > big || d->Hq > 65536 || d->P > big || d->S > big || d->B * d->Lq > big / d->Hq) return false;
     a.B = (int)d->B, a.Lq = (int)d->Lq, a.Hq = (int)d->Hq, a.Hkv = (int)d->Hkv, a.n_prefix = (int)d->n_prefix;
     a.G = a.B / a.n_prefix, a.gs = a.Hq / a.Hkv, a.P = (int)d->P, a.S = (int)d->S;
-    a.p_tiles = ceil_div((int64_t)a.G * a.Lq * a.gs, 16);
-    a.s_tiles = ceil_div((int64_t)a.Lq * a.gs, 16);
-    const int64_t up = (int64_t)a.n_prefix * a.Hkv * a.p_tiles, us = (int64_t)a.B * a.Hkv * a.s_tiles;
+    const int64_t pr = (int64_t)a.G * a.Lq * a.gs, sr = (int64_t)a.Lq * a.gs;
+    a.p_tiles = ceil_div(pr, 16), a.s_tiles = ceil_div(sr, 16);
+    a.p_tc = tc && pr > 32 && a.P >= 128;
+    a.s_tc = tc && sr > 32 && a.S >= 128;
+    a.grid_tc = num_sms();
+    const int64_t up = a.p_tc ? 0 : (int64_t)a.n_prefix * a.Hkv * a.p_tiles, us = a.s_tc ? 0 : (int64_t)a.B * a.Hkv * a.s_tiles;
     const int64_t want = (up * a.P + us * a.S) / (4 * num_sms());
     int64_t chunk = (want + 63) / 64 * 64;
     chunk = chunk < 64 ? 64 : chunk > 2048 ? 2048 : chunk;
     a.p_chunk = a.s_chunk = (int)chunk;
-    a.n_pp = ceil_div(a.P, chunk), a.n_sp = ceil_div(a.S, chunk);
+    a.n_pp = a.p_tc ? tc_parts_most(pr, a.P, a.Hkv, a.grid_tc) : ceil_div(a.P, chunk);
+    a.n_sp = a.s_tc ? tc_parts_most(sr, a.S, a.Hkv, a.grid_tc) : ceil_div(a.S, chunk);
     return up * a.n_pp + us * a.n_sp < 0x7FFFFFFF;
 }
 size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
@@ -317,15 +359,18 @@ size_t ws_total(const Args &a, int64_t D)
 }
 
 template <int D>
-qerl_status run(const Args &a, cudaStream_t s)
+qerl_status run(const Args &a, const void *maps, cudaStream_t s)
 {
-    const bool chain = g_chain.load() != 0;
-    const int64_t pi = (int64_t)a.n_prefix * a.Hkv * a.p_tiles * a.n_pp, si = (int64_t)a.B * a.Hkv * a.s_tiles * a.n_sp;
+    const bool chain = g_chain.load() != 0, tc = a.p_tc || a.s_tc;
+    if (tc) QERL_TRY(launched(tc_launch(a, D, maps, s, chain)));
+    const int64_t pi = a.p_tc ? 0 : (int64_t)a.n_prefix * a.Hkv * a.p_tiles * a.n_pp,
+                  si = a.s_tc ? 0 : (int64_t)a.B * a.Hkv * a.s_tiles * a.n_sp;
     if (pi + si > 0) {
         static const cudaError_t attr =
             cudaFuncSetAttribute(rows16_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
         if (attr != cudaSuccess) return QERL_ERR_CUDA;
-        QERL_TRY(launched(launch_k(rows16_kernel<D>, dim3((unsigned)(pi + si)), dim3(kWarps * 32), smem_bytes<D>(), s, chain, a, (int)pi)));
+        QERL_TRY(launched(launch_k(rows16_kernel<D>, dim3((unsigned)(pi + si)), dim3(kWarps * 32), smem_bytes<D>(), s, chain, a, (int)pi,
+                                   tc && chain ? 1 : 0)));
     }
     const int64_t rows = (int64_t)a.B * a.Lq * a.Hq;
     return launched(launch_k(join_kernel<D>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, chain, a));
@@ -339,10 +384,10 @@ using namespace qerl;
 
 extern "C" size_t qerl_prefix_attention_ws_bytes(const qerl_prefix_attn_dims *dims)
 {
-    attn::Args a = {};
-    if (!dims || !attn::shape(dims, a)) return 0;
-    const size_t n = attn::ws_total(a, dims->D);
-    return n ? n : 256;
+    attn::Args a = {}, b = {};  // with tcgen05, and without where the caches' strides fit no tensor map
+    if (!dims || !attn::shape(dims, a, true) || !attn::shape(dims, b, false)) return 0;
+    const size_t n = attn::ws_total(a, dims->D), m = attn::ws_total(b, dims->D);
+    return n > m ? n : m ? m : 256;
 }
 
 extern "C" qerl_status qerl_prefix_attention(const qerl_prefix_attn_dims *d, const void *q, const void *k_prefix, const void *v_prefix,
@@ -352,7 +397,7 @@ extern "C" qerl_status qerl_prefix_attention(const qerl_prefix_attn_dims *d, con
 {
     if (!d || !q || !out || !(scale > 0.0f) || !(scale <= FLT_MAX)) return QERL_ERR_INVALID_ARG;
     attn::Args a = {};
-    if (!attn::shape(d, a)) return QERL_ERR_SHAPE;
+    if (!attn::shape(d, a, true)) return QERL_ERR_SHAPE;
     if ((a.P && (!k_prefix || !v_prefix)) || (a.S && (!k_suffix || !v_suffix || !suffix_lens))) return QERL_ERR_INVALID_ARG;
     const int64_t *const strides[] = {d->q_stride, d->out_stride, d->k_prefix_stride, d->v_prefix_stride, d->k_suffix_stride, d->v_suffix_stride};
     for (int t = 0; t < 6; ++t)
@@ -371,8 +416,6 @@ extern "C" qerl_status qerl_prefix_attention(const qerl_prefix_attn_dims *d, con
     a.q = bf(q), a.kp = bf(k_prefix), a.vp = bf(v_prefix), a.ks = bf(k_suffix), a.vs = bf(v_suffix);
     a.plen = prefix_lens, a.slen = suffix_lens;
     a.out = static_cast<__nv_bfloat16 *>(out), a.lse = lse;
-    a.part_ml = static_cast<float2 *>(ws);
-    a.part_o = reinterpret_cast<float *>(static_cast<char *>(ws) + attn::ml_bytes(a));
     a.q_b = d->q_stride[0], a.q_l = d->q_stride[1], a.q_h = d->q_stride[2];
     a.o_b = d->out_stride[0], a.o_l = d->out_stride[1], a.o_h = d->out_stride[2];
     a.kp_g = d->k_prefix_stride[0], a.kp_t = d->k_prefix_stride[1], a.kp_h = d->k_prefix_stride[2];
@@ -380,5 +423,9 @@ extern "C" qerl_status qerl_prefix_attention(const qerl_prefix_attn_dims *d, con
     a.ks_b = d->k_suffix_stride[0], a.ks_t = d->k_suffix_stride[1], a.ks_h = d->k_suffix_stride[2];
     a.vs_b = d->v_suffix_stride[0], a.vs_t = d->v_suffix_stride[1], a.vs_h = d->v_suffix_stride[2];
     a.scale_log2 = (float)((double)scale * 1.4426950408889634);
-    return d->D == 128 ? attn::run<128>(a, as_cuda(stream)) : attn::run<64>(a, as_cuda(stream));
+    alignas(64) char maps[attn::kTcMapsBytes];
+    if ((a.p_tc || a.s_tc) && !attn::tc_maps(a, d->D, maps)) attn::shape(d, a, false);
+    a.part_ml = static_cast<float2 *>(ws);
+    a.part_o = reinterpret_cast<float *>(static_cast<char *>(ws) + attn::ml_bytes(a));
+    return d->D == 128 ? attn::run<128>(a, maps, as_cuda(stream)) : attn::run<64>(a, maps, as_cuda(stream));
 }

@@ -25,7 +25,8 @@ struct Args {
     int B, Lq, Hq, Hkv, G, gs, n_prefix;
     int P, S;
     int p_chunk, s_chunk, n_pp, n_sp, p_tiles, s_tiles;
-    float scale_log2;  // scale * log2(e)
+    int p_tc, s_tc, grid_tc;  // segments that the tcgen05 kernel takes, and its CTAs
+    float scale_log2;         // scale * log2(e)
 };
 
 constexpr float kNone = -3.402823466e+38f;  // m of a part without keys
@@ -36,12 +37,71 @@ __device__ __forceinline__ int prefix_len(const Args &a, int g)
 }
 __device__ __forceinline__ int suffix_len(const Args &a, int b) { return max(0, min(a.slen[b], a.S)); }
 
+// The tcgen05 kernel's schedule.  Its work is a line of steps that its CTAs share
+// evenly, in contiguous ranges.  The rows of a segment and kv head form tiles of
+// 128: two tiles together are a unit whose step is one 128-key tile for both; a
+// tile that is left over is a unit whose step is two key tiles, one per half of
+// the CTA.  Order: segment (prefixes, then suffixes), kv head, unit.
+struct Units {
+    int full, single;  // units of two row tiles; 1 if one tile is left over
+    __device__ __forceinline__ explicit Units(int rows)
+    {
+        const int t = (rows + 127) / 128;
+        full = t / 2;
+        single = t & 1;
+    }
+    __device__ __forceinline__ int64_t steps(int key_tiles) const  // of one kv head
+    {
+        return (int64_t)full * key_tiles + single * ((key_tiles + 1) / 2);
+    }
+};
+__device__ __forceinline__ int key_tiles(int len) { return (len + 127) / 128; }
+
+// Steps of all segments (t), and of those before segment s of the prefixes (pre) or suffixes, over a whole warp.
+__device__ __forceinline__ void steps_before(const Args &a, bool pre, int s, int64_t &before, int64_t &t)
+{
+    const int lane = threadIdx.x % 32;
+    int64_t b = 0, all = 0;
+    if (a.p_tc) {
+        const Units u(a.G * a.Lq * a.gs);
+        for (int g = lane; g < a.n_prefix; g += 32) {
+            const int64_t n = u.steps(key_tiles(prefix_len(a, g))) * a.Hkv;
+            all += n;
+            if (!pre || g < s) b += n;
+        }
+    }
+    if (a.s_tc) {
+        const Units u(a.Lq * a.gs);
+        for (int k = lane; k < a.B; k += 32) {
+            const int64_t n = u.steps(key_tiles(suffix_len(a, k))) * a.Hkv;
+            all += n;
+            if (!pre && k < s) b += n;
+        }
+    }
+    for (int o = 16; o; o >>= 1) {
+        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+        all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+    }
+    before = b;
+    t = all;
+}
+__device__ __forceinline__ int64_t steps_per_cta(const Args &a, int64_t total)
+{
+    const int64_t n = (total + a.grid_tc - 1) / a.grid_tc;
+    return n ? n : 1;
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// Launches the tcgen05 kernel; false where its tensor maps cannot describe the caches (nothing is launched).
+bool tc_maps(const Args &a, int64_t D, void *maps);
+cudaError_t tc_launch(const Args &a, int64_t D, const void *maps, cudaStream_t s, bool chain);
+constexpr size_t kTcMapsBytes = 4 * 128;
 
 }  // namespace attn
 }  // namespace qerl

@@ -1,0 +1,459 @@
+// Attention parts of many query rows on tcgen05 (see prefix_attn.cuh for the
+// schedule and the parts).
+//
+// A CTA works on two row tiles of 128 (or on two key tiles of one row tile) at a
+// time, so that the tensor core multiplies for one while the other is in its
+// softmax.  Warps 0-3 and 4-7: the softmax of the two, one thread per row; warp
+// 8: TMA loads of the key and value tiles; warp 9: the MMAs.  Per tile and half:
+//     S = Q K^T     Q, K in shared memory (K-major), S in TMEM, FP32
+//     P = 2^(S c - m)  read from TMEM, written back as bf16 over S
+//     O += P V      P from TMEM, V as it lies in the cache (MN-major), O in TMEM
+// m is raised only when a row's maximum outgrows it by 2^8 (the weights stay
+// below 2^8 and are normalised in the end all the same), so O is rescaled rarely.
+// S and P share columns: Q K^T of a half's next tile is issued once P V of its
+// last one has completed.
+// Shared memory: Q 64 KB, two K and two V tiles of 32 KB (D = 128).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "prefix_attn.cuh"
+#include "sm100_ptx.cuh"
+
+namespace qerl {
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // linear_tc.cu
+
+namespace attn {
+namespace {
+
+using namespace ptx;
+
+struct Maps {
+    CUtensorMap kp, vp, ks, vs;
+};
+static_assert(sizeof(CUtensorMap) == 128, "");
+static_assert(sizeof(Maps) == kTcMapsBytes, "");
+
+constexpr int kThreads = 320, kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kStages = 2;
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+        "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+          "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+template <int D>
+struct Smem {
+    static constexpr int SUB = D / 64;             // 64-element column blocks of a tile
+    static constexpr int TILE = SUB * 128 * 128;   // bytes of a 128-row tile
+    static constexpr int Q = 0, K = 2 * TILE, V = K + kStages * TILE, TOTAL = V + kStages * TILE;
+};
+
+// A contiguous range of steps inside one unit.
+struct Seg {
+    bool pre, single;
+    int seg, hk, pair, len, tile0, n_steps, part;
+    int n0, n1;  // tiles of the two halves
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_constant__ Maps maps, const Args a, unsigned int *err)
+{
+    using M = Smem<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // the swizzled tiles' alignment
+    __shared__ uint64_t b_q[2], b_kfull[kStages], b_kempty[kStages], b_vfull[kStages], b_vempty[kStages], b_s[2], b_p[2], b_o[2], b_end;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_stop;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    if (tid == 0) {
+        for (int k = 0; k < kStages; ++k) {
+            mbar_init(&b_kfull[k], 1);
+            mbar_init(&b_kempty[k], 1);
+            mbar_init(&b_vfull[k], 1);
+            mbar_init(&b_vempty[k], 1);
+        }
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(&b_q[h], 128);
+            mbar_init(&b_s[h], 1);
+            mbar_init(&b_p[h], 128);
+            mbar_init(&b_o[h], 1);
+        }
+        mbar_init(&b_end, 1);
+        s_stop = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&s_tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    pdl_wait();
+    pdl_trigger();  // a chained successor finds everything before this kernel finished
+
+    // Every wait is bounded: past two seconds the error is latched and the CTA winds up.
+    const uint64_t limit_ns = 2000000000ull;
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        bool ok = mbar_try_wait(bar, parity & 1u);
+        if (!ok) {
+            const uint64_t until = globaltimer_ns() + limit_ns;
+            while (!(ok = mbar_try_wait_sleep(bar, parity & 1u, 20000u))) {
+                if (*reinterpret_cast<volatile int *>(&s_stop)) break;
+                if (globaltimer_ns() > until) {
+                    *reinterpret_cast<volatile int *>(&s_stop) = 1;
+                    latch_error(err, QERL_ERR_TIMEOUT);
+                    break;
+                }
+            }
+        }
+        return __all_sync(0xFFFFFFFFu, ok);
+    };
+
+    int64_t before, total;
+    steps_before(a, false, 0, before, total);  // before: the prefixes' steps
+    const int64_t per_cta = steps_per_cta(a, total);
+    const int64_t begin = blockIdx.x * per_cta, end = min(begin + per_cta, total);
+    const Units up(a.G * a.Lq * a.gs), us(a.Lq * a.gs);
+    // the range of steps at `pos` that lies in one unit
+    auto locate = [&](int64_t pos) -> Seg {
+        Seg s;
+        s.pre = pos < before;
+        int64_t at = s.pre ? 0 : before;
+        const Units &u = s.pre ? up : us;
+        int64_t n = 0;
+        for (s.seg = 0;; ++s.seg, at += n) {
+            s.len = s.pre ? prefix_len(a, s.seg) : suffix_len(a, s.seg);
+            n = u.steps(key_tiles(s.len)) * a.Hkv;
+            if (pos < at + n) break;
+        }
+        const int T = key_tiles(s.len);
+        const int64_t per_head = u.steps(T);
+        s.hk = (int)((pos - at) / per_head);
+        at += s.hk * per_head;
+        s.pair = (int)min((int64_t)u.full, (pos - at) / T);
+        s.single = s.pair == u.full;
+        at += (int64_t)s.pair * T;
+        const int64_t unit = s.single ? (T + 1) / 2 : T;
+        const int first = (int)(pos - at);
+        s.n_steps = (int)(min(at + unit, end) - pos);
+        s.part = (int)(pos / per_cta - at / per_cta);
+        if (s.single) {  // half h takes tiles 2 (first + i) + h
+            s.tile0 = 2 * first;
+            s.n0 = s.n_steps;
+            s.n1 = min(s.n_steps, (T - s.tile0) / 2);
+        } else {
+            s.tile0 = first;
+            s.n0 = s.n1 = s.n_steps;
+        }
+        return s;
+    };
+
+    if (warp == kTmaWarp) {
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t pos = begin; ok && pos < end;) {
+            const Seg s = locate(pos);
+            const int tiles = s.single ? s.n0 + s.n1 : s.n0;
+            const CUtensorMap *mk = s.pre ? &maps.kp : &maps.ks, *mv = s.pre ? &maps.vp : &maps.vs;
+            for (int t = 0; ok && t < tiles; ++t, ++it) {
+                const int st = it % kStages, k0 = (s.tile0 + t) * 128;
+                const uint32_t round = it / kStages;
+                if (round > 0 && !(ok = wait(&b_kempty[st], round - 1))) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&b_kfull[st], M::TILE);
+                    for (int c = 0; c < M::SUB; ++c)
+                        tma_load_4d(smem + M::K + st * M::TILE + c * 16384, mk, &b_kfull[st], c * 64, s.hk, k0, s.seg);
+                }
+                __syncwarp();
+                if (round > 0 && !(ok = wait(&b_vempty[st], round - 1))) {
+                    ++it;  // its K load is in flight
+                    break;
+                }
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&b_vfull[st], M::TILE);
+                    for (int c = 0; c < M::SUB; ++c)
+                        tma_load_4d(smem + M::V + st * M::TILE + c * 16384, mv, &b_vfull[st], c * 64, s.hk, k0, s.seg);
+                }
+                __syncwarp();
+            }
+            pos += s.n_steps;
+        }
+        // no load may be in flight when the CTA ends
+        if (*reinterpret_cast<volatile int *>(&s_stop)) {
+            const uint64_t until = globaltimer_ns() + limit_ns;
+            for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k) {
+                while (!mbar_try_wait(&b_kfull[k % kStages], (k / kStages) & 1u) && globaltimer_ns() < until) {
+                }
+                // the last V load may not have been issued: its wait ends at the deadline
+                while (!mbar_try_wait(&b_vfull[k % kStages], (k / kStages) & 1u) && globaltimer_ns() < until) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        const uint32_t id_qk = idesc_bf16_f32(128, 128), id_pv = idesc_bf16_f32(128, D) | (1u << 16);  // V is MN-major
+        uint32_t kc = 0, vc = 0;               // tiles taken from the rings in earlier segments
+        uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // Q tiles and P V products so far
+        bool ok = true;
+        for (int64_t pos = begin; ok && pos < end;) {
+            const Seg s = locate(pos);
+            const int n[2] = {s.n0, s.n1};
+            const uint32_t tiles = (uint32_t)(s.single ? s.n0 + s.n1 : s.n0);
+            auto qk = [&](int h, int i) -> bool {
+                const uint32_t t = kc + (uint32_t)(s.single ? 2 * i + h : i);
+                if (i == 0 && !wait(&b_q[h], qn[h]++)) return false;
+                if (i > 0 && !wait(&b_o[h], pn[h] - 1)) return false;  // P of the last tile is read
+                if (!wait(&b_kfull[t % kStages], t / kStages)) return false;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t ad = desc_kmajor_sw128(smem_u32(smem + M::Q + h * M::TILE));
+                    const uint64_t bd = desc_kmajor_sw128(smem_u32(smem + M::K + (t % kStages) * M::TILE));
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t o = (uint64_t)((kk / 4) * (16384 >> 4) + 2 * (kk % 4));
+                        umma_bf16(tmem + h * 256, ad + o, bd + o, id_qk, kk > 0);
+                    }
+                    umma_commit(&b_s[h]);
+                    if (s.single || h == 1) umma_commit(&b_kempty[t % kStages]);
+                }
+                __syncwarp();
+                return true;
+            };
+            auto pv = [&](int h, int i) -> bool {
+                const uint32_t t = vc + (uint32_t)(s.single ? 2 * i + h : i);
+                if (!wait(&b_p[h], pn[h])) return false;
+                if (!wait(&b_vfull[t % kStages], t / kStages)) return false;
+                ++pn[h];
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t vt = smem_u32(smem + M::V + (t % kStages) * M::TILE);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)  // 16 keys: two 8-row groups of every column block
+                        umma_bf16_ts(tmem + h * 256 + 128, tmem + h * 256 + 8 * kk, desc_mnmajor_sw128(vt + 2048u * kk, 16384, 1024), id_pv,
+                                     i > 0 || kk > 0);
+                    umma_commit(&b_o[h]);
+                    if (s.single || h == 1) umma_commit(&b_vempty[t % kStages]);
+                }
+                __syncwarp();
+                return true;
+            };
+            ok = qk(0, 0) && (n[1] == 0 || qk(1, 0));
+            for (int i = 0; ok && i < n[0]; ++i)
+                for (int h = 0; ok && h < 2; ++h)
+                    if (i < n[h]) ok = pv(h, i) && (i + 1 >= n[h] || qk(h, i + 1));
+            kc += tiles;
+            vc += tiles;
+            pos += s.n_steps;
+        }
+        // every product issued has completed before TMEM is freed
+        if (elect_one()) umma_commit(&b_end);
+        __syncwarp();
+        const uint64_t until = globaltimer_ns() + limit_ns;
+        while (!mbar_try_wait(&b_end, 0) && globaltimer_ns() < until) {
+        }
+        __syncwarp();
+    } else {
+        const int h = warp / 4, t = tid % 128;
+        const uint32_t tm = tmem + h * 256 + ((uint32_t)((warp % 4) * 32) << 16);
+        uint32_t sn = 0;  // S tiles so far
+        uint32_t vc = 0, vnext = 0;  // value tiles of earlier segments
+        bool ok = true;
+        for (int64_t pos = begin; ok && pos < end;) {
+            const Seg s = locate(pos);
+            pos += s.n_steps;
+            vc = vnext;
+            vnext += (uint32_t)(s.single ? s.n0 + s.n1 : s.n0);
+            const int n = h ? s.n1 : s.n0, R = (s.pre ? a.G : 1) * a.Lq * a.gs;
+            const int tile = s.single ? 2 * s.pair : 2 * s.pair + h;  // row tile
+            auto row_of = [&](int r, int &b, int &l, int &head) {
+                const int rr = tile * 128 + r, per = a.Lq * a.gs;
+                const int bi = rr / per, in = rr - bi * per;
+                b = s.pre ? s.seg * a.G + bi : s.seg;
+                l = in / a.gs;
+                head = s.hk * a.gs + in - l * a.gs;
+                return rr < R;
+            };
+            int b, l, head;
+            const bool mine = row_of(t, b, l, head);
+            const int parts = a.n_pp + a.n_sp;
+            const int64_t at = (((int64_t)b * a.Lq + l) * a.Hq + head) * parts + (s.pre ? 0 : a.n_pp) + (s.single ? 2 * s.part + h : s.part);
+            if (n == 0) {  // the odd half of a single key tile
+                if (mine) a.part_ml[at] = make_float2(kNone, 0.0f);
+                continue;
+            }
+            // this half's query rows; the last tile's product that read the old ones has completed (b_s)
+            constexpr int CH = D / 8;
+#pragma unroll 4
+            for (int i = 0; i < CH; ++i) {
+                const int r = (warp % 4) * 32 + i * (32 / CH) + lane / CH, c = lane % CH;
+                int qb, ql, qh;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (row_of(r, qb, ql, qh)) v = *reinterpret_cast<const uint4 *>(a.q + qb * a.q_b + ql * a.q_l + qh * a.q_h + c * 8);
+                st_shared_v4(smem_u32(smem + M::Q + h * M::TILE) + (c / 8) * 16384 + r * 128 + (((c % 8) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&b_q[h]);
+
+            const int limit = s.pre ? s.len : s.len - a.Lq + 1 + l;
+            float m = kNone, sum = 0.0f;
+            for (int i = 0; i < n; ++i) {
+                const int k0 = (s.tile0 + (s.single ? 2 * i + h : i)) * 128;
+                if (!(ok = wait(&b_s[h], sn++))) break;
+                tc_fence_after();
+                // 64 columns in registers at a time: the upper half for its maximum, then the lower half, which P's first
+                // columns overwrite, and the upper half once more
+                uint32_t x[64];
+                const bool cut = k0 + 128 > limit;
+                auto fetch = [&](int c0) {
+                    tmem_ld32(tm + c0, x);
+                    tmem_ld32(tm + c0 + 32, x + 32);
+                    tmem_wait_ld();
+                    if (cut) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            if (k0 + c0 + c >= limit) x[c] = 0xFF800000u;
+                    }
+                    __syncwarp();
+                };
+                float top = kNone;
+                fetch(64);
+#pragma unroll
+                for (int c = 0; c < 64; ++c) top = fmaxf(top, __uint_as_float(x[c]));
+                fetch(0);
+#pragma unroll
+                for (int c = 0; c < 64; ++c) top = fmaxf(top, __uint_as_float(x[c]));
+                top = top == kNone ? kNone : top * a.scale_log2;
+                const bool raise = top > m + 8.0f;
+                const float to = raise ? top : m, f = raise ? ex2(m - top) : 1.0f;
+                if (i > 0 && __any_sync(0xFFFFFFFFu, raise)) {  // O is still: the product before S has completed
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tm + 128 + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st32(tm + 128 + c, o);
+                    }
+                }
+                m = to;
+                sum *= f;
+                float2 add = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (c) fetch(64);
+                    uint32_t p[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float p0 = ex2(fmaf(__uint_as_float(x[2 * e]), a.scale_log2, -m));
+                        const float p1 = ex2(fmaf(__uint_as_float(x[2 * e + 1]), a.scale_log2, -m));
+                        add.x += p0;
+                        add.y += p1;
+                        const __nv_bfloat162 pk = __floats2bfloat162_rn(p0, p1);
+                        p[e] = *reinterpret_cast<const uint32_t *>(&pk);
+                    }
+                    tmem_st32(tm + c * 32, p);
+                }
+                sum += add.x + add.y;
+                if (k0 + 128 > s.len) {  // what the cache holds past the segment must not reach O, not even as 0 * NaN
+                    const uint32_t vt = vc + (uint32_t)(s.single ? 2 * i + h : i), st = vt % kStages;
+                    if (!(ok = wait(&b_vfull[st], vt / kStages))) break;
+                    if (k0 + t >= s.len)
+                        for (int c = 0; c < M::SUB * 8; ++c)
+                            st_shared_v4(smem_u32(smem + M::V + st * M::TILE) + (c / 8) * 16384 + t * 128 + (c % 8) * 16, 0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&b_p[h]);
+            }
+            if (!ok) break;
+            if (!(ok = wait(&b_o[h], sn - 1))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(tm + 128 + c, o);
+                tmem_wait_ld();
+                if (mine) {
+                    float4 *to = reinterpret_cast<float4 *>(a.part_o + at * D + c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        to[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
+                                            __uint_as_float(o[4 * e + 3]));
+                }
+                __syncwarp();
+            }
+            if (mine) a.part_ml[at] = make_float2(m, sum);
+            tc_fence_before();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// The cache [segments, T, Hkv, D] as boxes of 128 tokens x 64 columns of one kv head.
+bool make_map(CUtensorMap *m, const void *base, int64_t D, int64_t Hkv, int64_t T, int64_t n, int64_t s_h, int64_t s_t, int64_t s_n)
+{
+    const auto fn = encode_fn();
+    if (!fn) return false;
+    const auto bytes = [](int64_t stride, int64_t size) { return (cuuint64_t)(size == 1 ? 16 : stride * 2); };  // unused: any
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)T, (cuuint64_t)n};
+    const cuuint64_t strides[3] = {bytes(s_h, Hkv), bytes(s_t, T), bytes(s_n, n)};
+    const cuuint32_t box[4] = {64, 1, 128, 1}, es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(const Args &a, const Maps &maps, cudaStream_t s, bool chain)
+{
+    constexpr size_t smem = Smem<D>::TOTAL + 1024;
+    static const cudaError_t attr = cudaFuncSetAttribute(rows128_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (attr != cudaSuccess) return attr;
+    return launch_k(rows128_kernel<D>, dim3((unsigned)a.grid_tc), dim3(kThreads), smem, s, chain, maps, a, error_word());
+}
+
+}  // namespace
+
+bool tc_maps(const Args &a, int64_t D, void *out)
+{
+    Maps *m = static_cast<Maps *>(out);
+    return (!a.p_tc || (make_map(&m->kp, a.kp, D, a.Hkv, a.P, a.n_prefix, a.kp_h, a.kp_t, a.kp_g) &&
+                        make_map(&m->vp, a.vp, D, a.Hkv, a.P, a.n_prefix, a.vp_h, a.vp_t, a.vp_g))) &&
+           (!a.s_tc || (make_map(&m->ks, a.ks, D, a.Hkv, a.S, a.B, a.ks_h, a.ks_t, a.ks_b) &&
+                        make_map(&m->vs, a.vs, D, a.Hkv, a.S, a.B, a.vs_h, a.vs_t, a.vs_b)));
+}
+
+cudaError_t tc_launch(const Args &a, int64_t D, const void *maps, cudaStream_t s, bool chain)
+{
+    const Maps &m = *static_cast<const Maps *>(maps);
+    return D == 128 ? launch<128>(a, m, s, chain) : launch<64>(a, m, s, chain);
+}
+
+}  // namespace attn
+}  // namespace qerl
