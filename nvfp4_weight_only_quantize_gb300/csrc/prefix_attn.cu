@@ -75,10 +75,10 @@ template <int D>
 __global__ void __launch_bounds__(kWarps * 32) rows16_kernel(const Args a, int prefix_items, int beside_tc)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
-    pdl_trigger();
     // Beside the tcgen05 kernel, whose CTAs let this one start once all work before both has finished, there is nothing to
     // wait for here; the kernel that joins the parts waits for both, because this one waits at its end.
     if (!beside_tc) pdl_wait();
+    pdl_trigger();
     // which rows, which keys
     int item = blockIdx.x;
     const bool pre = item < prefix_items;
@@ -249,63 +249,99 @@ __global__ void __launch_bounds__(kWarps * 32) rows16_kernel(const Args a, int p
 }
 
 // ------------------------------------------------------------------ joining a row's parts
-// Parts that the tcgen05 kernel left for row r of a segment and kv head.
-__device__ __forceinline__ int tc_parts(const Args &a, bool pre, int seg, int hk, int r, int len)
+// Parts that the tcgen05 kernel left for row r of a segment (the line's k-th) and kv head.
+__device__ __forceinline__ int tc_parts(const Args &a, bool pre, int k, int hk, int r, int len)
 {
-    const int T = key_tiles(len);
+    const int T = key_tiles(len), per_cta = a.line[0], start = a.line[1 + k];
     if (T == 0) return 0;
     const Units u((pre ? a.G : 1) * a.Lq * a.gs);
-    int64_t before, total;
-    steps_before(a, pre, seg, before, total);
-    const int64_t per_cta = steps_per_cta(a, total);
     const int pair = r / 256;
     const bool single = pair == u.full;
-    const int64_t first = before + hk * u.steps(T) + (int64_t)pair * T, n = single ? (T + 1) / 2 : T;
-    return (int)((first + n - 1) / per_cta - first / per_cta + 1) * (single ? 2 : 1);
+    const int first = start + hk * u.steps(T) + pair * (kStart + T) + kStart, n = single ? (T + 1) / 2 : T;
+    return ((first + n - 1) / per_cta - first / per_cta + 1) * (single ? 2 : 1);
 }
 
-// One warp per query row; the parts that exist follow from the lengths.
-template <int D>
+// W warps per query row (each takes every W-th part, eight in flight); the parts
+// that exist follow from the lengths.
+template <int D, int W>
 __global__ void __launch_bounds__(128) join_kernel(const Args a)
 {
+    constexpr int E = D / 32, RB = 4 / W;  // columns of a lane; rows of a block
+    __shared__ float s_o[W > 1 ? 4 : 1][W > 1 ? D : 1];
+    __shared__ float2 s_ml[4];
     pdl_trigger();
-    pdl_wait();
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int64_t row = (int64_t)blockIdx.x * 4 + warp;
-    if (row >= (int64_t)a.B * a.Lq * a.Hq) return;
-    const int h = (int)(row % a.Hq);
-    const int64_t bl = row / a.Hq;
-    const int l = (int)(bl % a.Lq), b = (int)(bl / a.Lq);
-    const int plen = a.n_pp ? prefix_len(a, b / a.G) : 0, slen = a.n_sp ? suffix_len(a, b) : 0;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, share = warp % W;
+    const int row = blockIdx.x * RB + warp / W;
+    const bool live = row < a.B * a.Lq * a.Hq;
+    const int h = row % a.Hq, bl = row / a.Hq, l = bl % a.Lq, b = live ? bl / a.Lq : 0, g = b / a.G;
+    // the kernels before this one let it start after all work before the call: the lengths are there
+    const int plen = a.n_pp ? prefix_len(a, g) : 0, slen = a.n_sp ? suffix_len(a, b) : 0;
     const int hk = h / a.gs, hi = h - hk * a.gs;
-    int np = a.n_pp ? (plen + a.p_chunk - 1) / a.p_chunk : 0;
-    int ns = a.n_sp ? (slen + a.s_chunk - 1) / a.s_chunk : 0;
-    if (a.p_tc) np = tc_parts(a, true, b / a.G, hk, ((b % a.G) * a.Lq + l) * a.gs + hi, plen);
-    if (a.s_tc) ns = tc_parts(a, false, b, hk, l * a.gs + hi, slen);
-    const int64_t base = row * (a.n_pp + a.n_sp);
+    pdl_wait();
+    const int np = a.p_tc ? tc_parts(a, true, g, hk, ((b - g * a.G) * a.Lq + l) * a.gs + hi, plen)
+                          : a.n_pp ? (plen + a.p_chunk - 1) / a.p_chunk : 0;
+    const int ns = a.s_tc ? tc_parts(a, false, (a.p_tc ? a.n_prefix : 0) + b, hk, l * a.gs + hi, slen)
+                          : a.n_sp ? (slen + a.s_chunk - 1) / a.s_chunk : 0;
+    const int n = live ? np + ns : 0;
+    const int64_t base = (int64_t)row * (a.n_pp + a.n_sp);
     const auto at = [&](int k) { return base + (k < np ? k : a.n_pp + k - np); };
-    float M = kNone;
-    for (int k = lane; k < np + ns; k += 32) M = fmaxf(M, a.part_ml[at(k)].x);
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-    float L = 0.0f;
-    constexpr int E = D / 32;
-    float acc[E] = {};
-#pragma unroll 4
-    for (int k = 0; k < np + ns; ++k) {
-        const float2 ml = a.part_ml[at(k)];
-        if (ml.y == 0.0f && ml.x == kNone) continue;  // saw no key, and may have left no o
-        const float w = ex2(ml.x - M);
-        L = fmaf(w, ml.y, L);
-        const float *p = a.part_o + at(k) * D + lane * E;
-        if (E == 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(p);
-            acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
-            acc[E - 2] = fmaf(w, v.z, acc[E - 2]), acc[E - 1] = fmaf(w, v.w, acc[E - 1]);
-        } else {
-            const float2 v = *reinterpret_cast<const float2 *>(p);
-            acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
+    float M = kNone, L = 0.0f, acc[E] = {};
+    for (int k0 = share; k0 < n; k0 += 8 * W) {
+        float2 ml[8];
+        float v[8][E];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int k = k0 + j * W;
+            ml[j] = make_float2(kNone, 0.0f);
+            if (k < n) {
+                ml[j] = a.part_ml[at(k)];
+                const float *p = a.part_o + at(k) * D + lane * E;
+                if (E == 4) {
+                    const float4 q = *reinterpret_cast<const float4 *>(p);
+                    v[j][0] = q.x, v[j][1] = q.y, v[j][E - 2] = q.z, v[j][E - 1] = q.w;
+                } else {
+                    const float2 q = *reinterpret_cast<const float2 *>(p);
+                    v[j][0] = q.x, v[j][1] = q.y;
+                }
+            }
+        }
+        float to = M;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) to = fmaxf(to, ml[j].x);
+        const float f = ex2(M - to);
+        M = to;
+        L *= f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool none = ml[j].y == 0.0f && ml[j].x == kNone;  // no part, or one that saw no key and may have left no o
+            const float w = none ? 0.0f : ex2(ml[j].x - M);
+            L = fmaf(w, ml[j].y, L);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(w, none ? 0.0f : v[j][e], acc[e]);
         }
     }
+    if (W > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
+        if (lane == 0) s_ml[warp] = make_float2(M, L);
+        __syncthreads();
+        if (share) return;
+#pragma unroll
+        for (int k = 1; k < W; ++k) M = fmaxf(M, s_ml[warp + k].x);
+        L = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const float w = ex2(s_ml[warp + k].x - M);
+            L = fmaf(w, s_ml[warp + k].y, L);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(w, s_o[warp + k][lane * E + e], acc[e]);
+        }
+    }
+    if (!live) return;
     const float inv = L == 0.0f ? 0.0f : __fdividef(1.0f, L);  // a row that sees no key: zeros, lse -inf
     uint32_t *out = reinterpret_cast<uint32_t *>(a.out + b * a.o_b + l * a.o_l + h * a.o_h + lane * E);
 #pragma unroll
@@ -316,7 +352,7 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a)
 int ceil_div(int64_t x, int64_t y) { return (int)((x + y - 1) / y); }
 
 // Most parts of a row that the tcgen05 kernel leaves: a unit's steps over a CTA's, which are at least the line's length
-// over the CTAs; of a left-over tile two each.
+// over the CTAs (its empty steps, which only lengthen it, left out); of a left-over tile two each.
 int tc_parts_most(int64_t rows, int64_t len, int64_t Hkv, int64_t ctas)
 {
     const int64_t t = (rows + 127) / 128, full = t / 2, T = (len + 127) / 128, half = (T + 1) / 2;
@@ -327,7 +363,8 @@ int tc_parts_most(int64_t rows, int64_t len, int64_t Hkv, int64_t ctas)
 }
 
 // Kernels, chunk lengths, tiles and parts of a call; false where a size is not covered.
-// tcgen05 takes a segment whose rows fill more than two tiles of 16.
+// A segment of more than 16 rows goes to tcgen05 where that is quicker.  What was measured: a step of its line takes
+// about 2 us and a CTA about 8 us besides; the other kernel reads every key once per 16 rows, at some 5 TB/s from L2.
 // Chunks of the other kernel: about four CTAs per SM over all rows and keys, 64 to 2048 keys each.
 bool shape(const qerl_prefix_attn_dims *d, Args &a, bool tc)
 {
@@ -339,9 +376,16 @@ bool shape(const qerl_prefix_attn_dims *d, Args &a, bool tc)
     a.G = a.B / a.n_prefix, a.gs = a.Hq / a.Hkv, a.P = (int)d->P, a.S = (int)d->S;
     const int64_t pr = (int64_t)a.G * a.Lq * a.gs, sr = (int64_t)a.Lq * a.gs;
     a.p_tiles = ceil_div(pr, 16), a.s_tiles = ceil_div(sr, 16);
-    a.p_tc = tc && pr > 32 && a.P >= 128;
-    a.s_tc = tc && sr > 32 && a.S >= 128;
     a.grid_tc = num_sms();
+    const auto quicker = [&](int64_t rows, int64_t len, int64_t segments) {
+        const int64_t steps = segments * a.Hkv * (rows / 256 + 1) * ((len + 127) / 128);
+        const double tc_us = 8.0 + 2.0 * (double)((steps + a.grid_tc - 1) / a.grid_tc);
+        return rows > 16 && len >= 128 && tc_us * 5e6 < (double)(segments * a.Hkv * ((rows + 15) / 16) * len) * (double)(d->D * 4);
+    };
+    a.p_tc = tc && quicker(pr, a.P, a.n_prefix);
+    a.s_tc = tc && quicker(sr, a.S, a.B);
+    if ((a.p_tc ? (pr / 256 + 1) * (a.P / 128 + 4) * a.Hkv * a.n_prefix : 0) + (a.s_tc ? (sr / 256 + 1) * (a.S / 128 + 4) * a.Hkv * a.B : 0) > big)
+        a.p_tc = a.s_tc = 0;  // more steps than the kernel counts
     const int64_t up = a.p_tc ? 0 : (int64_t)a.n_prefix * a.Hkv * a.p_tiles, us = a.s_tc ? 0 : (int64_t)a.B * a.Hkv * a.s_tiles;
     const int64_t want = (up * a.P + us * a.S) / (4 * num_sms());
     int64_t chunk = (want + 63) / 64 * 64;
@@ -353,9 +397,10 @@ bool shape(const qerl_prefix_attn_dims *d, Args &a, bool tc)
 }
 size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 size_t ml_bytes(const Args &a) { return round256((size_t)a.B * a.Lq * a.Hq * (a.n_pp + a.n_sp) * sizeof(float2)); }
+size_t line_bytes(const Args &a) { return round256((size_t)(1 + a.n_prefix + a.B) * sizeof(int)); }
 size_t ws_total(const Args &a, int64_t D)
 {
-    return ml_bytes(a) + (size_t)a.B * a.Lq * a.Hq * (a.n_pp + a.n_sp) * D * sizeof(float);
+    return ml_bytes(a) + line_bytes(a) + (size_t)a.B * a.Lq * a.Hq * (a.n_pp + a.n_sp) * D * sizeof(float);
 }
 
 template <int D>
@@ -372,8 +417,11 @@ qerl_status run(const Args &a, const void *maps, cudaStream_t s)
         QERL_TRY(launched(launch_k(rows16_kernel<D>, dim3((unsigned)(pi + si)), dim3(kWarps * 32), smem_bytes<D>(), s, chain, a, (int)pi,
                                    tc && chain ? 1 : 0)));
     }
-    const int64_t rows = (int64_t)a.B * a.Lq * a.Hq;
-    return launched(launch_k(join_kernel<D>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, chain, a));
+    // a warp per row where its parts fit one batch or the rows fill the SMs, else four
+    const int rows = a.B * a.Lq * a.Hq;
+    if (a.n_pp + a.n_sp <= 8 || rows > 32 * num_sms())
+        return launched(launch_k(join_kernel<D, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, chain, a));
+    return launched(launch_k(join_kernel<D, 4>, dim3((unsigned)rows), dim3(128), 0, s, chain, a));
 }
 
 }  // namespace
@@ -426,6 +474,7 @@ extern "C" qerl_status qerl_prefix_attention(const qerl_prefix_attn_dims *d, con
     alignas(64) char maps[attn::kTcMapsBytes];
     if ((a.p_tc || a.s_tc) && !attn::tc_maps(a, d->D, maps)) attn::shape(d, a, false);
     a.part_ml = static_cast<float2 *>(ws);
-    a.part_o = reinterpret_cast<float *>(static_cast<char *>(ws) + attn::ml_bytes(a));
+    a.line = reinterpret_cast<int *>(static_cast<char *>(ws) + attn::ml_bytes(a));
+    a.part_o = reinterpret_cast<float *>(static_cast<char *>(ws) + attn::ml_bytes(a) + attn::line_bytes(a));
     return d->D == 128 ? attn::run<128>(a, maps, as_cuda(stream)) : attn::run<64>(a, maps, as_cuda(stream));
 }

@@ -19,6 +19,7 @@ struct Args {
     float *lse;
     float *part_o;   // [row][part][D]
     float2 *part_ml;  // [row][part]
+    int *line;        // the tcgen05 kernel's line: steps per CTA, then where each prefix and each suffix starts
     int64_t q_b, q_l, q_h, o_b, o_l, o_h;
     int64_t kp_g, kp_t, kp_h, vp_g, vp_t, vp_h;
     int64_t ks_b, ks_t, ks_h, vs_b, vs_t, vs_h;
@@ -41,7 +42,10 @@ __device__ __forceinline__ int suffix_len(const Args &a, int b) { return max(0, 
 // evenly, in contiguous ranges.  The rows of a segment and kv head form tiles of
 // 128: two tiles together are a unit whose step is one 128-key tile for both; a
 // tile that is left over is a unit whose step is two key tiles, one per half of
-// the CTA.  Order: segment (prefixes, then suffixes), kv head, unit.
+// the CTA.  Order: segment (prefixes, then suffixes), kv head, unit.  A unit's
+// steps follow kStart empty ones, which stand for what it costs to begin a unit
+// (its rows' loads and stores, about as long as three steps).
+constexpr int kStart = 3;
 struct Units {
     int full, single;  // units of two row tiles; 1 if one tile is left over
     __device__ __forceinline__ explicit Units(int rows)
@@ -50,44 +54,34 @@ struct Units {
         full = t / 2;
         single = t & 1;
     }
-    __device__ __forceinline__ int64_t steps(int key_tiles) const  // of one kv head
+    __device__ __forceinline__ int steps(int key_tiles) const  // of one kv head
     {
-        return (int64_t)full * key_tiles + single * ((key_tiles + 1) / 2);
+        return key_tiles ? full * (kStart + key_tiles) + single * (kStart + (key_tiles + 1) / 2) : 0;
     }
 };
 __device__ __forceinline__ int key_tiles(int len) { return (len + 127) / 128; }
 
-// Steps of all segments (t), and of those before segment s of the prefixes (pre) or suffixes, over a whole warp.
-__device__ __forceinline__ void steps_before(const Args &a, bool pre, int s, int64_t &before, int64_t &t)
+// Steps of segment k of the line (prefixes, then suffixes).
+__device__ __forceinline__ int segment_steps(const Args &a, int k)
 {
-    const int lane = threadIdx.x % 32;
-    int64_t b = 0, all = 0;
-    if (a.p_tc) {
-        const Units u(a.G * a.Lq * a.gs);
-        for (int g = lane; g < a.n_prefix; g += 32) {
-            const int64_t n = u.steps(key_tiles(prefix_len(a, g))) * a.Hkv;
-            all += n;
-            if (!pre || g < s) b += n;
-        }
-    }
-    if (a.s_tc) {
-        const Units u(a.Lq * a.gs);
-        for (int k = lane; k < a.B; k += 32) {
-            const int64_t n = u.steps(key_tiles(suffix_len(a, k))) * a.Hkv;
-            all += n;
-            if (!pre && k < s) b += n;
-        }
-    }
-    for (int o = 16; o; o >>= 1) {
-        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-        all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
-    }
-    before = b;
-    t = all;
+    const int np = a.p_tc ? a.n_prefix : 0;
+    const bool pre = k < np;
+    const Units u((pre ? a.G : 1) * a.Lq * a.gs);
+    return u.steps(key_tiles(pre ? prefix_len(a, k) : suffix_len(a, k - np))) * a.Hkv;
 }
-__device__ __forceinline__ int64_t steps_per_cta(const Args &a, int64_t total)
+// Steps of the prefixes and of all segments, over a whole warp.  (The host sees to it that the line is shorter than 2^31.)
+__device__ __forceinline__ void line_length(const Args &a, int &prefixes, int &total)
 {
-    const int64_t n = (total + a.grid_tc - 1) / a.grid_tc;
+    const int lane = threadIdx.x % 32, np = a.p_tc ? a.n_prefix : 0, ns = a.s_tc ? a.B : 0;
+    int p = 0, s = 0;
+    for (int k = lane; k < np; k += 32) p += segment_steps(a, k);
+    for (int k = np + lane; k < np + ns; k += 32) s += segment_steps(a, k);
+    prefixes = __reduce_add_sync(0xFFFFFFFFu, p);
+    total = prefixes + __reduce_add_sync(0xFFFFFFFFu, s);
+}
+__device__ __forceinline__ int steps_per_cta(const Args &a, int total)
+{
+    const int n = (total + a.grid_tc - 1) / a.grid_tc;
     return n ? n : 1;
 }
 

@@ -3,8 +3,9 @@
 //
 // A CTA works on two row tiles of 128 (or on two key tiles of one row tile) at a
 // time, so that the tensor core multiplies for one while the other is in its
-// softmax.  Warps 0-3 and 4-7: the softmax of the two, one thread per row; warp
-// 8: TMA loads of the key and value tiles; warp 9: the MMAs.  Per tile and half:
+// softmax.  Warps 0-7 and 8-15: the softmax of the two, two threads per row (64
+// of the tile's 128 keys each); warp 16: TMA loads of the key and value tiles;
+// warps 17 and 18: the MMAs of the two.  Per tile and half:
 //     S = Q K^T     Q, K in shared memory (K-major), S in TMEM, FP32
 //     P = 2^(S c - m)  read from TMEM, written back as bf16 over S
 //     O += P V      P from TMEM, V as it lies in the cache (MN-major), O in TMEM
@@ -34,7 +35,7 @@ struct Maps {
 static_assert(sizeof(CUtensorMap) == 128, "");
 static_assert(sizeof(Maps) == kTcMapsBytes, "");
 
-constexpr int kThreads = 320, kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 608, kTmaWarp = 16, kMmaWarp = 17;  // and 18
 constexpr int kStages = 2;
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w)
@@ -58,6 +59,19 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r)
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 template <int D>
 struct Smem {
     static constexpr int SUB = D / 64;             // 64-element column blocks of a tile
@@ -68,7 +82,8 @@ struct Smem {
 // A contiguous range of steps inside one unit.
 struct Seg {
     bool pre, single;
-    int seg, hk, pair, len, tile0, n_steps, part;
+    int seg, hk, pair, len, tile0, part;
+    int next;    // where the next range starts
     int n0, n1;  // tiles of the two halves
 };
 
@@ -81,21 +96,22 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
     __shared__ uint64_t b_q[2], b_kfull[kStages], b_kempty[kStages], b_vfull[kStages], b_vempty[kStages], b_s[2], b_p[2], b_o[2], b_end;
     __shared__ uint32_t s_tmem;
     __shared__ int s_stop;
+    __shared__ float s_row[2][2][128];  // of each half's rows: what the threads of one key half tell the others
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (tid == 0) {
         for (int k = 0; k < kStages; ++k) {
             mbar_init(&b_kfull[k], 1);
-            mbar_init(&b_kempty[k], 1);
+            mbar_init(&b_kempty[k], 2);  // both MMA warps
             mbar_init(&b_vfull[k], 1);
-            mbar_init(&b_vempty[k], 1);
+            mbar_init(&b_vempty[k], 2);
         }
         for (int h = 0; h < 2; ++h) {
-            mbar_init(&b_q[h], 128);
+            mbar_init(&b_q[h], 256);
             mbar_init(&b_s[h], 1);
-            mbar_init(&b_p[h], 128);
+            mbar_init(&b_p[h], 256);
             mbar_init(&b_o[h], 1);
         }
-        mbar_init(&b_end, 1);
+        mbar_init(&b_end, 2);
         s_stop = 0;
         fence_mbar_init();
     }
@@ -113,7 +129,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
     // Every wait is bounded: past two seconds the error is latched and the CTA winds up.
     const uint64_t limit_ns = 2000000000ull;
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        bool ok = mbar_try_wait(bar, parity & 1u);
+        bool ok = false;
+        for (int k = 0; k < 32 && !ok; ++k) ok = mbar_try_wait(bar, parity & 1u);  // the usual case never looks at the clock
         if (!ok) {
             const uint64_t until = globaltimer_ns() + limit_ns;
             while (!(ok = mbar_try_wait_sleep(bar, parity & 1u, 20000u))) {
@@ -128,41 +145,56 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
         return __all_sync(0xFFFFFFFFu, ok);
     };
 
-    int64_t before, total;
-    steps_before(a, false, 0, before, total);  // before: the prefixes' steps
-    const int64_t per_cta = steps_per_cta(a, total);
-    const int64_t begin = blockIdx.x * per_cta, end = min(begin + per_cta, total);
+    int before, total;
+    line_length(a, before, total);  // before: the prefixes' steps
+    const int per_cta = steps_per_cta(a, total);
+    if (blockIdx.x == 0 && warp == 0) {  // for the kernel that joins the parts
+        if (lane == 0) a.line[0] = per_cta;
+        int at = 0;
+        const int segs = (a.p_tc ? a.n_prefix : 0) + (a.s_tc ? a.B : 0);
+        for (int k0 = 0; k0 < segs; k0 += 32) {
+            const int n = k0 + lane < segs ? segment_steps(a, k0 + lane) : 0;
+            int sum = n;
+            for (int o = 1; o < 32; o *= 2) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            if (k0 + lane < segs) a.line[1 + k0 + lane] = at + sum - n;
+            at += __shfl_sync(0xFFFFFFFFu, sum, 31);
+        }
+    }
+    const int begin = min((int)blockIdx.x * per_cta, total), end = min(begin + per_cta, total);
     const Units up(a.G * a.Lq * a.gs), us(a.Lq * a.gs);
     // the range of steps at `pos` that lies in one unit
-    auto locate = [&](int64_t pos) -> Seg {
+    auto locate = [&](int pos) -> Seg {
         Seg s;
         s.pre = pos < before;
-        int64_t at = s.pre ? 0 : before;
+        int at = s.pre ? 0 : before;
         const Units &u = s.pre ? up : us;
-        int64_t n = 0;
+        int n = 0;
         for (s.seg = 0;; ++s.seg, at += n) {
             s.len = s.pre ? prefix_len(a, s.seg) : suffix_len(a, s.seg);
             n = u.steps(key_tiles(s.len)) * a.Hkv;
             if (pos < at + n) break;
         }
         const int T = key_tiles(s.len);
-        const int64_t per_head = u.steps(T);
-        s.hk = (int)((pos - at) / per_head);
+        const int per_head = u.steps(T);
+        s.hk = (pos - at) / per_head;
         at += s.hk * per_head;
-        s.pair = (int)min((int64_t)u.full, (pos - at) / T);
+        s.pair = min(u.full, (pos - at) / (kStart + T));
         s.single = s.pair == u.full;
-        at += (int64_t)s.pair * T;
-        const int64_t unit = s.single ? (T + 1) / 2 : T;
-        const int first = (int)(pos - at);
-        s.n_steps = (int)(min(at + unit, end) - pos);
-        s.part = (int)(pos / per_cta - at / per_cta);
+        at += s.pair * (kStart + T) + kStart;
+        const int unit = s.single ? (T + 1) / 2 : T, first = max(pos - at, 0);
+        s.next = min(at + unit, end);
+        const int steps = max(s.next - at - first, 0);  // none where the range ends among the empty steps
+        s.part = (at + first) / per_cta - at / per_cta;
         if (s.single) {  // half h takes tiles 2 (first + i) + h
             s.tile0 = 2 * first;
-            s.n0 = s.n_steps;
-            s.n1 = min(s.n_steps, (T - s.tile0) / 2);
+            s.n0 = steps;
+            s.n1 = min(steps, (T - s.tile0) / 2);
         } else {
             s.tile0 = first;
-            s.n0 = s.n1 = s.n_steps;
+            s.n0 = s.n1 = steps;
         }
         return s;
     };
@@ -170,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
     if (warp == kTmaWarp) {
         uint32_t it = 0;
         bool ok = true;
-        for (int64_t pos = begin; ok && pos < end;) {
+        for (int pos = begin; ok && pos < end;) {
             const Seg s = locate(pos);
             const int tiles = s.single ? s.n0 + s.n1 : s.n0;
             const CUtensorMap *mk = s.pre ? &maps.kp : &maps.ks, *mv = s.pre ? &maps.vp : &maps.vs;
@@ -195,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
                 }
                 __syncwarp();
             }
-            pos += s.n_steps;
+            pos = s.next;
         }
         // no load may be in flight when the CTA ends
         if (*reinterpret_cast<volatile int *>(&s_stop)) {
@@ -209,176 +241,170 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
             }
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else if (warp >= kMmaWarp) {
+        const int h = warp - kMmaWarp;
         const uint32_t id_qk = idesc_bf16_f32(128, 128), id_pv = idesc_bf16_f32(128, D) | (1u << 16);  // V is MN-major
-        uint32_t kc = 0, vc = 0;               // tiles taken from the rings in earlier segments
-        uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};  // Q tiles and P V products so far
+        const uint32_t d_s = tmem + h * 256, d_o = d_s + 128;
+        const uint64_t q_desc = desc_kmajor_sw128(smem_u32(smem + M::Q + h * M::TILE)), k_desc = desc_kmajor_sw128(smem_u32(smem + M::K)),
+                       v_desc = desc_mnmajor_sw128(smem_u32(smem + M::V), 16384, 1024);
+        uint32_t tc = 0;           // tiles of earlier segments
+        uint32_t qn = 0, pn = 0;   // Q tiles and P V products so far
         bool ok = true;
-        for (int64_t pos = begin; ok && pos < end;) {
+        for (int pos = begin; ok && pos < end;) {
             const Seg s = locate(pos);
-            const int n[2] = {s.n0, s.n1};
-            const uint32_t tiles = (uint32_t)(s.single ? s.n0 + s.n1 : s.n0);
-            auto qk = [&](int h, int i) -> bool {
-                const uint32_t t = kc + (uint32_t)(s.single ? 2 * i + h : i);
-                if (i == 0 && !wait(&b_q[h], qn[h]++)) return false;
-                if (i > 0 && !wait(&b_o[h], pn[h] - 1)) return false;  // P of the last tile is read
-                if (!wait(&b_kfull[t % kStages], t / kStages)) return false;
+            pos = s.next;
+            const int n = h ? s.n1 : s.n0;
+            const uint32_t t0 = tc + (s.single ? h : 0), dt = s.single ? 2 : 1;
+            tc += (uint32_t)(s.single ? s.n0 + s.n1 : s.n0);
+            if (n == 0) continue;
+            if (!(ok = wait(&b_q[h], qn++))) break;
+            for (int i = 0; i < n; ++i) {
+                const uint32_t t = t0 + i * dt, st = t % kStages;
+                if (i > 0 && !(ok = wait(&b_o[h], pn - 1))) break;  // P of the last tile is read: S may overwrite it
+                if (!(ok = wait(&b_kfull[st], t / kStages))) break;
                 tc_fence_after();
+                const uint64_t bd = k_desc + st * (uint32_t)(M::TILE >> 4);
                 if (elect_one()) {
-                    const uint64_t ad = desc_kmajor_sw128(smem_u32(smem + M::Q + h * M::TILE));
-                    const uint64_t bd = desc_kmajor_sw128(smem_u32(smem + M::K + (t % kStages) * M::TILE));
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint64_t o = (uint64_t)((kk / 4) * (16384 >> 4) + 2 * (kk % 4));
-                        umma_bf16(tmem + h * 256, ad + o, bd + o, id_qk, kk > 0);
+                        umma_bf16(d_s, q_desc + o, bd + o, id_qk, kk > 0);
                     }
                     umma_commit(&b_s[h]);
-                    if (s.single || h == 1) umma_commit(&b_kempty[t % kStages]);
+                    umma_commit(&b_kempty[st]);
+                    if (s.single) umma_commit(&b_kempty[st]);  // the other warp does not use this tile
                 }
                 __syncwarp();
-                return true;
-            };
-            auto pv = [&](int h, int i) -> bool {
-                const uint32_t t = vc + (uint32_t)(s.single ? 2 * i + h : i);
-                if (!wait(&b_p[h], pn[h])) return false;
-                if (!wait(&b_vfull[t % kStages], t / kStages)) return false;
-                ++pn[h];
+                if (!(ok = wait(&b_vfull[st], t / kStages) && wait(&b_p[h], pn))) break;
+                ++pn;
                 tc_fence_after();
+                const uint64_t vd = v_desc + st * (uint32_t)(M::TILE >> 4);
                 if (elect_one()) {
-                    const uint32_t vt = smem_u32(smem + M::V + (t % kStages) * M::TILE);
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)  // 16 keys: two 8-row groups of every column block
-                        umma_bf16_ts(tmem + h * 256 + 128, tmem + h * 256 + 8 * kk, desc_mnmajor_sw128(vt + 2048u * kk, 16384, 1024), id_pv,
-                                     i > 0 || kk > 0);
+                        umma_bf16_ts(d_o, d_s + 8 * kk, vd + (uint64_t)(kk * (2048 >> 4)), id_pv, i > 0 || kk > 0);
                     umma_commit(&b_o[h]);
-                    if (s.single || h == 1) umma_commit(&b_vempty[t % kStages]);
+                    umma_commit(&b_vempty[st]);
+                    if (s.single) umma_commit(&b_vempty[st]);
                 }
                 __syncwarp();
-                return true;
-            };
-            ok = qk(0, 0) && (n[1] == 0 || qk(1, 0));
-            for (int i = 0; ok && i < n[0]; ++i)
-                for (int h = 0; ok && h < 2; ++h)
-                    if (i < n[h]) ok = pv(h, i) && (i + 1 >= n[h] || qk(h, i + 1));
-            kc += tiles;
-            vc += tiles;
-            pos += s.n_steps;
+            }
         }
         // every product issued has completed before TMEM is freed
         if (elect_one()) umma_commit(&b_end);
         __syncwarp();
-        const uint64_t until = globaltimer_ns() + limit_ns;
-        while (!mbar_try_wait(&b_end, 0) && globaltimer_ns() < until) {
-        }
-        __syncwarp();
     } else {
-        const int h = warp / 4, t = tid % 128;
+        const int h = warp / 8, ch = (warp / 4) & 1, t = (warp % 4) * 32 + lane;  // half, key half, row
+        const int pair_bar = 1 + h * 4 + warp % 4;                              // of the two warps that share rows
         const uint32_t tm = tmem + h * 256 + ((uint32_t)((warp % 4) * 32) << 16);
-        uint32_t sn = 0;  // S tiles so far
+        uint32_t sn = 0;             // S tiles so far
         uint32_t vc = 0, vnext = 0;  // value tiles of earlier segments
         bool ok = true;
-        for (int64_t pos = begin; ok && pos < end;) {
+        for (int pos = begin; ok && pos < end;) {
             const Seg s = locate(pos);
-            pos += s.n_steps;
+            pos = s.next;
             vc = vnext;
             vnext += (uint32_t)(s.single ? s.n0 + s.n1 : s.n0);
             const int n = h ? s.n1 : s.n0, R = (s.pre ? a.G : 1) * a.Lq * a.gs;
-            const int tile = s.single ? 2 * s.pair : 2 * s.pair + h;  // row tile
-            auto row_of = [&](int r, int &b, int &l, int &head) {
-                const int rr = tile * 128 + r, per = a.Lq * a.gs;
-                const int bi = rr / per, in = rr - bi * per;
-                b = s.pre ? s.seg * a.G + bi : s.seg;
-                l = in / a.gs;
-                head = s.hk * a.gs + in - l * a.gs;
-                return rr < R;
-            };
-            int b, l, head;
-            const bool mine = row_of(t, b, l, head);
-            const int parts = a.n_pp + a.n_sp;
-            const int64_t at = (((int64_t)b * a.Lq + l) * a.Hq + head) * parts + (s.pre ? 0 : a.n_pp) + (s.single ? 2 * s.part + h : s.part);
+            if (s.n0 == 0) continue;
+            const int rr = (s.single ? 2 * s.pair : 2 * s.pair + h) * 128 + t, rows_b = a.Lq * a.gs;
+            const bool mine = rr < R;
+            const int bi = rr / rows_b, in = rr - bi * rows_b, l = in / a.gs;
+            const int b = s.pre ? s.seg * a.G + bi : s.seg, head = s.hk * a.gs + in - l * a.gs;
+            const int64_t at = (((int64_t)b * a.Lq + l) * a.Hq + head) * (a.n_pp + a.n_sp) + (s.pre ? 0 : a.n_pp) +
+                               (s.single ? 2 * s.part + h : s.part);
             if (n == 0) {  // the odd half of a single key tile
-                if (mine) a.part_ml[at] = make_float2(kNone, 0.0f);
+                if (mine && ch == 0) a.part_ml[at] = make_float2(kNone, 0.0f);
                 continue;
             }
-            // this half's query rows; the last tile's product that read the old ones has completed (b_s)
-            constexpr int CH = D / 8;
-#pragma unroll 4
-            for (int i = 0; i < CH; ++i) {
-                const int r = (warp % 4) * 32 + i * (32 / CH) + lane / CH, c = lane % CH;
-                int qb, ql, qh;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (row_of(r, qb, ql, qh)) v = *reinterpret_cast<const uint4 *>(a.q + qb * a.q_b + ql * a.q_l + qh * a.q_h + c * 8);
-                st_shared_v4(smem_u32(smem + M::Q + h * M::TILE) + (c / 8) * 16384 + r * 128 + (((c % 8) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
+            // this half's query rows, 64 columns by each of the two warps; the last product that read the old rows has
+            // completed (b_s)
+            constexpr int CH = D / 16, RI = 32 / CH;  // 16-byte chunks of half a row; rows per access
+            const uint32_t qs = smem_u32(smem + M::Q + h * M::TILE);
+            const int64_t q_at = mine ? b * a.q_b + l * a.q_l + head * a.q_h : -1;
+            {
+                uint4 v[CH];
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                    const int64_t from = __shfl_sync(0xFFFFFFFFu, q_at, i * RI + lane / CH);
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (from >= 0) v[i] = *reinterpret_cast<const uint4 *>(a.q + from + (ch * CH + lane % CH) * 8);
+                }
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                    const int r = (warp % 4) * 32 + i * RI + lane / CH, c = ch * CH + lane % CH;
+                    st_shared_v4(qs + (c / 8) * 16384 + r * 128 + (((c % 8) ^ (r & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+                }
             }
             fence_proxy_async_smem();
             mbar_arrive(&b_q[h]);
 
             const int limit = s.pre ? s.len : s.len - a.Lq + 1 + l;
+            const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
             float m = kNone, sum = 0.0f;
             for (int i = 0; i < n; ++i) {
-                const int k0 = (s.tile0 + (s.single ? 2 * i + h : i)) * 128;
+                const int k0 = (s.tile0 + (s.single ? 2 * i + h : i)) * 128 + ch * 64;
                 if (!(ok = wait(&b_s[h], sn++))) break;
                 tc_fence_after();
-                // 64 columns in registers at a time: the upper half for its maximum, then the lower half, which P's first
-                // columns overwrite, and the upper half once more
                 uint32_t x[64];
-                const bool cut = k0 + 128 > limit;
-                auto fetch = [&](int c0) {
-                    tmem_ld32(tm + c0, x);
-                    tmem_ld32(tm + c0 + 32, x + 32);
-                    tmem_wait_ld();
-                    if (cut) {
+                tmem_ld32(tm + ch * 64, x);
+                tmem_ld32(tm + ch * 64 + 32, x + 32);
+                tmem_wait_ld();
+                if (k0 + 64 > limit) {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            if (k0 + c0 + c >= limit) x[c] = 0xFF800000u;
-                    }
-                    __syncwarp();
-                };
-                float top = kNone;
-                fetch(64);
+                    for (int c = 0; c < 64; ++c)
+                        if (k0 + c >= limit) x[c] = 0xFF800000u;
+                }
+                __syncwarp();
+                float top = kNone, top1 = kNone;
 #pragma unroll
-                for (int c = 0; c < 64; ++c) top = fmaxf(top, __uint_as_float(x[c]));
-                fetch(0);
-#pragma unroll
-                for (int c = 0; c < 64; ++c) top = fmaxf(top, __uint_as_float(x[c]));
+                for (int c = 0; c < 64; c += 2) {
+                    top = fmaxf(top, __uint_as_float(x[c]));
+                    top1 = fmaxf(top1, __uint_as_float(x[c + 1]));
+                }
+                top = fmaxf(top, top1);
+                s_row[h][ch][t] = top;
+                named_bar_sync(pair_bar, 64);  // and both have S in registers: P may overwrite it
+                top = fmaxf(top, s_row[h][ch ^ 1][t]);
                 top = top == kNone ? kNone : top * a.scale_log2;
                 const bool raise = top > m + 8.0f;
                 const float to = raise ? top : m, f = raise ? ex2(m - top) : 1.0f;
                 if (i > 0 && __any_sync(0xFFFFFFFFu, raise)) {  // O is still: the product before S has completed
-#pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(tm + 128 + c, o);
+#pragma unroll 1
+                    for (int c = 0; c < D / 2; c += 8) {
+                        uint32_t o[8];
+                        tmem_ld8(tm + 128 + ch * (D / 2) + c, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st32(tm + 128 + c, o);
+                        for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st8(tm + 128 + ch * (D / 2) + c, o);
                     }
                 }
                 m = to;
                 sum *= f;
-                float2 add = make_float2(0.0f, 0.0f);
+                float2 add = make_float2(0.0f, 0.0f), add1 = add;
+                const float2 minus = make_float2(-m, -m);
+                uint32_t p[32];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    if (c) fetch(64);
-                    uint32_t p[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float p0 = ex2(fmaf(__uint_as_float(x[2 * e]), a.scale_log2, -m));
-                        const float p1 = ex2(fmaf(__uint_as_float(x[2 * e + 1]), a.scale_log2, -m));
-                        add.x += p0;
-                        add.y += p1;
-                        const __nv_bfloat162 pk = __floats2bfloat162_rn(p0, p1);
-                        p[e] = *reinterpret_cast<const uint32_t *>(&pk);
-                    }
-                    tmem_st32(tm + c * 32, p);
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 y0 = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), scale2, minus);
+                    const float2 y1 = fma2(make_float2(__uint_as_float(x[2 * e + 2]), __uint_as_float(x[2 * e + 3])), scale2, minus);
+                    const float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
+                    add = add2(add, p0);
+                    add1 = add2(add1, p1);
+                    const __nv_bfloat162 b0 = __floats2bfloat162_rn(p0.x, p0.y), b1 = __floats2bfloat162_rn(p1.x, p1.y);
+                    p[e] = *reinterpret_cast<const uint32_t *>(&b0);
+                    p[e + 1] = *reinterpret_cast<const uint32_t *>(&b1);
                 }
+                tmem_st32(tm + ch * 32, p);
+                add = add2(add, add1);
                 sum += add.x + add.y;
-                if (k0 + 128 > s.len) {  // what the cache holds past the segment must not reach O, not even as 0 * NaN
+                const int kt = k0 - ch * 64;
+                if (kt + 128 > s.len) {  // what the cache holds past the segment must not reach O, not even as 0 * NaN
                     const uint32_t vt = vc + (uint32_t)(s.single ? 2 * i + h : i), st = vt % kStages;
                     if (!(ok = wait(&b_vfull[st], vt / kStages))) break;
-                    if (k0 + t >= s.len)
-                        for (int c = 0; c < M::SUB * 8; ++c)
+                    if (kt + t >= s.len)
+                        for (int c = ch * (D / 16); c < (ch + 1) * (D / 16); ++c)
                             st_shared_v4(smem_u32(smem + M::V + st * M::TILE) + (c / 8) * 16384 + t * 128 + (c % 8) * 16, 0, 0, 0, 0);
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -390,27 +416,44 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
             if (!ok) break;
             if (!(ok = wait(&b_o[h], sn - 1))) break;
             tc_fence_after();
+            // O's rows through this half's Q tile (read for the last time), which holds D / 2 columns of all of them, so that a
+            // row leaves in whole pieces: row r's 16-byte chunk c lies at chunk c ^ (r % OC).  The two warps of a row take
+            // turns: each stages and stores its columns of its 32 rows.
+            constexpr int OC = D / 8, RO = 32 / OC;  // chunks of a piece; rows per access
+            s_row[h][ch][t] = sum;
+            for (int turn = 0; turn < 2; ++turn) {
+                if (turn == ch) {
 #pragma unroll
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(tm + 128 + c, o);
-                tmem_wait_ld();
-                if (mine) {
-                    float4 *to = reinterpret_cast<float4 *>(a.part_o + at * D + c);
+                    for (int c = 0; c < D / 2; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tm + 128 + ch * (D / 2) + c, o);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        to[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
-                                            __uint_as_float(o[4 * e + 3]));
+                        for (int e = 0; e < 8; ++e)
+                            st_shared_v4(qs + t * (OC * 16) + (((c / 4 + e) ^ (t % OC)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                    __syncwarp();
+#pragma unroll 8
+                    for (int i = 0; i < OC; ++i) {
+                        const int from = i * RO + lane / OC, r = (warp % 4) * 32 + from;
+                        const int64_t to = __shfl_sync(0xFFFFFFFFu, mine ? at : (int64_t)-1, from);
+                        const uint4 v = ld_shared_v4(qs + r * (OC * 16) + (((lane % OC) ^ (r % OC)) << 4));
+                        if (to >= 0) *reinterpret_cast<uint4 *>(a.part_o + to * D + ch * (D / 2) + (lane % OC) * 4) = v;
+                    }
                 }
-                __syncwarp();
+                named_bar_sync(pair_bar, 64);
             }
-            if (mine) a.part_ml[at] = make_float2(m, sum);
+            if (mine && ch == 0) a.part_ml[at] = make_float2(m, sum + s_row[h][1][t]);
             tc_fence_before();
         }
     }
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
+        const uint64_t until = globaltimer_ns() + limit_ns;
+        while (!mbar_try_wait(&b_end, 0) && globaltimer_ns() < until) {
+        }
+        __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
