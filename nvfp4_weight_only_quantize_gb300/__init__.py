@@ -71,6 +71,8 @@ def build(force: bool = False) -> str:
 def lib() -> C.CDLL:
     """The loaded libqerl.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -143,12 +145,19 @@ def _check(status: int, where: str):
 
 
 def _p(t):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# The current stream's handle without the Stream object around it, whose making takes longer than a small kernel.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return C.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None or not torch.cuda.is_initialized():
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch._C._cuda_getDevice())
 
 
 def workspace_bytes(op: int, M: int, N: int, K: int, r: int) -> int:
@@ -512,29 +521,34 @@ class PrefixAttention:
         if nbytes == 0:
             raise QerlError(2, "qerl_prefix_attention_ws_bytes")
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=k_suffix.device) if ws is None else ws
-        self._q_shape = (B, q_len, q_heads, D)
+        self._ws = (self.ws.data_ptr(), self.ws.numel())
+        self._q_shape = torch.Size((B, q_len, q_heads, D))
         self._scale = D ** -0.5 if scale is None else float(scale)
         self._p = [_p(t) for t in self._keep]
+        self._strides = None  # of the last q and out
+        self._ref = C.byref(self._d)
 
     def run(self, q, suffix_lens, prefix_lens=None, out=None, lse=None, stream=None):
         """q bf16 [B, Lq, Hq, D], suffix_lens int32 [B] (new tokens included),
         prefix_lens int32 [n_prefix] or None (P) -> out bf16 like q; lse f32 [B, Lq, Hq] is filled if given."""
         d = self._d
-        assert q.shape == self._q_shape and q.dtype == torch.bfloat16 and q.stride(3) == 1
+        if out is None:
+            out = torch.empty(self._q_shape, dtype=torch.bfloat16, device=q.device)
+        assert q.shape == self._q_shape and out.shape == self._q_shape and q.dtype == out.dtype == torch.bfloat16
         assert suffix_lens.dtype == torch.int32 and suffix_lens.is_contiguous() and suffix_lens.numel() == d.B
         if prefix_lens is not None:
             assert prefix_lens.dtype == torch.int32 and prefix_lens.is_contiguous() and prefix_lens.numel() == d.n_prefix
-        if out is None:
-            out = torch.empty(self._q_shape, dtype=torch.bfloat16, device=q.device)
-        assert out.shape == self._q_shape and out.dtype == torch.bfloat16 and out.stride(3) == 1
         if lse is not None:
             assert lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == self._q_shape[:3]
-        d.q_stride[:] = q.stride()[:3]
-        d.out_stride[:] = out.stride()[:3]
+        strides = (q.stride(), out.stride())
+        if strides != self._strides:
+            assert strides[0][3] == strides[1][3] == 1
+            d.q_stride[:], d.out_stride[:] = strides[0][:3], strides[1][:3]
+            self._strides = strides
         kp, vp, ks, vs = self._p
-        _check(lib().qerl_prefix_attention(C.byref(d), q.data_ptr(), kp, vp, _p(prefix_lens), ks, vs, suffix_lens.data_ptr(),
-                                           self._scale, out.data_ptr(), _p(lse), self.ws.data_ptr(), self.ws.numel(),
-                                           _stream(stream)), "qerl_prefix_attention")
+        _check(lib().qerl_prefix_attention(self._ref, q.data_ptr(), kp, vp, _p(prefix_lens), ks, vs, suffix_lens.data_ptr(),
+                                           self._scale, out.data_ptr(), _p(lse), self._ws[0], self._ws[1], _stream(stream)),
+               "qerl_prefix_attention")
         return out
 
 
@@ -551,17 +565,18 @@ class _PolicyOpts(C.Structure):
 
 
 _DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+_ID_BITS = {torch.int32: 32, torch.int64: 64}
 
 
 def _logits_args(logits, ids, vectors):
     """(pointer, dtype, T, V, ld, ids pointer, ids bits) of a logits matrix, after the checks of its companions."""
-    T, V = logits.shape
-    assert logits.dtype in _DTYPES and (logits.stride(1) == 1 or V == 1)
-    assert ids.dtype in (torch.int32, torch.int64) and ids.shape == (T,) and ids.is_contiguous()
+    T, V = shape = logits.shape
+    ld, one = logits.stride()
+    vec, f32, bits = shape[:1], torch.float32, _ID_BITS[ids.dtype]
+    assert logits.dtype in _DTYPES and (one == 1 or V == 1) and ids.shape == vec and ids.is_contiguous()
     for t in vectors:
-        assert t is None or (t.dtype == torch.float32 and t.shape == (T,) and t.is_contiguous())
-    return (logits.data_ptr(), _DTYPES[logits.dtype], T, V, logits.stride(0) if T > 1 else V, ids.data_ptr(),
-            32 if ids.dtype == torch.int32 else 64)
+        assert t is None or (t.dtype is f32 and t.shape == vec and t.is_contiguous())
+    return logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld if T > 1 else V, ids.data_ptr(), bits
 
 
 def qerl_token_logp(logits, ids, weights=None, temperature: float = 1.0, logp=None, entropy=None, stream=None):
