@@ -3,16 +3,18 @@
 //
 // A CTA works on two row tiles of 128 (or on two key tiles of one row tile) at a
 // time, so that the tensor core multiplies for one while the other is in its
-// softmax.  Warps 0-7 and 8-15: the softmax of the two, two threads per row (64
-// of the tile's 128 keys each); warp 16: TMA loads of the key and value tiles;
-// warps 17 and 18: the MMAs of the two.  Per tile and half:
+// softmax.  Warps 0-7 and 8-15: the softmax of the two, two threads per row; warp 16: TMA loads of the key and value tiles;
+// warps 17 and 18: the MMAs of the two.  Per half and 64 keys of a tile:
 //     S = Q K^T     Q, K in shared memory (K-major), S in TMEM, FP32
 //     P = 2^(S c - m)  read from TMEM, written back as bf16 over S
 //     O += P V      P from TMEM, V as it lies in the cache (MN-major), O in TMEM
+// There are two S of 64 keys per half, so that the next one is there when a
+// softmax ends; with one S of 128 keys a softmax waited for P V and Q K^T each
+// time (2.0 us per step against CHECK_US).
 // m is raised only when a row's maximum outgrows it by 2^8 (the weights stay
 // below 2^8 and are normalised in the end all the same), so O is rescaled rarely.
-// S and P share columns: Q K^T of a half's next tile is issued once P V of its
-// last one has completed.
+// S and P share columns: the Q K^T that overwrites a P is issued once its P V has
+// completed.
 // Shared memory: Q 64 KB, two K and two V tiles of 32 KB (D = 128).
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -66,6 +68,13 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
                  : "r"(taddr)
                  : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+                 "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
@@ -93,10 +102,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
     using M = Smem<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // the swizzled tiles' alignment
-    __shared__ uint64_t b_q[2], b_kfull[kStages], b_kempty[kStages], b_vfull[kStages], b_vempty[kStages], b_s[2], b_p[2], b_o[2], b_end;
+    __shared__ uint64_t b_q[2], b_kfull[kStages], b_kempty[kStages], b_vfull[kStages], b_vempty[kStages], b_s[2][2], b_p[2][2], b_o[2], b_end;
     __shared__ uint32_t s_tmem;
     __shared__ int s_stop;
-    __shared__ float s_row[2][2][128];  // of each half's rows: what the threads of one key half tell the others
+    __shared__ float s_row[2][2][2][128];  // of each half's rows: what the threads of one key half tell the others
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (tid == 0) {
         for (int k = 0; k < kStages; ++k) {
@@ -107,8 +116,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
         }
         for (int h = 0; h < 2; ++h) {
             mbar_init(&b_q[h], 256);
-            mbar_init(&b_s[h], 1);
-            mbar_init(&b_p[h], 256);
+            for (int k = 0; k < 2; ++k) {
+                mbar_init(&b_s[h][k], 1);
+                mbar_init(&b_p[h][k], 256);
+            }
             mbar_init(&b_o[h], 1);
         }
         mbar_init(&b_end, 2);
@@ -243,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
         __syncwarp();
     } else if (warp >= kMmaWarp) {
         const int h = warp - kMmaWarp;
-        const uint32_t id_qk = idesc_bf16_f32(128, 128), id_pv = idesc_bf16_f32(128, D) | (1u << 16);  // V is MN-major
+        const uint32_t id_qk = idesc_bf16_f32(128, 64), id_pv = idesc_bf16_f32(128, D) | (1u << 16);  // V is MN-major
         const uint32_t d_s = tmem + h * 256, d_o = d_s + 128;
         const uint64_t q_desc = desc_kmajor_sw128(smem_u32(smem + M::Q + h * M::TILE)), k_desc = desc_kmajor_sw128(smem_u32(smem + M::K)),
                        v_desc = desc_mnmajor_sw128(smem_u32(smem + M::V), 16384, 1024);
@@ -253,41 +264,51 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
         for (int pos = begin; ok && pos < end;) {
             const Seg s = locate(pos);
             pos = s.next;
-            const int n = h ? s.n1 : s.n0;
+            const int n = 2 * (h ? s.n1 : s.n0);  // S of 64 keys
             const uint32_t t0 = tc + (s.single ? h : 0), dt = s.single ? 2 : 1;
             tc += (uint32_t)(s.single ? s.n0 + s.n1 : s.n0);
             if (n == 0) continue;
             if (!(ok = wait(&b_q[h], qn++))) break;
-            for (int i = 0; i < n; ++i) {
-                const uint32_t t = t0 + i * dt, st = t % kStages;
-                if (i > 0 && !(ok = wait(&b_o[h], pn - 1))) break;  // P of the last tile is read: S may overwrite it
-                if (!(ok = wait(&b_kfull[st], t / kStages))) break;
+            auto qk = [&](int j) -> bool {
+                const uint32_t t = t0 + (j / 2) * dt, st = t % kStages, half = j & 1;
+                if (half == 0 && !wait(&b_kfull[st], t / kStages)) return false;
                 tc_fence_after();
-                const uint64_t bd = k_desc + st * (uint32_t)(M::TILE >> 4);
+                const uint64_t bd = k_desc + st * (uint32_t)(M::TILE >> 4) + half * (uint32_t)(64 * 128 >> 4);
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint64_t o = (uint64_t)((kk / 4) * (16384 >> 4) + 2 * (kk % 4));
-                        umma_bf16(d_s, q_desc + o, bd + o, id_qk, kk > 0);
+                        umma_bf16(d_s + half * 64, q_desc + o, bd + o, id_qk, kk > 0);
                     }
-                    umma_commit(&b_s[h]);
-                    umma_commit(&b_kempty[st]);
-                    if (s.single) umma_commit(&b_kempty[st]);  // the other warp does not use this tile
+                    umma_commit(&b_s[h][half]);
+                    if (half) {
+                        umma_commit(&b_kempty[st]);
+                        if (s.single) umma_commit(&b_kempty[st]);  // the other warp does not use this tile
+                    }
                 }
                 __syncwarp();
-                if (!(ok = wait(&b_vfull[st], t / kStages) && wait(&b_p[h], pn))) break;
+                return true;
+            };
+            ok = qk(0) && qk(1);
+            for (int j = 0; ok && j < n; ++j) {
+                const uint32_t t = t0 + (j / 2) * dt, st = t % kStages, half = j & 1;
+                if (half == 0 && !(ok = wait(&b_vfull[st], t / kStages))) break;
+                if (!(ok = wait(&b_p[h][half], pn / 2))) break;  // pn is even at the start of a segment
                 ++pn;
                 tc_fence_after();
-                const uint64_t vd = v_desc + st * (uint32_t)(M::TILE >> 4);
+                const uint64_t vd = v_desc + st * (uint32_t)(M::TILE >> 4) + half * (uint32_t)(64 * 128 >> 4);
                 if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)  // 16 keys: two 8-row groups of every column block
-                        umma_bf16_ts(d_o, d_s + 8 * kk, vd + (uint64_t)(kk * (2048 >> 4)), id_pv, i > 0 || kk > 0);
+                    for (int kk = 0; kk < 4; ++kk)  // 16 keys: two 8-row groups of every column block
+                        umma_bf16_ts(d_o, d_s + half * 64 + 8 * kk, vd + (uint64_t)(kk * (2048 >> 4)), id_pv, j > 0 || kk > 0);
                     umma_commit(&b_o[h]);
-                    umma_commit(&b_vempty[st]);
-                    if (s.single) umma_commit(&b_vempty[st]);
+                    if (half) {
+                        umma_commit(&b_vempty[st]);
+                        if (s.single) umma_commit(&b_vempty[st]);
+                    }
                 }
                 __syncwarp();
+                if (j + 2 < n) ok = wait(&b_o[h], pn - 1) && qk(j + 2);  // this P is read: its S may be overwritten
             }
         }
         // every product issued has completed before TMEM is freed
@@ -297,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
         const int h = warp / 8, ch = (warp / 4) & 1, t = (warp % 4) * 32 + lane;  // half, key half, row
         const int pair_bar = 1 + h * 4 + warp % 4;                              // of the two warps that share rows
         const uint32_t tm = tmem + h * 256 + ((uint32_t)((warp % 4) * 32) << 16);
-        uint32_t sn = 0;             // S tiles so far
+        uint32_t sn = 0;             // S so far
         uint32_t vc = 0, vnext = 0;  // value tiles of earlier segments
         bool ok = true;
         for (int pos = begin; ok && pos < end;) {
@@ -305,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
             pos = s.next;
             vc = vnext;
             vnext += (uint32_t)(s.single ? s.n0 + s.n1 : s.n0);
-            const int n = h ? s.n1 : s.n0, R = (s.pre ? a.G : 1) * a.Lq * a.gs;
+            const int n = 2 * (h ? s.n1 : s.n0), R = (s.pre ? a.G : 1) * a.Lq * a.gs;
             if (s.n0 == 0) continue;
             const int rr = (s.single ? 2 * s.pair : 2 * s.pair + h) * 128 + t, rows_b = a.Lq * a.gs;
             const bool mine = rr < R;
@@ -342,34 +363,38 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
             const int limit = s.pre ? s.len : s.len - a.Lq + 1 + l;
             const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
             float m = kNone, sum = 0.0f;
-            for (int i = 0; i < n; ++i) {
-                const int k0 = (s.tile0 + (s.single ? 2 * i + h : i)) * 128 + ch * 64;
-                if (!(ok = wait(&b_s[h], sn++))) break;
+            for (int j = 0; j < n; ++j, ++sn) {
+                const int half = j & 1, kt = (s.tile0 + (s.single ? 2 * (j / 2) + h : j / 2)) * 128;  // S of the tile; the tile's first key
+                const int k0 = kt + half * 64 + ch * 32;                                             // this thread's first key
+                const uint32_t ts = tm + half * 64;
+                ok = wait(&b_s[h][half], sn / 2) && ok;  // sn is even at the start of a segment
                 tc_fence_after();
-                uint32_t x[64];
-                tmem_ld32(tm + ch * 64, x);
-                tmem_ld32(tm + ch * 64 + 32, x + 32);
+                uint32_t x[32];
+                tmem_ld32(ts + ch * 32, x);
                 tmem_wait_ld();
-                if (k0 + 64 > limit) {
+                if (k0 + 32 > limit) {
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
+                    for (int c = 0; c < 32; ++c)
                         if (k0 + c >= limit) x[c] = 0xFF800000u;
                 }
                 __syncwarp();
                 float top = kNone, top1 = kNone;
 #pragma unroll
-                for (int c = 0; c < 64; c += 2) {
+                for (int c = 0; c < 32; c += 2) {
                     top = fmaxf(top, __uint_as_float(x[c]));
                     top1 = fmaxf(top1, __uint_as_float(x[c + 1]));
                 }
                 top = fmaxf(top, top1);
-                s_row[h][ch][t] = top;
-                named_bar_sync(pair_bar, 64);  // and both have S in registers: P may overwrite it
-                top = fmaxf(top, s_row[h][ch ^ 1][t]);
+                s_row[h][ch][half][t] = top;
+                // and both have S in registers: P may overwrite it (the two leave the loop together, or not)
+                if (!(ok = named_bar_and(pair_bar, 64, ok))) break;
+                top = fmaxf(top, s_row[h][ch ^ 1][half][t]);
                 top = top == kNone ? kNone : top * a.scale_log2;
                 const bool raise = top > m + 8.0f;
                 const float to = raise ? top : m, f = raise ? ex2(m - top) : 1.0f;
-                if (i > 0 && __any_sync(0xFFFFFFFFu, raise)) {  // O is still: the product before S has completed
+                if (j > 0 && __any_sync(0xFFFFFFFFu, raise)) {
+                    ok = wait(&b_o[h], sn - 1);  // O is still
+                    tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < D / 2; c += 8) {
                         uint32_t o[8];
@@ -384,9 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
                 sum *= f;
                 float2 add = make_float2(0.0f, 0.0f), add1 = add;
                 const float2 minus = make_float2(-m, -m);
-                uint32_t p[32];
+                uint32_t p[16];
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
+                for (int e = 0; e < 16; e += 2) {
                     const float2 y0 = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), scale2, minus);
                     const float2 y1 = fma2(make_float2(__uint_as_float(x[2 * e + 2]), __uint_as_float(x[2 * e + 3])), scale2, minus);
                     const float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
@@ -396,13 +421,12 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
                     p[e] = *reinterpret_cast<const uint32_t *>(&b0);
                     p[e + 1] = *reinterpret_cast<const uint32_t *>(&b1);
                 }
-                tmem_st32(tm + ch * 32, p);
+                tmem_st16(ts + ch * 16, p);
                 add = add2(add, add1);
                 sum += add.x + add.y;
-                const int kt = k0 - ch * 64;
-                if (kt + 128 > s.len) {  // what the cache holds past the segment must not reach O, not even as 0 * NaN
-                    const uint32_t vt = vc + (uint32_t)(s.single ? 2 * i + h : i), st = vt % kStages;
-                    if (!(ok = wait(&b_vfull[st], vt / kStages))) break;
+                if (half == 0 && kt + 128 > s.len) {  // what the cache holds past the segment must not reach O, not even as 0 * NaN
+                    const uint32_t vt = vc + (uint32_t)(s.single ? j + h : j / 2), st = vt % kStages;
+                    ok = wait(&b_vfull[st], vt / kStages) && ok;
                     if (kt + t >= s.len)
                         for (int c = ch * (D / 16); c < (ch + 1) * (D / 16); ++c)
                             st_shared_v4(smem_u32(smem + M::V + st * M::TILE) + (c / 8) * 16384 + t * 128 + (c % 8) * 16, 0, 0, 0, 0);
@@ -411,16 +435,16 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&b_p[h]);
+                mbar_arrive(&b_p[h][half]);
             }
-            if (!ok) break;
-            if (!(ok = wait(&b_o[h], sn - 1))) break;
+            // the last two products, one after the other: a barrier tells only one phase from the next
+            if (ok) ok = wait(&b_o[h], sn - 2) && wait(&b_o[h], sn - 1);
             tc_fence_after();
             // O's rows through this half's Q tile (read for the last time), which holds D / 2 columns of all of them, so that a
             // row leaves in whole pieces: row r's 16-byte chunk c lies at chunk c ^ (r % OC).  The two warps of a row take
             // turns: each stages and stores its columns of its 32 rows.
             constexpr int OC = D / 8, RO = 32 / OC;  // chunks of a piece; rows per access
-            s_row[h][ch][t] = sum;
+            s_row[h][ch][0][t] = sum;
             for (int turn = 0; turn < 2; ++turn) {
                 if (turn == ch) {
 #pragma unroll
@@ -443,8 +467,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
                 }
                 named_bar_sync(pair_bar, 64);
             }
-            if (mine && ch == 0) a.part_ml[at] = make_float2(m, sum + s_row[h][1][t]);
+            if (mine && ch == 0) a.part_ml[at] = make_float2(m, sum + s_row[h][1][0][t]);
             tc_fence_before();
+            // the next rows of Q go where other warps' O may still lie; the half's warps leave together
+            ok = named_bar_and(9 + h, 256, ok);
         }
     }
     tc_fence_before();
