@@ -3,8 +3,9 @@
 //
 // A CTA works on two row tiles of 128 (or on two key tiles of one row tile) at a
 // time, so that the tensor core multiplies for one while the other is in its
-// softmax.  Warps 0-7 and 8-15: the softmax of the two, two threads per row; warp 16: TMA loads of the key and value tiles;
-// warps 17 and 18: the MMAs of the two.  Per half and 64 keys of a tile:
+// softmax.  Warps 0-3 and 4-7: the softmax of the two, one thread per row; warp
+// 8: TMA loads of the key and value tiles; warps 9 and 10: the MMAs of the two.
+// Per half and 64 keys of a tile:
 //     S = Q K^T     Q, K in shared memory (K-major), S in TMEM, FP32
 //     P = 2^(S c - m)  read from TMEM, written back as bf16 over S
 //     O += P V      P from TMEM, V as it lies in the cache (MN-major), O in TMEM
@@ -37,7 +38,7 @@ struct Maps {
 static_assert(sizeof(CUtensorMap) == 128, "");
 static_assert(sizeof(Maps) == kTcMapsBytes, "");
 
-constexpr int kThreads = 608, kTmaWarp = 16, kMmaWarp = 17;  // and 18
+constexpr int kThreads = 352, kTmaWarp = 8, kMmaWarp = 9;  // and 10
 constexpr int kStages = 2;
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w)
@@ -66,13 +67,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr)
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-                 "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
                  : "memory");
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
@@ -105,7 +99,6 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
     __shared__ uint64_t b_q[2], b_kfull[kStages], b_kempty[kStages], b_vfull[kStages], b_vempty[kStages], b_s[2][2], b_p[2][2], b_o[2], b_end;
     __shared__ uint32_t s_tmem;
     __shared__ int s_stop;
-    __shared__ float s_row[2][2][2][128];  // of each half's rows: what the threads of one key half tell the others
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (tid == 0) {
         for (int k = 0; k < kStages; ++k) {
@@ -115,10 +108,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
             mbar_init(&b_vempty[k], 2);
         }
         for (int h = 0; h < 2; ++h) {
-            mbar_init(&b_q[h], 256);
+            mbar_init(&b_q[h], 128);
             for (int k = 0; k < 2; ++k) {
                 mbar_init(&b_s[h][k], 1);
-                mbar_init(&b_p[h][k], 256);
+                mbar_init(&b_p[h][k], 128);
             }
             mbar_init(&b_o[h], 1);
         }
@@ -315,8 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
         if (elect_one()) umma_commit(&b_end);
         __syncwarp();
     } else {
-        const int h = warp / 8, ch = (warp / 4) & 1, t = (warp % 4) * 32 + lane;  // half, key half, row
-        const int pair_bar = 1 + h * 4 + warp % 4;                              // of the two warps that share rows
+        const int h = warp / 4, t = tid % 128;  // half, row
         const uint32_t tm = tmem + h * 256 + ((uint32_t)((warp % 4) * 32) << 16);
         uint32_t sn = 0;             // S so far
         uint32_t vc = 0, vnext = 0;  // value tiles of earlier segments
@@ -335,12 +327,11 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
             const int64_t at = (((int64_t)b * a.Lq + l) * a.Hq + head) * (a.n_pp + a.n_sp) + (s.pre ? 0 : a.n_pp) +
                                (s.single ? 2 * s.part + h : s.part);
             if (n == 0) {  // the odd half of a single key tile
-                if (mine && ch == 0) a.part_ml[at] = make_float2(kNone, 0.0f);
+                if (mine) a.part_ml[at] = make_float2(kNone, 0.0f);
                 continue;
             }
-            // this half's query rows, 64 columns by each of the two warps; the last product that read the old rows has
-            // completed (b_s)
-            constexpr int CH = D / 16, RI = 32 / CH;  // 16-byte chunks of half a row; rows per access
+            // this half's query rows; the last product that read the old rows has completed (b_s)
+            constexpr int CH = D / 8, RI = 32 / CH;  // 16-byte chunks of a row; rows per access
             const uint32_t qs = smem_u32(smem + M::Q + h * M::TILE);
             const int64_t q_at = mine ? b * a.q_b + l * a.q_l + head * a.q_h : -1;
             {
@@ -349,11 +340,11 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
                 for (int i = 0; i < CH; ++i) {
                     const int64_t from = __shfl_sync(0xFFFFFFFFu, q_at, i * RI + lane / CH);
                     v[i] = make_uint4(0, 0, 0, 0);
-                    if (from >= 0) v[i] = *reinterpret_cast<const uint4 *>(a.q + from + (ch * CH + lane % CH) * 8);
+                    if (from >= 0) v[i] = *reinterpret_cast<const uint4 *>(a.q + from + (lane % CH) * 8);
                 }
 #pragma unroll
                 for (int i = 0; i < CH; ++i) {
-                    const int r = (warp % 4) * 32 + i * RI + lane / CH, c = ch * CH + lane % CH;
+                    const int r = (warp % 4) * 32 + i * RI + lane / CH, c = lane % CH;
                     st_shared_v4(qs + (c / 8) * 16384 + r * 128 + (((c % 8) ^ (r & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
                 }
             }
@@ -365,53 +356,50 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
             float m = kNone, sum = 0.0f;
             for (int j = 0; j < n; ++j, ++sn) {
                 const int half = j & 1, kt = (s.tile0 + (s.single ? 2 * (j / 2) + h : j / 2)) * 128;  // S of the tile; the tile's first key
-                const int k0 = kt + half * 64 + ch * 32;                                             // this thread's first key
+                const int k0 = kt + half * 64;
                 const uint32_t ts = tm + half * 64;
-                ok = wait(&b_s[h][half], sn / 2) && ok;  // sn is even at the start of a segment
+                if (!(ok = wait(&b_s[h][half], sn / 2))) break;  // sn is even at the start of a segment
                 tc_fence_after();
-                uint32_t x[32];
-                tmem_ld32(ts + ch * 32, x);
+                uint32_t x[64];
+                tmem_ld32(ts, x);
+                tmem_ld32(ts + 32, x + 32);
                 tmem_wait_ld();
-                if (k0 + 32 > limit) {
+                if (k0 + 64 > limit) {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
+                    for (int c = 0; c < 64; ++c)
                         if (k0 + c >= limit) x[c] = 0xFF800000u;
                 }
                 __syncwarp();
                 float top = kNone, top1 = kNone;
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) {
+                for (int c = 0; c < 64; c += 2) {
                     top = fmaxf(top, __uint_as_float(x[c]));
                     top1 = fmaxf(top1, __uint_as_float(x[c + 1]));
                 }
                 top = fmaxf(top, top1);
-                s_row[h][ch][half][t] = top;
-                // and both have S in registers: P may overwrite it (the two leave the loop together, or not)
-                if (!(ok = named_bar_and(pair_bar, 64, ok))) break;
-                top = fmaxf(top, s_row[h][ch ^ 1][half][t]);
                 top = top == kNone ? kNone : top * a.scale_log2;
                 const bool raise = top > m + 8.0f;
                 const float to = raise ? top : m, f = raise ? ex2(m - top) : 1.0f;
                 if (j > 0 && __any_sync(0xFFFFFFFFu, raise)) {
-                    ok = wait(&b_o[h], sn - 1);  // O is still
+                    if (!(ok = wait(&b_o[h], sn - 1))) break;  // O is still
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < D / 2; c += 8) {
+                    for (int c = 0; c < D; c += 8) {
                         uint32_t o[8];
-                        tmem_ld8(tm + 128 + ch * (D / 2) + c, o);
+                        tmem_ld8(tm + 128 + c, o);
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st8(tm + 128 + ch * (D / 2) + c, o);
+                        tmem_st8(tm + 128 + c, o);
                     }
                 }
                 m = to;
                 sum *= f;
                 float2 add = make_float2(0.0f, 0.0f), add1 = add;
                 const float2 minus = make_float2(-m, -m);
-                uint32_t p[16];
+                uint32_t p[32];
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
+                for (int e = 0; e < 32; e += 2) {
                     const float2 y0 = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), scale2, minus);
                     const float2 y1 = fma2(make_float2(__uint_as_float(x[2 * e + 2]), __uint_as_float(x[2 * e + 3])), scale2, minus);
                     const float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
@@ -421,14 +409,14 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
                     p[e] = *reinterpret_cast<const uint32_t *>(&b0);
                     p[e + 1] = *reinterpret_cast<const uint32_t *>(&b1);
                 }
-                tmem_st16(ts + ch * 16, p);
+                tmem_st32(ts, p);
                 add = add2(add, add1);
                 sum += add.x + add.y;
                 if (half == 0 && kt + 128 > s.len) {  // what the cache holds past the segment must not reach O, not even as 0 * NaN
                     const uint32_t vt = vc + (uint32_t)(s.single ? j + h : j / 2), st = vt % kStages;
-                    ok = wait(&b_vfull[st], vt / kStages) && ok;
+                    if (!(ok = wait(&b_vfull[st], vt / kStages))) break;
                     if (kt + t >= s.len)
-                        for (int c = ch * (D / 16); c < (ch + 1) * (D / 16); ++c)
+                        for (int c = 0; c < D / 8; ++c)
                             st_shared_v4(smem_u32(smem + M::V + st * M::TILE) + (c / 8) * 16384 + t * 128 + (c % 8) * 16, 0, 0, 0, 0);
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -441,36 +429,33 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
             if (ok) ok = wait(&b_o[h], sn - 2) && wait(&b_o[h], sn - 1);
             tc_fence_after();
             // O's rows through this half's Q tile (read for the last time), which holds D / 2 columns of all of them, so that a
-            // row leaves in whole pieces: row r's 16-byte chunk c lies at chunk c ^ (r % OC).  The two warps of a row take
-            // turns: each stages and stores its columns of its 32 rows.
+            // row leaves in whole pieces: row r's 16-byte chunk c lies at chunk c ^ (r % OC)
             constexpr int OC = D / 8, RO = 32 / OC;  // chunks of a piece; rows per access
-            s_row[h][ch][0][t] = sum;
-            for (int turn = 0; turn < 2; ++turn) {
-                if (turn == ch) {
 #pragma unroll
-                    for (int c = 0; c < D / 2; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(tm + 128 + ch * (D / 2) + c, o);
-                        tmem_wait_ld();
+            for (int c0 = 0; c0 < D; c0 += D / 2) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            st_shared_v4(qs + t * (OC * 16) + (((c / 4 + e) ^ (t % OC)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                    }
-                    __syncwarp();
-#pragma unroll 8
-                    for (int i = 0; i < OC; ++i) {
-                        const int from = i * RO + lane / OC, r = (warp % 4) * 32 + from;
-                        const int64_t to = __shfl_sync(0xFFFFFFFFu, mine ? at : (int64_t)-1, from);
-                        const uint4 v = ld_shared_v4(qs + r * (OC * 16) + (((lane % OC) ^ (r % OC)) << 4));
-                        if (to >= 0) *reinterpret_cast<uint4 *>(a.part_o + to * D + ch * (D / 2) + (lane % OC) * 4) = v;
-                    }
+                for (int c = 0; c < D / 2; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(tm + 128 + c0 + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        st_shared_v4(qs + t * (OC * 16) + (((c / 4 + e) ^ (t % OC)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 }
-                named_bar_sync(pair_bar, 64);
+                __syncwarp();
+#pragma unroll 8
+                for (int i = 0; i < OC; ++i) {
+                    const int from = i * RO + lane / OC, r = (warp % 4) * 32 + from;
+                    const int64_t to = __shfl_sync(0xFFFFFFFFu, mine ? at : (int64_t)-1, from);
+                    const uint4 v = ld_shared_v4(qs + r * (OC * 16) + (((lane % OC) ^ (r % OC)) << 4));
+                    if (to >= 0) *reinterpret_cast<uint4 *>(a.part_o + to * D + c0 + (lane % OC) * 4) = v;
+                }
+                __syncwarp();
             }
-            if (mine && ch == 0) a.part_ml[at] = make_float2(m, sum + s_row[h][1][0][t]);
+            if (mine) a.part_ml[at] = make_float2(m, sum);
             tc_fence_before();
             // the next rows of Q go where other warps' O may still lie; the half's warps leave together
-            ok = named_bar_and(9 + h, 256, ok);
+            ok = named_bar_and(1 + h, 128, ok);
         }
     }
     tc_fence_before();
