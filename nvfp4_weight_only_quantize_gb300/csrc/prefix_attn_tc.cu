@@ -3,8 +3,10 @@
 //
 // A CTA works on two row tiles of 128 (or on two key tiles of one row tile) at a
 // time, so that the tensor core multiplies for one while the other is in its
-// softmax.  Warps 0-3 and 4-7: the softmax of the two, one thread per row; warp
-// 8: TMA loads of the key and value tiles; warps 9 and 10: the MMAs of the two.
+// softmax.  Warps 0-3 and 4-7: the softmax of the two, one thread per row; warps
+// 8 and 9: TMA loads of the key and the value tiles (one instruction a tile: some
+// 130 ns each, which with four per 64 keys had been what bounded a step); warps
+// 10 and 11: the MMAs of the two.
 // Per half and 64 keys of a tile:
 //     S = Q K^T     Q, K in shared memory (K-major), S in TMEM, FP32
 //     P = 2^(S c - m)  read from TMEM, written back as bf16 over S
@@ -16,7 +18,9 @@
 // below 2^8 and are normalised in the end all the same), so O is rescaled rarely.
 // S and P share columns: the Q K^T that overwrites a P is issued once its P V has
 // completed.
-// Shared memory: Q 64 KB, two K and two V tiles of 32 KB (D = 128).
+// Shared memory (D = 128): Q 64 KB, five K and five V tiles of 64 keys, 16 KB each.
+// A tile's load has to hide behind the four before it: with two tiles of 128 keys
+// a step took 1.9 us, the latency of its loads.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -38,15 +42,15 @@ struct Maps {
 static_assert(sizeof(CUtensorMap) == 128, "");
 static_assert(sizeof(Maps) == kTcMapsBytes, "");
 
-constexpr int kThreads = 352, kTmaWarp = 8, kMmaWarp = 9;  // and 10
-constexpr int kStages = 2;
+constexpr int kThreads = 384, kTmaWarp = 8, kMmaWarp = 10;  // and the warp after each
+constexpr int kStages = 5;  // tiles of 64 keys: K and V each
 
-__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w)
+__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w, int v)
 {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(
             smem_u32(dst)),
-        "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+        "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
         : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r)
@@ -78,8 +82,9 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 template <int D>
 struct Smem {
     static constexpr int SUB = D / 64;             // 64-element column blocks of a tile
-    static constexpr int TILE = SUB * 128 * 128;   // bytes of a 128-row tile
-    static constexpr int Q = 0, K = 2 * TILE, V = K + kStages * TILE, TOTAL = V + kStages * TILE;
+    static constexpr int TILE = SUB * 128 * 128;   // bytes of 128 query rows
+    static constexpr int KV = SUB * 64 * 128;      // bytes of 64 keys
+    static constexpr int Q = 0, K = 2 * TILE, V = K + kStages * KV, TOTAL = V + kStages * KV;
 };
 
 // A contiguous range of steps inside one unit.
@@ -203,31 +208,22 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
         return s;
     };
 
-    if (warp == kTmaWarp) {
+    if (warp == kTmaWarp || warp == kTmaWarp + 1) {
+        const bool keys = warp == kTmaWarp;
+        uint64_t *const full = keys ? b_kfull : b_vfull, *const empty = keys ? b_kempty : b_vempty;
+        uint8_t *const ring = smem + (keys ? M::K : M::V);
         uint32_t it = 0;
         bool ok = true;
         for (int pos = begin; ok && pos < end;) {
             const Seg s = locate(pos);
-            const int tiles = s.single ? s.n0 + s.n1 : s.n0;
-            const CUtensorMap *mk = s.pre ? &maps.kp : &maps.ks, *mv = s.pre ? &maps.vp : &maps.vs;
-            for (int t = 0; ok && t < tiles; ++t, ++it) {
-                const int st = it % kStages, k0 = (s.tile0 + t) * 128;
-                const uint32_t round = it / kStages;
-                if (round > 0 && !(ok = wait(&b_kempty[st], round - 1))) break;
+            const int tiles = 2 * (s.single ? s.n0 + s.n1 : s.n0);
+            const CUtensorMap *map = s.pre ? (keys ? &maps.kp : &maps.vp) : keys ? &maps.ks : &maps.vs;
+            for (int t = 0; t < tiles; ++t, ++it) {
+                const uint32_t st = it % kStages, round = it / kStages;
+                if (round > 0 && !(ok = wait(&empty[st], round - 1))) break;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(&b_kfull[st], M::TILE);
-                    for (int c = 0; c < M::SUB; ++c)
-                        tma_load_4d(smem + M::K + st * M::TILE + c * 16384, mk, &b_kfull[st], c * 64, s.hk, k0, s.seg);
-                }
-                __syncwarp();
-                if (round > 0 && !(ok = wait(&b_vempty[st], round - 1))) {
-                    ++it;  // its K load is in flight
-                    break;
-                }
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(&b_vfull[st], M::TILE);
-                    for (int c = 0; c < M::SUB; ++c)
-                        tma_load_4d(smem + M::V + st * M::TILE + c * 16384, mv, &b_vfull[st], c * 64, s.hk, k0, s.seg);
+                    mbar_arrive_expect_tx(&full[st], M::KV);
+                    tma_load_5d(ring + st * M::KV, map, &full[st], 0, s.tile0 * 128 + t * 64, 0, s.hk, s.seg);
                 }
                 __syncwarp();
             }
@@ -236,13 +232,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
         // no load may be in flight when the CTA ends
         if (*reinterpret_cast<volatile int *>(&s_stop)) {
             const uint64_t until = globaltimer_ns() + limit_ns;
-            for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k) {
-                while (!mbar_try_wait(&b_kfull[k % kStages], (k / kStages) & 1u) && globaltimer_ns() < until) {
+            for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k)
+                while (!mbar_try_wait(&full[k % kStages], (k / kStages) & 1u) && globaltimer_ns() < until) {
                 }
-                // the last V load may not have been issued: its wait ends at the deadline
-                while (!mbar_try_wait(&b_vfull[k % kStages], (k / kStages) & 1u) && globaltimer_ns() < until) {
-                }
-            }
         }
         __syncwarp();
     } else if (warp >= kMmaWarp) {
@@ -250,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
         const uint32_t id_qk = idesc_bf16_f32(128, 64), id_pv = idesc_bf16_f32(128, D) | (1u << 16);  // V is MN-major
         const uint32_t d_s = tmem + h * 256, d_o = d_s + 128;
         const uint64_t q_desc = desc_kmajor_sw128(smem_u32(smem + M::Q + h * M::TILE)), k_desc = desc_kmajor_sw128(smem_u32(smem + M::K)),
-                       v_desc = desc_mnmajor_sw128(smem_u32(smem + M::V), 16384, 1024);
+                       v_desc = desc_mnmajor_sw128(smem_u32(smem + M::V), 8192, 1024);
         uint32_t tc = 0;           // tiles of earlier segments
         uint32_t qn = 0, pn = 0;   // Q tiles and P V products so far
         bool ok = true;
@@ -263,42 +255,37 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
             if (n == 0) continue;
             if (!(ok = wait(&b_q[h], qn++))) break;
             auto qk = [&](int j) -> bool {
-                const uint32_t t = t0 + (j / 2) * dt, st = t % kStages, half = j & 1;
-                if (half == 0 && !wait(&b_kfull[st], t / kStages)) return false;
+                const uint32_t half = j & 1, t = 2 * (t0 + (j / 2) * dt) + half, st = t % kStages;
+                if (!wait(&b_kfull[st], t / kStages)) return false;
                 tc_fence_after();
-                const uint64_t bd = k_desc + st * (uint32_t)(M::TILE >> 4) + half * (uint32_t)(64 * 128 >> 4);
+                const uint64_t bd = k_desc + st * (uint32_t)(M::KV >> 4);
                 if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t o = (uint64_t)((kk / 4) * (16384 >> 4) + 2 * (kk % 4));
-                        umma_bf16(d_s + half * 64, q_desc + o, bd + o, id_qk, kk > 0);
-                    }
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        umma_bf16(d_s + half * 64, q_desc + (uint64_t)((kk / 4) * (16384 >> 4) + 2 * (kk % 4)),
+                                  bd + (uint64_t)((kk / 4) * (8192 >> 4) + 2 * (kk % 4)), id_qk, kk > 0);
                     umma_commit(&b_s[h][half]);
-                    if (half) {
-                        umma_commit(&b_kempty[st]);
-                        if (s.single) umma_commit(&b_kempty[st]);  // the other warp does not use this tile
-                    }
+                    umma_commit(&b_kempty[st]);
+                    if (s.single) umma_commit(&b_kempty[st]);  // the other warp does not use this tile
                 }
                 __syncwarp();
                 return true;
             };
             ok = qk(0) && qk(1);
             for (int j = 0; ok && j < n; ++j) {
-                const uint32_t t = t0 + (j / 2) * dt, st = t % kStages, half = j & 1;
-                if (half == 0 && !(ok = wait(&b_vfull[st], t / kStages))) break;
+                const uint32_t half = j & 1, t = 2 * (t0 + (j / 2) * dt) + half, st = t % kStages;
+                if (!(ok = wait(&b_vfull[st], t / kStages))) break;
                 if (!(ok = wait(&b_p[h][half], pn / 2))) break;  // pn is even at the start of a segment
                 ++pn;
                 tc_fence_after();
-                const uint64_t vd = v_desc + st * (uint32_t)(M::TILE >> 4) + half * (uint32_t)(64 * 128 >> 4);
+                const uint64_t vd = v_desc + st * (uint32_t)(M::KV >> 4);
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)  // 16 keys: two 8-row groups of every column block
                         umma_bf16_ts(d_o, d_s + half * 64 + 8 * kk, vd + (uint64_t)(kk * (2048 >> 4)), id_pv, j > 0 || kk > 0);
                     umma_commit(&b_o[h]);
-                    if (half) {
-                        umma_commit(&b_vempty[st]);
-                        if (s.single) umma_commit(&b_vempty[st]);
-                    }
+                    umma_commit(&b_vempty[st]);
+                    if (s.single) umma_commit(&b_vempty[st]);
                 }
                 __syncwarp();
                 if (j + 2 < n) ok = wait(&b_o[h], pn - 1) && qk(j + 2);  // this P is read: its S may be overwritten
@@ -412,12 +399,14 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
                 tmem_st32(ts, p);
                 add = add2(add, add1);
                 sum += add.x + add.y;
-                if (half == 0 && kt + 128 > s.len) {  // what the cache holds past the segment must not reach O, not even as 0 * NaN
-                    const uint32_t vt = vc + (uint32_t)(s.single ? j + h : j / 2), st = vt % kStages;
+                if (k0 + 64 > s.len) {  // what the cache holds past the segment must not reach O, not even as 0 * NaN
+                    const uint32_t vt = 2 * (vc + (uint32_t)(s.single ? 2 * (j / 2) + h : j / 2)) + half, st = vt % kStages;
                     if (!(ok = wait(&b_vfull[st], vt / kStages))) break;
-                    if (kt + t >= s.len)
-                        for (int c = 0; c < D / 8; ++c)
-                            st_shared_v4(smem_u32(smem + M::V + st * M::TILE) + (c / 8) * 16384 + t * 128 + (c % 8) * 16, 0, 0, 0, 0);
+                    if (k0 + t % 64 >= s.len)  // two threads per key
+                        for (int c = 0; c < D / 16; ++c)
+                            st_shared_v4(smem_u32(smem + M::V + st * M::KV) + (D == 128 ? t / 64 : 0) * 8192 + (t % 64) * 128 +
+                                             (D == 128 ? c : (t / 64) * (D / 16) + c) * 16,
+                                         0, 0, 0, 0);
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
@@ -470,16 +459,17 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
     }
 }
 
-// The cache [segments, T, Hkv, D] as boxes of 128 tokens x 64 columns of one kv head.
+// The cache [segments, T, Hkv, D] as (64 columns, token, column block, kv head, segment): a box of 64 tokens of one head
+// lands as D / 64 blocks of 64 tokens x 64 columns.
 bool make_map(CUtensorMap *m, const void *base, int64_t D, int64_t Hkv, int64_t T, int64_t n, int64_t s_h, int64_t s_t, int64_t s_n)
 {
     const auto fn = encode_fn();
     if (!fn) return false;
-    const auto bytes = [](int64_t stride, int64_t size) { return (cuuint64_t)(size == 1 ? 16 : stride * 2); };  // unused: any
-    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)T, (cuuint64_t)n};
-    const cuuint64_t strides[3] = {bytes(s_h, Hkv), bytes(s_t, T), bytes(s_n, n)};
-    const cuuint32_t box[4] = {64, 1, 128, 1}, es[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const auto bytes = [](int64_t stride, int64_t size) { return (cuuint64_t)(size == 1 ? 128 : stride * 2); };  // unused: any
+    const cuuint64_t dims[5] = {64, (cuuint64_t)T, (cuuint64_t)(D / 64), (cuuint64_t)Hkv, (cuuint64_t)n};
+    const cuuint64_t strides[4] = {bytes(s_t, T), 128, bytes(s_h, Hkv), bytes(s_n, n)};
+    const cuuint32_t box[5] = {64, 64, (cuuint32_t)(D / 64), 1, 1}, es[5] = {1, 1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
