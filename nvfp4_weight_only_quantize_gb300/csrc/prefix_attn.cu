@@ -76,8 +76,9 @@ __global__ void __launch_bounds__(kWarps * 32) rows16_kernel(const Args a, int p
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     // Beside the tcgen05 kernel, whose CTAs let this one start once all work before both has finished, there is nothing to
-    // wait for here; the kernel that joins the parts waits for both, because this one waits at its end.
+    // wait for here; the kernel that joins the parts waits for both, because this one's last CTA waits at its end.
     if (!beside_tc) pdl_wait();
+    beside_tc = beside_tc && blockIdx.x == gridDim.x - 1;
     pdl_trigger();
     // which rows, which keys
     int item = blockIdx.x;
@@ -384,6 +385,18 @@ bool shape(const qerl_prefix_attn_dims *d, Args &a, bool tc)
     };
     a.p_tc = tc && quicker(pr, a.P, a.n_prefix);
     a.s_tc = tc && quicker(sr, a.S, a.B);
+    if (a.p_tc && !a.s_tc) {
+        // The prefixes on tcgen05 leave SMs to the suffixes, which then run beside them: an SM takes 2 us per step, or reads
+        // 50 bytes per ns.  As many as make the later of the two end soonest, against one after the other.
+        const double steps = (double)a.n_prefix * a.Hkv * (pr / 256 + 1) * ((a.P + 127) / 128);
+        const double bytes = 0.6 * (double)a.B * a.Hkv * a.S * (double)(d->D * 4);
+        const int sms = num_sms();
+        double best = 2.0 * ceil(steps / sms) + bytes / 6.0e6;
+        for (int n = sms - 4; n >= sms / 2; n -= 4) {
+            const double t = 2.0 * ceil(steps / n), u = bytes / ((sms - n) * 50.0e3), later = t > u ? t : u;
+            if (later < best) best = later, a.grid_tc = n;
+        }
+    }
     if ((a.p_tc ? (pr / 256 + 1) * (a.P / 128 + 4) * a.Hkv * a.n_prefix : 0) + (a.s_tc ? (sr / 256 + 1) * (a.S / 128 + 4) * a.Hkv * a.B : 0) > big)
         a.p_tc = a.s_tc = 0;  // more steps than the kernel counts
     const int64_t up = a.p_tc ? 0 : (int64_t)a.n_prefix * a.Hkv * a.p_tiles, us = a.s_tc ? 0 : (int64_t)a.B * a.Hkv * a.s_tiles;
