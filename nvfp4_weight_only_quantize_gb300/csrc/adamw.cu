@@ -74,6 +74,7 @@ struct Pairs {
     __device__ __forceinline__ explicit Pairs(const Step &s) : one(make_float2(s.one, s.one)), nought(make_float2(s.nought, s.nought)) {}
     __device__ __forceinline__ float2 mul(float2 a, float2 b) const { return fma2(a, b, nought); }
     __device__ __forceinline__ float2 add(float2 a, float2 b) const { return fma2(a, one, b); }
+    __device__ __forceinline__ float2 sub(float2 a, float2 b) const { return fma2(make_float2(-b.x, -b.y), one, a); }
 };
 
 __device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint32_t k0, uint32_t k1)
@@ -241,7 +242,7 @@ __device__ __forceinline__ uint32_t signed_code(uint32_t code, float like) { ret
 
 // A CTA takes one chunk, its warps' blocks side by side.  clip: nullptr, or {c, skip flag} from norm_kernel.
 template <bool PB, bool GB, bool S8>
-__global__ void __launch_bounds__(kThreads, S8 ? 6 : 4) step_kernel(const Rec *recs, const Chunk *chunks, Step st, const float *clip)
+__global__ void __launch_bounds__(kThreads, S8 ? 6 : 3) step_kernel(const Rec *recs, const Chunk *chunks, Step st, const float *clip)
 {
     __shared__ float s_lr, s_decay;
     pdl_trigger();
@@ -263,18 +264,43 @@ __global__ void __launch_bounds__(kThreads, S8 ? 6 : 4) step_kernel(const Rec *r
     const Pairs X(st);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     float *const p32 = PB ? R.master : static_cast<float *>(R.param);
+    // a block as it lies in memory
+    struct Raw {
+        float2 g[4], p[4], m[S8 ? 1 : 4], v[S8 ? 1 : 4];
+        uint2 cm, cv;
+        float ms, vs;
+    };
+    auto fetch = [&](int b, Raw &r) {
+        const int64_t blk = (int64_t)ch.blk + b, i = blk * kBlk + lane * 8;
+        if (b >= st.chunk || blk * kBlk >= n) return;
+        const bool full = i + 8 <= n;
+        load8<GB>(R.grad, i, n, full, r.g);
+        load8<false>(p32, i, n, full, r.p);
+        if constexpr (S8) {
+            r.cm = load_codes(R.m, i, n, full), r.cv = load_codes(R.v, i, n, full);
+            r.ms = R.m_scale[blk], r.vs = R.v_scale[blk];
+        } else {
+            load8<false>(R.m, i, n, full, r.m);
+            load8<false>(R.v, i, n, full, r.v);
+        }
+    };
+    // FP32 states: the next block's loads run under this one's arithmetic (417 -> 414 us on 80 M elements); 8-bit states
+    // take the registers for twice the warps instead (463 -> 436 us)
+    Raw next;
+    if (!S8) fetch(warp, next);
     {
         for (int b = warp; b < st.chunk; b += kThreads / 32) {
             const int64_t blk = (int64_t)ch.blk + b;
             if (blk * kBlk >= n) break;
             const int64_t i = blk * kBlk + lane * 8;
             const bool full = i + 8 <= n;
+            if (S8) fetch(b, next);
             float2 g[4], p[4], m[4], v[4];
-            load8<GB>(R.grad, i, n, full, g);
-            load8<false>(p32, i, n, full, p);
-            if (S8) {
-                const uint2 cm = load_codes(R.m, i, n, full), cv = load_codes(R.v, i, n, full);
-                const float ms = R.m_scale[blk], vs = R.v_scale[blk];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) g[j] = next.g[j], p[j] = next.p[j];
+            if constexpr (S8) {
+                const uint2 cm = next.cm, cv = next.cv;
+                const float ms = next.ms, vs = next.vs;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t wm = j < 2 ? cm.x : cm.y, wv = j < 2 ? cv.x : cv.y;
@@ -285,9 +311,10 @@ __global__ void __launch_bounds__(kThreads, S8 ? 6 : 4) step_kernel(const Rec *r
                     v[j] = X.mul(v[j], v[j]);
                 }
             } else {
-                load8<false>(R.m, i, n, full, m);
-                load8<false>(R.v, i, n, full, v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m[j] = next.m[j], v[j] = next.v[j];
             }
+            if (!S8) fetch(b + kThreads / 32, next);
             float2 root[4];
             float mtop = 0.0f, vtop = 0.0f;
 #pragma unroll
@@ -357,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, S8 ? 6 : 4) step_kernel(const Rec *r
 // out: {c, 1 if the norm is not finite}; norm_out may be null.
 template <bool GB>
 __global__ void __launch_bounds__(kNormThreads, kNormPerSm)
-    norm_kernel(const Rec *recs, const Chunk *chunks, uint32_t n_chunks, int chunk, double max_norm, double *partial, unsigned int *arrived,
+    norm_kernel(const Rec *recs, const Chunk *chunks, uint32_t n_chunks, Step st, double max_norm, double *partial, unsigned int *arrived,
                 float *out, float *norm_out)
 {
     __shared__ double s_sum[kNormThreads / 32];
@@ -366,17 +393,17 @@ __global__ void __launch_bounds__(kNormThreads, kNormPerSm)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     Chunk next = blockIdx.x < n_chunks ? chunks[blockIdx.x] : Chunk{0, 0};  // the table does not change
     pdl_wait();
-    float s = 0.0f, e = 0.0f;
-    auto two_sum = [&](float p, float pe) {  // s + e += p + pe
-        const float t = __fadd_rn(s, p), bb = __fsub_rn(t, s);
-        const float se = __fadd_rn(__fsub_rn(s, __fsub_rn(t, bb)), __fsub_rn(p, bb));
+    const Pairs X(st);
+    float2 s = both(0.0f), e = both(0.0f);
+    auto two_sum = [&](float2 p, float2 pe) {  // s + e += p + pe
+        const float2 t = X.add(s, p), bb = X.sub(t, s);
+        e = X.add(e, X.add(pe, X.add(X.sub(s, X.sub(t, bb)), X.sub(p, bb))));
         s = t;
-        e = __fadd_rn(e, __fadd_rn(pe, se));
     };
     for (uint32_t k = blockIdx.x; k < n_chunks; k += gridDim.x) {
         const Chunk ch = next;
         if (k + gridDim.x < n_chunks) next = chunks[k + gridDim.x];
-        const int64_t n = min(recs[ch.tensor].n, ((int64_t)ch.blk + chunk) * kBlk), i0 = ((int64_t)ch.blk + warp) * kBlk + lane * 8;
+        const int64_t n = min(recs[ch.tensor].n, ((int64_t)ch.blk + st.chunk) * kBlk), i0 = ((int64_t)ch.blk + warp) * kBlk + lane * 8;
         const void *grad = recs[ch.tensor].grad;
         constexpr int kEach = kChunkBlks / (kNormThreads / 32), kGap = kNormThreads / 32 * kBlk;
         float2 g[kEach][4];
@@ -385,17 +412,16 @@ __global__ void __launch_bounds__(kNormThreads, kNormPerSm)
 #pragma unroll
         for (int b = 0; b < kEach; ++b)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float x = j % 2 ? g[b][j / 2].y : g[b][j / 2].x, p = __fmul_rn(x, x);
-                two_sum(p, __fmaf_rn(x, x, -p));
+            for (int j = 0; j < 4; ++j) {
+                const float2 x = g[b][j], p = X.mul(x, x);
+                two_sum(p, fma2(x, x, make_float2(-p.x, -p.y)));
             }
     }
-    for (int o = 16; o; o >>= 1) {
-        const float p = __shfl_xor_sync(0xFFFFFFFFu, s, o), pe = __shfl_xor_sync(0xFFFFFFFFu, e, o);
-        two_sum(p, pe);
-    }
+    for (int o = 16; o; o >>= 1)
+        two_sum(make_float2(__shfl_xor_sync(0xFFFFFFFFu, s.x, o), __shfl_xor_sync(0xFFFFFFFFu, s.y, o)),
+                make_float2(__shfl_xor_sync(0xFFFFFFFFu, e.x, o), __shfl_xor_sync(0xFFFFFFFFu, e.y, o)));
     // An overflowed sum leaves NaN in its error term; the sum itself tells.
-    const double d = isfinite(s) ? (double)s + (double)e : (double)s;
+    const double d = isfinite(s.x + s.y) ? ((double)s.x + (double)s.y) + ((double)e.x + (double)e.y) : (double)s.x + (double)s.y;
     if (lane == 0) s_sum[warp] = d;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -621,7 +647,7 @@ extern "C" qerl_status qerl_adamw_step(const qerl_adamw *h, const qerl_adamw_hyp
         if (grid > kNormCtasMax) grid = kNormCtasMax;
         auto *fn = gb ? norm_kernel<true> : norm_kernel<false>;
         QERL_TRY(launched(launch_k(fn, dim3((unsigned)grid), dim3(kNormThreads), 0, as_cuda(stream), chain, (const Rec *)h->recs,
-                                   (const Chunk *)h->chunks, h->n_chunks, h->chunk, hy->max_grad_norm, h->partial, h->counter, h->clip,
+                                   (const Chunk *)h->chunks, h->n_chunks, st, hy->max_grad_norm, h->partial, h->counter, h->clip,
                                    grad_norm)));
     }
     if (h->n_chunks == 0) return QERL_OK;

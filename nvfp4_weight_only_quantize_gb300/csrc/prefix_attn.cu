@@ -20,7 +20,7 @@ namespace {
 
 // ------------------------------------------------------------------ chunks of up to 16 rows
 constexpr int kWarps = 4;    // a warp takes every fourth 16-key tile of the chunk
-constexpr int kStages = 3;   // tiles in flight per warp
+constexpr int kStages = 2;   // tiles in flight per warp
 constexpr int kTile = 16;
 
 template <int D>
@@ -366,7 +366,8 @@ int tc_parts_most(int64_t rows, int64_t len, int64_t Hkv, int64_t ctas)
 // Kernels, chunk lengths, tiles and parts of a call; false where a size is not covered.
 // A segment of more than 16 rows goes to tcgen05 where that is quicker.  What was measured: a step of its line takes
 // about 2 us and a CTA about 8 us besides; the other kernel reads every key once per 16 rows, at some 5 TB/s from L2.
-// Chunks of the other kernel: about four CTAs per SM over all rows and keys, 64 to 2048 keys each.
+// Chunks of the other kernel: about six CTAs per SM over all rows and keys, 64 to 1024 keys each.  Measured on 64 answers
+// of up to 4096 tokens: 256 keys 131 us, 512 108 us, 1024 99 us, 2048 109 us (too few to even the SMs out).
 bool shape(const qerl_prefix_attn_dims *d, Args &a, bool tc)
 {
     if (d->B < 1 || d->Lq < 1 || d->Hq < 1 || d->Hkv < 1 || d->n_prefix < 1 || d->P < 0 || d->S < 0) return false;
@@ -400,9 +401,9 @@ bool shape(const qerl_prefix_attn_dims *d, Args &a, bool tc)
     if ((a.p_tc ? (pr / 256 + 1) * (a.P / 128 + 4) * a.Hkv * a.n_prefix : 0) + (a.s_tc ? (sr / 256 + 1) * (a.S / 128 + 4) * a.Hkv * a.B : 0) > big)
         a.p_tc = a.s_tc = 0;  // more steps than the kernel counts
     const int64_t up = a.p_tc ? 0 : (int64_t)a.n_prefix * a.Hkv * a.p_tiles, us = a.s_tc ? 0 : (int64_t)a.B * a.Hkv * a.s_tiles;
-    const int64_t want = (up * a.P + us * a.S) / (4 * num_sms());
+    const int64_t want = (up * a.P + us * a.S) / (6 * num_sms());
     int64_t chunk = (want + 63) / 64 * 64;
-    chunk = chunk < 64 ? 64 : chunk > 2048 ? 2048 : chunk;
+    chunk = chunk < 64 ? 64 : chunk > 1024 ? 1024 : chunk;
     a.p_chunk = a.s_chunk = (int)chunk;
     a.n_pp = a.p_tc ? tc_parts_most(pr, a.P, a.Hkv, a.grid_tc) : ceil_div(a.P, chunk);
     a.n_sp = a.s_tc ? tc_parts_most(sr, a.S, a.Hkv, a.grid_tc) : ceil_div(a.S, chunk);
