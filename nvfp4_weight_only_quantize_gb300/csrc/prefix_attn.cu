@@ -262,12 +262,12 @@ __device__ __forceinline__ int tc_parts(const Args &a, bool pre, int k, int hk, 
     return ((first + n - 1) / per_cta - first / per_cta + 1) * (single ? 2 : 1);
 }
 
-// W warps per query row (each takes every W-th part, eight in flight); the parts
+// W warps per query row (each takes every W-th part); the parts
 // that exist follow from the lengths.
 template <int D, int W>
 __global__ void __launch_bounds__(128) join_kernel(const Args a)
 {
-    constexpr int E = D / 32, RB = 4 / W;  // columns of a lane; rows of a block
+    constexpr int E = D / 32, RB = 4 / W, NB = W == 1 ? 4 : 8;  // columns of a lane; rows of a block; parts in flight
     __shared__ float s_o[W > 1 ? 4 : 1][W > 1 ? D : 1];
     __shared__ float2 s_ml[4];
     pdl_trigger();
@@ -287,11 +287,11 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a)
     const int64_t base = (int64_t)row * (a.n_pp + a.n_sp);
     const auto at = [&](int k) { return base + (k < np ? k : a.n_pp + k - np); };
     float M = kNone, L = 0.0f, acc[E] = {};
-    for (int k0 = share; k0 < n; k0 += 8 * W) {
-        float2 ml[8];
-        float v[8][E];
+    for (int k0 = share; k0 < n; k0 += NB * W) {
+        float2 ml[NB];
+        float v[NB][E];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < NB; ++j) {
             const int k = k0 + j * W;
             ml[j] = make_float2(kNone, 0.0f);
             if (k < n) {
@@ -308,14 +308,14 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a)
         }
         float to = M;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) to = fmaxf(to, ml[j].x);
+        for (int j = 0; j < NB; ++j) to = fmaxf(to, ml[j].x);
         const float f = ex2(M - to);
         M = to;
         L *= f;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] *= f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < NB; ++j) {
             const bool none = ml[j].y == 0.0f && ml[j].x == kNone;  // no part, or one that saw no key and may have left no o
             const float w = none ? 0.0f : ex2(ml[j].x - M);
             L = fmaf(w, ml[j].y, L);

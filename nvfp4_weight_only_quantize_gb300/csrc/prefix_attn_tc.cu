@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
     using M = Smem<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // the swizzled tiles' alignment
-    __shared__ uint64_t b_q[2], b_kfull[kStages], b_kempty[kStages], b_vfull[kStages], b_vempty[kStages], b_s[2][2], b_p[2][2], b_o[2], b_end;
+    __shared__ uint64_t b_q[2], b_kfull[kStages], b_kempty[kStages], b_vfull[kStages], b_vempty[kStages], b_s[2][2], b_p[2][2], b_o[2], b_done[2], b_end;
     __shared__ uint32_t s_tmem;
     __shared__ int s_stop;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
                 mbar_init(&b_p[h][k], 128);
             }
             mbar_init(&b_o[h], 1);
+            mbar_init(&b_done[h], 1);
         }
         mbar_init(&b_end, 2);
         s_stop = 0;
@@ -243,7 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
         const uint32_t d_s = tmem + h * 256, d_o = d_s + 128;
         const uint64_t q_desc = desc_kmajor_sw128(smem_u32(smem + M::Q + h * M::TILE)), k_desc = desc_kmajor_sw128(smem_u32(smem + M::K)),
                        v_desc = desc_mnmajor_sw128(smem_u32(smem + M::V), 8192, 1024);
-        uint32_t tc = 0;           // tiles of earlier segments
+        uint32_t tc = 0;           // tiles of 128 keys in earlier segments
+        uint32_t kn = 0, vn = 0;   // K and V tiles passed: every one of both, so that no phase of a barrier goes unseen
         uint32_t qn = 0, pn = 0;   // Q tiles and P V products so far
         bool ok = true;
         for (int pos = begin; ok && pos < end;) {
@@ -252,11 +254,24 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
             const int n = 2 * (h ? s.n1 : s.n0);  // S of 64 keys
             const uint32_t t0 = tc + (s.single ? h : 0), dt = s.single ? 2 : 1;
             tc += (uint32_t)(s.single ? s.n0 + s.n1 : s.n0);
-            if (n == 0) continue;
+            // the tiles before `to` that only the other half uses
+            auto pass = [&](uint64_t *full, uint64_t *empty, uint32_t &seen, uint32_t to) -> bool {
+                for (; seen < to; ++seen) {
+                    if (!wait(&full[seen % kStages], seen / kStages)) return false;
+                    if (elect_one()) mbar_arrive(&empty[seen % kStages]);
+                    __syncwarp();
+                }
+                return true;
+            };
+            if (n == 0) {
+                ok = pass(b_kfull, b_kempty, kn, 2 * tc) && pass(b_vfull, b_vempty, vn, 2 * tc);
+                continue;
+            }
             if (!(ok = wait(&b_q[h], qn++))) break;
             auto qk = [&](int j) -> bool {
                 const uint32_t half = j & 1, t = 2 * (t0 + (j / 2) * dt) + half, st = t % kStages;
-                if (!wait(&b_kfull[st], t / kStages)) return false;
+                if (!pass(b_kfull, b_kempty, kn, t) || !wait(&b_kfull[st], t / kStages)) return false;
+                ++kn;
                 tc_fence_after();
                 const uint64_t bd = k_desc + st * (uint32_t)(M::KV >> 4);
                 if (elect_one()) {
@@ -266,7 +281,6 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
                                   bd + (uint64_t)((kk / 4) * (8192 >> 4) + 2 * (kk % 4)), id_qk, kk > 0);
                     umma_commit(&b_s[h][half]);
                     umma_commit(&b_kempty[st]);
-                    if (s.single) umma_commit(&b_kempty[st]);  // the other warp does not use this tile
                 }
                 __syncwarp();
                 return true;
@@ -274,7 +288,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
             ok = qk(0) && qk(1);
             for (int j = 0; ok && j < n; ++j) {
                 const uint32_t half = j & 1, t = 2 * (t0 + (j / 2) * dt) + half, st = t % kStages;
-                if (!(ok = wait(&b_vfull[st], t / kStages))) break;
+                if (!(ok = pass(b_vfull, b_vempty, vn, t) && wait(&b_vfull[st], t / kStages))) break;
+                ++vn;
                 if (!(ok = wait(&b_p[h][half], pn / 2))) break;  // pn is even at the start of a segment
                 ++pn;
                 tc_fence_after();
@@ -284,12 +299,13 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
                     for (int kk = 0; kk < 4; ++kk)  // 16 keys: two 8-row groups of every column block
                         umma_bf16_ts(d_o, d_s + half * 64 + 8 * kk, vd + (uint64_t)(kk * (2048 >> 4)), id_pv, j > 0 || kk > 0);
                     umma_commit(&b_o[h]);
+                    if (j + 1 == n) umma_commit(&b_done[h]);
                     umma_commit(&b_vempty[st]);
-                    if (s.single) umma_commit(&b_vempty[st]);
                 }
                 __syncwarp();
                 if (j + 2 < n) ok = wait(&b_o[h], pn - 1) && qk(j + 2);  // this P is read: its S may be overwritten
             }
+            ok = ok && pass(b_kfull, b_kempty, kn, 2 * tc) && pass(b_vfull, b_vempty, vn, 2 * tc);
         }
         // every product issued has completed before TMEM is freed
         if (elect_one()) umma_commit(&b_end);
@@ -297,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
     } else {
         const int h = warp / 4, t = tid % 128;  // half, row
         const uint32_t tm = tmem + h * 256 + ((uint32_t)((warp % 4) * 32) << 16);
-        uint32_t sn = 0;             // S so far
+        uint32_t sn = 0, units = 0;  // S and units so far
         uint32_t vc = 0, vnext = 0;  // value tiles of earlier segments
         bool ok = true;
         for (int pos = begin; ok && pos < end;) {
@@ -414,8 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows128_kernel(const __grid_const
                 tc_fence_before();
                 mbar_arrive(&b_p[h][half]);
             }
-            // the last two products, one after the other: a barrier tells only one phase from the next
-            if (ok) ok = wait(&b_o[h], sn - 2) && wait(&b_o[h], sn - 1);
+            if (ok) ok = wait(&b_done[h], units++);  // not b_o, which may be one product behind or, with both done, past it
             tc_fence_after();
             // O's rows through this half's Q tile (read for the last time), which holds D / 2 columns of all of them, so that a
             // row leaves in whole pieces: row r's 16-byte chunk c lies at chunk c ^ (r % OC)

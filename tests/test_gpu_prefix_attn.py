@@ -227,3 +227,19 @@ def test_other_stream_repeats_and_graph():
         torch.cuda.synchronize()
         fresh = q.qerl_prefix_attention(*x, i32([max(1, n - step) for n in sl]))
         assert torch.equal(out, fresh)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_short_units(D):
+    """More row and key tiles than there are SMs, of every length: tiles in pairs and alone, halves that end a tile apart."""
+    B, Lq, Hq, Hkv, P, S = 8, 129, 16, 2, 1000, 700
+    qq, kp, vp, ks, vs = inputs(B, 2, Lq, Hq, Hkv, D, P, S, 21)
+    sl = [129, 700, 0, 257, 640, 300, 513, 384]
+    pl = [1000, 130]
+    plan = q.PrefixAttention(kp, vp, ks, vs, Hq, Lq, D ** -0.5)
+    first, lse = check(qq, kp, vp, ks, vs, pl, sl, plan=plan)
+    for _ in range(300):
+        out, again = torch.full_like(first, NAN), torch.full_like(lse, NAN)
+        plan.run(qq, i32(sl), i32(pl), out=out, lse=again)
+        assert torch.equal(out, first) and torch.equal(again, lse)
+    assert q.get_error() == 0
