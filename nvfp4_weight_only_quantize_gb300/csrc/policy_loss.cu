@@ -10,11 +10,20 @@
 //
 // Bound by HBM: the logits read once and the gradient written once.  The factor
 // dL/dlogp needs only its own row's sums, so one pass does both directions: a
-// row is split over the CTAs of a cluster, every thread keeps its vectors in
-// registers (32 of them at most), the threads' (max, sum, entropy sum) meet by
-// warp shuffles, shared memory and one exchange through the cluster's distributed
-// shared memory, and the gradient is formed from the registers.  Rows longer
-// than a cluster's registers are read a second time (from L2, as a rule).
+// row is held on the chip by a cluster of up to eight CTAs, whose sums meet by warp
+// shuffles, shared memory and one exchange through distributed shared memory, and
+// the gradient is formed from what was read.  Two kernels:
+//   - few or short rows: a cluster per row, the row in registers, (max, sum,
+//     entropy sum) per thread.  16 rows of 16000 bf16: 8 us in a graph, of
+//     which both launches are the most part;
+//   - many long rows: clusters that stay, one CTA per SM, each row's slice copied
+//     to a ring in shared memory while the rows before it are worked on.
+//     Read and write together, of the measured copy rate: 4096 rows of 131072 bf16,
+//     a tenth masked, 327 us (93 %); 1001 rows of 100003 FP32, 30 % masked, 130 us
+//     (78 %: 144 of 152 SMs hold clusters of eight, and 39 read rows a cluster leave
+//     a tail); log-probabilities of 2048 x 131072 bf16 84 us (95 %).
+// Rows longer than the cluster's registers or shared memory are read a second time
+// (from L2, as a rule).
 // Rows may start at any alignment: a row is walked in the aligned 16-byte
 // vectors that hold it, whose two end vectors are read and written by element.
 #include <float.h>
@@ -528,6 +537,55 @@ struct Stage {
     }
 };
 
+// The rows [first, end) of cluster c of n.  A row that takes no part is written but not read, so the rows are shared out by
+// what they move (a read and a write cost 16 each, a row itself 1); a row is of the cluster that its middle falls to.
+// Against every n-th row, of 1001 rows of 100003 FP32 logits with 30 % masked (the fullest of 18 clusters has 7 % more than
+// the mean there): 135 -> 130 us.  4096 rows of 131072 bf16 with 10 % masked, which every n-th row balances by itself, pay
+// for the sums over the weights: 323 -> 327 us.  Masks in long runs would be worse for every n-th row than either.
+template <bool BF16>
+__device__ __forceinline__ void my_rows(const LossArgs &a, int64_t c, int64_t n, int64_t &first, int64_t &end)
+{
+    if (!a.weight) {
+        first = a.T * c / n, end = a.T * (c + 1) / n;
+        return;
+    }
+    __shared__ int64_t s_cost[kRingThreads / 32];
+    __shared__ unsigned int s_before[2];
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int64_t per = (a.T + kRingThreads - 1) / kRingThreads;
+    const int64_t t0 = min((int64_t)tid * per, a.T), t1 = min(t0 + per, a.T);
+    const auto cost = [&](int64_t row) { return (token<BF16>(a, row).takes ? 16 : 0) + (a.dx ? 16 : 0) + 1; };
+    int64_t mine = 0;
+    for (int64_t t = t0; t < t1; ++t) mine += cost(t);
+    int64_t to = mine;  // the costs of the warp's threads up to this one
+    for (int o = 1; o < 32; o *= 2) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, to, o);
+        if (lane >= o) to += v;
+    }
+    if (lane == 31) s_cost[warp] = to;
+    if (tid < 2) s_before[tid] = 0;
+    __syncthreads();
+    int64_t all = 0, at = to - mine;
+    for (int w = 0; w < kRingThreads / 32; ++w) {
+        if (w < warp) at += s_cost[w];
+        all += s_cost[w];
+    }
+    unsigned int before[2] = {0, 0};  // rows of the clusters before this one, and of those up to it
+    for (int64_t t = t0; t < t1; ++t) {
+        const int k = cost(t);
+        const int64_t middle = (2 * at + k) * n;
+        before[0] += middle < 2 * all * c;
+        before[1] += middle < 2 * all * (c + 1);
+        at += k;
+    }
+    for (int j = 0; j < 2; ++j) {
+        const unsigned int sum = __reduce_add_sync(0xFFFFFFFFu, before[j]);
+        if (lane == 0) atomicAdd(&s_before[j], sum);
+    }
+    __syncthreads();
+    first = s_before[0], end = s_before[1];
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(kRingThreads, 1)
     policy_ring_kernel(LossArgs a, int log_cs, int stages, int depth, uint32_t stage_bytes, unsigned int *err)
@@ -549,7 +607,6 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     __shared__ int s_stop;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int cs = 1 << log_cs, rank = blockIdx.x & (cs - 1);
-    const int64_t first = blockIdx.x >> log_cs, step = gridDim.x >> log_cs;
     if (tid == 0) {
         for (int k = 0; k < stages; ++k) {
             ptx::mbar_init(&s_full[k], 1);
@@ -573,6 +630,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         cluster_wait();
     }
     pdl_wait();
+    int64_t first, end;
+    my_rows<BF16>(a, blockIdx.x >> log_cs, gridDim.x >> log_cs, first, end);
 
     const uint64_t limit_ns = 2000000000ull;
     // true for the whole warp, or false for it
@@ -617,11 +676,11 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         int n = 0;
         Token tok = {};
         Stage at = {0, 0};
-        for (int64_t row = first; row < a.T; row += step, ++n, at.next(stages)) {
+        for (int64_t row = first; row < end; ++row, ++n, at.next(stages)) {
             const int st = at.st;
-            if (n % 32 == 0 && row + lane * step < a.T) {  // the next 32 rows' tokens, one per lane
-                tok = token<BF16>(a, row + lane * step);
-                if (tok.takes) token_inputs<BF16>(a, row + lane * step, tok);
+            if (n % 32 == 0 && row + lane < end) {  // the next 32 rows' tokens, one per lane
+                tok = token<BF16>(a, row + lane);
+                if (tok.takes) token_inputs<BF16>(a, row + lane, tok);
             }
             __syncwarp();
             const bool takes = __shfl_sync(0xFFFFFFFFu, tok.takes, n % 32) != 0;
@@ -630,16 +689,16 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             slice(r, v0, len);
             // the row's ends by element: lane 0 the first vector, lane 1 the last
             const int last = r.nvec - 1;
-            const bool end = takes && (lane == 0 ? v0 == 0 && r.full0 : lane == 1 && last >= max(v0, r.full1) && last < v0 + len && (last > 0 || !r.full0));
+            const bool edge = takes && (lane == 0 ? v0 == 0 && r.full0 : lane == 1 && last >= max(v0, r.full1) && last < v0 + len && (last > 0 || !r.full0));
             uint4 e = make_uint4(0, 0, 0, 0);
-            if (end) e = r.load_end(lane == 0 ? 0 : last);
+            if (edge) e = r.load_end(lane == 0 ? 0 : last);
             __syncwarp();
             if (n >= stages && !wait(&s_empty[st], at.parity ^ 1)) break;
             uint8_t *to = ring + st * stage_bytes;
             const int b0 = max(v0, r.full0), b1 = min(v0 + len, r.full1);
             const uint32_t bytes = takes && b1 > b0 ? (uint32_t)(b1 - b0) * 16u : 0u;
             if (lane == 0 && bytes) bulk_load(to + (b0 - v0) * 16, r.vec() + b0, bytes, &s_full[st]);
-            if (end) *reinterpret_cast<uint4 *>(to + (lane == 0 ? 0 : last - v0) * 16) = e;
+            if (edge) *reinterpret_cast<uint4 *>(to + (lane == 0 ? 0 : last - v0) * 16) = e;
             if (lane == n % 32) s_tok[n % kTokens] = tok;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive_expect_tx(&s_full[st], bytes);
@@ -654,7 +713,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         }
     } else if (warp == kRingWarps + 1) {  // sends
         int met = 0;
-        const int rows = (int)((a.T - first + step - 1) / step);
+        const int rows = (int)(end - first);
         for (int n = 0; n < rows; ++n) {
             const int buf = n % kRows;
             if (!wait(&s_part[buf], (n / kRows) & 1)) break;
@@ -677,7 +736,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             if ((lane & 7) < cs) q = from[lane & 7];
             return true;
         };
-        for (int64_t row = first; row < a.T; row += step, ++n) {
+        for (int64_t row = first; row < end; ++row, ++n) {
             const int buf = n % kRows;
             const Token &tok = s_tok[n % kTokens];
             if (!wait(&s_part[buf], (n / kRows) & 1)) break;
@@ -734,7 +793,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         }
     } else {
         int again = 0;
-        const int64_t x_step = step * a.ld * (16 / E), dx_step = step * a.ldd * (16 / E);
+        const int64_t x_step = a.ld * (16 / E), dx_step = a.ldd * (16 / E);
         const char *x_in = static_cast<const char *>(a.x) + first * a.ld * (16 / E), *x_out = x_in;
         char *dx = a.dx ? static_cast<char *>(a.dx) + first * a.ldd * (16 / E) : nullptr;
         Stage in = {0, 0}, out = {0, 0};
@@ -832,7 +891,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             return true;
         };
         bool ok = true;
-        const int rows = (int)((a.T - first + step - 1) / step);
+        const int rows = (int)(end - first);
         for (int n = 0; ok && n < rows + depth; ++n) {
             if (n < rows) ok = measure(n);
             if (ok && n >= depth) ok = finish(n - depth);
