@@ -19,9 +19,9 @@
 //   - many long rows: clusters that stay, one CTA per SM, each row's slice copied
 //     to a ring in shared memory while the rows before it are worked on.
 //     Read and write together, of the measured copy rate: 4096 rows of 131072 bf16,
-//     a tenth masked, 327 us (93 %); 1001 rows of 100003 FP32, 30 % masked, 130 us
-//     (78 %: 144 of 152 SMs hold clusters of eight, and 39 read rows a cluster leave
-//     a tail); log-probabilities of 2048 x 131072 bf16 84 us (95 %).
+//     a tenth masked, 329 us (92 %); 1001 rows of 100003 FP32, 30 % masked, 124 us
+//     (82 %: 138 of 152 SMs hold clusters of six, and 30 read rows a cluster leave
+//     a tail); log-probabilities of 2048 x 131072 bf16 85 us (94 %).
 // Rows longer than the cluster's registers or shared memory are read a second time
 // (from L2, as a rule).
 // Rows may start at any alignment: a row is walked in the aligned 16-byte
@@ -539,8 +539,8 @@ struct Stage {
 
 // The rows [first, end) of cluster c of n.  A row that takes no part is written but not read, so the rows are shared out by
 // what they move (a read and a write cost 16 each, a row itself 1); a row is of the cluster that its middle falls to.
-// Against every n-th row, of 1001 rows of 100003 FP32 logits with 30 % masked (the fullest of 18 clusters has 7 % more than
-// the mean there): 135 -> 130 us.  4096 rows of 131072 bf16 with 10 % masked, which every n-th row balances by itself, pay
+// Against every n-th row, of 1001 rows of 100003 FP32 logits with 30 % masked (the fullest of 15 clusters has some 6 % more
+// than the mean there): 135 -> 130 us.  4096 rows of 131072 bf16 with 10 % masked, which every n-th row balances by itself, pay
 // for the sums over the weights: 323 -> 327 us.  Masks in long runs would be worse for every n-th row than either.
 template <bool BF16>
 __device__ __forceinline__ void my_rows(const LossArgs &a, int64_t c, int64_t n, int64_t &first, int64_t &end)
@@ -588,7 +588,7 @@ __device__ __forceinline__ void my_rows(const LossArgs &a, int64_t c, int64_t n,
 
 template <bool BF16>
 __global__ void __launch_bounds__(kRingThreads, 1)
-    policy_ring_kernel(LossArgs a, int log_cs, int stages, int depth, uint32_t stage_bytes, unsigned int *err)
+    policy_ring_kernel(LossArgs a, int cs, int stages, int depth, uint32_t stage_bytes, unsigned int *err)
 {
     using V = Vec<BF16>;
     constexpr int E = V::E, NT = kRingWarps * 32;
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     __shared__ float2 s_factor[kRows];
     __shared__ int s_stop;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int cs = 1 << log_cs, rank = blockIdx.x & (cs - 1);
+    const int rank = blockIdx.x % cs;
     if (tid == 0) {
         for (int k = 0; k < stages; ++k) {
             ptx::mbar_init(&s_full[k], 1);
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     }
     pdl_wait();
     int64_t first, end;
-    my_rows<BF16>(a, blockIdx.x >> log_cs, gridDim.x >> log_cs, first, end);
+    my_rows<BF16>(a, blockIdx.x / cs, gridDim.x / cs, first, end);
 
     const uint64_t limit_ns = 2000000000ull;
     // true for the whole warp, or false for it
@@ -650,8 +650,10 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         }
         return __all_sync(0xFFFFFFFFu, ok);
     };
+    // x / cs for the few 10^4 vectors of a row, without a division's latency at every row (84 us against 88)
+    const uint32_t inv_cs = 0xFFFFFFFFu / (uint32_t)cs + 1;
     const auto slice = [&](const Row<BF16> &r, int &v0, int &len) {
-        const int per = (r.nvec + cs - 1) >> log_cs;
+        const int per = cs == 1 ? r.nvec : (int)__umulhi((uint32_t)(r.nvec + cs - 1), inv_cs);
         v0 = rank * per;
         len = max(0, min(per, r.nvec - v0));
     };
@@ -966,58 +968,70 @@ cudaError_t launch_nv(const LossArgs &a, int cs, int64_t nv, cudaStream_t s)
     return launch<BF16, NT, 4, false>(a, cs, s);
 }
 
-template <bool BF16>
-cudaError_t launch_ring(const LossArgs &a, int cs, int stages, size_t slice, cudaStream_t s)
+void set_cluster(cudaLaunchConfig_t &cfg, int cs)
 {
-    static const cudaError_t attr =
+    cudaLaunchAttribute &at = cfg.attrs[cfg.numAttrs++];
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)cs;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+}
+
+// Clusters of the ring's kernel that fit at once: fewer than the SMs would hold, since a cluster stays within a GPC, and
+// GPCs differ in size.
+template <bool BF16>
+cudaError_t ring_clusters(int cs, int &most)
+{
+    static const cudaError_t smem =
         cudaFuncSetAttribute(policy_ring_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
-    if (attr != cudaSuccess) return attr;
+    if (smem != cudaSuccess) return smem;
+    static std::atomic<int> fit[kMaxCluster + 1];
+    most = fit[cs].load();
+    if (most) return cudaSuccess;
+    most = num_sms();
+    if (cs > 1) {
+        cudaLaunchAttribute attr[1];
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(num_sms() / cs * cs));
+        cfg.blockDim = dim3(kRingThreads);
+        cfg.dynamicSmemBytes = kRingBytes;
+        cfg.attrs = attr;
+        set_cluster(cfg, cs);
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&most, policy_ring_kernel<BF16>, &cfg);
+        if (e != cudaSuccess) return e;
+        if (most < 1) most = 1;
+    }
+    fit[cs].store(most);
+    return cudaSuccess;
+}
+
+template <bool BF16>
+cudaError_t launch_ring(const LossArgs &a, int cs, int clusters, int stages, size_t slice, cudaStream_t s)
+{
+    cudaLaunchAttribute attrs[2];
     cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((clusters < a.T ? clusters : a.T) * cs));
     cfg.blockDim = dim3(kRingThreads);
     cfg.dynamicSmemBytes = kRingBytes;  // whatever the slices take: one CTA per SM
     cfg.stream = s;
-    cudaLaunchAttribute attrs[2];
-    int n = 0;
-    if (cs > 1) {
-        attrs[n].id = cudaLaunchAttributeClusterDimension;
-        attrs[n].val.clusterDim.x = (unsigned)cs;
-        attrs[n].val.clusterDim.y = attrs[n].val.clusterDim.z = 1;
-        ++n;
-    }
     cfg.attrs = attrs;
-    cfg.numAttrs = n;
-    // clusters that fit at once (fewer than the SMs would hold: a cluster stays within a GPC)
-    static std::atomic<int> fit[4];
-    const int log_cs = cs == 1 ? 0 : cs == 2 ? 1 : cs == 4 ? 2 : 3;
-    std::atomic<int> &known = fit[log_cs];
-    int64_t clusters = known.load();
-    if (clusters == 0) {
-        clusters = num_sms();
-        if (cs > 1) {
-            int most = 0;
-            cfg.gridDim = dim3((unsigned)(clusters / cs * cs));
-            const cudaError_t e = cudaOccupancyMaxActiveClusters(&most, policy_ring_kernel<BF16>, &cfg);
-            if (e != cudaSuccess) return e;
-            clusters = most > 0 ? most : 1;
-        }
-        known.store((int)clusters);
-    }
-    if (clusters > a.T) clusters = a.T;
-    cfg.gridDim = dim3((unsigned)(clusters * cs));
+    if (cs > 1) set_cluster(cfg, cs);
     if (g_chain.load() != 0) {
-        attrs[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attrs[n].val.programmaticStreamSerializationAllowed = 1;
-        ++n;
+        attrs[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attrs[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
     }
-    cfg.numAttrs = n;
     // without a gradient a slice is free after its statistics; with one, half the stages are left to the copies
     const int depth = !a.dx ? kRows - 1 : stages >= 5 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, policy_ring_kernel<BF16>, a, log_cs, stages, depth, (uint32_t)slice, error_word());
+    return cudaLaunchKernelEx(&cfg, policy_ring_kernel<BF16>, a, cs, stages, depth, (uint32_t)slice, error_word());
 }
 
+// Bytes of a stage: a CTA's slice of a row, to 128.
+size_t ring_slice(int64_t nvec, int cs) { return ((size_t)((nvec + cs - 1) / cs) * 16 + 127) & ~size_t(127); }
+
 // Which kernel, and its cluster.  The ring: rows of 16 KB and more, when there
-// are more of them than clusters that fit at once; the smallest cluster whose
-// slices leave three stages, else two.  Otherwise one cluster per row: 128
+// are more of them than clusters that fit at once; of the clusters whose slices
+// leave three stages, else two, the smallest, unless a larger one puts CTAs on a
+// sixteenth more SMs (1001 rows of 100003 FP32: 23 clusters of six 123 us, 15 of
+// eight, which leave a fourth stage but 32 SMs idle, 130 us).  Otherwise one cluster per row: 128
 // threads where eight vectors each hold a row, else 256; the smallest cluster
 // whose registers hold a row (eight vectors a thread), then larger ones while
 // the launch would leave SMs idle and every CTA keeps a vector for half its
@@ -1029,13 +1043,20 @@ cudaError_t launch_any(const LossArgs &a, cudaStream_t s)
     const bool even = aligned16(a.x) && a.ld % E == 0;  // every row starts with a vector
     const int64_t nvec = (a.V + (even ? 0 : E - 1) + E - 1) / E;
     if (nvec >= 1024) {
-        for (int least = 3; least >= 2; --least)
-            for (int cs = 1; cs <= kMaxCluster; cs *= 2) {
-                const size_t slice = ((size_t)((nvec + cs - 1) / cs) * 16 + 127) & ~size_t(127);
-                const int64_t stages = kRingBytes / slice;
-                if (stages >= least && a.T * cs > num_sms())
-                    return launch_ring<BF16>(a, cs, stages > kMaxStages ? kMaxStages : (int)stages, slice, s);
+        for (int least = 3; least >= 2; --least) {
+            int best = 0, best_clusters = 0;
+            for (int cs = 1; cs <= kMaxCluster; ++cs) {
+                int clusters = 0;
+                if ((int64_t)(kRingBytes / ring_slice(nvec, cs)) < least || a.T * cs <= num_sms()) continue;
+                const cudaError_t e = ring_clusters<BF16>(cs, clusters);
+                if (e != cudaSuccess) return e;
+                if (16 * clusters * cs > 17 * best_clusters * best) best = cs, best_clusters = clusters;
             }
+            if (!best) continue;
+            const size_t slice = ring_slice(nvec, best);
+            const int64_t stages = kRingBytes / slice;
+            return launch_ring<BF16>(a, best, best_clusters, stages > kMaxStages ? kMaxStages : (int)stages, slice, s);
+        }
     }
     const int nt = nvec <= 128 * 8 ? 128 : 256;
     int cs = 1;
