@@ -19,9 +19,9 @@
 //   - many long rows: clusters that stay, one CTA per SM, each row's slice copied
 //     to a ring in shared memory while the rows before it are worked on.
 //     Read and write together, of the measured copy rate: 4096 rows of 131072 bf16,
-//     a tenth masked, 329 us (92 %); 1001 rows of 100003 FP32, 30 % masked, 124 us
+//     a tenth masked, 330 us (92 %); 1001 rows of 100003 FP32, 30 % masked, 123 us
 //     (82 %: 138 of 152 SMs hold clusters of six, and 30 read rows a cluster leave
-//     a tail); log-probabilities of 2048 x 131072 bf16 85 us (94 %).
+//     a tail); log-probabilities of 2048 x 131072 bf16 86 us (93 %).
 // Rows longer than the cluster's registers or shared memory are read a second time
 // (from L2, as a rule).
 // Rows may start at any alignment: a row is walked in the aligned 16-byte
@@ -111,6 +111,14 @@ struct Vec<true> {
         };
         return make_uint4(up(v.x), up(v.y), up(v.z), up(v.w));
     }
+    static __device__ __forceinline__ uint4 without(const uint4 &v, int e)  // element e -inf
+    {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j == e / 2) w[j] = e % 2 ? (w[j] & 0xFFFFu) | 0xFF800000u : (w[j] & 0xFFFF0000u) | 0xFF80u;
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
     static __device__ __forceinline__ float get(const void *p, int64_t i) { return bf16f(static_cast<const __nv_bfloat16 *>(p)[i]); }
     static __device__ __forceinline__ void put(void *p, int64_t i, float v) { static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v); }
 };
@@ -138,6 +146,14 @@ struct Vec<false> {
             return m;
         };
         return make_uint4(up(v.x), up(v.y), up(v.z), up(v.w));
+    }
+    static __device__ __forceinline__ uint4 without(const uint4 &v, int e)
+    {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j == e) w[j] = 0xFF800000u;
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
     static __device__ __forceinline__ float get(const void *p, int64_t i) { return static_cast<const float *>(p)[i]; }
     static __device__ __forceinline__ void put(void *p, int64_t i, float v) { static_cast<float *>(p)[i] = v; }
@@ -252,18 +268,42 @@ __device__ __forceinline__ void token_inputs(const LossArgs &a, int64_t row, Tok
 }
 
 // From the row's statistics: its outputs (where `write`), the factor of its
-// gradient and 1 - p of the chosen token.  `plain`: see below.
-__device__ __forceinline__ float2 factor(const LossArgs &a, int64_t row, const Token &t, const Stat &all, bool plain, bool write)
+// gradient, 1 - p of the chosen token, and the gradient's weight of e^((x - m) c).
+// The statistics leave the chosen token out: with r the others' sum in units of
+// its e^x, log p = -log(1 + r), which a sum that holds the 1 would round to
+// 2^-24 absolutely, and tokens next to certain have r far below 1.  (The second
+// attempt, `plain`, see below, takes them all.)
+__device__ __forceinline__ float4 factor(const LossArgs &a, int64_t row, const Token &t, const Stat &all, bool plain, bool write)
 {
-    const bool empty = all.z == 0.0f;  // every logit -inf: no distribution, no part in the loss
-    const float lz = logf(all.z);
-    const float y_id = plain ? (t.x_id - all.m) * a.c : fmaf(t.x_id, a.c, -all.m * a.c);
-    const float logp = empty ? -INFINITY : y_id * kLn2 - lz;
+    const bool empty = plain && all.z == 0.0f;  // every logit -inf: no distribution, no part in the loss
+    float logp, H, z;
+    if (plain) {
+        const float lz = logf(all.z);
+        z = all.z;
+        logp = empty ? -INFINITY : (t.x_id - all.m) * a.c * kLn2 - lz;
+        H = empty ? 0.0f : lz - all.s / z * kLn2;
+    } else {
+        // +inf gives no distribution either: NaN, as NaN does
+        const float y = t.x_id <= FLT_MAX ? fmaf(t.x_id, a.c, -all.m * a.c) : NAN;
+        if (y >= -1.0f) {
+            const float f = ex2(-y), r = all.z * f, lz = log1pf(r);
+            z = all.z + ex2(y);
+            logp = 0.0f - lz;
+            H = lz - f * fmaf(-y, all.z, all.s) / (1.0f + r) * kLn2;
+        } else {
+            const float e = ex2(y);
+            z = all.z + e;
+            const float lz = logf(z);
+            logp = y * kLn2 - lz;
+            H = lz - fmaf(e, fmaxf(y, -1e4f), all.s) / z * kLn2;
+        }
+    }
     float dlogp = 0.0f;
     if (write) {
         a.logp[row] = logp;
-        if (a.entropy) a.entropy[row] = empty ? 0.0f : lz - all.s / all.z * kLn2;
+        if (a.entropy) a.entropy[row] = H;
     }
+    if (!a.dx && !a.old_logp) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (a.old_logp) {
         const float A = t.adv, rho = expf(logp - t.old_logp);
         const float d = a.ref_logp ? t.ref - logp : 0.0f, em = expm1f(d);
@@ -276,7 +316,8 @@ __device__ __forceinline__ float2 factor(const LossArgs &a, int64_t row, const T
             a.terms[3 * row + 2] = empty || keeps ? 0.0f : t.w;
         }
     }
-    return make_float2(dlogp * a.gscale, empty ? 0.0f : -expm1f(logp));
+    const float coef = dlogp * a.gscale;
+    return make_float4(coef, empty ? 0.0f : -expm1f(logp), empty ? 0.0f : -coef / z, 0.0f);
 }
 __device__ __forceinline__ void no_part(const LossArgs &a, int64_t row)
 {
@@ -384,7 +425,7 @@ __global__ void __launch_bounds__(NT, (NV > 4 ? 512 : 1024) / NT) policy_kernel(
     static_assert(NW <= kMaxCluster, "the warps' statistics are joined in eight lanes");
     __shared__ float4 s_warp[NW];
     __shared__ alignas(16) float4 s_cta[2][kMaxCluster];
-    __shared__ float2 s_factor;
+    __shared__ float4 s_factor;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int64_t row = blockIdx.x / cs;
     const int rank = blockIdx.x % cs;
@@ -406,6 +447,8 @@ __global__ void __launch_bounds__(NT, (NV > 4 ? 512 : 1024) / NT) policy_kernel(
     }
     if (tid == 0) token_inputs<BF16>(a, row, tok);  // arrives beside the logits
 
+    const int own = (tok.id + r.off) / E;  // the vector that holds the chosen token
+    const bool owner = own >= v0 && own < v1 && (own - v0) % NT == tid;
     const uint4 nothing = make_uint4(V::kFill, V::kFill, V::kFill, V::kFill);
     uint4 hold[NV];
     Stat st = {-FLT_MAX, 0.0f, 0.0f}, all;
@@ -423,6 +466,11 @@ __global__ void __launch_bounds__(NT, (NV > 4 ? 512 : 1024) / NT) policy_kernel(
                 if (i < v1 && !r.inside(i)) hold[k] = r.load_end(i);
             }
         }
+        if (owner) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                if (v0 + k * NT + tid == own) hold[k] = V::without(hold[k], (tok.id + r.off) % E);
+        }
         add_block<BF16, NV>(st, hold, a.c);
     } else {
         for (int i = v0 + tid; i < v1; i += NV * NT) {
@@ -434,6 +482,11 @@ __global__ void __launch_bounds__(NT, (NV > 4 ? 512 : 1024) / NT) policy_kernel(
 #pragma unroll
             for (int k = 0; k < NV; ++k)
                 if (i + k * NT < v1 && !r.inside(i + k * NT)) hold[k] = r.load_end(i + k * NT);
+            if (owner) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    if (i + k * NT == own) hold[k] = V::without(hold[k], (tok.id + r.off) % E);
+            }
             add_block<BF16, NV>(st, hold, a.c);
         }
     }
@@ -475,8 +528,7 @@ __global__ void __launch_bounds__(NT, (NV > 4 ? 512 : 1024) / NT) policy_kernel(
     if (tid == 0) s_factor = factor(a, row, tok, all, plain, rank == 0);
     if (!r.dx) return;
     __syncthreads();
-    const float coef = s_factor.x, k = all.z == 0.0f ? 0.0f : -coef / all.z;
-    const int own = (tok.id + r.off) / E;  // the vector that holds the chosen token
+    const float coef = s_factor.x, k = s_factor.z;
     if (HOLD && !plain) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -486,12 +538,12 @@ __global__ void __launch_bounds__(NT, (NV > 4 ? 512 : 1024) / NT) policy_kernel(
     } else {
         for (int i = v0 + tid; i < v1; i += NT) grad<BF16>(r, i, r.inside(i) ? xv[i] : r.load_end(i), all, a.c, k, plain);
     }
-    if (own >= v0 && own < v1 && (own - v0) % NT == tid) V::put(r.dx, tok.id, coef * s_factor.y);
+    if (owner) V::put(r.dx, tok.id, coef * s_factor.y);
 }
 
 // ------------------------------------------------------------------ many long rows: a ring of row slices in shared memory
-// The statistics are taken relative to the chosen token's logit, which the copies bring along: no maximum, and sums that
-// only add.  Where they overflow (a token some 88 nats below the maximum) or are not finite, the row is taken again with
+// The others' statistics are taken relative to the chosen token's logit, which the copies bring along: no maximum, and sums
+// that only add.  Where they overflow (a token some 88 nats below the maximum) or are not finite, the row is taken again with
 // its maximum.
 // Persistent clusters, one CTA per SM; a CTA's slice of a row is one bulk copy
 // into a stage of its ring.  Three roles run apart, joined by barriers only:
@@ -603,7 +655,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     __shared__ bool s_plain[kRows];
     __shared__ Token s_tok[kTokens];
     __shared__ Stat s_all[kRows];
-    __shared__ float2 s_factor[kRows];
+    __shared__ float4 s_factor[kRows];
     __shared__ int s_stop;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int rank = blockIdx.x % cs;
@@ -699,6 +751,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             uint8_t *to = ring + st * stage_bytes;
             const int b0 = max(v0, r.full0), b1 = min(v0 + len, r.full1);
             const uint32_t bytes = takes && b1 > b0 ? (uint32_t)(b1 - b0) * 16u : 0u;
+            ptx::fence_proxy_async_smem();  // what was stored into the stage comes before the copy
             if (lane == 0 && bytes) bulk_load(to + (b0 - v0) * 16, r.vec() + b0, bytes, &s_full[st]);
             if (edge) *reinterpret_cast<uint4 *>(to + (lane == 0 ? 0 : last - v0) * 16) = e;
             if (lane == n % 32) s_tok[n % kTokens] = tok;
@@ -762,7 +815,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                     z.y += __shfl_xor_sync(0xFFFFFFFFu, z.y, o);
                 }
             }
-            Stat t = {tok.x_id, z.x, z.y};
+            Stat t = {tok.x_id, z.x, z.y};  // of the others
             ++met;
             const bool plain = far_off(t) || !isfinite(t.z) || !isfinite(t.s);
             if (lane == 0) {
@@ -808,8 +861,11 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                 const Row<BF16> r(a, x_in, nullptr);
                 int v0, len;
                 slice(r, v0, len);
-                const uint4 *sl = reinterpret_cast<const uint4 *>(ring + in.st * stage_bytes);
+                uint4 *sl = reinterpret_cast<uint4 *>(ring + in.st * stage_bytes);
                 const float shift = -tok.x_id * a.c;
+                // the chosen token leaves the sums, and the slice (its gradient is written by itself)
+                const uint32_t at = (uint32_t)(tok.id + r.off - v0 * E);
+                if (at / E % NT == tid && at < (uint32_t)(len * E)) V::put(sl, at, -INFINITY);
                 int i = tid;
                 for (; i + 3 * NT < len; i += 4 * NT) {
                     const uint4 q[4] = {sl[i], sl[i + NT], sl[i + 2 * NT], sl[i + 3 * NT]};
@@ -857,7 +913,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
                     if (dx) {
                         const uint4 *sl = reinterpret_cast<const uint4 *>(ring + out.st * stage_bytes);
                         const Stat all = s_all[buf];
-                        const float coef = s_factor[buf].x, k = all.z == 0.0f ? 0.0f : -coef / all.z;
+                        const float coef = s_factor[buf].x, k = s_factor[buf].z;
                         int i = tid;
                         if (!plain && r.dx_vec) {  // whole vectors, but for the row's ends
                             const int in0 = max(r.full0 - v0, 0), in1 = min(r.full1 - v0, len);

@@ -8,6 +8,13 @@
 // query rows share its tiles.  Segments are cut along the keys into chunks that
 // run side by side; each leaves (o, m, l) in the workspace and a second kernel
 // joins a row's parts.
+//
+// Bound by HBM where the suffixes are most of the keys (rows16_kernel: each is read
+// by one CTA, for its up to 16 rows), by the tensor cores and shared memory where
+// many rows share a prefix (the tcgen05 kernel), by latency below some 10 us.
+// 64 sequences of up to 4096 own tokens, 40 / 8 heads, D = 128: 99 us, 82 % of
+// the measured copy rate.  Eight of a group of 512 + 1024 keys 11 us; one
+// sequence over 512 keys 9 us a call, 6 us in a graph.
 #include <float.h>
 #include <math.h>
 

@@ -12,15 +12,22 @@
 //     P = 2^(S c - m)  read from TMEM, written back as bf16 over S
 //     O += P V      P from TMEM, V as it lies in the cache (MN-major), O in TMEM
 // There are two S of 64 keys per half, so that the next one is there when a
-// softmax ends; with one S of 128 keys a softmax waited for P V and Q K^T each
-// time (2.0 us per step against CHECK_US).
-// m is raised only when a row's maximum outgrows it by 2^8 (the weights stay
-// below 2^8 and are normalised in the end all the same), so O is rescaled rarely.
-// S and P share columns: the Q K^T that overwrites a P is issued once its P V has
-// completed.
+// softmax ends.  m is raised only when a row's maximum outgrows it by 2^8 (the
+// weights stay below 2^8 and are normalised in the end all the same), so O is
+// rescaled rarely.  S and P share columns: the Q K^T that overwrites a P is issued
+// once its P V has completed.
 // Shared memory (D = 128): Q 64 KB, five K and five V tiles of 64 keys, 16 KB each.
-// A tile's load has to hide behind the four before it: with two tiles of 128 keys
-// a step took 1.9 us, the latency of its loads.
+// A tile's load has to hide behind the four before it.
+// What bounds it: a step (two row tiles, 128 keys: 17 MFLOP) takes 1.9 us, 69 % of
+// the measured bf16 rate.  For 64 keys of a half Q K^T takes 389 clocks (its 6 KB of operands per
+// instruction are all of shared memory's rate) and P V 260, measured alone; both
+// halves and the tiles' arrival in shared memory come to some 0.78 of the 0.95 us.
+// One S with two P instead, so that Q K^T waits for no P V, took as long.  A unit's
+// rows cost about 6 us besides (loads of Q, first S, stores of O).
+// 28 query heads of 64 sequences over a prefix of 16384 keys: 12 steps on each of 88
+// CTAs, 36 us; with the suffixes, on the other SMs meanwhile, and the join 46 us.
+// 129 tokens of eight sequences, 16 heads, over 4001 keys and their own: 18 steps a
+// CTA, its starts among them, 54 us, and 14 for the join of 2 to 5 parts a row.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -245,3 +245,29 @@ def test_empty_repeat_and_other_stream():
     with torch.cuda.stream(s):
         got = check(x, ids, old, ref, adv, w)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,V", [(1, 501), (5, 9000), (3, 300007), (400, 40001)])
+@pytest.mark.parametrize("gap", [9.0, 24.0, 60.0])
+def test_nearly_certain_tokens_keep_their_digits(dtype, T, V, gap):
+    """log p = -log(1 + r) and the entropy of tokens with r, the others' sum over the token's own e^x, far below 1: errors
+    relative to the values.  r: s = (80 + V / 4096) u + 2^-22 as above, 2^-22 for the change of its unit, and 3 u |y| of
+    exponents y, taken twice; twice that for the entropy, whose two terms have one sign; log1p and the products: 16 u."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = (torch.randn(T, V, generator=g, device="cuda") * 2).to(dtype)
+    ids, at = torch.randint(V, (T,), generator=g, device="cuda"), torch.arange(T, device="cuda")
+    x[at, ids] = math.log(V) + 2.0 + gap
+    nan = lambda: torch.full((T,), NAN, device="cuda")  # noqa: E731
+    logp, ent = q.qerl_token_logp(x, ids, logp=nan(), entropy=nan())
+    d = x.double() - x.double()[at, ids][:, None]
+    d[at, ids] = -INF
+    e = d.exp()
+    r = e.sum(-1)
+    want = -torch.log1p(r)
+    H = torch.log1p(r) - (e * d.clamp_min(-1e4)).sum(-1) / (1 + r)
+    ymax = float(-d.clamp_min(-1e4).masked_fill(d == -INF, 0.0).min()) / math.log(2)
+    rel = (80 + V / 4096) * U + 2.0 ** -21 + 6 * U * ymax
+    assert bool(((logp.double() - want).abs() <= (rel + 16 * U) * want.abs()).all())
+    assert bool(((ent.double() - H).abs() <= (2 * rel + 16 * U) * H).all())
+    assert q.get_error() == 0
