@@ -6,9 +6,13 @@
 //
 // Elementwise and bound by HBM: with a bf16 parameter beside its FP32 master an
 // element moves 30 bytes with FP32 states and 18 with 8-bit ones (plus 8/256 of
-// scales), for some 90 instructions.  A warp owns one block of 256 elements,
+// scales), for some 100 instructions.  A warp owns one block of 256 elements,
 // eight per lane, so every access is a 16-byte vector and a block's largest
-// magnitude is one warp reduction; a CTA takes 32 blocks of one tensor.
+// magnitude is one warp reduction; a CTA takes 32 blocks of one tensor.  On 80.7 M
+// elements, the norm's read of the FP32 gradients (48 us at the copy rate) among
+// it: FP32 states 413 us, 99 % of the measured copy rate; 8-bit states 439 us with
+// the 80 us that handing both out in bf16 takes, 72 %: their step issues in 71 % of
+// all slots, 100 instructions an element, most of them for the codes.
 //
 // 8-bit states, per block of 256 with an FP32 scale: m as sign, 3 exponent and 4
 // mantissa bits; sqrt(v) (half of v's exponent range) as 3 exponent and 5
