@@ -44,7 +44,8 @@ struct LossArgs {
     const void *ids;
     int ids64;
     const float *old_logp, *ref_logp, *adv, *weight;  // old_logp NULL: log-probabilities only
-    float c;                                          // log2(e) / tau
+    float c, dc;                                      // log2(e) / tau, and ln 2 times what its rounding left relative to it
+    float it, it_rest;                                // 1 / tau
     float lo, hi, beta, gscale;                       // 1 - clip_low, 1 + clip_high, beta, grad_scale / tau
     float *logp, *entropy, *terms;                    // terms [T, 3]: w policy, w kl, w clipped
     void *dx;
@@ -272,7 +273,9 @@ __device__ __forceinline__ void token_inputs(const LossArgs &a, int64_t row, Tok
 // The statistics leave the chosen token out: with r the others' sum in units of
 // its e^x, log p = -log(1 + r), which a sum that holds the 1 would round to
 // 2^-24 absolutely, and tokens next to certain have r far below 1.  (The second
-// attempt, `plain`, see below, takes them all.)
+// attempt, `plain`, see below, takes them all.)  With mean = sum p y over the row's
+// exponents, c's rounding moves ln z by its relative size times mean ln 2, up to
+// 1e-6 at exponents of 20: taken back here.
 __device__ __forceinline__ float4 factor(const LossArgs &a, int64_t row, const Token &t, const Stat &all, bool plain, bool write)
 {
     const bool empty = plain && all.z == 0.0f;  // every logit -inf: no distribution, no part in the loss
@@ -285,17 +288,24 @@ __device__ __forceinline__ float4 factor(const LossArgs &a, int64_t row, const T
     } else {
         // +inf gives no distribution either: NaN, as NaN does
         const float y = t.x_id <= FLT_MAX ? fmaf(t.x_id, a.c, -all.m * a.c) : NAN;
-        if (y >= -1.0f) {
-            const float f = ex2(-y), r = all.z * f, lz = log1pf(r);
+        const float f = y >= -1.0f ? ex2(-y) : INFINITY, r = all.z * f;
+        if (r < 0.5f) {
+            const float lz = log1pf(r);
             z = all.z + ex2(y);
-            logp = 0.0f - lz;
-            H = lz - f * fmaf(-y, all.z, all.s) / (1.0f + r) * kLn2;
+            const float mean = f * fmaf(-y, all.z, all.s) / (1.0f + r);
+            logp = 0.0f - fmaf(a.dc, mean, lz);
+            H = lz - mean * kLn2;
         } else {
             const float e = ex2(y);
             z = all.z + e;
             const float lz = logf(z);
-            logp = y * kLn2 - lz;
-            H = lz - fmaf(e, fmaxf(y, -1e4f), all.s) / z * kLn2;
+            const float mean = fmaf(e, fmaxf(y, -1e4f), all.s) / z;
+            // (x - m) / tau in nats with its rest, and ln z without what rounding m c moved the sums' unit by: y ln 2 would be
+            // off by half a last place of y
+            const float d = t.x_id - all.m, b = d - t.x_id, rest = (t.x_id - (d - b)) - (all.m + b);
+            const float unit = fmaf(all.m, a.c, -all.m * a.c);
+            logp = y == -INFINITY ? y : fmaf(d, a.it, fmaf(d, a.it_rest, fmaf(rest, a.it, fmaf(unit, kLn2, fmaf(-a.dc, mean, -lz)))));
+            H = lz - mean * kLn2;
         }
     }
     float dlogp = 0.0f;
@@ -1124,6 +1134,15 @@ cudaError_t launch_any(const LossArgs &a, cudaStream_t s)
 
 bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+void set_scale(LossArgs &a, double tau)
+{
+    const double c = 1.4426950408889634 / tau;
+    a.c = (float)c;
+    a.dc = (float)((c - (double)a.c) / (double)a.c * 0.69314718055994531);
+    a.it = (float)(1.0 / tau);
+    a.it_rest = (float)(1.0 / tau - (double)a.it);
+}
+
 // Checks shared by both entry points, for T >= 1.
 qerl_status check(const void *logits, int dtype, int64_t T, int64_t V, int64_t ld, const void *ids, int ids_bits, const float *logp)
 {
@@ -1153,7 +1172,7 @@ extern "C" qerl_status qerl_token_logp(const void *logits, int dtype, int64_t T,
     QERL_TRY(check_device());
     LossArgs a = {};
     a.x = logits, a.ld = ld, a.T = T, a.V = V, a.ids = ids, a.ids64 = ids_bits == 64, a.weight = weight;
-    a.c = (float)(1.4426950408889634 / (double)temperature);
+    set_scale(a, temperature);
     a.logp = logp, a.entropy = entropy;
     return launched(dtype == QERL_DTYPE_BF16 ? launch_any<true>(a, as_cuda(stream)) : launch_any<false>(a, as_cuda(stream)));
 }
@@ -1190,7 +1209,7 @@ extern "C" qerl_status qerl_policy_loss(const void *logits, int dtype, int64_t T
     LossArgs a = {};
     a.x = logits, a.ld = ld, a.T = T, a.V = V, a.ids = ids, a.ids64 = ids_bits == 64;
     a.old_logp = old_logp, a.ref_logp = ref_logp, a.adv = adv, a.weight = weight;
-    a.c = (float)(1.4426950408889634 / (double)opts->temperature);
+    set_scale(a, opts->temperature);
     a.lo = 1.0f - opts->clip_low, a.hi = 1.0f + opts->clip_high, a.beta = opts->beta;
     a.gscale = opts->grad_scale / opts->temperature;
     a.logp = logp, a.entropy = entropy, a.terms = static_cast<float *>(ws), a.dx = dlogits, a.ldd = ldd;
