@@ -553,8 +553,9 @@ __global__ void __launch_bounds__(NT, (NV > 4 ? 512 : 1024) / NT) policy_kernel(
 
 // ------------------------------------------------------------------ many long rows: a ring of row slices in shared memory
 // The others' statistics are taken relative to the chosen token's logit, which the copies bring along: no maximum, and sums
-// that only add.  Where they overflow (a token some 88 nats below the maximum) or are not finite, the row is taken again with
-// its maximum.
+// that only add.  Where their sum reaches kManyTimes (a token some 33 nats below the maximum) or is not finite, the row is
+// taken again with its maximum: beyond, the exponents' own rounding grows, and the gradient's factor -coef / z would lose its
+// digits among FP32's subnormals (from 75 nats on, at weights that a loss has).
 // Persistent clusters, one CTA per SM; a CTA's slice of a row is one bulk copy
 // into a stage of its ring.  Three roles run apart, joined by barriers only:
 //   - sixteen warps compute: the statistics of row n + depth, then the gradient of
@@ -566,6 +567,7 @@ __global__ void __launch_bounds__(NT, (NV > 4 ? 512 : 1024) / NT) policy_kernel(
 // Every wait is bounded: past two seconds the error is latched and the CTA winds up.
 constexpr int kRingWarps = 16, kRingThreads = (kRingWarps + 3) * 32, kMaxStages = 6;
 constexpr size_t kRingBytes = 204 << 10;
+constexpr float kManyTimes = 281474976710656.0f;  // 2^48
 // Rows between a row's statistics and its gradient: at most kRows - 1.  Rows whose tokens are in flight: those, the
 // stages that the copies may run ahead, and one.
 constexpr int kRows = 4, kTokens = 16;
@@ -827,7 +829,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             }
             Stat t = {tok.x_id, z.x, z.y};  // of the others
             ++met;
-            const bool plain = far_off(t) || !isfinite(t.z) || !isfinite(t.s);
+            const bool plain = far_off(t) || !(t.z < kManyTimes) || !isfinite(t.s);
             if (lane == 0) {
                 s_all[buf] = t;
                 s_plain[buf] = plain;

@@ -271,3 +271,21 @@ def test_nearly_certain_tokens_keep_their_digits(dtype, T, V, gap):
     assert bool(((logp.double() - want).abs() <= (rel + 16 * U) * want.abs()).all())
     assert bool(((ent.double() - H).abs() <= (2 * rel + 16 * U) * H).all())
     assert q.get_error() == 0
+
+
+# rows that the ring's kernel takes, and a shape for one cluster per row
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,V", [(160, 40001), (8, 9000)])
+@pytest.mark.parametrize("gap", [30.0, 45.0, 70.0, 80.0, 83.0, 90.0])
+def test_gradient_of_improbable_tokens(dtype, T, V, gap):
+    """A chosen token far below the row's maximum, at weights from 1 down to 1e-9: the likely tokens' gradient keeps its
+    digits (the tolerances are relative to the loss term's amplitude)."""
+    x, ids, _, _, adv, _ = make(T, V, dtype, 13, std=1.0)
+    g = torch.Generator(device="cuda").manual_seed(V)
+    at = torch.arange(T, device="cuda")
+    for k in range(3):  # the likely tokens
+        x[at, (ids + 17 + 5000 * k) % V] = gap - 10.0 + k
+    x[at, ids] = -10.0
+    lp = torch.log_softmax(x.double(), -1)[at, ids]
+    w = 10.0 ** (-9.0 * torch.rand(T, generator=g, device="cuda"))
+    check(x, ids, (lp - 0.05).float(), (lp + 0.1).float(), adv.sign() * (adv.abs() + 0.5), w)
