@@ -317,13 +317,14 @@ __device__ __forceinline__ float4 factor(const LossArgs &a, int64_t row, const T
     if (a.old_logp) {
         const float A = t.adv, rho = expf(logp - t.old_logp);
         const float d = a.ref_logp ? t.ref - logp : 0.0f, em = expm1f(d);
-        const bool keeps = A >= 0.0f ? rho <= a.hi : rho >= a.lo;
-        const float policy = -fminf(rho * A, fminf(fmaxf(rho, a.lo), a.hi) * A);
-        if (!empty) dlogp = t.w * ((a.beta != 0.0f ? -a.beta * em : 0.0f) - (keeps ? rho * A : 0.0f));
+        // a NaN ratio or advantage is not clipped: it reaches the loss and the gradient
+        const bool cut = A >= 0.0f ? rho > a.hi : A < 0.0f && rho < a.lo;
+        const float policy = -((cut ? (A >= 0.0f ? a.hi : a.lo) : rho) * A);
+        if (!empty) dlogp = t.w * ((a.beta != 0.0f ? -a.beta * em : 0.0f) - (cut ? 0.0f : rho * A));
         if (write) {
             a.terms[3 * row] = empty ? 0.0f : t.w * policy;
             a.terms[3 * row + 1] = empty ? 0.0f : t.w * (em - d);
-            a.terms[3 * row + 2] = empty || keeps ? 0.0f : t.w;
+            a.terms[3 * row + 2] = !empty && cut ? t.w : 0.0f;
         }
     }
     const float coef = dlogp * a.gscale;

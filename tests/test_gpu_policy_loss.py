@@ -289,3 +289,28 @@ def test_gradient_of_improbable_tokens(dtype, T, V, gap):
     lp = torch.log_softmax(x.double(), -1)[at, ids]
     w = 10.0 ** (-9.0 * torch.rand(T, generator=g, device="cuda"))
     check(x, ids, (lp - 0.05).float(), (lp + 0.1).float(), adv.sign() * (adv.abs() + 0.5), w)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,V", [(8, 5000), (160, 40001)])
+def test_nan_shows_without_the_kl_term(dtype, T, V):
+    """beta = 0 and no reference: a NaN logit, an infinite one, a NaN old log-probability and a NaN advantage reach the loss
+    and their own rows' gradient, and no other row."""
+    x, ids, old, _, adv, w = make(T, V, dtype, 14, masked=0.0)
+    adv = adv.sign() * (adv.abs() + 0.1)
+    clean = q.qerl_policy_loss(x, ids, old, adv, w)
+    assert bool(torch.isfinite(clean[3]).all()) and bool(torch.isfinite(clean[0]).all())
+    for row, name in ((1, "logit"), (3, "inf"), (4, "old"), (6, "adv")):
+        y, o, a = x.clone(), old.clone(), adv.clone()
+        if name == "logit":
+            y[row, 77] = NAN
+        elif name == "inf":
+            y[row, 78] = INF
+        else:
+            (o if name == "old" else a)[row] = NAN
+        sums, lp, ent, dx = q.qerl_policy_loss(y, ids, o, a, w)
+        rest = torch.arange(T, device="cuda") != row
+        assert bool(torch.isnan(sums[:2]).all()), name
+        assert bool(torch.isnan(dx[row]).any()), name
+        assert bool(torch.isnan(lp[row])) == (name in ("logit", "inf")), name
+        assert torch.equal(dx[rest], clean[3][rest]) and torch.equal(lp[rest], clean[1][rest]), name
