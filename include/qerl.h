@@ -534,7 +534,7 @@ qerl_status qerl_prefix_attention(const qerl_prefix_attn_dims *dims, const void 
  * A row takes no part where its weight is 0 or its id lies outside [0, V): its
  * logits are not read and its results are 0.  A row whose logits are all -inf
  * has logp -inf and entropy 0.  Inf or NaN in a row that takes part shows in its
- * results.  temperature finite and > 0.
+ * results.  temperature in (1e-30, 1e30].
  */
 qerl_status qerl_token_logp(const void *logits, int dtype, int64_t T, int64_t V, int64_t ld, const void *ids, int ids_bits,
                             const float *weight, float temperature, float *logp, float *entropy, qerl_stream_t stream);
@@ -562,7 +562,7 @@ qerl_status qerl_token_logp(const void *logits, int dtype, int64_t T, int64_t V,
 typedef struct {
     float clip_low, clip_high; /* in [0, 1] and >= 0 */
     float beta;                /* KL weight, >= 0 */
-    float temperature;         /* finite, > 0 */
+    float temperature;         /* in (1e-30, 1e30] */
     float grad_scale;          /* factor of dlogits, e.g. of a scaled loss */
 } qerl_policy_opts;
 qerl_status qerl_policy_loss(const void *logits, int dtype, int64_t T, int64_t V, int64_t ld, const void *ids, int ids_bits,

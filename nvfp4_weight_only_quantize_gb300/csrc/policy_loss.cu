@@ -46,6 +46,7 @@ struct LossArgs {
     const float *old_logp, *ref_logp, *adv, *weight;  // old_logp NULL: log-probabilities only
     float c, dc;                                      // log2(e) / tau, and ln 2 times what its rounding left relative to it
     float it, it_rest;                                // 1 / tau
+    int far_tau;                                      // every row is taken by its second attempt
     float lo, hi, beta, gscale;                       // 1 - clip_low, 1 + clip_high, beta, grad_scale / tau
     float *logp, *entropy, *terms;                    // terms [T, 3]: w policy, w kl, w clipped
     void *dx;
@@ -61,7 +62,9 @@ __device__ __forceinline__ float ex2(float x)
 }
 // Logits below kLow count as kLow; a row whose maximum lies beyond +-kFar is left to the second attempt.  kLow is the
 // lower by far, so that a thread without values (all kLow, its maximum taken as -kFar) adds e^(kLow + kFar) = 0.
-constexpr float kLow = -1e30f, kFar = 1e29f;
+// That needs (kLow + kFar) / tau to be far below 0, and kLow / tau to be finite: temperatures outside [kTauLow, kTauHigh]
+// leave every row to the second attempt.
+constexpr float kLow = -1e30f, kFar = 1e29f, kTauLow = 1e-8f, kTauHigh = 1e20f;
 
 __device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -529,7 +532,7 @@ __global__ void __launch_bounds__(NT, (NV > 4 ? 512 : 1024) / NT) policy_kernel(
         return over_warp(Stat{q.x, q.y, q.z}, a.c, 4);
     };
     all = join(st, 0);
-    const bool plain = far_off(all);
+    const bool plain = a.far_tau || far_off(all);
     if (plain) {
         if (cs > 1) cluster_arrive();
         st = Stat{-FLT_MAX, 0.0f, 0.0f};
@@ -830,7 +833,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             }
             Stat t = {tok.x_id, z.x, z.y};  // of the others
             ++met;
-            const bool plain = far_off(t) || !(t.z < kManyTimes) || !isfinite(t.s);
+            const bool plain = a.far_tau || far_off(t) || !(t.z < kManyTimes) || !isfinite(t.s);
             if (lane == 0) {
                 s_all[buf] = t;
                 s_plain[buf] = plain;
@@ -1144,6 +1147,7 @@ void set_scale(LossArgs &a, double tau)
     a.dc = (float)((c - (double)a.c) / (double)a.c * 0.69314718055994531);
     a.it = (float)(1.0 / tau);
     a.it_rest = (float)(1.0 / tau - (double)a.it);
+    a.far_tau = !(tau >= kTauLow && tau <= kTauHigh);
 }
 
 // Checks shared by both entry points, for T >= 1.

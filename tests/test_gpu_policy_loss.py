@@ -314,3 +314,25 @@ def test_nan_shows_without_the_kl_term(dtype, T, V):
         assert bool(torch.isnan(dx[row]).any()), name
         assert bool(torch.isnan(lp[row])) == (name in ("logit", "inf")), name
         assert torch.equal(dx[rest], clean[3][rest]) and torch.equal(lp[rest], clean[1][rest]), name
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,V", [(6, 9000), (160, 40001)])
+def test_extreme_temperatures(dtype, T, V):
+    """Every temperature that is taken, with -inf logits: at 1e30 the rest is uniform, at 1e-12 the largest takes all."""
+    x, ids, *_ = make(T, V, dtype, 15)
+    at = torch.arange(T, device="cuda")
+    keep = torch.zeros(T, V, dtype=torch.bool, device="cuda")
+    keep[:, ::3] = True
+    keep[at, ids] = True
+    x[at, ids] = 20.0
+    x = torch.where(keep, x, torch.full_like(x, -INF))
+    n = keep.sum(-1).double().log()
+    lp, ent = q.qerl_token_logp(x, ids, temperature=1e30)
+    tol = (80 + V / 4096) * U + 2.0 ** -22 + 4 * U * float(n.max())
+    assert bool(((lp.double() + n).abs() <= tol).all()) and bool(((ent.double() - n).abs() <= 3 * tol).all())
+    lp, ent = q.qerl_token_logp(x, ids, temperature=1e-12)
+    assert bool((lp == 0).all()) and bool((ent == 0).all())
+    sums, lp, ent, dx = q.qerl_policy_loss(x, ids, -n.float(), torch.ones(T, device="cuda"), temperature=1e30, grad_scale=1e30)
+    assert bool((dx[~keep] == 0).all()) and bool(torch.isfinite(dx).all())
+    assert abs(float(sums[1]) + T) < 1e-4 * T  # rho = 1
