@@ -69,6 +69,7 @@ struct Step {
     float b1, c1, b2, c2, rs2, eps;
     uint32_t key0, key1, t;
     float one, nought;  // 1 and -0
+    bool tame;          // eps is in the range where the approximate inverse of root + eps is a normal number
     int chunk;          // blocks of a chunk
 };
 
@@ -209,8 +210,8 @@ __device__ __forceinline__ bool roots(const Pairs &X, const float2 (&v)[4], floa
     }
     return plain;
 }
-// a / b; `plain`: b comes from such roots, and the approximate inverse's quotient corrected by its residual will do (to a
-// unit, and seldom that much).
+// a / b; `plain`: b comes from such roots and a tame eps, and the approximate inverse's quotient corrected by its residual
+// will do (to a unit, and seldom that much).
 __device__ __forceinline__ float2 quotient(const Pairs &X, float2 a, float2 b, bool plain)
 {
     if (!plain) return make_float2(__fdiv_rn(a.x, b.x), __fdiv_rn(a.y, b.y));
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, S8 ? 6 : 3) step_kernel(const Rec *r
                 m[j] = X.add(X.mul(m[j], both(st.b1)), X.mul(gc, both(st.c1)));
                 v[j] = X.add(X.mul(v[j], both(st.b2)), X.mul(X.mul(gc, gc), both(st.c2)));
             }
-            const bool plain = roots(X, v, root);
+            const bool plain = roots(X, v, root) && st.tame;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 den = X.add(X.mul(root[j], both(st.rs2)), both(st.eps));
@@ -641,6 +642,7 @@ extern "C" qerl_status qerl_adamw_step(const qerl_adamw *h, const qerl_adamw_hyp
     st.c2 = (float)(1.0 - hy->beta2);
     st.rs2 = (float)(1.0 / sqrt(1.0 - pow(hy->beta2, (double)hy->step)));
     st.eps = (float)hy->eps;
+    st.tame = st.eps >= 1e-30f && st.eps <= 1e30f;
     st.key0 = (uint32_t)hy->seed;
     st.key1 = (uint32_t)(hy->seed >> 32);
     st.t = (uint32_t)hy->step;

@@ -300,3 +300,19 @@ def test_step_refusals():
     with pytest.raises(q.QerlError):  # FP32 states have no codes to read
         opt.read_state(torch.empty(10, device="cuda"), torch.empty(10, device="cuda"))
     assert q.get_error() == 0
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-300, 1e-39, 1e-30, 1e30, 1e39])
+def test_any_eps(bits, eps):
+    """An eps beyond FP32's normal range: weights without a gradient stay, and the others take the step of the formula
+    (none where eps is beyond FP32's largest)."""
+    p = torch.full((600,), 0.5, device="cuda")
+    g = torch.zeros(600, device="cuda")
+    g[300:] = 2.0
+    opt = q.AdamW([p], [g], state_bits=bits, weight_decay=0.0, eps=eps)
+    opt.step(1e-2, 1, seed=1)
+    if eps > 1e-50:  # else 0 / 0, as the formula has it in FP32
+        assert bool((p[:300] == 0.5).all())
+    want = 0.5 - 1e-2 * 2.0 / (2.0 + eps)
+    assert bool(((p[300:].double() - want).abs() <= 16 * U).all())
