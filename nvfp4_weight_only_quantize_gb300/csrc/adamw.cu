@@ -593,7 +593,10 @@ extern "C" qerl_status qerl_adamw_plan(const qerl_adamw_tensor *tensors, int64_t
         h->chunk = lo.chunk;
         h->fmt = *format;
         cudaGetDevice(&h->device);
-        if (cudaMemcpy(h->recs, recs, sizeof(Rec) * n_tensors, cudaMemcpyHostToDevice) != cudaSuccess ||
+        // Work that is still queued on any stream may write to the workspace's memory on behalf of its last owner (an allocator
+        // that orders by stream hands it out at once), and these copies wait for no non-blocking stream by themselves.
+        if (cudaDeviceSynchronize() != cudaSuccess ||
+            cudaMemcpy(h->recs, recs, sizeof(Rec) * n_tensors, cudaMemcpyHostToDevice) != cudaSuccess ||
             (lo.n_chunks &&
              cudaMemcpy(h->chunks, chunks, sizeof(Chunk) * lo.n_chunks, cudaMemcpyHostToDevice) != cudaSuccess) ||
             cudaMemset(h->counter, 0, 256) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)

@@ -316,3 +316,28 @@ def test_any_eps(bits, eps):
         assert bool((p[:300] == 0.5).all())
     want = 0.5 - 1e-2 * 2.0 / (2.0 + eps)
     assert bool(((p[300:].double() - want).abs() <= 16 * U).all())
+
+
+def test_plan_on_a_busy_stream():
+    """A plan made while its stream still writes to the memory that the allocator hands out for its table."""
+    ps, gs, _ = make([5000, 300, 70000], torch.float32, torch.float32, 9)
+    want = [p.clone() for p in ps]
+    ref = q.AdamW(want, gs)
+    ref.step(1e-3, 1)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        opt0 = q.AdamW([p.clone() for p in ps], gs)
+        size = opt0.ws.numel()
+        del opt0
+        m, v = ([torch.zeros_like(p) for p in ps] for _ in range(2))
+        for _ in range(20):
+            big = torch.empty(1 << 28, device="cuda").normal_()  # some ms each
+        junk = torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0xAB)
+        at = junk.data_ptr()
+        del junk, big
+        opt = q.AdamW(ps, gs, m=m, v=v)
+        opt.step(1e-3, 1)
+    torch.cuda.synchronize()
+    assert opt.ws.data_ptr() == at  # the block that the stream had still to fill
+    assert q.get_error() == 0 and all(torch.equal(a, b) for a, b in zip(ps, want))
