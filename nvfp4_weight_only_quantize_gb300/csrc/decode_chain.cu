@@ -1138,8 +1138,10 @@ extern "C" qerl_status qerl_decoder_chain_plan(const qerl_decoder_layer *layers,
         (int)ptotal.size() != z.n_phases)
         return QERL_ERR_SHAPE;
 
-    // tables to the device (once, synchronously: the plan is built outside any capture)
-    if (cudaMemcpy(W + lo.off_maps, maps.data(), sizeof(LinMaps) * maps.size(), cudaMemcpyHostToDevice) != cudaSuccess ||
+    // tables to the device (once, synchronously: the plan is built outside any capture); first, what may still be queued on a
+    // non-blocking stream for the memory's last owner has to be done
+    if (cudaDeviceSynchronize() != cudaSuccess ||
+        cudaMemcpy(W + lo.off_maps, maps.data(), sizeof(LinMaps) * maps.size(), cudaMemcpyHostToDevice) != cudaSuccess ||
         cudaMemcpy(W + lo.off_lins, lins.data(), sizeof(Lin) * lins.size(), cudaMemcpyHostToDevice) != cudaSuccess ||
         cudaMemcpy(W + lo.off_glues, glues.data(), sizeof(Glue) * glues.size(), cudaMemcpyHostToDevice) != cudaSuccess ||
         cudaMemcpy(W + lo.off_gammas, gammas.data(), sizeof(void *) * gammas.size(), cudaMemcpyHostToDevice) !=

@@ -266,3 +266,24 @@ def test_chain_one_layer_matches_unfused_norm(M, r):
     """One small layer, every token, against the textbook norm -> bf16 -> linear."""
     ch = Chain(1, M, 512, 512, 128, 768, r, cfg=14)
     check_chain(ch, np.arange(M), 1e-2, 7, 3, (0,), "unfused", fused=False, compose=False)
+
+
+def test_plan_on_a_busy_stream():
+    """A plan made while its stream still writes to the memory that the allocator hands out for its tables."""
+    c = Chain(1, 8, 512, 512, 256, 1024, 16)
+    want, got = torch.empty_like(c.x), torch.empty_like(c.x)
+    c.plan(0, 1, c.x, want).run(1e-2, 7, 3)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        size = c.plan(0, 1, c.x, got).ws.numel()
+        for _ in range(20):
+            big = torch.empty(1 << 28, device="cuda").normal_()  # some ms each
+        junk = torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0xAB)
+        at = junk.data_ptr()
+        del junk, big
+        plan = c.plan(0, 1, c.x, got)
+        plan.run(1e-2, 7, 3)
+    torch.cuda.synchronize()
+    assert plan.ws.data_ptr() == at  # the block that the stream had still to fill
+    assert q.get_error() == 0 and torch.equal(got, want)
