@@ -9,6 +9,7 @@ the computation runs in the library's CUDA kernels; there is no fallback.  If
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 import threading
@@ -169,6 +170,29 @@ def workspace(op: int, M: int, N: int, K: int, r: int, device="cuda") -> torch.T
     return torch.empty(max(workspace_bytes(op, M, N, K, r), 1), dtype=torch.uint8, device=device)
 
 
+def _new(make, stream, *args, **kw):
+    """make(*args, **kw), a tensor of a call's own.  With `stream` it comes from that stream's memory, so that nothing still
+    queued elsewhere for its last owner meets the call; the caller goes on with it on the current stream."""
+    if stream is None:
+        return make(*args, **kw)
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    t.record_stream(current)
+    return t
+
+
+def _launch_on(stream, seen, tensors):
+    """The launch stream's handle.  An object's own tensors stay allocated, after it is dropped, until every stream that
+    it was launched on (`seen`: at first the one that it was made on) has finished with them."""
+    handle = _stream(stream)
+    if handle not in seen:
+        for t in tensors:
+            t.record_stream(torch.cuda.current_stream() if stream is None else stream)
+        seen.add(handle)
+    return handle
+
+
 def set_linear_algo(algo: int):
     _check(lib().qerl_set_linear_algo(algo), "qerl_set_linear_algo")
 
@@ -192,11 +216,11 @@ def qerl_nvfp4_quantize(W: torch.Tensor, scale_round: int = SCALE_ROUND_UP, out=
     assert W.dtype == torch.bfloat16 and W.dim() == 2 and W.stride(1) == 1
     N, K = W.shape
     if out is None:
-        out = (torch.empty(N, K // 2, dtype=torch.uint8, device=W.device),
-               torch.empty(N, K // 16, dtype=torch.uint8, device=W.device),
-               torch.empty(1, dtype=torch.float32, device=W.device))
+        out = (_new(torch.empty, stream, N, K // 2, dtype=torch.uint8, device=W.device),
+               _new(torch.empty, stream, N, K // 16, dtype=torch.uint8, device=W.device),
+               _new(torch.empty, stream, 1, dtype=torch.float32, device=W.device))
     codes, scales, ts = out
-    ws = workspace(OP_QUANTIZE, 0, N, K, 0, W.device) if ws is None else ws
+    ws = _new(workspace, stream, OP_QUANTIZE, 0, N, K, 0, W.device) if ws is None else ws
     opts = _QuantOpts(scale_round)
     _check(lib().qerl_nvfp4_quantize(_p(W), N, K, W.stride(0), _p(codes), _p(scales), _p(ts), C.byref(opts),
                                      _p(ws), ws.numel(), _stream(stream)), "qerl_nvfp4_quantize")
@@ -205,7 +229,7 @@ def qerl_nvfp4_quantize(W: torch.Tensor, scale_round: int = SCALE_ROUND_UP, out=
 
 def qerl_nvfp4_dequantize(codes, scales, tensor_scale, N: int, K: int, apply_tensor_scale: bool = True,
                           out=None, stream=None):
-    out = torch.empty(N, K, dtype=torch.bfloat16, device=codes.device) if out is None else out
+    out = _new(torch.empty, stream, N, K, dtype=torch.bfloat16, device=codes.device) if out is None else out
     _check(lib().qerl_nvfp4_dequantize(_p(codes), _p(scales), _p(tensor_scale), N, K, _p(out),
                                        int(apply_tensor_scale), _stream(stream)), "qerl_nvfp4_dequantize")
     return out
@@ -215,8 +239,8 @@ def qerl_nvfp4_dequantize(codes, scales, tensor_scale, N: int, K: int, apply_ten
 def _fwd(name, x, codes, scales, tensor_scale, A, B, lora_scale, y, t_out, ws, stream):
     M, K = x.shape
     N, r = B.shape
-    y = torch.empty(M, N, dtype=torch.bfloat16, device=x.device) if y is None else y
-    ws = workspace(OP_LINEAR_FWD, M, N, K, r, x.device) if ws is None else ws
+    y = _new(torch.empty, stream, M, N, dtype=torch.bfloat16, device=x.device) if y is None else y
+    ws = _new(workspace, stream, OP_LINEAR_FWD, M, N, K, r, x.device) if ws is None else ws
     _check(getattr(lib(), name)(_p(x), M, K, N, _p(codes), _p(scales), _p(tensor_scale), _p(A), _p(B), r,
                                 float(lora_scale), _p(y), _p(t_out), _p(ws), ws.numel(), _stream(stream)), name)
     return y
@@ -251,13 +275,13 @@ def qerl_nvfp4_lora_linear_fwd_grouped(x, groups, lora_scale: float, packed: boo
     M, K = x.shape
     r = groups[0][3].shape[0]
     Ns = [g[4].shape[0] for g in groups]
-    ys = [torch.empty(M, N, dtype=torch.bfloat16, device=x.device) for N in Ns] if ys is None else ys
+    ys = [_new(torch.empty, stream, M, N, dtype=torch.bfloat16, device=x.device) for N in Ns] if ys is None else ys
     t_outs = [None] * len(groups) if t_outs is None else t_outs
     arr = (_Group * len(groups))()
     for i, (codes, scales, ts, A, B) in enumerate(groups):
         arr[i] = _Group(Ns[i], _p(codes), _p(scales), _p(ts), _p(A), _p(B), _p(ys[i]), _p(t_outs[i]))
     if ws is None:
-        ws = torch.empty(max(grouped_ws_bytes(M, K, r, Ns), 1), dtype=torch.uint8, device=x.device)
+        ws = _new(torch.empty, stream, max(grouped_ws_bytes(M, K, r, Ns), 1), dtype=torch.uint8, device=x.device)
     _check(lib().qerl_nvfp4_lora_linear_fwd_grouped(_p(x), M, K, r, float(lora_scale), C.cast(arr, C.c_void_p),
                                                     len(groups), int(bool(packed)), _p(ws), ws.numel(),
                                                     _stream(stream)), "qerl_nvfp4_lora_linear_fwd_grouped")
@@ -267,7 +291,7 @@ def qerl_nvfp4_lora_linear_fwd_grouped(x, groups, lora_scale: float, packed: boo
 def qerl_nvfp4_pack_codes(codes, out=None, stream=None):
     """Standard NVFP4 codes [N, K/2] -> the packed layout (same shape; out may be codes itself)."""
     N, half = codes.shape
-    out = torch.empty_like(codes) if out is None else out
+    out = _new(torch.empty_like, stream, codes) if out is None else out
     _check(lib().qerl_nvfp4_pack_codes(_p(codes), N, 2 * half, _p(out), _stream(stream)), "qerl_nvfp4_pack_codes")
     return out
 
@@ -275,7 +299,7 @@ def qerl_nvfp4_pack_codes(codes, out=None, stream=None):
 def qerl_nvfp4_unpack_codes(packed, out=None, stream=None):
     """Inverse of qerl_nvfp4_pack_codes."""
     N, half = packed.shape
-    out = torch.empty_like(packed) if out is None else out
+    out = _new(torch.empty_like, stream, packed) if out is None else out
     _check(lib().qerl_nvfp4_unpack_codes(_p(packed), N, 2 * half, _p(out), _stream(stream)),
            "qerl_nvfp4_unpack_codes")
     return out
@@ -287,7 +311,7 @@ def qerl_nvfp4_lora_linear_fwd_noalloc(x, codes, scales, tensor_scale, A, B, lor
     (for callers that cannot allocate device memory; see include/qerl.h)."""
     M, K = x.shape
     N, r = B.shape
-    y = torch.empty(M, N, dtype=torch.bfloat16, device=x.device) if y is None else y
+    y = _new(torch.empty, stream, M, N, dtype=torch.bfloat16, device=x.device) if y is None else y
     _check(lib().qerl_nvfp4_lora_linear_fwd_noalloc(_p(x), M, K, N, _p(codes), _p(scales), _p(tensor_scale), _p(A),
                                                     _p(B), r, float(lora_scale), _p(y), _p(t_out), _stream(stream)),
            "qerl_nvfp4_lora_linear_fwd_noalloc")
@@ -317,12 +341,12 @@ def _bwd(name, dy, x, codes, scales, tensor_scale, A, B, lora_scale, t_saved, dx
     r = A.shape[0]
     dev = x.device
     if dx is None and "dx" in want:
-        dx = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
+        dx = _new(torch.empty, stream, M, K, dtype=torch.bfloat16, device=dev)
     if dA is None and "dA" in want:
-        dA = torch.zeros(r, K, dtype=torch.float32, device=dev)
+        dA = _new(torch.zeros, stream, r, K, dtype=torch.float32, device=dev)
     if dB is None and "dB" in want:
-        dB = torch.zeros(N, r, dtype=torch.float32, device=dev)
-    ws = workspace(OP_LINEAR_BWD, M, N, K, r, dev) if ws is None else ws
+        dB = _new(torch.zeros, stream, N, r, dtype=torch.float32, device=dev)
+    ws = _new(workspace, stream, OP_LINEAR_BWD, M, N, K, r, dev) if ws is None else ws
     _check(getattr(lib(), name)(_p(dy), _p(x), M, K, N, _p(codes), _p(scales), _p(tensor_scale), _p(A), _p(B), r,
                                 float(lora_scale), _p(t_saved), _p(dx), _p(dA), _p(dB), int(accumulate), _p(ws),
                                 ws.numel(), _stream(stream)), name)
@@ -335,8 +359,8 @@ def qerl_mxfp4_quantize(W: torch.Tensor, out=None, stream=None):
     assert W.dtype == torch.bfloat16 and W.dim() == 2 and W.stride(1) == 1
     N, K = W.shape
     if out is None:
-        out = (torch.empty(N, K // 2, dtype=torch.uint8, device=W.device),
-               torch.empty(N, K // 32, dtype=torch.uint8, device=W.device))
+        out = (_new(torch.empty, stream, N, K // 2, dtype=torch.uint8, device=W.device),
+               _new(torch.empty, stream, N, K // 32, dtype=torch.uint8, device=W.device))
     codes, scales = out
     _check(lib().qerl_mxfp4_quantize(_p(W), N, K, W.stride(0), _p(codes), _p(scales), _stream(stream)),
            "qerl_mxfp4_quantize")
@@ -346,8 +370,8 @@ def qerl_mxfp4_quantize(W: torch.Tensor, out=None, stream=None):
 def qerl_mxfp4_lora_linear_fwd(x, codes, scales, A, B, lora_scale: float, y=None, t_out=None, ws=None, stream=None):
     M, K = x.shape
     N, r = B.shape
-    y = torch.empty(M, N, dtype=torch.bfloat16, device=x.device) if y is None else y
-    ws = workspace(OP_MXFP4_FWD, M, N, K, r, x.device) if ws is None else ws
+    y = _new(torch.empty, stream, M, N, dtype=torch.bfloat16, device=x.device) if y is None else y
+    ws = _new(workspace, stream, OP_MXFP4_FWD, M, N, K, r, x.device) if ws is None else ws
     _check(lib().qerl_mxfp4_lora_linear_fwd(_p(x), M, K, N, _p(codes), _p(scales), _p(A), _p(B), r, float(lora_scale),
                                             _p(y), _p(t_out), _p(ws), ws.numel(), _stream(stream)),
            "qerl_mxfp4_lora_linear_fwd")
@@ -360,8 +384,8 @@ def qerl_nvfp4_lora_linear_fwd_f32ab(x, codes, scales, tensor_scale, A, B, lora_
     assert A.dtype == torch.float32 and B.dtype == torch.float32
     M, K = x.shape
     N, r = B.shape
-    y = torch.empty(M, N, dtype=torch.bfloat16, device=x.device) if y is None else y
-    ws = workspace(OP_LINEAR_FWD_F32AB, M, N, K, r, x.device) if ws is None else ws
+    y = _new(torch.empty, stream, M, N, dtype=torch.bfloat16, device=x.device) if y is None else y
+    ws = _new(workspace, stream, OP_LINEAR_FWD_F32AB, M, N, K, r, x.device) if ws is None else ws
     _check(lib().qerl_nvfp4_lora_linear_fwd_f32ab(_p(x), M, K, N, _p(codes), _p(scales), _p(tensor_scale), _p(A),
                                                   _p(B), r, float(lora_scale), _p(y), _p(t_out), _p(ws), ws.numel(),
                                                   _stream(stream)),
@@ -373,7 +397,7 @@ def qerl_nvfp4_lora_linear_fwd_f32ab(x, codes, scales, tensor_scale, A, B, lora_
 def qerl_residual_add(h, y, out=None, stream=None):
     """out = bf16(h + y) elementwise (bf16 tensors of one shape); out may be h."""
     assert h.shape == y.shape and h.dtype == y.dtype == torch.bfloat16
-    out = torch.empty_like(h) if out is None else out
+    out = _new(torch.empty_like, stream, h) if out is None else out
     _check(lib().qerl_residual_add(_p(h), _p(y), h.numel(), _p(out), _stream(stream)), "qerl_residual_add")
     return out
 
@@ -381,7 +405,7 @@ def qerl_residual_add(h, y, out=None, stream=None):
 def qerl_swiglu(g, u, out=None, stream=None):
     """out = bf16(silu(g) * u) elementwise (bf16 tensors of one shape)."""
     assert g.shape == u.shape and g.dtype == u.dtype == torch.bfloat16
-    out = torch.empty_like(g) if out is None else out
+    out = _new(torch.empty_like, stream, g) if out is None else out
     _check(lib().qerl_swiglu(_p(g), _p(u), g.numel(), _p(out), _stream(stream)), "qerl_swiglu")
     return out
 
@@ -392,8 +416,8 @@ def qerl_aqn_rmsnorm(x, gamma, eps: float, sigma: float, seed: int, step: int, l
     """noise_mode None: qerl_aqn_rmsnorm (additive); AQN_NOISE_ADD / AQN_NOISE_MUL:
     qerl_aqn_rmsnorm_mode."""
     M, H = x.shape
-    y = torch.empty_like(x) if y is None else y
-    ws = workspace(OP_AQN_RMSNORM, M, 0, H, 0, x.device) if ws is None else ws
+    y = _new(torch.empty_like, stream, x) if y is None else y
+    ws = _new(workspace, stream, OP_AQN_RMSNORM, M, 0, H, 0, x.device) if ws is None else ws
     if noise_mode is None:
         _check(lib().qerl_aqn_rmsnorm(_p(x), M, H, _p(gamma), float(eps), float(sigma), seed, step, layer_id, _p(y),
                                       _p(ws), ws.numel(), _stream(stream)), "qerl_aqn_rmsnorm")
@@ -406,8 +430,8 @@ def qerl_aqn_rmsnorm(x, gamma, eps: float, sigma: float, seed: int, step: int, l
 
 def qerl_aqn_noise(H: int, seed: int, step: int, layer_id: int, want_raw: bool = False, device="cuda",
                    stream=None):
-    z = torch.empty(H, dtype=torch.float32, device=device)
-    raw = torch.empty(H, dtype=torch.int64, device=device) if want_raw else None
+    z = _new(torch.empty, stream, H, dtype=torch.float32, device=device)
+    raw = _new(torch.empty, stream, H, dtype=torch.int64, device=device) if want_raw else None
     _check(lib().qerl_aqn_noise(H, seed, step, layer_id, _p(z), _p(raw), _stream(stream)), "qerl_aqn_noise")
     return (z, raw) if want_raw else z
 
@@ -456,6 +480,7 @@ class DecoderChain:
         if n == 0:
             raise QerlError(2, "qerl_decoder_chain_ws_bytes")
         self.ws = torch.empty(n, dtype=torch.uint8, device=x_in.device) if ws is None else ws
+        self._launched_on = {_stream()}
         arr = (_Layer * len(layers))()
         for i, Ly in enumerate(layers):
             for nm in CHAIN_LINEARS:
@@ -473,7 +498,8 @@ class DecoderChain:
         self._h = h
 
     def run(self, sigma: float, seed: int, step: int, first_layer: int = 0, stream=None):
-        _check(lib().qerl_decoder_chain_run(self._h, float(sigma), seed, step, first_layer, _stream(stream)),
+        _check(lib().qerl_decoder_chain_run(self._h, float(sigma), seed, step, first_layer,
+                                            _launch_on(stream, self._launched_on, (self.ws,))),
                "qerl_decoder_chain_run")
 
     def close(self):
@@ -504,7 +530,9 @@ class PrefixAttention:
     contiguous); sequence b reads prefix b // (B // n_prefix).  q_heads: query
     heads; q_len: new tokens per sequence and call; scale: 1 / sqrt(D) if None.
     The tensors are kept referenced; the workspace is this object's (calls that
-    may overlap need an object each)."""
+    may overlap need an object each).  A stream other than the one that was
+    current when the object was made has to wait for that one before its first
+    run, as for any tensor made there."""
 
     def __init__(self, k_prefix, v_prefix, k_suffix, v_suffix, q_heads: int, q_len: int = 1, scale: float = None, ws=None):
         n, P, Hkv, D = k_prefix.shape
@@ -522,6 +550,7 @@ class PrefixAttention:
             raise QerlError(2, "qerl_prefix_attention_ws_bytes")
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=k_suffix.device) if ws is None else ws
         self._ws = (self.ws.data_ptr(), self.ws.numel())
+        self._launched_on = {_stream()}
         self._q_shape = torch.Size((B, q_len, q_heads, D))
         self._scale = D ** -0.5 if scale is None else float(scale)
         self._p = [_p(t) for t in self._keep]
@@ -533,7 +562,7 @@ class PrefixAttention:
         prefix_lens int32 [n_prefix] or None (P) -> out bf16 like q; lse f32 [B, Lq, Hq] is filled if given."""
         d = self._d
         if out is None:
-            out = torch.empty(self._q_shape, dtype=torch.bfloat16, device=q.device)
+            out = _new(torch.empty, stream, self._q_shape, dtype=torch.bfloat16, device=q.device)
         assert q.shape == self._q_shape and out.shape == self._q_shape and q.dtype == out.dtype == torch.bfloat16
         assert suffix_lens.dtype == torch.int32 and suffix_lens.is_contiguous() and suffix_lens.numel() == d.B
         if prefix_lens is not None:
@@ -547,7 +576,8 @@ class PrefixAttention:
             self._strides = strides
         kp, vp, ks, vs = self._p
         _check(lib().qerl_prefix_attention(self._ref, q.data_ptr(), kp, vp, _p(prefix_lens), ks, vs, suffix_lens.data_ptr(),
-                                           self._scale, out.data_ptr(), _p(lse), self._ws[0], self._ws[1], _stream(stream)),
+                                           self._scale, out.data_ptr(), _p(lse), self._ws[0], self._ws[1],
+                                           _launch_on(stream, self._launched_on, (self.ws,))),
                "qerl_prefix_attention")
         return out
 
@@ -555,7 +585,8 @@ class PrefixAttention:
 def qerl_prefix_attention(q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_lens, prefix_lens=None, scale: float = None,
                           out=None, lse=None, ws=None, stream=None):
     """One call of PrefixAttention: out bf16 [B, Lq, Hq, D]."""
-    plan = PrefixAttention(k_prefix, v_prefix, k_suffix, v_suffix, q.shape[2], q.shape[1], scale, ws)
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):  # the workspace is that stream's
+        plan = PrefixAttention(k_prefix, v_prefix, k_suffix, v_suffix, q.shape[2], q.shape[1], scale, ws)
     return plan.run(q, suffix_lens, prefix_lens, out, lse, stream)
 
 
@@ -582,8 +613,8 @@ def _logits_args(logits, ids, vectors):
 def qerl_token_logp(logits, ids, weights=None, temperature: float = 1.0, logp=None, entropy=None, stream=None):
     """logits bf16/f32 [T, V], ids int32/int64 [T] -> (logp, entropy) f32 [T]; rows of weight 0 are not read."""
     T = logits.shape[0]
-    logp = torch.empty(T, dtype=torch.float32, device=logits.device) if logp is None else logp
-    entropy = torch.empty(T, dtype=torch.float32, device=logits.device) if entropy is None else entropy
+    logp = _new(torch.empty, stream, T, dtype=torch.float32, device=logits.device) if logp is None else logp
+    entropy = _new(torch.empty, stream, T, dtype=torch.float32, device=logits.device) if entropy is None else entropy
     args = _logits_args(logits, ids, (weights, logp, entropy))
     _check(lib().qerl_token_logp(*args, _p(weights), float(temperature), _p(logp), _p(entropy), _stream(stream)),
            "qerl_token_logp")
@@ -598,12 +629,12 @@ def qerl_policy_loss(logits, ids, old_logp, advantages, weights=None, ref_logp=N
     or None without want_grad).  dlogits may be logits."""
     T, V = logits.shape
     dev = logits.device
-    logp = torch.empty(T, dtype=torch.float32, device=dev) if logp is None else logp
-    entropy = torch.empty(T, dtype=torch.float32, device=dev) if entropy is None else entropy
-    sums = torch.empty(4, dtype=torch.float32, device=dev) if sums is None else sums
+    logp = _new(torch.empty, stream, T, dtype=torch.float32, device=dev) if logp is None else logp
+    entropy = _new(torch.empty, stream, T, dtype=torch.float32, device=dev) if entropy is None else entropy
+    sums = _new(torch.empty, stream, 4, dtype=torch.float32, device=dev) if sums is None else sums
     if dlogits is None and want_grad:
-        dlogits = torch.empty(T, V, dtype=logits.dtype, device=dev)
-    ws = workspace(OP_POLICY_LOSS, T, V, 0, 0, dev) if ws is None else ws
+        dlogits = _new(torch.empty, stream, T, V, dtype=logits.dtype, device=dev)
+    ws = _new(workspace, stream, OP_POLICY_LOSS, T, V, 0, 0, dev) if ws is None else ws
     args = _logits_args(logits, ids, (old_logp, ref_logp, advantages, weights, logp, entropy))
     assert sums.dtype == torch.float32 and sums.numel() == 4 and sums.is_contiguous()
     ldd = V
@@ -684,6 +715,9 @@ class AdamW:
         _check(lib().qerl_adamw_plan(C.cast(table, C.c_void_p), n, C.byref(fmt), _p(self.ws), self.ws.numel(), C.byref(h)),
                "qerl_adamw_plan")
         self._h = h
+        self._launched_on = {_stream()}
+        made = [(m, self.m), (v, self.v)] + ([(m_scale, self.m_scale), (v_scale, self.v_scale)] if state_bits == 8 else [])
+        self._own = [self.ws] + [t for given, tensors in made if given is None for t in tensors]
         self._flat = sum(-(-p.numel() // self.BLOCK) for p in params[:-1]) * self.BLOCK + params[-1].numel()
         self._hyper = _AdamHyper(0.0, betas[0], betas[1], eps, 0.0, 1, 0)
 
@@ -692,14 +726,16 @@ class AdamW:
         them, which goes to grad_norm (f32 [1]) if given."""
         hy = self._hyper
         hy.lr, hy.step, hy.seed, hy.max_grad_norm = lr, step, seed, max_grad_norm
-        _check(lib().qerl_adamw_step(self._h, C.byref(hy), _p(grad_norm), _stream(stream)), "qerl_adamw_step")
+        _check(lib().qerl_adamw_step(self._h, C.byref(hy), _p(grad_norm), _launch_on(stream, self._launched_on, self._own)),
+               "qerl_adamw_step")
 
     def read_state(self, m_out, v_out, stream=None):
         """The values of the 8-bit states, f32 or bf16: the tensors in order, each from a multiple of 256 elements on."""
         size = self._flat
         assert m_out.dtype == v_out.dtype and m_out.dtype in _DTYPES and m_out.is_contiguous() and v_out.is_contiguous()
         assert m_out.numel() >= size and v_out.numel() >= size
-        _check(lib().qerl_adamw_read_state(self._h, _p(m_out), _p(v_out), _DTYPES[m_out.dtype], _stream(stream)),
+        _check(lib().qerl_adamw_read_state(self._h, _p(m_out), _p(v_out), _DTYPES[m_out.dtype],
+                                           _launch_on(stream, self._launched_on, self._own)),
                "qerl_adamw_read_state")
 
     def close(self):
