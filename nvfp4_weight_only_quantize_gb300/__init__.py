@@ -684,7 +684,7 @@ class AdamW:
         sdt = torch.uint8 if state_bits == 8 else torch.float32
         new = lambda: [torch.zeros(p.numel(), dtype=sdt, device=p.device) for p in params]  # noqa: E731
         news = lambda: [torch.zeros(-(-p.numel() // self.BLOCK), dtype=torch.float32, device=p.device) for p in params]  # noqa: E731
-        self.params, self.grads, self.masters = list(params), list(grads), masters
+        self.params, self.grads, self.masters = list(params), list(grads), None if masters is None else list(masters)
         self.m = new() if m is None else list(m)
         self.v = new() if v is None else list(v)
         self.m_scale = self.v_scale = [None] * n

@@ -341,3 +341,18 @@ def test_plan_on_a_busy_stream():
     torch.cuda.synchronize()
     assert opt.ws.data_ptr() == at  # the block that the stream had still to fill
     assert q.get_error() == 0 and all(torch.equal(a, b) for a, b in zip(ps, want))
+
+
+def test_plan_keeps_every_tensor():
+    """The lists that were given may change afterwards; the plan's tensors stay."""
+    import gc
+    import weakref
+    ps, gs, masters = make([100, 300], torch.bfloat16, torch.float32, 10)
+    opt = q.AdamW(ps, gs, masters=masters, state_bits=8)
+    kept = [weakref.ref(t) for t in (*ps, *gs, *masters)]
+    ps.clear(), gs.clear(), masters.clear()
+    gc.collect()
+    assert all(r() is not None for r in kept)
+    opt.step(1e-3, 1)
+    torch.cuda.synchronize()
+    assert q.get_error() == 0
