@@ -474,7 +474,7 @@ class DecoderChain:
     "k_out", "v_out".  The tensors are kept referenced while the plan lives."""
 
     def __init__(self, layers, M, hidden, q_dim, kv_dim, intermediate, r, lora_scale, eps, x_in, x_out, ws=None):
-        self._keep = [layers, x_in, x_out]
+        self._keep = [[{k: Ly[k] for k in Ly} for Ly in layers], x_in, x_out]
         d = _Dims(M, hidden, q_dim, kv_dim, intermediate, r, lora_scale, eps)
         n = lib().qerl_decoder_chain_ws_bytes(C.byref(d), len(layers))
         if n == 0:

@@ -287,3 +287,19 @@ def test_plan_on_a_busy_stream():
     torch.cuda.synchronize()
     assert plan.ws.data_ptr() == at  # the block that the stream had still to fill
     assert q.get_error() == 0 and torch.equal(got, want)
+
+
+def test_plan_keeps_every_tensor():
+    """The layers' dicts may change afterwards; the plan's tensors stay."""
+    import gc
+    import weakref
+    c = Chain(1, 8, 512, 512, 256, 1024, 16)
+    out = torch.empty_like(c.x)
+    plan = c.plan(0, 1, c.x, out)
+    kept = [weakref.ref(t) for v in c.layers[0].values() for t in (v if isinstance(v, tuple) else (v,))]
+    c.layers[0].clear()
+    gc.collect()
+    assert all(r() is not None for r in kept)
+    plan.run(1e-2, 7, 3)
+    torch.cuda.synchronize()
+    assert q.get_error() == 0
