@@ -16,7 +16,6 @@ std::atomic<int> g_chain{1};
 static __device__ unsigned int g_device_error;
 
 namespace {
-constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 int g_dev_state[kMaxDevices];            // 0 unknown, 1 ok, 2 unsupported
 unsigned int *g_err_addr[kMaxDevices];   // device address of g_device_error

@@ -7,6 +7,7 @@
 
 #include <atomic>
 
+#include "per_device.cuh"
 #include "qerl.h"
 
 namespace qerl {
@@ -28,16 +29,27 @@ inline cudaStream_t as_cuda(qerl_stream_t s) { return reinterpret_cast<cudaStrea
 
 inline int num_sms()
 {
-    static int cached[64] = {0};
+    static int cached[kMaxDevices] = {0};
     int dev = 0;
     cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64) return 152;
+    if (dev < 0 || dev >= kMaxDevices) return 152;
     if (!cached[dev]) {
         int v = 0;
         cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
         cached[dev] = v > 0 ? v : 152;
     }
     return cached[dev];
+}
+
+// The current device's limit of a kernel's dynamic shared memory, set at its first launch there (the limit belongs to the
+// device).  `once` is the kernel's own.
+template <typename... Params>
+cudaError_t allow_smem(OncePerDevice &once, void (*kernel)(Params...), size_t bytes)
+{
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    return once(dev, [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes); });
 }
 
 // After a launch: count it and turn a launch error into QERL_ERR_CUDA.

@@ -19,7 +19,6 @@ namespace {
 // GPU race.
 static __device__ __align__(256) unsigned char g_noalloc_scratch[QERL_NOALLOC_SCRATCH_BYTES];
 
-constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 void *g_scratch_addr[kMaxDevices];
 

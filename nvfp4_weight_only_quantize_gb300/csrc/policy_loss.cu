@@ -1053,11 +1053,14 @@ void set_cluster(cudaLaunchConfig_t &cfg, int cs)
 template <bool BF16>
 cudaError_t ring_clusters(int cs, int &most)
 {
-    static const cudaError_t smem =
-        cudaFuncSetAttribute(policy_ring_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
-    if (smem != cudaSuccess) return smem;
-    static std::atomic<int> fit[kMaxCluster + 1];
-    most = fit[cs].load();
+    static OncePerDevice once;
+    cudaError_t e = allow_smem(once, policy_ring_kernel<BF16>, kRingBytes);
+    if (e != cudaSuccess) return e;
+    static std::atomic<int> fit[kMaxDevices][kMaxCluster + 1];
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev >= kMaxDevices) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    most = fit[dev][cs].load();
     if (most) return cudaSuccess;
     most = num_sms();
     if (cs > 1) {
@@ -1068,11 +1071,11 @@ cudaError_t ring_clusters(int cs, int &most)
         cfg.dynamicSmemBytes = kRingBytes;
         cfg.attrs = attr;
         set_cluster(cfg, cs);
-        const cudaError_t e = cudaOccupancyMaxActiveClusters(&most, policy_ring_kernel<BF16>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&most, policy_ring_kernel<BF16>, &cfg);
         if (e != cudaSuccess) return e;
         if (most < 1) most = 1;
     }
-    fit[cs].store(most);
+    fit[dev][cs].store(most);
     return cudaSuccess;
 }
 

@@ -432,9 +432,8 @@ qerl_status run(const Args &a, const void *maps, cudaStream_t s)
     const int64_t pi = a.p_tc ? 0 : (int64_t)a.n_prefix * a.Hkv * a.p_tiles * a.n_pp,
                   si = a.s_tc ? 0 : (int64_t)a.B * a.Hkv * a.s_tiles * a.n_sp;
     if (pi + si > 0) {
-        static const cudaError_t attr =
-            cudaFuncSetAttribute(rows16_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
-        if (attr != cudaSuccess) return QERL_ERR_CUDA;
+        static OncePerDevice once;
+        if (allow_smem(once, rows16_kernel<D>, smem_bytes<D>()) != cudaSuccess) return QERL_ERR_CUDA;
         QERL_TRY(launched(launch_k(rows16_kernel<D>, dim3((unsigned)(pi + si)), dim3(kWarps * 32), smem_bytes<D>(), s, chain, a, (int)pi,
                                    tc && chain ? 1 : 0)));
     }

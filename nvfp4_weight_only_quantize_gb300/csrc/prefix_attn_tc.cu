@@ -499,8 +499,9 @@ template <int D>
 cudaError_t launch(const Args &a, const Maps &maps, cudaStream_t s, bool chain)
 {
     constexpr size_t smem = Smem<D>::TOTAL + 1024;
-    static const cudaError_t attr = cudaFuncSetAttribute(rows128_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (attr != cudaSuccess) return attr;
+    static OncePerDevice once;
+    const cudaError_t e = allow_smem(once, rows128_kernel<D>, smem);
+    if (e != cudaSuccess) return e;
     return launch_k(rows128_kernel<D>, dim3((unsigned)a.grid_tc), dim3(kThreads), smem, s, chain, maps, a, error_word());
 }
 
