@@ -651,6 +651,15 @@ qerl_status qerl_set_linear_algo(int algo);
 /* Number of kernels this library launched since load (host-side counter). */
 uint64_t qerl_launch_count(void);
 
+/* The same for the kernels between which a call chooses by its sizes (0 for any other number). */
+enum {
+    QERL_KERNEL_ATTN_ROWS16 = 0,  /* qerl_prefix_attention: tiles of up to 16 rows that share keys */
+    QERL_KERNEL_ATTN_ROWS128 = 1, /* and of 128, on tcgen05 */
+    QERL_KERNEL_LOSS_ROW = 2,     /* qerl_policy_loss, qerl_token_logp: a cluster per row */
+    QERL_KERNEL_LOSS_RING = 3     /* and clusters that stay, rows through a ring in shared memory */
+};
+uint64_t qerl_kernel_launch_count(int kernel);
+
 #ifdef __cplusplus
 }
 #endif

@@ -31,6 +31,7 @@ OP_POLICY_LOSS = 6
 DTYPE_F32, DTYPE_BF16 = 0, 1
 ALGO_AUTO, ALGO_SIMT, ALGO_TCGEN05, ALGO_GEMV = 0, 1, 2, 3
 AQN_NOISE_ADD, AQN_NOISE_MUL = 0, 1
+KERNEL_ATTN_ROWS16, KERNEL_ATTN_ROWS128, KERNEL_LOSS_ROW, KERNEL_LOSS_RING = 0, 1, 2, 3
 
 # Every C symbol include/qerl.h declares (checked by the CPU test suite).
 EXPORTED = ["qerl_nvfp4_quantize", "qerl_nvfp4_dequantize", "qerl_nvfp4_lora_linear_fwd",
@@ -41,7 +42,7 @@ EXPORTED = ["qerl_nvfp4_quantize", "qerl_nvfp4_dequantize", "qerl_nvfp4_lora_lin
             "qerl_workspace_bytes", "qerl_get_error", "qerl_status_string", "qerl_set_linear_algo",
             "qerl_set_launch_chaining", "qerl_lora_linear_fwd_grouped_ws_bytes",
             "qerl_nvfp4_lora_linear_fwd_grouped",
-            "qerl_launch_count", "qerl_decoder_chain_ws_bytes", "qerl_decoder_chain_plan",
+            "qerl_launch_count", "qerl_kernel_launch_count", "qerl_decoder_chain_ws_bytes", "qerl_decoder_chain_plan",
             "qerl_decoder_chain_run", "qerl_decoder_chain_destroy", "qerl_mxfp4_quantize",
             "qerl_mxfp4_lora_linear_fwd", "qerl_nvfp4_lora_linear_fwd_f32ab", "qerl_residual_add", "qerl_swiglu",
             "qerl_prefix_attention_ws_bytes", "qerl_prefix_attention", "qerl_token_logp", "qerl_policy_loss",
@@ -103,6 +104,7 @@ def lib() -> C.CDLL:
                 "qerl_set_linear_algo": ([i32], i32),
                 "qerl_set_launch_chaining": ([i32], i32),
                 "qerl_launch_count": ([], u64),
+                "qerl_kernel_launch_count": ([i32], u64),
             }
             sig["qerl_lora_linear_fwd_grouped_ws_bytes"] = ([i64, i64, i32, vp, i32], sz)
             sig["qerl_nvfp4_lora_linear_fwd_grouped"] = ([vp, i64, i64, i32, f32, vp, i32, i32, vp, sz, vp], i32)
@@ -204,6 +206,11 @@ def set_launch_chaining(on: bool):
 
 def launch_count() -> int:
     return lib().qerl_launch_count()
+
+
+def kernel_launch_count(kernel: int) -> int:
+    """Launches of one of KERNEL_*, between which a call chooses by its sizes."""
+    return lib().qerl_kernel_launch_count(kernel)
 
 
 def get_error(stream=None) -> int:

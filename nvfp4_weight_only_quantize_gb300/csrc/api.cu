@@ -10,6 +10,7 @@
 namespace qerl {
 
 std::atomic<uint64_t> g_launches{0};
+std::atomic<uint64_t> g_kernel_launches[kCountedKernels];
 std::atomic<int> g_chain{1};
 
 // First error a kernel found on this device (0 = none); cleared by qerl_get_error.
@@ -118,6 +119,11 @@ extern "C" float qerl_aqn_sigma(int64_t step, int64_t total_steps, float sigma_s
 }
 
 extern "C" uint64_t qerl_launch_count(void) { return g_launches.load(); }
+
+extern "C" uint64_t qerl_kernel_launch_count(int kernel)
+{
+    return kernel >= 0 && kernel < kCountedKernels ? g_kernel_launches[kernel].load() : 0;
+}
 
 extern "C" qerl_status qerl_set_launch_chaining(int on)
 {

@@ -14,6 +14,9 @@ namespace qerl {
 
 // Host-side count of kernel launches made by the library (qerl_launch_count).
 extern std::atomic<uint64_t> g_launches;
+// The same by QERL_KERNEL_* (qerl_kernel_launch_count).
+constexpr int kCountedKernels = 4;
+extern std::atomic<uint64_t> g_kernel_launches[kCountedKernels];
 
 // QERL_OK when the current device is compute capability 10.3, else
 // QERL_ERR_UNSUPPORTED_DEVICE (or QERL_ERR_CUDA).  Cached per device.
@@ -87,6 +90,11 @@ inline qerl_status launched(cudaError_t e)
 {
     if (e != cudaSuccess) return QERL_ERR_CUDA;
     return launched();
+}
+inline qerl_status launched(cudaError_t e, int kernel)
+{
+    if (e == cudaSuccess) g_kernel_launches[kernel].fetch_add(1, std::memory_order_relaxed);
+    return launched(e);
 }
 
 #define QERL_TRY(expr)                          \

@@ -1112,7 +1112,7 @@ size_t ring_slice(int64_t nvec, int cs) { return ((size_t)((nvec + cs - 1) / cs)
 // the launch would leave SMs idle and every CTA keeps a vector for half its
 // threads.
 template <bool BF16>
-cudaError_t launch_any(const LossArgs &a, cudaStream_t s)
+qerl_status launch_any(const LossArgs &a, cudaStream_t s)
 {
     constexpr int E = Vec<BF16>::E;
     const bool even = aligned16(a.x) && a.ld % E == 0;  // every row starts with a vector
@@ -1124,13 +1124,14 @@ cudaError_t launch_any(const LossArgs &a, cudaStream_t s)
                 int clusters = 0;
                 if ((int64_t)(kRingBytes / ring_slice(nvec, cs)) < least || a.T * cs <= num_sms()) continue;
                 const cudaError_t e = ring_clusters<BF16>(cs, clusters);
-                if (e != cudaSuccess) return e;
+                if (e != cudaSuccess) return QERL_ERR_CUDA;
                 if (16 * clusters * cs > 17 * best_clusters * best) best = cs, best_clusters = clusters;
             }
             if (!best) continue;
             const size_t slice = ring_slice(nvec, best);
             const int64_t stages = kRingBytes / slice;
-            return launch_ring<BF16>(a, best, best_clusters, stages > kMaxStages ? kMaxStages : (int)stages, slice, s);
+            return launched(launch_ring<BF16>(a, best, best_clusters, stages > kMaxStages ? kMaxStages : (int)stages, slice, s),
+                            QERL_KERNEL_LOSS_RING);
         }
     }
     const int nt = nvec <= 128 * 8 ? 128 : 256;
@@ -1138,7 +1139,7 @@ cudaError_t launch_any(const LossArgs &a, cudaStream_t s)
     while (cs < kMaxCluster && nvec > int64_t(nt) * 8 * cs) cs *= 2;
     while (cs < kMaxCluster && a.T * cs * 2 <= num_sms() && nvec >= int64_t(nt) * cs) cs *= 2;
     const int64_t per = (nvec + cs - 1) / cs, nv = (per + nt - 1) / nt;
-    return nt == 128 ? launch_nv<BF16, 128>(a, cs, nv, s) : launch_nv<BF16, 256>(a, cs, nv, s);
+    return launched(nt == 128 ? launch_nv<BF16, 128>(a, cs, nv, s) : launch_nv<BF16, 256>(a, cs, nv, s), QERL_KERNEL_LOSS_ROW);
 }
 
 bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -1184,7 +1185,7 @@ extern "C" qerl_status qerl_token_logp(const void *logits, int dtype, int64_t T,
     a.x = logits, a.ld = ld, a.T = T, a.V = V, a.ids = ids, a.ids64 = ids_bits == 64, a.weight = weight;
     set_scale(a, temperature);
     a.logp = logp, a.entropy = entropy;
-    return launched(dtype == QERL_DTYPE_BF16 ? launch_any<true>(a, as_cuda(stream)) : launch_any<false>(a, as_cuda(stream)));
+    return dtype == QERL_DTYPE_BF16 ? launch_any<true>(a, as_cuda(stream)) : launch_any<false>(a, as_cuda(stream));
 }
 
 extern "C" qerl_status qerl_policy_loss(const void *logits, int dtype, int64_t T, int64_t V, int64_t ld, const void *ids, int ids_bits,
@@ -1225,7 +1226,7 @@ extern "C" qerl_status qerl_policy_loss(const void *logits, int dtype, int64_t T
     a.logp = logp, a.entropy = entropy, a.terms = static_cast<float *>(ws), a.dx = dlogits, a.ldd = ldd;
     a.dx_vec = dlogits && ((reinterpret_cast<uintptr_t>(logits) ^ reinterpret_cast<uintptr_t>(dlogits)) & 15u) == 0 &&
                (uint64_t)(ld - ldd) * esize % 16 == 0;
-    if (T) QERL_TRY(launched(dtype == QERL_DTYPE_BF16 ? launch_any<true>(a, as_cuda(stream)) : launch_any<false>(a, as_cuda(stream))));
+    if (T) QERL_TRY(dtype == QERL_DTYPE_BF16 ? launch_any<true>(a, as_cuda(stream)) : launch_any<false>(a, as_cuda(stream)));
     return launched(launch_k(sum_kernel, dim3(1), dim3(kSumThreads), 0, as_cuda(stream), g_chain.load() != 0, (const float *)a.terms, T,
                              opts->beta, sums));
 }

@@ -428,14 +428,15 @@ template <int D>
 qerl_status run(const Args &a, const void *maps, cudaStream_t s)
 {
     const bool chain = g_chain.load() != 0, tc = a.p_tc || a.s_tc;
-    if (tc) QERL_TRY(launched(tc_launch(a, D, maps, s, chain)));
+    if (tc) QERL_TRY(launched(tc_launch(a, D, maps, s, chain), QERL_KERNEL_ATTN_ROWS128));
     const int64_t pi = a.p_tc ? 0 : (int64_t)a.n_prefix * a.Hkv * a.p_tiles * a.n_pp,
                   si = a.s_tc ? 0 : (int64_t)a.B * a.Hkv * a.s_tiles * a.n_sp;
     if (pi + si > 0) {
         static OncePerDevice once;
         if (allow_smem(once, rows16_kernel<D>, smem_bytes<D>()) != cudaSuccess) return QERL_ERR_CUDA;
         QERL_TRY(launched(launch_k(rows16_kernel<D>, dim3((unsigned)(pi + si)), dim3(kWarps * 32), smem_bytes<D>(), s, chain, a, (int)pi,
-                                   tc && chain ? 1 : 0)));
+                                   tc && chain ? 1 : 0),
+                          QERL_KERNEL_ATTN_ROWS16));
     }
     // a warp per row where its parts fit one batch or the rows fill the SMs, else four
     const int rows = a.B * a.Lq * a.Hq;

@@ -356,3 +356,27 @@ def test_plan_keeps_every_tensor():
     opt.step(1e-3, 1)
     torch.cuda.synchronize()
     assert q.get_error() == 0
+
+
+def test_roots_are_correctly_rounded():
+    """sqrt(v) against numpy's over v's whole range, by the scale it leaves (the block's largest root over the largest code):
+    a block per value, one element of it not zero, no gradient."""
+    nb = 1 << 16
+    r = np.random.RandomState(11)
+    code = r.randint(1, 256, nb).astype(np.uint8)
+    at = r.randint(0, 256, nb)
+    want_s = np.exp(r.uniform(np.log(1e-18), np.log(1e17), nb))
+    want_s[::4] = np.exp(r.uniform(np.log(1e-6), np.log(1e-1), len(want_s[::4])))  # where gradients' roots lie
+    scale = (want_s / value(code.astype(np.int64), 5)).astype(F)
+    codes = np.zeros((nb, 256), np.uint8)
+    codes[np.arange(nb), at] = code
+    dev = lambda x: torch.from_numpy(x).cuda()  # noqa: E731
+    n = nb * 256
+    p, g = torch.ones(n, device="cuda"), torch.zeros(n, device="cuda")
+    opt = q.AdamW([p], [g], m=[torch.zeros(n, dtype=torch.uint8, device="cuda")], v=[dev(codes.reshape(-1))],
+                  m_scale=[torch.zeros(nb, device="cuda")], v_scale=[dev(scale)], betas=(B1, B2), weight_decay=0.0)
+    opt.step(1e-3, 3, seed=1)
+    s = value(code.astype(np.int64), 5).astype(F) * scale
+    v = (s * s) * F(B2)
+    assert np.array_equal(opt.v_scale[0].cpu().numpy(), np.sqrt(v) / F(1.96875))
+    assert bool((p == 1.0).all()) and q.get_error() == 0
