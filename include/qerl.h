@@ -500,7 +500,8 @@ qerl_status qerl_swiglu(const void *g, const void *u, int64_t n, void *out, qerl
  *   lse     (device) optional float [B, Lq, Hq]
  *   P and S are capacities (either may be 0, its pointers NULL); the lengths are
  *   read on the device and taken into [0, P] and [0, S].  What lies beyond them
- *   is never used, whatever it holds.
+ *   is never used, whatever it holds; nor is, for a row, a key or value of a
+ *   later new token.
  *   D is 64 or 128, Hq % Hkv == 0, B % n_prefix == 0 (QERL_ERR_SHAPE); scale
  *   finite and > 0; the last dimension is contiguous, strides are multiples of
  *   8 elements and >= 0, pointers 16-byte aligned (QERL_ERR_ALIGN).

@@ -269,6 +269,50 @@ __device__ __forceinline__ int tc_parts(const Args &a, bool pre, int k, int hk, 
     return ((first + n - 1) / per_cta - first / per_cta + 1) * (single ? 2 : 1);
 }
 
+// The products of a tile run over keys that some of its rows do not see, with weight 0, and 0 times an Inf or NaN of V is NaN.
+// Over a warp, for a row whose sum is not finite while it has such keys (the new tokens after its own): where one of those
+// values is not finite, the columns that are not are summed again over the keys that the row sees.
+template <int D>
+__device__ __forceinline__ void sum_again(const Args &a, int b, int l, int h, int plen, int slen, float M, float (&acc)[D / 32])
+{
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x % 32, hk = h / a.gs, g = b / a.G, sees = max(0, slen - a.Lq + 1 + l);
+    const auto pair = [](const __nv_bfloat16 *p, int e) { return *reinterpret_cast<const uint32_t *>(p + e); };
+    const __nv_bfloat16 *vs = a.vs + b * a.vs_b + hk * a.vs_h + lane * E;
+    bool bad = false;
+    for (int k = sees; k < slen; ++k)
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            const uint32_t v = pair(vs + k * a.vs_t, e);
+            bad = bad || !isfinite(bf16lo(v)) || !isfinite(bf16hi(v));
+        }
+    if (!__any_sync(0xFFFFFFFFu, bad)) return;
+    float x[E], sum[E] = {};
+    const __nv_bfloat16 *q = a.q + b * a.q_b + l * a.q_l + h * a.q_h + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) x[e] = bf16lo(pair(q, e)) * a.scale_log2, x[e + 1] = bf16hi(pair(q, e)) * a.scale_log2;
+    const auto add = [&](const __nv_bfloat16 *k, const __nv_bfloat16 *v, int64_t k_t, int64_t v_t, int n) {
+#pragma unroll 1
+        for (int t = 0; t < n; ++t) {
+            float s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; e += 2) s = fmaf(x[e], bf16lo(pair(k + t * k_t, e)), fmaf(x[e + 1], bf16hi(pair(k + t * k_t, e)), s));
+            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+            const float w = ex2(s - M);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                sum[e] = fmaf(w, bf16lo(pair(v + t * v_t, e)), sum[e]);
+                sum[e + 1] = fmaf(w, bf16hi(pair(v + t * v_t, e)), sum[e + 1]);
+            }
+        }
+    };
+    add(a.kp + g * a.kp_g + hk * a.kp_h + lane * E, a.vp + g * a.vp_g + hk * a.vp_h + lane * E, a.kp_t, a.vp_t, plen);
+    add(a.ks + b * a.ks_b + hk * a.ks_h + lane * E, vs, a.ks_t, a.vs_t, min(sees, slen));
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (!isfinite(acc[e])) acc[e] = sum[e];
+}
+
 // W warps per query row (each takes every W-th part); the parts
 // that exist follow from the lengths.
 template <int D, int W>
@@ -350,6 +394,12 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a)
         }
     }
     if (!live) return;
+    if (a.Lq > 1) {
+        bool finite = true;
+#pragma unroll
+        for (int e = 0; e < E; ++e) finite = finite && isfinite(acc[e]);
+        if (!__all_sync(0xFFFFFFFFu, finite) && l + 1 < a.Lq && isfinite(L)) sum_again<D>(a, b, l, h, plen, slen, M, acc);
+    }
     const float inv = L == 0.0f ? 0.0f : __fdividef(1.0f, L);  // a row that sees no key: zeros, lse -inf
     uint32_t *out = reinterpret_cast<uint32_t *>(a.out + b * a.o_b + l * a.o_l + h * a.o_h + lane * E);
 #pragma unroll

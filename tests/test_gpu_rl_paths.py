@@ -308,3 +308,32 @@ def test_ring_repeats_on_another_stream_and_in_a_graph(T, V, dtype):
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and q.get_error() == 0
+
+
+@pytest.mark.parametrize("shape,kernels", [((5, 1, 3, 8, 2, 128, 40, 90), (q.KERNEL_ATTN_ROWS16,)), ((2, 2, 33, 8, 2, 64, 100, 300), (q.KERNEL_ATTN_ROWS16,))]
+                         + [SHAPES[k] for k in (0, 1, 2, 5)])
+@pytest.mark.parametrize("junk", [NAN, INF, -INF])
+def test_values_that_a_new_token_does_not_see(shape, kernels, junk):
+    """A value of a later new token that is not finite reaches no earlier row, and no other column of the rows that see it;
+    those get the formula's Inf or NaN."""
+    B, n, Lq, Hq, Hkv, D, P, S = shape
+    x = at.inputs(*shape, 46)
+    pn = at.spread(n, P // 2, P)
+    sn = [S - (k * 29) % (S - Lq) for k in range(B)]
+    with takes(*kernels):
+        _, wl = at.check(*x, pn, sn)
+    want, _, tol, _ = at.reference(*x, pn, sn, D ** -0.5)
+    seen = torch.zeros(B, Lq, Hq, D, dtype=torch.bool, device="cuda")
+    for b in range(B):
+        for i, j in enumerate(sorted({Lq - 1, Lq // 2, 1, (b * 37) % Lq})):  # new token j, one kv head, every few columns
+            hk, cols = (b + i) % Hkv, slice(i, D, 24)
+            x[4][b, sn[b] - Lq + j, hk, cols] = junk
+            seen[b, j:, hk * (Hq // Hkv):(hk + 1) * (Hq // Hkv), cols] = True
+    with takes(*kernels):
+        got, lse = torch.full_like(x[0], NAN), torch.full_like(wl, NAN)
+        q.PrefixAttention(*x[1:], Hq, Lq).run(x[0], at.i32(sn), at.i32(pn), out=got, lse=lse)
+    assert torch.equal(lse, wl)
+    assert bool(((got.double() - want).abs() <= tol)[~seen].all())
+    there = got[seen].float()
+    assert bool((torch.isnan(there) if math.isnan(junk) else there == junk).all())
+    assert q.get_error() == 0
