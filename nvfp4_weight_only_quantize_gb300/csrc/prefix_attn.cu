@@ -446,8 +446,11 @@ bool shape(const qerl_prefix_attn_dims *d, Args &a, bool tc)
     if (a.p_tc && !a.s_tc) {
         // The prefixes on tcgen05 leave SMs to the suffixes, which then run beside them: an SM takes 2 us per step, or reads
         // 50 bytes per ns.  As many as make the later of the two end soonest, against one after the other.
+        // The suffixes are taken as half full, which a rollout's caches are on average (the host does not know the lengths).
+        // 64 sequences, 28 / 4 heads, 16384 + up to 999 keys, the caches 2, 50 and 100 % full: 42, 44, 56 us; taken as full
+        // 48, 51, 56 us, as 30 % full 40, 47, 57 us.
         const double steps = (double)a.n_prefix * a.Hkv * (pr / 256 + 1) * ((a.P + 127) / 128);
-        const double bytes = 0.6 * (double)a.B * a.Hkv * a.S * (double)(d->D * 4);
+        const double bytes = 0.5 * (double)a.B * a.Hkv * a.S * (double)(d->D * 4);
         const int sms = num_sms();
         double best = 2.0 * ceil(steps / sms) + bytes / 6.0e6;
         for (int n = sms - 4; n >= sms / 2; n -= 4) {
