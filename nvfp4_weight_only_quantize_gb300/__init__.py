@@ -184,15 +184,12 @@ def _new(make, stream, *args, **kw):
     return t
 
 
-def _launch_on(stream, seen, tensors):
-    """The launch stream's handle.  An object's own tensors stay allocated, after it is dropped, until every stream that
-    it was launched on (`seen`: at first the one that it was made on) has finished with them."""
-    handle = _stream(stream)
-    if handle not in seen:
-        for t in tensors:
-            t.record_stream(torch.cuda.current_stream() if stream is None else stream)
-        seen.add(handle)
-    return handle
+def _hold(stream, handle, seen, tensors):
+    """Called for a launch stream that is not among `seen`, those that an object was launched on (at first the one that it was
+    made on): its own tensors then stay allocated, after it is dropped, until that stream has finished with them."""
+    for t in tensors:
+        t.record_stream(torch.cuda.current_stream() if stream is None else stream)
+    seen.add(handle)
 
 
 def set_linear_algo(algo: int):
@@ -505,8 +502,10 @@ class DecoderChain:
         self._h = h
 
     def run(self, sigma: float, seed: int, step: int, first_layer: int = 0, stream=None):
-        _check(lib().qerl_decoder_chain_run(self._h, float(sigma), seed, step, first_layer,
-                                            _launch_on(stream, self._launched_on, (self.ws,))),
+        handle = _stream(stream)
+        if handle not in self._launched_on:
+            _hold(stream, handle, self._launched_on, (self.ws,))
+        _check(lib().qerl_decoder_chain_run(self._h, float(sigma), seed, step, first_layer, handle),
                "qerl_decoder_chain_run")
 
     def close(self):
@@ -581,10 +580,12 @@ class PrefixAttention:
             assert strides[0][3] == strides[1][3] == 1
             d.q_stride[:], d.out_stride[:] = strides[0][:3], strides[1][:3]
             self._strides = strides
+        handle = _stream(stream)
+        if handle not in self._launched_on:
+            _hold(stream, handle, self._launched_on, (self.ws,))
         kp, vp, ks, vs = self._p
         _check(lib().qerl_prefix_attention(self._ref, q.data_ptr(), kp, vp, _p(prefix_lens), ks, vs, suffix_lens.data_ptr(),
-                                           self._scale, out.data_ptr(), _p(lse), self._ws[0], self._ws[1],
-                                           _launch_on(stream, self._launched_on, (self.ws,))),
+                                           self._scale, out.data_ptr(), _p(lse), self._ws[0], self._ws[1], handle),
                "qerl_prefix_attention")
         return out
 
@@ -733,16 +734,20 @@ class AdamW:
         them, which goes to grad_norm (f32 [1]) if given."""
         hy = self._hyper
         hy.lr, hy.step, hy.seed, hy.max_grad_norm = lr, step, seed, max_grad_norm
-        _check(lib().qerl_adamw_step(self._h, C.byref(hy), _p(grad_norm), _launch_on(stream, self._launched_on, self._own)),
-               "qerl_adamw_step")
+        handle = _stream(stream)
+        if handle not in self._launched_on:
+            _hold(stream, handle, self._launched_on, self._own)
+        _check(lib().qerl_adamw_step(self._h, C.byref(hy), _p(grad_norm), handle), "qerl_adamw_step")
 
     def read_state(self, m_out, v_out, stream=None):
         """The values of the 8-bit states, f32 or bf16: the tensors in order, each from a multiple of 256 elements on."""
         size = self._flat
         assert m_out.dtype == v_out.dtype and m_out.dtype in _DTYPES and m_out.is_contiguous() and v_out.is_contiguous()
         assert m_out.numel() >= size and v_out.numel() >= size
-        _check(lib().qerl_adamw_read_state(self._h, _p(m_out), _p(v_out), _DTYPES[m_out.dtype],
-                                           _launch_on(stream, self._launched_on, self._own)),
+        handle = _stream(stream)
+        if handle not in self._launched_on:
+            _hold(stream, handle, self._launched_on, self._own)
+        _check(lib().qerl_adamw_read_state(self._h, _p(m_out), _p(v_out), _DTYPES[m_out.dtype], handle),
                "qerl_adamw_read_state")
 
     def close(self):
