@@ -479,8 +479,9 @@ qerl_status qerl_residual_add(const void *h, const void *y, int64_t n, void *out
 qerl_status qerl_swiglu(const void *g, const void *u, int64_t n, void *out, qerl_stream_t stream);
 
 /*
- * The rest of an RL step around the linears: attention of the rollout batch,
- * the policy loss with its gradient, and the adapters' optimizer ("QeRL: Beyond
+ * Three more parts of an RL step around the linears: attention of the rollout
+ * batch (forward only), the policy loss with its gradient, and the adapters'
+ * optimizer ("QeRL: Beyond
  * Efficiency", summary: GRPO and DAPO; bitsofall, "Workflow: Rollout, Update,
  * Quantization": several answers are sampled for each prompt and only the LoRA
  * matrices are updated).
@@ -596,7 +597,9 @@ qerl_status qerl_policy_loss(const void *logits, int dtype, int64_t T, int64_t V
  * 1; a block whose largest magnitude is below 2^-100 is stored as zero.
  * step counts from 1 and is a host value: a captured graph repeats its step.
  * With max_grad_norm > 0 the norm of all gradients goes to grad_norm (device,
- * optional), and a norm that is not finite leaves everything unchanged.  Without
+ * optional), and a norm that is not finite leaves everything unchanged.  Its
+ * squares are FP32: an element beyond 1.8e19 makes it infinite, elements below
+ * 1e-19 may count as 0.  Without
  * it Inf and NaN enter the tensors they are in.  Results are the same on every
  * run, clip included.
  */

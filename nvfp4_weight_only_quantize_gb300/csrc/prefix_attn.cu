@@ -12,7 +12,7 @@
 // Bound by HBM where the suffixes are most of the keys (rows16_kernel: each is read
 // by one CTA, for its up to 16 rows), by the tensor cores and shared memory where
 // many rows share a prefix (the tcgen05 kernel), by latency below some 10 us.
-// 64 sequences of up to 4096 own tokens, 40 / 8 heads, D = 128: 99 us, 82 % of
+// 64 sequences of up to 4096 own tokens, 40 / 8 heads, D = 128: 100 us, 82 % of
 // the measured copy rate.  Eight of a group of 512 + 1024 keys 11 us; one
 // sequence over 512 keys 9 us a call, 6 us in a graph.
 #include <float.h>
@@ -27,7 +27,7 @@ namespace {
 
 // ------------------------------------------------------------------ chunks of up to 16 rows
 constexpr int kWarps = 4;    // a warp takes every fourth 16-key tile of the chunk
-constexpr int kStages = 2;   // tiles in flight per warp
+constexpr int kStages = 2;   // tile buffers per warp (a tile's load is issued after the products of the one before it)
 constexpr int kTile = 16;
 
 template <int D>

@@ -24,8 +24,8 @@
 // halves and the tiles' arrival in shared memory come to some 0.78 of the 0.95 us.
 // One S with two P instead, so that Q K^T waits for no P V, took as long.  A unit's
 // rows cost about 6 us besides (loads of Q, first S, stores of O).
-// 28 query heads of 64 sequences over a prefix of 16384 keys: 12 steps on each of 88
-// CTAs, 36 us; with the suffixes, on the other SMs meanwhile, and the join 46 us.
+// 28 query heads of 64 sequences over a prefix of 16384 keys: 11 steps on each of 96
+// CTAs; with the suffixes, on the other SMs meanwhile, and the join (8 us) 45 us.
 // 129 tokens of eight sequences, 16 heads, over 4001 keys and their own: 18 steps a
 // CTA, its starts among them, 54 us, and 14 for the join of 2 to 5 parts a row.
 #include <cuda.h>
