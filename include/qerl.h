@@ -527,6 +527,66 @@ qerl_status qerl_prefix_attention(const qerl_prefix_attn_dims *dims, const void 
                                   qerl_stream_t stream);
 
 /*
+ * Keys and values in 4 bits: a cache in NVFP4 ("bitsofall", "NVFP4" section: E2M1
+ * codes, an E4M3 scale per 16 values, here with one fixed FP32 factor per cache
+ * instead of a tensor scale, because tokens arrive one after the other), the
+ * quantisation of new tokens into it, its values back, and the attention over it.
+ * The pages keep the cache in bf16; this is the library's own.
+ *
+ * data (device): for sequence i of n, kv head h and tile t of 32 tokens, 36 D bytes
+ * at i * stride[0] + h * stride[1] + t * stride[2] (bytes, multiples of 16, any
+ * order, no overlap), ceil(T / 32) tiles.  What a tile holds is the library's affair.
+ * T is the capacity in tokens; D is 64 or 128; factors in [1e-30, 1e30].
+ */
+typedef struct {
+    void *data;
+    int64_t n, T, Hkv, D;
+    int64_t stride[3];
+    float k_scale, v_scale;
+} qerl_kv4_cache;
+
+/*
+ * Quantises L new tokens of every sequence into the cache, and reads back what it
+ * holds of the last L tokens.
+ *   k, v (device) bf16 [n, L, Hkv, D], strides of n, L, Hkv in elements (multiples
+ *   of 8, >= 0), 16-byte aligned.  lens (device) int32 [n]: tokens of each sequence,
+ *   the new ones among them, taken into [0, T].  counts (device) int32 [n] or NULL
+ *   (L): how many of the L are tokens; the rest is not read.  New token l gets
+ *   position len - count + l; one before position 0 is left out.
+ *   Per block of 16 along D: scale byte s = smallest E4M3 >= amax / (6 factor),
+ *   code = nearest E2M1 of w / (s factor), ties to the even code.  Inf or NaN latches
+ *   QERL_ERR_NONFINITE; Inf is stored as the largest value, NaN as 0.
+ * Read returns e2m1 * e4m3 * factor rounded to bf16 (exact where the factor is a
+ * power of two), and zeros for positions before 0.
+ */
+qerl_status qerl_kv4_append(const qerl_kv4_cache *cache, int64_t L, const void *k, const int64_t *k_stride, const void *v,
+                            const int64_t *v_stride, const int32_t *lens, const int32_t *counts, qerl_stream_t stream);
+qerl_status qerl_kv4_read(const qerl_kv4_cache *cache, int64_t L, const int32_t *lens, void *k, const int64_t *k_stride, void *v,
+                          const int64_t *v_stride, qerl_stream_t stream);
+
+/*
+ * qerl_prefix_attention over 4-bit caches: sequence b of B sees all keys of prefix
+ * b / (B / prefix->n) and, token l of its Lq new ones, the own keys 0 .. len_b - Lq + l.
+ *   q, out (device) bf16 [B, Lq, Hq, D], lse (device) optional float [B, Lq, Hq],
+ *   lengths, strides, alignment and empty rows as there.  prefix (n divides B) or
+ *   suffix (n = B) may be NULL; both have the same Hkv and D; prefix_lens NULL means
+ *   full.  What lies beyond the lengths is never used, whatever it holds.
+ *   ws (device) >= qerl_kv4_attention_ws_bytes, contents on entry ignored; calls that
+ *   may overlap need a workspace each.
+ * Keys are multiplied exactly as bf16; probabilities are rounded to fp16, and their
+ * product with a value's scale again; sums are FP32.  Results are the same on every
+ * run.
+ */
+typedef struct {
+    int64_t B, Lq, Hq;
+    int64_t q_stride[3], out_stride[3]; /* B, Lq, Hq */
+} qerl_kv4_attn_dims;
+size_t qerl_kv4_attention_ws_bytes(const qerl_kv4_attn_dims *dims, const qerl_kv4_cache *prefix, const qerl_kv4_cache *suffix);
+qerl_status qerl_kv4_attention(const qerl_kv4_attn_dims *dims, const void *q, const qerl_kv4_cache *prefix, const int32_t *prefix_lens,
+                               const qerl_kv4_cache *suffix, const int32_t *suffix_lens, float scale, void *out, float *lse, void *ws,
+                               size_t ws_bytes, qerl_stream_t stream);
+
+/*
  * Log-probability of each row's chosen token and the entropy of its
  * distribution p = softmax(x / temperature):
  *     logp[t] = ln p[ids[t]],   entropy[t] = -sum_j p_j ln p_j

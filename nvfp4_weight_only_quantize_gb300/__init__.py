@@ -46,7 +46,8 @@ EXPORTED = ["qerl_nvfp4_quantize", "qerl_nvfp4_dequantize", "qerl_nvfp4_lora_lin
             "qerl_decoder_chain_run", "qerl_decoder_chain_destroy", "qerl_mxfp4_quantize",
             "qerl_mxfp4_lora_linear_fwd", "qerl_nvfp4_lora_linear_fwd_f32ab", "qerl_residual_add", "qerl_swiglu",
             "qerl_prefix_attention_ws_bytes", "qerl_prefix_attention", "qerl_token_logp", "qerl_policy_loss",
-            "qerl_adamw_ws_bytes", "qerl_adamw_plan", "qerl_adamw_step", "qerl_adamw_read_state", "qerl_adamw_destroy"]
+            "qerl_adamw_ws_bytes", "qerl_adamw_plan", "qerl_adamw_step", "qerl_adamw_read_state", "qerl_adamw_destroy",
+            "qerl_kv4_append", "qerl_kv4_read", "qerl_kv4_attention_ws_bytes", "qerl_kv4_attention"]
 
 
 class QerlError(RuntimeError):
@@ -128,6 +129,10 @@ def lib() -> C.CDLL:
             sig["qerl_adamw_step"] = ([vp, vp, vp, vp], i32)
             sig["qerl_adamw_read_state"] = ([vp, vp, vp, i32, vp], i32)
             sig["qerl_adamw_destroy"] = ([vp], None)
+            sig["qerl_kv4_append"] = ([vp, i64, vp, vp, vp, vp, vp, vp, vp], i32)
+            sig["qerl_kv4_read"] = ([vp, i64, vp, vp, vp, vp, vp, vp], i32)
+            sig["qerl_kv4_attention_ws_bytes"] = ([vp, vp, vp], sz)
+            sig["qerl_kv4_attention"] = ([vp, vp, vp, vp, vp, vp, f32, vp, vp, vp, sz, vp], i32)
             sig["qerl_nvfp4_lora_linear_fwd_packed"] = sig["qerl_nvfp4_lora_linear_fwd"]
             sig["qerl_nvfp4_lora_linear_bwd_packed"] = sig["qerl_nvfp4_lora_linear_bwd"]
             for name, (args, res) in sig.items():
@@ -596,6 +601,117 @@ def qerl_prefix_attention(q, k_prefix, v_prefix, k_suffix, v_suffix, suffix_lens
     with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):  # the workspace is that stream's
         plan = PrefixAttention(k_prefix, v_prefix, k_suffix, v_suffix, q.shape[2], q.shape[1], scale, ws)
     return plan.run(q, suffix_lens, prefix_lens, out, lse, stream)
+
+
+# ---------------------------------------------------------------- keys and values in 4 bits
+class _Kv4Cache(C.Structure):
+    _fields_ = [("data", C.c_void_p)] + [(n, C.c_int64) for n in ("n", "T", "Hkv", "D")] + [
+        ("stride", C.c_int64 * 3), ("k_scale", C.c_float), ("v_scale", C.c_float)]
+
+
+class _Kv4AttnDims(C.Structure):
+    _fields_ = [(n, C.c_int64) for n in ("B", "Lq", "Hq")] + [("q_stride", C.c_int64 * 3), ("out_stride", C.c_int64 * 3)]
+
+
+class Kv4Cache:
+    """Keys and values of n sequences in NVFP4, up to T tokens each (qerl_kv4_cache): append and read.
+
+    k_scale, v_scale: the fixed factors of the keys' and the values' scales (values from about 1e-3 to 2688 times the
+    factor are held well).  data: uint8 [n, Hkv, ceil(T / 32), 36 D], zeros if None; its strides may be any multiples of 16
+    with the last dimension contiguous.  A stream other than the one that was current when the object was made has to
+    wait for that one before its first call, as for any tensor made there."""
+
+    def __init__(self, n: int, T: int, Hkv: int, D: int, k_scale: float = 1.0, v_scale: float = 1.0, device="cuda", data=None):
+        shape = (n, Hkv, -(-T // 32), 36 * D)
+        self._own = data is None
+        self.data = torch.zeros(shape, dtype=torch.uint8, device=device) if data is None else data
+        assert self.data.shape == shape and self.data.dtype == torch.uint8 and self.data.stride(3) == 1
+        self.n, self.T, self.Hkv, self.D = n, T, Hkv, D
+        self._c = _Kv4Cache(self.data.data_ptr(), n, T, Hkv, D, (C.c_int64 * 3)(*self.data.stride()[:3]), k_scale, v_scale)
+        self._ref = C.byref(self._c)
+        self._launched_on = {_stream()} if self.data.is_cuda else set()
+
+    def _tokens(self, k, v, lens):
+        assert k.dtype == v.dtype == torch.bfloat16 and k.shape == v.shape and k.shape[::2] == (self.n, self.Hkv) and k.shape[3] == self.D
+        assert (k.stride(3) == v.stride(3) == 1) or k.numel() == 0
+        assert lens.dtype == torch.int32 and lens.is_contiguous() and lens.numel() == self.n
+        st = C.c_int64 * 3
+        return (_p(k) or 16, st(*k.stride()[:3]), _p(v) or 16, st(*v.stride()[:3]))  # an empty tensor has no address
+
+    def _launch(self, stream):
+        handle = _stream(stream)
+        if self._own and handle not in self._launched_on:
+            _hold(stream, handle, self._launched_on, (self.data,))
+        return handle
+
+    def append(self, k, v, lens, counts=None, stream=None):
+        """k, v bf16 [n, L, Hkv, D]: the last tokens of sequences that are lens (int32 [n]) long with them; counts
+        (int32 [n]): how many of the L each sequence has, all if None."""
+        args = self._tokens(k, v, lens)
+        assert counts is None or (counts.dtype == torch.int32 and counts.is_contiguous() and counts.numel() == self.n)
+        _check(lib().qerl_kv4_append(self._ref, k.shape[1], *args, lens.data_ptr(), _p(counts), self._launch(stream)), "qerl_kv4_append")
+
+    def read(self, lens, L: int, k=None, v=None, stream=None):
+        """The values held of the last L tokens of sequences that are lens long: (k, v) bf16 [n, L, Hkv, D]."""
+        k = _new(torch.empty, stream, self.n, L, self.Hkv, self.D, dtype=torch.bfloat16, device=self.data.device) if k is None else k
+        v = _new(torch.empty, stream, self.n, L, self.Hkv, self.D, dtype=torch.bfloat16, device=self.data.device) if v is None else v
+        kp, ks, vp, vs = self._tokens(k, v, lens)
+        assert k.shape[1] == L
+        _check(lib().qerl_kv4_read(self._ref, L, lens.data_ptr(), kp, ks, vp, vs, self._launch(stream)), "qerl_kv4_read")
+        return k, v
+
+
+class Kv4Attention:
+    """PrefixAttention over 4-bit caches (qerl_kv4_attention).
+
+    suffix: Kv4Cache of the B sequences' own tokens; prefix: Kv4Cache of n_prefix shared ones (sequence b reads prefix
+    b // (B // n_prefix)), or None; suffix None: batch sequences that have only their prefix.  The caches are kept
+    referenced; the workspace is this object's (calls that may overlap need an object each)."""
+
+    def __init__(self, suffix, q_heads: int, q_len: int = 1, prefix=None, scale: float = None, batch: int = None, ws=None):
+        one = suffix if suffix is not None else prefix
+        B = suffix.n if suffix is not None else batch
+        self._caches = (prefix, suffix)
+        self._pref, self._suf = (None if c is None else c._ref for c in self._caches)
+        self._d = _Kv4AttnDims(B, q_len, q_heads)
+        nbytes = lib().qerl_kv4_attention_ws_bytes(C.byref(self._d), self._pref, self._suf)
+        if nbytes == 0:
+            raise QerlError(2, "qerl_kv4_attention_ws_bytes")
+        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=one.data.device) if ws is None else ws
+        self._ws = (self.ws.data_ptr(), self.ws.numel())
+        self._launched_on = {_stream()}
+        self._q_shape = torch.Size((B, q_len, q_heads, one.D))
+        self._scale = one.D ** -0.5 if scale is None else float(scale)
+        self._strides = None  # of the last q and out
+        self._ref = C.byref(self._d)
+
+    def run(self, q, suffix_lens=None, prefix_lens=None, out=None, lse=None, stream=None):
+        """q bf16 [B, Lq, Hq, D], suffix_lens int32 [B] (new tokens included), prefix_lens int32 [n_prefix] or None
+        (full) -> out bf16 like q; lse f32 [B, Lq, Hq] is filled if given."""
+        d = self._d
+        prefix, suffix = self._caches
+        if out is None:
+            out = _new(torch.empty, stream, self._q_shape, dtype=torch.bfloat16, device=q.device)
+        assert q.shape == self._q_shape and out.shape == self._q_shape and q.dtype == out.dtype == torch.bfloat16
+        assert (suffix is None) == (suffix_lens is None) and (prefix is not None or prefix_lens is None)
+        for t, n in ((suffix_lens, d.B), (prefix_lens, prefix.n if prefix is not None else 0)):
+            assert t is None or (t.dtype == torch.int32 and t.is_contiguous() and t.numel() == n)
+        if lse is not None:
+            assert lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == self._q_shape[:3]
+        strides = (q.stride(), out.stride())
+        if strides != self._strides:
+            assert strides[0][3] == strides[1][3] == 1
+            d.q_stride[:], d.out_stride[:] = strides[0][:3], strides[1][:3]
+            self._strides = strides
+        handle = _stream(stream)
+        if handle not in self._launched_on:
+            _hold(stream, handle, self._launched_on, (self.ws,))
+        for c in self._caches:
+            if c is not None and handle not in c._launched_on:
+                c._launch(stream)
+        _check(lib().qerl_kv4_attention(self._ref, q.data_ptr(), self._pref, _p(prefix_lens), self._suf, _p(suffix_lens), self._scale,
+                                        out.data_ptr(), _p(lse), self._ws[0], self._ws[1], handle), "qerl_kv4_attention")
+        return out
 
 
 # ---------------------------------------------------------------- policy loss

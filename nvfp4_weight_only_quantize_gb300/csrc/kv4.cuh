@@ -1,0 +1,55 @@
+// The 4-bit key/value cache: keys and values in NVFP4 (E2M1 codes, an E4M3 scale
+// per 16 values along the head, one fixed FP32 factor per cache).
+//
+// A tile holds 32 tokens of one sequence and kv head in 36 D bytes, in one piece,
+// so that one bulk copy brings it to shared memory:
+//   keys' codes    [32 tokens][D / 2]: words of eight dims in the packed code order
+//                  (packed_layout.cuh), which the dequantizer takes as it is;
+//   values' codes  16 D bytes: a word holds eight tokens of one dim (token 8 q + n
+//                  in nibble n), because the second product sums over tokens;
+//   keys' scales   2 D bytes,  values' scales 2 D bytes.
+// Codes and scales lie in the order in which the lanes of a warp take them for
+// the tensor core's fragments (lane = 4 r + q): 16 bytes a lane, no bank conflict.
+#pragma once
+
+#include "common.cuh"
+
+namespace qerl {
+namespace kv4 {
+
+constexpr int kTok = 32;  // tokens of a tile
+
+struct Cache {
+    uint8_t *data;
+    int64_t s_n, s_h, s_t;  // bytes from sequence to sequence, head to head, tile to tile
+    int n, T, Hkv;
+    float k_scale, v_scale;
+};
+
+template <int D>
+struct Tile {
+    static constexpr int B = D / 16;  // blocks of a token
+    static constexpr int KC = 0, VC = kTok * D / 2, KS = 2 * VC, VS = KS + kTok * B, BYTES = VS + kTok * B;
+    // offset of the key word that holds dims 8 w .. 8 w + 7 of token t
+    static __device__ __forceinline__ int k_word(int t, int w) { return KC + t * (D / 2) + w * 4; }
+    // Offset of the key scale of token t, block b.  Lane (r, q) multiplies tokens 8 (r / 2) + r % 2 + 2 e, e = 0..3, and dims
+    // from D / 4 q on.
+    static __device__ __forceinline__ int k_scale(int t, int b)
+    {
+        constexpr int per = D / 64;  // blocks of a lane
+        const int r = 2 * (t / 8) + t % 2, e = (t % 8) / 2;
+        return KS + ((r * 4 + b / per) * 4 + e) * per + b % per;
+    }
+    // offset of the word of dim d, tokens 8 q .. 8 q + 7: sixteen dims are a row tile of the product, two of them a 16-byte piece
+    static __device__ __forceinline__ int v_word(int d, int q)
+    {
+        return VC + (((d / 32) * 32 + (d % 8) * 4 + q) * 4 + (d % 32) / 8) * 4;
+    }
+    static __device__ __forceinline__ int v_scale(int t, int b) { return VS + ((t / 8) * B + b) * 8 + t % 8; }
+};
+
+// What the entry points share: the cache's description checked and taken over.
+qerl_status check_cache(const qerl_kv4_cache *c, Cache &out);
+
+}  // namespace kv4
+}  // namespace qerl

@@ -1,0 +1,640 @@
+// Attention over 4-bit caches: prefixes that groups of sequences share, and every
+// sequence's own tokens, in one softmax.
+//
+//   a_k = scale q . k_k,  lse = log sum_k e^(a_k),  out = sum_k e^(a_k - lse) v_k
+//
+// A warp takes whole tiles of 32 keys, which bulk copies bring to its own ring in
+// shared memory, and multiplies them as the m operand of mma.sync, so that the
+// query rows, few in decoding, are the narrow side (8 columns) and nothing is
+// padded to 16:
+//   S^T = K Q^T     K dequantised in registers to bf16 (e2m1 * e4m3 is exact there),
+//                   Q as it is;
+//   P = 2^(S c - m) per column, rounded to fp16 and turned (movmatrix);
+//   O^T += V^T (P s)  V's codes converted to fp16 as they are; their scales s, which
+//                   differ by key, multiply P instead (half as many products).  P
+//                   stays at most 2^7, so that P s stays finite (s <= 448).
+// m is raised only when a column's maximum outgrows it by 2^7.
+// K takes the integer pipe (bit fields) and V the conversion pipe, which alone
+// would each bound a tile at about HBM's rate.
+#include "kv4_attn.cuh"
+
+#include <float.h>
+#include <math.h>
+
+#include "dequant.cuh"
+#include "sm100_ptx.cuh"
+
+namespace qerl {
+namespace kv4 {
+namespace {
+
+using namespace ptx;
+
+constexpr int kWarps = 4, kStages = 3;
+constexpr float kHead = 4.0f, kRoom = 7.0f;  // m is set kHead below a maximum, and raised above kRoom
+constexpr uint64_t kLimitNs = 2000000000ull;
+
+template <int D, int NT>
+struct Smem {
+    static constexpr int RING = kWarps * kStages * Tile<D>::BYTES, ROW = D + 4;  // padded: the warps' rows meet without bank conflicts
+    static constexpr int O = RING, ML = O + kWarps * 8 * NT * ROW * 4, TOTAL = ML + kWarps * 8 * NT * 8;
+};
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t turned(uint32_t a)
+{
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+// The four code pairs of a word as fp16 pairs, and the two scale pairs of a word.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&o)[4])
+{
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+        : "r"(w));
+}
+__device__ __forceinline__ void scales_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w));
+}
+
+// Where a warp stands on its CTA's range of the line.
+struct Place {
+    int seg, unit, T, i0, i1, left, off;  // segment, unit in it, its tiles, the range inside it, steps from i0 to the end, from the CTA's start to i0
+};
+__device__ __forceinline__ bool next_unit(const Side &s, int units, Place &p)
+{
+    p.off += p.i1 - p.i0;
+    p.left -= p.i1 - p.i0;
+    if (p.left <= 0) return false;
+    if (++p.unit == units) {
+        p.unit = 0;
+        do p.T = tiles_of(length(s, ++p.seg));
+        while (p.T == 0);
+    }
+    p.i0 = 0;
+    p.i1 = min(p.T, p.left);
+    return true;
+}
+
+template <int D, int NT, int PER_SM>
+__global__ void __launch_bounds__(kWarps * 32, PER_SM) rows_kernel(const Call a, const Side s, int beside, unsigned int *err)
+{
+    using M = Tile<D>;
+    using S = Smem<D, NT>;
+    constexpr int MT = D / 16, KW = D / 32, R = 8 * NT;  // row tiles of O^T; key words of a lane; query rows
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t s_full[kWarps][kStages];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, q = lane % 4;
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < kWarps * kStages; ++k) mbar_init(&s_full[0][0] + k, 1);
+        fence_mbar_init();
+    }
+    // Beside the prefixes' kernel, whose CTAs let this one start once all work before both has finished, there is nothing to
+    // wait for; its last CTA waits at its end, so that the join, which waits for this kernel, has both.
+    if (!beside) pdl_wait();
+    pdl_trigger();
+    __syncthreads();
+
+    const int units = s.c.Hkv * s.row_tiles;
+    int total = 0;
+    for (int k = lane; k < s.c.n; k += 32) total += tiles_of(length(s, k)) * units;
+    total = __reduce_add_sync(0xFFFFFFFFu, total);
+    const int per = max((total + s.grid - 1) / s.grid, kWarps);
+    const int begin = min((int64_t)blockIdx.x * per, (int64_t)total), end = min(begin + per, total);
+    Place at = {};
+    for (int k0 = 0, before = 0; k0 < s.c.n; k0 += 32) {
+        const int k = k0 + lane, T = k < s.c.n ? tiles_of(length(s, k)) : 0;
+        int sum = T * units;
+        for (int o = 1; o < 32; o *= 2) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        const int from = before + sum - T * units;
+        if (blockIdx.x == 0 && warp == 0) {
+            if (k < s.c.n) s.line[1 + k] = from;
+            if (k == 0) s.line[0] = per;
+        }
+        const uint32_t here = __ballot_sync(0xFFFFFFFFu, begin >= from && begin < before + sum);
+        if (here) {
+            const int src = __ffs(here) - 1;
+            at.seg = k0 + src;
+            at.T = __shfl_sync(0xFFFFFFFFu, T, src);
+            const int in = begin - __shfl_sync(0xFFFFFFFFu, from, src);
+            at.unit = in / at.T;
+            at.i0 = in - at.unit * at.T;
+            at.left = end - begin;
+            at.i1 = min(at.T, at.i0 + at.left);
+        }
+        before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    if (begin < end) {
+        uint8_t *const ring = smem + warp * kStages * M::BYTES;
+        // the first of this warp's tiles from i0 on: every fourth step of the CTA's range
+        const auto first = [&](const Place &p) { return p.i0 + ((warp - p.off) & (kWarps - 1)); };
+        Place ahead = at;
+        int fi = first(ahead), fetched = 0, used = 0;
+        bool more = true, dead = false;
+        const auto fetch = [&]() {
+            while (more && fi >= ahead.i1) {
+                more = next_unit(s, units, ahead);
+                if (more) fi = first(ahead);
+            }
+            if (!more || dead) return;
+            const int st = fetched % kStages;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&s_full[warp][st], M::BYTES);
+                bulk_load(ring + st * M::BYTES, s.c.data + ahead.seg * s.c.s_n + (ahead.unit / s.row_tiles) * s.c.s_h + fi * s.c.s_t, M::BYTES,
+                          &s_full[warp][st]);
+            }
+            ++fetched;
+            fi += kWarps;
+        };
+#pragma unroll
+        for (int k = 0; k < kStages - 1; ++k) fetch();
+
+        for (bool go = true; go; go = next_unit(s, units, at)) {
+            const int len = length(s, at.seg), hk = at.unit / s.row_tiles, tile = at.unit - hk * s.row_tiles;
+            // Q^T: lane (r, q) holds dims D / 4 q .. of row r, four of them a step
+            uint32_t qf[NT][D / 16][2];
+            int limit[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int rr = tile * R + n * 8 + r;
+                const Row w = row_of(a, s, at.seg, hk, rr);
+                const uint4 *from = reinterpret_cast<const uint4 *>(a.q + w.b * a.q_b + w.l * a.q_l + w.h * a.q_h + q * (D / 4));
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint4 v = rr < s.rows ? from[i] : make_uint4(0, 0, 0, 0);
+                    qf[n][2 * i][0] = v.x, qf[n][2 * i][1] = v.y, qf[n][2 * i + 1][0] = v.z, qf[n][2 * i + 1][1] = v.w;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    limit[n][e] = s.suffix ? len - a.Lq + 1 + row_of(a, s, at.seg, hk, tile * R + n * 8 + 2 * q + e).l : len;
+            }
+            const int all_see = s.suffix ? len - a.Lq + 1 : len;  // keys that every row sees
+            float o[MT][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                m[n][0] = m[n][1] = kNone;
+                l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+                for (int t = 0; t < MT; ++t) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.0f;
+            }
+            for (int i = first(at); i < at.i1; i += kWarps) {
+                const int st = used % kStages;
+                if (!dead) {
+                    bool ok = false;
+                    for (int k = 0; k < 64 && !ok; ++k) ok = mbar_try_wait(&s_full[warp][st], (used / kStages) & 1);
+                    if (!ok) {
+                        const uint64_t until = globaltimer_ns() + kLimitNs;
+                        while (!(ok = mbar_try_wait_sleep(&s_full[warp][st], (used / kStages) & 1, 20000u)))
+                            if (globaltimer_ns() > until) break;
+                    }
+                    dead = !__all_sync(0xFFFFFFFFu, ok);
+                    if (dead && lane == 0) latch_error(err, QERL_ERR_TIMEOUT);
+                }
+                if (dead) break;
+                ++used;
+                fetch();
+                uint8_t *const tl = ring + st * M::BYTES;
+                const uint32_t tb = smem_u32(tl);
+                const int k0 = i * kTok;
+                if (k0 + kTok > len) {  // what lies past the segment may be anything: its scales become 0
+                    for (int e = lane; e < 4 * MT; e += 32) {
+                        const int keys = max(0, min(8, len - k0 - 8 * (e / MT)));
+                        uint64_t *const p = reinterpret_cast<uint64_t *>(tl + M::VS) + e;
+                        *p = keys == 8 ? *p : *p & ((uint64_t(1) << (8 * keys)) - 1);
+                    }
+                    fence_proxy_async_smem();  // before the next copy into this place
+                    __syncwarp();
+                }
+                // S^T: column c (16 keys) in turn
+                float x[2][NT][4];
+                uint32_t ks[D / 64];  // the lane's key scales
+                if (D == 128) {
+                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(ks[0]), "=r"(ks[D / 64 - 1]) : "r"(tb + M::KS + lane * 8) : "memory");
+                } else {
+                    ks[0] = ld_shared_u32(tb + M::KS + lane * 4);
+                }
+                const float up = pow2f(119);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t kw[2][KW], f[2][D / 64];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t from = tb + M::KC + (8 * (r / 2) + 4 * c + r % 2 + 2 * h) * (D / 2) + q * (D / 8);
+                        if (D == 128) {
+                            const uint4 v = ld_shared_v4(from);
+                            kw[h][0] = v.x, kw[h][1] = v.y, kw[h][KW - 2] = v.z, kw[h][KW - 1] = v.w;
+                        } else {
+                            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(kw[h][0]), "=r"(kw[h][1]) : "r"(from) : "memory");
+                        }
+                        // scales of token e = 2 c + h
+                        if (D == 128) {
+                            const uint32_t w = ks[c * (D / 64 - 1)];
+                            f[h][0] = scale_factor_bf16x2(h ? w << 4 : w << 20, up);
+                            f[h][D / 64 - 1] = scale_factor_bf16x2(h ? w >> 4 : w << 12, up);
+                        } else {
+                            const int sh = 8 * (2 * c + h);
+                            f[h][0] = scale_factor_bf16x2(sh <= 20 ? ks[0] << (20 - sh) : ks[0] >> (sh - 20), up);
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) x[c][n][0] = x[c][n][1] = x[c][n][2] = x[c][n][3] = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < KW; ++w) {
+                        uint32_t k0w[4], k1w[4];
+                        dequant_word<true>(kw[0][w], f[0][w / 2], k0w);
+                        dequant_word<true>(kw[1][w], f[1][w / 2], k1w);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma_bf16(x[c][n], k0w[0], k1w[0], k0w[1], k1w[1], qf[n][2 * w][0], qf[n][2 * w][1]);
+                            mma_bf16(x[c][n], k0w[2], k1w[2], k0w[3], k1w[3], qf[n][2 * w + 1][0], qf[n][2 * w + 1][1]);
+                        }
+                    }
+                }
+                if (k0 + kTok > all_see) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (k0 + 8 * (r / 2) + 4 * c + r % 2 + 2 * (e / 2) >= limit[n][e % 2]) x[c][n][e] = -INFINITY;
+                }
+                uint32_t p[2][NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float top[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        top[e] = fmaxf(fmaxf(fmaxf(x[0][n][e], x[0][n][e + 2]), fmaxf(x[1][n][e], x[1][n][e + 2])), kNone) * s.scale_log2;
+                    if (__any_sync(0xFFFFFFFFu, top[0] > m[n][0] + kRoom || top[1] > m[n][1] + kRoom)) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                            for (int k = 4; k < 32; k *= 2) top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], k));
+                            const float to = top[e] > m[n][e] + kRoom ? top[e] - kHead : m[n][e], f = ex2(m[n][e] - to);
+                            m[n][e] = to;
+                            l[n][e] *= f;
+#pragma unroll
+                            for (int t = 0; t < MT; ++t) o[t][n][e] *= f, o[t][n][e + 2] *= f;
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[c][n][e] = ex2(fmaf(x[c][n][e], s.scale_log2, -m[n][e % 2]));
+                            l[n][e % 2] += x[c][n][e];
+                        }
+                        p[c][n][0] = turned(f16x2(x[c][n][0], x[c][n][1]));
+                        p[c][n][1] = turned(f16x2(x[c][n][2], x[c][n][3]));
+                    }
+                }
+                // O^T: lane (r, q) holds keys 8 q .. 8 q + 7 of dims r and r + 8 of a row tile
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) {
+                    const uint4 w = ld_shared_v4(tb + M::VC + (j * 32 + lane) * 16), sc = ld_shared_v4(tb + M::VS + (q * MT + 2 * j) * 8);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        uint32_t v0[4], v1[4], s0[2], s1[2];
+                        codes_f16(t ? w.z : w.x, v0);
+                        codes_f16(t ? w.w : w.y, v1);
+                        scales_f16(t ? sc.z : sc.x, s0[0], s1[0]);
+                        scales_f16(t ? sc.w : sc.y, s0[1], s1[1]);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma_f16(o[2 * j + t][n], v0[2 * c], v1[2 * c], v0[2 * c + 1], v1[2 * c + 1], f16x2_mul(p[c][n][0], s0[c]),
+                                        f16x2_mul(p[c][n][1], s1[c]));
+                    }
+                }
+                __syncwarp();  // the place is free for the copy that the next turn issues
+            }
+            // the warps' sums meet
+            float *const so = reinterpret_cast<float *>(smem + S::O);
+            float2 *const sml = reinterpret_cast<float2 *>(smem + S::ML);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int k = 4; k < 32; k *= 2) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], k);
+                    const int row = warp * R + n * 8 + 2 * q + e;
+                    if (r == 0) sml[row] = make_float2(m[n][e], l[n][e]);
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        so[row * S::ROW + t * 16 + r] = o[t][n][e];
+                        so[row * S::ROW + t * 16 + r + 8] = o[t][n][e + 2];
+                    }
+                }
+            __syncthreads();
+            const int64_t part = (int64_t)at.seg * units + at.unit + blockIdx.x;
+            for (int row = warp; row < R; row += kWarps) {
+                float M_ = kNone, L = 0.0f, w[kWarps];
+#pragma unroll
+                for (int k = 0; k < kWarps; ++k) M_ = fmaxf(M_, sml[k * R + row].x);
+#pragma unroll
+                for (int k = 0; k < kWarps; ++k) {
+                    w[k] = ex2(sml[k * R + row].x - M_);
+                    L = fmaf(w[k], sml[k * R + row].y, L);
+                }
+                if (lane < D / 4) {
+                    float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                    for (int k = 0; k < kWarps; ++k) {
+                        const float4 v = *reinterpret_cast<const float4 *>(so + (k * R + row) * S::ROW + lane * 4);
+                        t.x = fmaf(w[k], v.x, t.x), t.y = fmaf(w[k], v.y, t.y), t.z = fmaf(w[k], v.z, t.z), t.w = fmaf(w[k], v.w, t.w);
+                    }
+                    *reinterpret_cast<float4 *>(s.part_o + (part * R + row) * D + lane * 4) = t;
+                }
+                if (lane == 0) s.part_ml[part * R + row] = make_float2(M_, L);
+            }
+            __syncthreads();
+        }
+        if (dead) {  // no copy may be in flight when the CTA ends
+            const uint64_t until = globaltimer_ns() + kLimitNs;
+            for (int k = used; k < fetched; ++k)
+                while (!mbar_try_wait(&s_full[warp][k % kStages], (k / kStages) & 1) && globaltimer_ns() < until) {
+                }
+            __syncwarp();
+        }
+    }
+    if (beside && blockIdx.x == gridDim.x - 1) pdl_wait();
+}
+
+// ------------------------------------------------------------------ joining a row's parts
+struct Parts {
+    const float *o;
+    const float2 *ml;
+    int n;
+    int64_t step;  // from part to part, in rows
+    float v_scale;
+};
+__device__ __forceinline__ Parts parts_of(const Side &s, int k, int hk, int r, int D)
+{
+    Parts p = {};
+    const int T = tiles_of(length(s, k));
+    if (T == 0) return p;
+    const int per = s.line[0], tile = r / s.tile_rows, u = hk * s.row_tiles + tile, start = s.line[1 + k] + u * T;
+    const int c0 = start / per;
+    const int64_t row = ((int64_t)k * s.c.Hkv * s.row_tiles + u + c0) * s.tile_rows + r % s.tile_rows;
+    p.n = (start + T - 1) / per - c0 + 1;
+    p.o = s.part_o + row * D;
+    p.ml = s.part_ml + row;
+    p.step = s.tile_rows;
+    p.v_scale = s.c.v_scale;
+    return p;
+}
+
+// W warps per query row, each takes every W-th part; in a fixed order, so that results repeat.
+template <int D, int W>
+__global__ void __launch_bounds__(128) join_kernel(const Call a, const Side pre, const Side suf)
+{
+    constexpr int E = D / 32, RB = 4 / W, NB = 4;  // columns of a lane; rows of a block; parts in flight
+    __shared__ float s_o[W > 1 ? 4 : 1][W > 1 ? D : 1];
+    __shared__ float2 s_ml[4];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, share = warp % W;
+    const int row = blockIdx.x * RB + warp / W;
+    const bool live = row < a.B * a.Lq * a.Hq;
+    const int h = row % a.Hq, bl = row / a.Hq, l = bl % a.Lq, b = live ? bl / a.Lq : 0, g = b / a.G;
+    const int hk = h / a.gs, hi = h - hk * a.gs;
+    pdl_wait();
+    pdl_trigger();
+    Parts pp = {}, ps = {};
+    if (live && pre.on) pp = parts_of(pre, g, hk, ((b - g * a.G) * a.Lq + l) * a.gs + hi, D);
+    if (live && suf.on) ps = parts_of(suf, b, hk, l * a.gs + hi, D);
+    const int n = pp.n + ps.n;
+    float M = kNone, L = 0.0f, acc[E] = {};
+    for (int k0 = share; k0 < n; k0 += NB * W) {
+        float2 ml[NB];
+        float v[NB][E];
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            const int k = k0 + j * W;
+            ml[j] = make_float2(kNone, 0.0f);
+            if (k < n) {
+                const Parts &p = k < pp.n ? pp : ps;
+                const int64_t at = (k < pp.n ? k : k - pp.n) * p.step;
+                ml[j] = p.ml[at];
+                const float *o = p.o + at * D + lane * E;
+                if (E == 4) {
+                    const float4 t = *reinterpret_cast<const float4 *>(o);
+                    v[j][0] = t.x, v[j][1] = t.y, v[j][E - 2] = t.z, v[j][E - 1] = t.w;
+                } else {
+                    const float2 t = *reinterpret_cast<const float2 *>(o);
+                    v[j][0] = t.x, v[j][1] = t.y;
+                }
+            }
+        }
+        float to = M;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) to = fmaxf(to, ml[j].x);
+        const float f = ex2(M - to);
+        M = to;
+        L *= f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= f;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            const bool none = ml[j].x == kNone && ml[j].y == 0.0f;
+            const float w = none ? 0.0f : ex2(ml[j].x - M), wv = w * (k0 + j * W < pp.n ? pp.v_scale : ps.v_scale);
+            L = fmaf(w, ml[j].y, L);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(wv, none ? 0.0f : v[j][e], acc[e]);
+        }
+    }
+    if (W > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
+        if (lane == 0) s_ml[warp] = make_float2(M, L);
+        __syncthreads();
+        if (share) return;
+#pragma unroll
+        for (int k = 1; k < W; ++k) M = fmaxf(M, s_ml[warp + k].x);
+        L = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const float w = ex2(s_ml[warp + k].x - M);
+            L = fmaf(w, s_ml[warp + k].y, L);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(w, s_o[warp + k][lane * E + e], acc[e]);
+        }
+    }
+    if (!live) return;
+    const float inv = L == 0.0f ? 0.0f : __fdividef(1.0f, L);  // a row that sees no key: zeros, lse -inf
+    uint32_t *out = reinterpret_cast<uint32_t *>(a.out + b * a.o_b + l * a.o_l + h * a.o_h + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+        out[e / 2] = *reinterpret_cast<const uint32_t *>(&t);
+    }
+    if (lane == 0 && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : (float)((double)M * 0.6931471805599453 + (double)logf(L));
+}
+
+// ------------------------------------------------------------------ host side
+int ceil_div(int64_t x, int64_t y) { return (int)((x + y - 1) / y); }
+size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
+
+constexpr int kPerSm1 = 3, kPerSm2 = 2;  // CTAs per SM with 8 and with 16 rows
+
+bool side(Side &s, int64_t n, int64_t T, int64_t Hkv, int64_t rows, bool suffix)
+{
+    const int64_t big = 1 << 30;
+    s.suffix = suffix;
+    s.rows = (int)rows;
+    s.tile_rows = rows <= 8 ? 8 : 16;
+    s.row_tiles = ceil_div(rows, s.tile_rows);
+    const int64_t units = n * Hkv * s.row_tiles, steps = units * ((T + kTok - 1) / kTok);
+    if (units > big || steps > big) return false;
+    const int64_t most = (int64_t)num_sms() * (s.tile_rows == 8 ? kPerSm1 : kPerSm2), want = (steps + kWarps - 1) / kWarps;
+    s.grid = (int)(want < most ? want : most);
+    s.on = true;
+    return true;
+}
+// the part area of a side: m and l, the line, o
+size_t ml_bytes(const Side &s, int64_t units) { return round256((size_t)(units + s.grid) * s.tile_rows * sizeof(float2)); }
+size_t side_bytes(const Side &s, int64_t D)
+{
+    if (!s.on) return 0;
+    const int64_t units = (int64_t)s.c.n * s.c.Hkv * s.row_tiles;
+    return ml_bytes(s, units) + round256((size_t)(1 + s.c.n) * sizeof(int)) + (size_t)(units + s.grid) * s.tile_rows * D * sizeof(float);
+}
+void place(Side &s, char *ws)
+{
+    const int64_t units = (int64_t)s.c.n * s.c.Hkv * s.row_tiles;
+    s.part_ml = reinterpret_cast<float2 *>(ws);
+    s.line = reinterpret_cast<int *>(ws + ml_bytes(s, units));
+    s.part_o = reinterpret_cast<float *>(ws + ml_bytes(s, units) + round256((size_t)(1 + s.c.n) * sizeof(int)));
+}
+
+template <int D, int NT>
+qerl_status launch_rows(const Call &a, const Side &s, int beside, cudaStream_t st, bool chain)
+{
+    constexpr int per_sm = NT == 1 ? kPerSm1 : kPerSm2;
+    static OncePerDevice once;
+    const auto kernel = rows_kernel<D, NT, per_sm>;
+    if (allow_smem(once, kernel, Smem<D, NT>::TOTAL) != cudaSuccess) return QERL_ERR_CUDA;
+    return launched(launch_k(kernel, dim3((unsigned)s.grid), dim3(kWarps * 32), Smem<D, NT>::TOTAL, st, chain, a, s, beside, error_word()));
+}
+template <int D>
+qerl_status run(const Call &a, const Side &pre, const Side &suf, cudaStream_t st)
+{
+    const bool chain = g_chain.load() != 0;
+    if (pre.on) QERL_TRY(pre.tile_rows == 8 ? (launch_rows<D, 1>(a, pre, 0, st, chain)) : (launch_rows<D, 2>(a, pre, 0, st, chain)));
+    const int beside = pre.on && chain ? 1 : 0;
+    if (suf.on) QERL_TRY(suf.tile_rows == 8 ? (launch_rows<D, 1>(a, suf, beside, st, chain)) : (launch_rows<D, 2>(a, suf, beside, st, chain)));
+    // a warp per row where the rows fill the SMs or have few parts, else four
+    const int64_t rows = (int64_t)a.B * a.Lq * a.Hq;
+    const auto parts = [](const Side &s) { return s.on ? s.grid / ((int64_t)s.c.n * s.c.Hkv * s.row_tiles) + 2 : 0; };
+    if (parts(pre) + parts(suf) <= 8 || rows > 32 * num_sms())
+        return launched(launch_k(join_kernel<D, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, chain, a, pre, suf));
+    return launched(launch_k(join_kernel<D, 4>, dim3((unsigned)rows), dim3(128), 0, st, chain, a, pre, suf));
+}
+
+// The call's sizes and the workspace it needs.
+qerl_status shape(const qerl_kv4_attn_dims *d, const qerl_kv4_cache *prefix, const qerl_kv4_cache *suffix, Call &a, Side &pre, Side &suf,
+                  size_t &bytes)
+{
+    if (!d || (!prefix && !suffix)) return QERL_ERR_INVALID_ARG;
+    if (prefix) QERL_TRY(check_cache(prefix, pre.c));
+    if (suffix) QERL_TRY(check_cache(suffix, suf.c));
+    const int64_t big = 1 << 30, Hkv = (prefix ? prefix : suffix)->Hkv, D = (prefix ? prefix : suffix)->D;
+    if (d->B < 1 || d->Lq < 1 || d->Hq < 1 || d->B > big || d->Lq > big || d->Hq > 65536 || d->Hq % Hkv || d->B * d->Lq > big / d->Hq)
+        return QERL_ERR_SHAPE;
+    if (prefix && d->B % prefix->n) return QERL_ERR_SHAPE;
+    if (suffix && (suffix->n != d->B || suffix->Hkv != Hkv || suffix->D != D)) return QERL_ERR_SHAPE;
+    a.B = (int)d->B, a.Lq = (int)d->Lq, a.Hq = (int)d->Hq, a.Hkv = (int)Hkv, a.gs = (int)(d->Hq / Hkv), a.G = prefix ? (int)(d->B / prefix->n) : 1;
+    if (prefix && !side(pre, prefix->n, prefix->T, Hkv, (int64_t)a.G * a.Lq * a.gs, false)) return QERL_ERR_SHAPE;
+    if (suffix && !side(suf, suffix->n, suffix->T, Hkv, (int64_t)a.Lq * a.gs, true)) return QERL_ERR_SHAPE;
+    bytes = round256(side_bytes(pre, D)) + round256(side_bytes(suf, D));
+    return QERL_OK;
+}
+
+}  // namespace
+}  // namespace kv4
+}  // namespace qerl
+
+using namespace qerl;
+
+extern "C" size_t qerl_kv4_attention_ws_bytes(const qerl_kv4_attn_dims *d, const qerl_kv4_cache *prefix, const qerl_kv4_cache *suffix)
+{
+    kv4::Call a = {};
+    kv4::Side pre = {}, suf = {};
+    size_t bytes = 0;
+    return kv4::shape(d, prefix, suffix, a, pre, suf, bytes) == QERL_OK ? bytes : 0;
+}
+
+extern "C" qerl_status qerl_kv4_attention(const qerl_kv4_attn_dims *d, const void *q, const qerl_kv4_cache *prefix, const int32_t *prefix_lens,
+                                          const qerl_kv4_cache *suffix, const int32_t *suffix_lens, float scale, void *out, float *lse, void *ws,
+                                          size_t ws_bytes, qerl_stream_t stream)
+{
+    if (!d || !q || !out || !(scale > 0.0f) || !(scale <= FLT_MAX) || (suffix && !suffix_lens)) return QERL_ERR_INVALID_ARG;
+    kv4::Call a = {};
+    kv4::Side pre = {}, suf = {};
+    size_t need = 0;
+    QERL_TRY(kv4::shape(d, prefix, suffix, a, pre, suf, need));
+    for (int i = 0; i < 3; ++i) {
+        if (d->q_stride[i] < 0 || d->out_stride[i] < 0 || d->q_stride[i] > (int64_t(1) << 40) || d->out_stride[i] > (int64_t(1) << 40))
+            return QERL_ERR_SHAPE;
+        if (d->q_stride[i] % 8 || d->out_stride[i] % 8) return QERL_ERR_ALIGN;
+    }
+    if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(prefix_lens) & 3u) ||
+        (reinterpret_cast<uintptr_t>(suffix_lens) & 3u))
+        return QERL_ERR_ALIGN;
+    // the keys' factor, and the 2^-7 that their products carry
+    for (kv4::Side *s : {&pre, &suf})
+        if (s->on) {
+            const double c = (double)scale * s->c.k_scale * 128.0 * 1.4426950408889634;
+            if (!(c >= FLT_MIN && c <= FLT_MAX)) return QERL_ERR_INVALID_ARG;
+            s->scale_log2 = (float)c;
+        }
+    if (!ws || ws_bytes < need) return QERL_ERR_WORKSPACE;
+    if (!aligned16(ws)) return QERL_ERR_ALIGN;
+    QERL_TRY(check_device());
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.out = static_cast<__nv_bfloat16 *>(out), a.lse = lse;
+    a.q_b = d->q_stride[0], a.q_l = d->q_stride[1], a.q_h = d->q_stride[2];
+    a.o_b = d->out_stride[0], a.o_l = d->out_stride[1], a.o_h = d->out_stride[2];
+    const int64_t D = (prefix ? prefix : suffix)->D;
+    pre.lens = prefix_lens, suf.lens = suffix_lens;
+    if (pre.on) kv4::place(pre, static_cast<char *>(ws));
+    if (suf.on) kv4::place(suf, static_cast<char *>(ws) + kv4::round256(kv4::side_bytes(pre, D)));
+    return D == 128 ? kv4::run<128>(a, pre, suf, as_cuda(stream)) : kv4::run<64>(a, pre, suf, as_cuda(stream));
+}

@@ -12,6 +12,7 @@
 // nearest-even E2M1.  Every decision is taken in IEEE FP32 with explicitly
 // rounded operations so that it is reproducible bit for bit.
 #include "common.cuh"
+#include "fp4_round.cuh"
 
 namespace qerl {
 namespace {
@@ -103,28 +104,6 @@ __global__ void __launch_bounds__(kAmaxThreads) amax_kernel(const __nv_bfloat16 
     if (threadIdx.x == 0) partial[blockIdx.x] = m;
 }
 
-// Smallest non-negative finite E4M3 value >= t, as a byte (saturates at 448).
-__device__ __forceinline__ uint32_t e4m3_ceil(float t)
-{
-    if (!(t > 0.0f)) return 0u;
-    if (t > 448.0f) return 0x7Eu;
-    const uint32_t u = __float_as_uint(t);
-    const int e = (int)(u >> 23) - 127;
-    if (e < -6) {
-        // Subnormal E4M3 range m * 2^-9 (m = 8 is 2^-6, the first normal, whose
-        // byte 0x08 continues the sequence).  t * 512 is exact.
-        return (uint32_t)ceilf(t * 512.0f);
-    }
-    uint32_t m3 = (u >> 20) & 7u, E = (uint32_t)(e + 7);
-    if (u & 0xFFFFFu) {  // bits below the 3 kept mantissa bits: round up
-        if (++m3 == 8u) {
-            m3 = 0u;
-            ++E;
-        }
-    }
-    return (E << 3) | m3;
-}
-
 // Nearest-even E4M3 with saturation at 448 (the hardware conversion).
 __device__ __forceinline__ uint32_t e4m3_rne(float t)
 {
@@ -132,17 +111,6 @@ __device__ __forceinline__ uint32_t e4m3_rne(float t)
     uint16_t pair;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pair) : "f"(0.0f), "f"(t));
     return pair & 0xFFu;
-}
-
-// E2M1 code of q: nearest of {0,.5,1,1.5,2,3,4,6} in magnitude, ties to the even
-// code (the midpoints .25,1.25,2.5,5 fall down, .75,1.75,3.5 fall up), > 6
-// saturates; a zero result is code 0 whatever the sign.
-__device__ __forceinline__ uint32_t e2m1_code(float q)
-{
-    const float a = fabsf(q);
-    uint32_t c = (uint32_t)(a > 0.25f) + (uint32_t)(a >= 0.75f) + (uint32_t)(a > 1.25f) + (uint32_t)(a >= 1.75f) +
-                 (uint32_t)(a > 2.5f) + (uint32_t)(a >= 3.5f) + (uint32_t)(a > 5.0f);
-    return (c != 0u && q < 0.0f) ? (c | 8u) : c;
 }
 
 // Pass 2: reduce the partials to s_t, then quantize one 16-block per thread,
