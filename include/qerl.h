@@ -602,6 +602,32 @@ qerl_status qerl_token_logp(const void *logits, int dtype, int64_t T, int64_t V,
                             const float *weight, float temperature, float *logp, float *entropy, qerl_stream_t stream);
 
 /*
+ * The next token of every row of logits, from a given uniform number.  With
+ * p = softmax(x / temperature) and the tokens in order of p, equal ones by index,
+ * kept is the shortest of these beginnings: the first top_k (0: all); those until
+ * their sum reaches top_p of the first top_k's sum; those with p >= min_p max p.
+ *     ids[t]  = the first kept token, by index, whose sum of kept p up to it exceeds
+ *               u[t] times the sum of all kept p
+ *     logp[t] = ln p[ids[t]],   logq[t] = ln (p[ids[t]] / sum of kept p)
+ *   logits as in qerl_token_logp, 1 <= V <= 2^20; u (device) float [T], taken into
+ *   [0, 1) (NaN counts as 0); ids (device) int64 [T]; logp, logq (device) float [T].
+ *   Each setting holds for all rows, or is a device array [T] where its pointer is
+ *   not NULL: there top_k < 0 counts as 0, top_p <= 0 keeps one token, top_p that is
+ *   not below 1 all, min_p is taken into [0, 1] (NaN as 0).
+ * The token is that of the definition: sums are exact integers, and it does not
+ * depend on how the work is split.  A row with NaN or +inf, or with a temperature
+ * outside (1e-30, 1e30], gets id -1 and NaN; one of nothing but -inf id -1 and -inf.
+ */
+typedef struct {
+    float temperature, top_p, min_p;
+    int32_t top_k;
+    const float *temperatures, *top_ps, *min_ps;
+    const int32_t *top_ks;
+} qerl_sample_opts;
+qerl_status qerl_sample(const void *logits, int dtype, int64_t T, int64_t V, int64_t ld, const float *u, const qerl_sample_opts *opts,
+                        int64_t *ids, float *logp, float *logq, qerl_stream_t stream);
+
+/*
  * Clipped policy loss with a KL term (GRPO; DAPO with clip_high > clip_low), and
  * the gradient of the logits in the same pass over them:
  *     rho = e^(logp - old),  d = ref - logp

@@ -47,7 +47,7 @@ EXPORTED = ["qerl_nvfp4_quantize", "qerl_nvfp4_dequantize", "qerl_nvfp4_lora_lin
             "qerl_mxfp4_lora_linear_fwd", "qerl_nvfp4_lora_linear_fwd_f32ab", "qerl_residual_add", "qerl_swiglu",
             "qerl_prefix_attention_ws_bytes", "qerl_prefix_attention", "qerl_token_logp", "qerl_policy_loss",
             "qerl_adamw_ws_bytes", "qerl_adamw_plan", "qerl_adamw_step", "qerl_adamw_read_state", "qerl_adamw_destroy",
-            "qerl_kv4_append", "qerl_kv4_read", "qerl_kv4_attention_ws_bytes", "qerl_kv4_attention"]
+            "qerl_kv4_append", "qerl_kv4_read", "qerl_kv4_attention_ws_bytes", "qerl_kv4_attention", "qerl_sample"]
 
 
 class QerlError(RuntimeError):
@@ -133,6 +133,7 @@ def lib() -> C.CDLL:
             sig["qerl_kv4_read"] = ([vp, i64, vp, vp, vp, vp, vp, vp], i32)
             sig["qerl_kv4_attention_ws_bytes"] = ([vp, vp, vp], sz)
             sig["qerl_kv4_attention"] = ([vp, vp, vp, vp, vp, vp, f32, vp, vp, vp, sz, vp], i32)
+            sig["qerl_sample"] = ([vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp], i32)
             sig["qerl_nvfp4_lora_linear_fwd_packed"] = sig["qerl_nvfp4_lora_linear_fwd"]
             sig["qerl_nvfp4_lora_linear_bwd_packed"] = sig["qerl_nvfp4_lora_linear_bwd"]
             for name, (args, res) in sig.items():
@@ -770,6 +771,35 @@ def qerl_policy_loss(logits, ids, old_logp, advantages, weights=None, ref_logp=N
                                   _p(logp), _p(entropy), _p(dlogits), ldd, _p(ws), ws.numel(), _stream(stream)),
            "qerl_policy_loss")
     return sums, logp, entropy, dlogits
+
+
+class _SampleOpts(C.Structure):
+    _fields_ = [(n, C.c_float) for n in ("temperature", "top_p", "min_p")] + [("top_k", C.c_int32)] + [
+        (n, C.c_void_p) for n in ("temperatures", "top_ps", "min_ps", "top_ks")]
+
+
+def qerl_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, ids=None, logp=None, logq=None, stream=None):
+    """The next tokens from logits bf16/f32 [T, V] and uniform numbers u f32 [T]: (ids int64 [T], logp f32 [T] in the whole
+    distribution, logq f32 [T] in the cut one).  temperature, top_p, min_p: numbers or f32 [T]; top_k: a number or int32 [T]."""
+    T, V = shape = logits.shape
+    ld, one = logits.stride()
+    vec, f32, dev = shape[:1], torch.float32, logits.device
+    ids = _new(torch.empty, stream, T, dtype=torch.int64, device=dev) if ids is None else ids
+    logp = _new(torch.empty, stream, T, dtype=f32, device=dev) if logp is None else logp
+    logq = _new(torch.empty, stream, T, dtype=f32, device=dev) if logq is None else logq
+    assert logits.dtype in _DTYPES and (one == 1 or V == 1) and ids.dtype is torch.int64 and ids.shape == vec and ids.is_contiguous()
+    for t in (u, logp, logq):
+        assert t.dtype is f32 and t.shape == vec and t.is_contiguous()
+    o = _SampleOpts(1.0, 1.0, 0.0, 0)
+    for name, v, dt in (("temperature", temperature, f32), ("top_p", top_p, f32), ("min_p", min_p, f32), ("top_k", top_k, torch.int32)):
+        if isinstance(v, torch.Tensor):
+            assert v.dtype is dt and v.shape == vec and v.is_contiguous()
+            setattr(o, name + "s", v.data_ptr())
+        else:
+            setattr(o, name, v)
+    _check(lib().qerl_sample(logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld if T > 1 else V, u.data_ptr(), C.byref(o), ids.data_ptr(),
+                             logp.data_ptr(), logq.data_ptr(), _stream(stream)), "qerl_sample")
+    return ids, logp, logq
 
 
 # ---------------------------------------------------------------- AdamW
