@@ -14,11 +14,17 @@
 // A choice that kEps could change is made again with exact sums.
 //
 // A row is swept by one CTA, or by a cluster of up to eight where there are few
-// rows; the sweeps after the first find it in L2.  Sweeps: the chunks' maxima and
-// sums; with a cut, histograms of the order-preserving integer keys of the logits
-// below the maximum, refined until the border is a single key (bf16: as a rule the
-// first histogram's bins are single keys already, and their masses exact); the
-// chunks' sums of what is kept.  At last one chunk is read again for the token.
+// rows.  The first sweep takes it from HBM: the maximum and the fast sum of each
+// chunk.  Without a cut that is enough to know the token's chunk, which is read
+// again.  With a cut the first sweep also leaves a sample of the logits, from which
+// two thresholds are chosen such that the border of what is kept lies between them,
+// with a few thousand tokens at most.  The second sweep (L2; chunks whose maximum
+// is below are skipped) lists the tokens between, with their indices, and sums what
+// is above by chunk, and below.  The list is sorted and the border found in it with
+// exact masses.  top_p compares what is left below the border with 1 - top_p of the
+// sum: with top_p near 1 the fast part of that is small.  Where the sample misled,
+// or more tokens than the list holds are as good as equal, histograms of the keys
+// find the border.
 #include <float.h>
 #include <math.h>
 
@@ -32,11 +38,16 @@ constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCluster = 8;
 constexpr int kVec = 4, kChunkVecs = 32 * kVec;  // 16-byte vectors of a lane and of a chunk
 constexpr int kBins = 2048, kBinBits = 11;
 constexpr int64_t kMaxV = 1 << 20;  // 2^42 times that fits 62 bits
-constexpr int kMaxChunks = kMaxV * 4 / (kChunkVecs * 16) + 1;
+constexpr int kMostChunks = kMaxV * 4 / (kChunkVecs * 16) + 1;
 constexpr int kScale = 42;
-// Of a chunk's fast sum: per value 2 roundings of the exponent y, up to 2^-23 |y| ln 2 with c's own (2^-25), where the
-// mean of |y| over a chunk is at most log2 1024; ex2.approx 2^-22; some 25 roundings of the sum, 2^-24 each.
-constexpr double kEps = 3e-6;
+constexpr int kList = 8192, kSamples = 8192;
+// What a fast sum is taken to be off by, relative to it.  ex2.approx is off by -5e-8 on average over an octave (measured, the
+// same in all of them) and 1.4e-7 at most; the exponent y by up to 2 * 2^-24 |y| and the sum by some 20 roundings, neither of
+// one sign.  Weighted by the masses the mean of |y| is at most log2 N where N tokens count, so that six deviations of those
+// two, which shrink with the root of N, stay below 3e-7 and 2.5e-7.
+// A draw compares a sum with u times the total, which moves by at most kEps 2 u (1 - u) of the total: total >> kOff.
+constexpr double kEps = 6e-7;
+constexpr int kOff = 21;
 
 struct Args {
     const void *x;
@@ -48,7 +59,7 @@ struct Args {
     const int32_t *top_ks;
     int64_t *ids;
     float *logp, *logq;
-    int cluster;
+    int cluster, chunks;  // CTAs of a row; chunks that a row may take, wherever it starts
 };
 
 // 2^(j / 64) in two FP32 numbers.
@@ -93,24 +104,39 @@ __device__ __forceinline__ float value_of(uint32_t key)
 // e^((x - top) / tau) 2^42, c = log2(e) / tau in two FP32 numbers.  With y = (x - top) c in two numbers, k = round(64 y) and
 // r = y - k / 64 it is 2^(k / 64) e^(r ln 2); the exponential of |t| < 0.0055 by its series to t^4 / 24.
 struct Exp {
-    float top, c, c_lo;
+    float top, c, c_lo, low;  // low: 200 octaves below 0
     const float2 *roots;
 };
+// The same in FP32 for a difference d <= 0, 1 for d = 0; NaN stays.
+__device__ __forceinline__ float fast(const Exp &e, float d)
+{
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(d) : "f"(e.low));  // no -inf times a c_lo below 0
+    return ex2(fmaf(d, e.c, d * e.c_lo));
+}
 __device__ __forceinline__ uint64_t mass(const Exp &e, float x)
 {
-    const float d = x - e.top, b = d - x, rest = (x - (d - b)) - (e.top + b);
+    const float d0 = x - e.top;
+    const bool some = d0 * e.c > -60.0f;  // false for NaN
+    const float d = some ? d0 : 0.0f, b = d - x, rest = some ? (x - (d - b)) - (e.top + b) : 0.0f;
     const float y = d * e.c;
-    if (!(y > -60.0f)) return 0;
     const float y_lo = fmaf(d, e.c, -y) + fmaf(d, e.c_lo, rest * e.c);
-    const float k = rintf(y * 64.0f), r0 = fmaf(k, -0.015625f, y), r = r0 + y_lo, r_lo = (r0 - r) + y_lo;
+    const float magic = 12582912.0f, ky = fmaf(y, 64.0f, magic), k = ky - magic, r0 = fmaf(k, -0.015625f, y), r = r0 + y_lo, r_lo = (r0 - r) + y_lo;
     const float t = r * 0x1.62e430p-1f, t_lo = fmaf(r, 0x1.62e430p-1f, -t) + fmaf(r, -0x1.05c610p-29f, r_lo * 0x1.62e430p-1f);
     const float q = t * t * fmaf(t, fmaf(t, 1.0f / 24.0f, 1.0f / 6.0f), 0.5f), s = t_lo + q;
     const float p = t + s, p_lo = (t - p) + s;
-    const int n = (int)k;
+    // 2^(k / 64) (1 + p): its first term is an integer of 24 bits times a power of two; the rest, below 2^-7 of it, in two steps
+    // of 2^14 and 1, each below 2^22 and rounded by adding 3 * 2^22
+    const int n = __float_as_int(ky) - 0x4B400000;
     const float2 T = e.roots[n & 63];
-    const float mid = T.x * p, low = fmaf(T.x, p, -mid) + fmaf(T.x, p_lo, fmaf(T.y, p, T.y));
-    const float unit = pow2f(kScale + (n >> 6));
-    return (uint64_t)(__float2ll_rn(T.x * unit) + __float2ll_rn(mid * unit) + __float2ll_rn(low * unit));
+    const int down = -(n >> 6);  // 0 .. 60
+    const float unit = pow2f(kScale - down), mid = T.x * p;
+    const float low = fmaf(T.x, p, -mid) + fmaf(T.x, p_lo, fmaf(T.y, p, T.y));
+    const float coarse = fmaf(mid, unit * 0x1p-14f, magic), a = coarse - magic;
+    const float fine = fmaf(low, unit, fmaf(a, -16384.0f, mid * unit)) + magic;
+    const uint64_t first = (uint64_t)((__float_as_uint(T.x) & 0x7FFFFFu) | 0x800000u) << (kScale - 23);
+    const uint64_t head = (first + ((uint64_t(1) << down) >> 1)) >> down;
+    const uint64_t all = head + (int64_t)(__float_as_int(coarse) - 0x4B400000) * 16384 + (int64_t)(__float_as_int(fine) - 0x4B400000);
+    return some ? all : 0;
 }
 
 // A row as the aligned 16-byte vectors that hold it; elements outside it read as -inf.
@@ -128,7 +154,7 @@ struct Row {
     }
     __device__ __forceinline__ float at(int e) const
     {
-        if (e < 0 || e >= n) return -INFINITY;
+        if (!inside(e)) return -INFINITY;
         return BF16 ? bf16f(reinterpret_cast<const __nv_bfloat16 *>(x)[e]) : reinterpret_cast<const float *>(x)[e];
     }
     __device__ __forceinline__ uint4 load(int i) const
@@ -136,7 +162,7 @@ struct Row {
         constexpr uint32_t fill = BF16 ? 0xFF80FF80u : 0xFF800000u;
         uint32_t w[4] = {fill, fill, fill, fill};
         if (i >= nvec) return make_uint4(fill, fill, fill, fill);
-        if (i * E >= off && (i + 1) * E <= off + n) return *(reinterpret_cast<const uint4 *>(x - off * S) + i);
+        if (whole(i)) return *(reinterpret_cast<const uint4 *>(x - off * S) + i);
 #pragma unroll
         for (int j = 0; j < E; ++j) {
             const int e = i * E + j - off;
@@ -151,7 +177,9 @@ struct Row {
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    __device__ __forceinline__ bool holds(int i, int j) const { return (uint32_t)(i * E + j - off) < (uint32_t)n; }
+    __device__ __forceinline__ bool whole(int i) const { return i * E >= off && (i + 1) * E <= off + n; }  // vector i
+    __device__ __forceinline__ bool inside(int e) const { return e >= 0 && e < n; }
+    __device__ __forceinline__ bool holds(int i, int j) const { return inside(i * E + j - off); }
     static __device__ __forceinline__ void unpack(const uint4 &v, float (&f)[E])
     {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -160,16 +188,22 @@ struct Row {
     }
 };
 
-// What the CTAs of a row share; the first one's copy counts.
+// A token's place in the order: larger logits first, equal ones by index.
+__device__ __forceinline__ uint64_t place_of(uint32_t key, uint32_t index) { return (uint64_t)~key << 32 | index; }
+
+// What the CTAs of a row share; the first one's copy counts, but for the chunks' maxima, of which each also has its own.
 struct Shared {
     float2 roots[64];
-    float chunk_m[kMaxChunks], chunk_s[kMaxChunks];
-    uint64_t chunk[kMaxChunks];  // masses of what is kept
-    uint32_t ties[kMaxChunks];   // tokens at the border's key
-    uint32_t hist[kBins];      // tokens of a bin
-    uint64_t weight[kBins];    // and their masses, where they are asked for
-    uint64_t sum;       // of a sweep
-    float top;          // the row's maximum
+    union {
+        float sample[kSamples];
+        uint64_t list[kList];  // places
+    };
+    uint64_t small[kThreads];  // those near the border
+    uint32_t hist[kBins];    // tokens of a bin
+    uint64_t weight[kBins];  // and their masses, where they are asked for
+    uint64_t sum;            // of a sweep
+    uint32_t listed;
+    float top;  // the row's maximum
     // the next sweep
     int what;
     uint32_t hi, lo;
@@ -178,11 +212,18 @@ struct Shared {
     uint64_t w64[kWarps];
     float wf[kWarps];
     uint64_t got64[2];
-    uint32_t got32[2];
+    uint32_t got32[2], mark[4];
+    // and behind it, by chunk: the masses of what is kept, the maximum, the sum, the tokens at the border's key
+    static constexpr int kChunkBytes = 8 + 4 + 4 + 4;
 };
-enum { kDone, kHist, kWeigh, kSum, kChunksFast, kChunksExact };
+enum { kDone, kHist, kWeigh, kSum, kBetween, kBetweenSums, kKeptFast, kKeptExact };
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v)
+{
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v)
 {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
@@ -208,17 +249,72 @@ __device__ __forceinline__ uint64_t block_scan(Shared &s, uint64_t v, uint64_t &
     all = total;
     return before + v;
 }
+__device__ __forceinline__ uint64_t fixed(float v) { return (uint64_t)__float2ll_rn(v * pow2f(kScale)); }  // 2^20 tokens at most
 
-__device__ __forceinline__ uint32_t remote(const void *p, int rank)
+// Shared memory of the row's first CTA.
+template <bool CLUSTER>
+struct Lead {
+    static __device__ __forceinline__ uint32_t remote(const void *p, int rank)
+    {
+        uint32_t to;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(ptx::smem_u32(p)), "r"(rank));
+        return to;
+    }
+    static __device__ __forceinline__ void put(uint32_t *p, uint32_t v, int rank = 0)
+    {
+        if (CLUSTER)
+            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(remote(p, rank)), "r"(v) : "memory");
+        else
+            *p = v;
+    }
+    static __device__ __forceinline__ void put(float *p, float v) { put(reinterpret_cast<uint32_t *>(p), __float_as_uint(v)); }
+    static __device__ __forceinline__ void put(uint64_t *p, uint64_t v)
+    {
+        if (CLUSTER)
+            asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(remote(p, 0)), "l"(v) : "memory");
+        else
+            *p = v;
+    }
+    static __device__ __forceinline__ uint32_t add(uint32_t *p, uint32_t v)
+    {
+        uint32_t old;
+        if (CLUSTER)
+            asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(remote(p, 0)), "r"(v) : "memory");
+        else
+            old = atomicAdd(p, v);
+        return old;
+    }
+    static __device__ __forceinline__ void add(uint64_t *p, uint64_t v)
+    {
+        if (CLUSTER)
+            asm volatile("red.shared::cluster.add.u64 [%0], %1;" ::"r"(remote(p, 0)), "l"(v) : "memory");
+        else
+            atomicAdd(reinterpret_cast<unsigned long long *>(p), (unsigned long long)v);
+    }
+};
+
+// The first n <= kThreads entries of s.small in order; returns this thread's.
+__device__ __forceinline__ uint64_t sort_small(Shared &s, int n)
 {
-    uint32_t to;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(ptx::smem_u32(p)), "r"(rank));
-    return to;
+    const int tid = threadIdx.x;
+    uint64_t v = tid < n ? s.small[tid] : ~uint64_t(0);
+    for (int k = 2; k < 2 * n; k *= 2)
+        for (int j = k / 2; j; j /= 2) {
+            uint64_t y;
+            if (j >= 32) {  // near exchanges stay in a warp
+                __syncthreads();
+                s.small[tid] = v;
+                __syncthreads();
+                y = s.small[tid ^ j];
+            } else {
+                y = __shfl_xor_sync(0xFFFFFFFFu, v, j);
+            }
+            const bool smaller = ((tid & j) == 0) == ((tid & k) == 0);  // this place gets the smaller one
+            if ((y < v) == smaller) v = y;
+        }
+    __syncthreads();
+    return v;
 }
-__device__ __forceinline__ void put(uint32_t to, uint32_t v) { asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to), "r"(v) : "memory"); }
-__device__ __forceinline__ void put64(uint32_t to, uint64_t v) { asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(to), "l"(v) : "memory"); }
-__device__ __forceinline__ void add32(uint32_t to, uint32_t v) { asm volatile("red.shared::cluster.add.u32 [%0], %1;" ::"r"(to), "r"(v) : "memory"); }
-__device__ __forceinline__ void add64(uint32_t to, uint64_t v) { asm volatile("red.shared::cluster.add.u64 [%0], %1;" ::"r"(to), "l"(v) : "memory"); }
 
 template <bool BF16, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
@@ -226,7 +322,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
     extern __shared__ __align__(16) uint8_t smem[];
     Shared &s = *reinterpret_cast<Shared *>(smem);
     using R = Row<BF16>;
+    using L = Lead<CLUSTER>;
     constexpr int E = R::E, kUnit = BF16 ? 16 : 0;  // a key's low bits that say nothing
+    constexpr int kChunk = kChunkVecs * E;          // tokens of a chunk
+    const auto key_of = [](float x) { return qerl::key_of<BF16>(x); };
+    const auto value_of = [](uint32_t k) { return qerl::value_of<BF16>(k); };
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     int rank = 0, ranks = 1;
     if (CLUSTER) {
@@ -244,7 +344,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
     };
     if (tid < 64) s.roots[tid] = kRoots[tid];
     for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0, s.weight[i] = 0;
-    if (tid == 0) s.sum = 0;
     if (CLUSTER) meet();  // every CTA of the cluster runs: the first one's memory may be written
     pdl_wait();
     pdl_trigger();
@@ -252,18 +351,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
     const int64_t row = blockIdx.x / ranks;
     const R r(a, row);
     const float tau = a.taus ? a.taus[row] : a.tau;
+    int k = a.top_ks ? a.top_ks[row] : a.top_k;
+    const float top_p = a.top_ps ? a.top_ps[row] : a.top_p, min_p = a.min_ps ? a.min_ps[row] : a.min_p;
+    if (top_p <= 0.0f) k = 1;
+    const bool cut_k = k > 0 && k < r.n, cut_p = top_p > 0.0f && top_p < 1.0f, cut_m = min_p > 0.0f;
     const int chunks = (r.nvec + kChunkVecs - 1) / kChunkVecs;
-    const double c64 = 1.4426950408889634 / (double)tau;
-    Exp ex = {0.0f, (float)c64, 0.0f, s.roots};
-    ex.c_lo = (float)(c64 - (double)ex.c);
-    const bool tau_ok = tau > 1e-30f && tau <= 1e30f;
-    if (!tau_ok) {
+    uint64_t *const s_chunk = reinterpret_cast<uint64_t *>(smem + sizeof(Shared));
+    float *const s_chunk_m = reinterpret_cast<float *>(s_chunk + a.chunks), *const s_chunk_s = s_chunk_m + a.chunks;
+    uint32_t *const s_ties = reinterpret_cast<uint32_t *>(s_chunk_s + a.chunks);
+    // log2(e) / tau in two numbers; log2(e) = 0x1.715476p+0 + 0x1.4ae0cp-26
+    Exp ex = {0.0f, __fdiv_rn(0x1.715476p+0f, tau), 0.0f, -138.0f * tau, s.roots};
+    ex.c_lo = __fdiv_rn(fmaf(-ex.c, tau, 0x1.715476p+0f) + 0x1.4ae0cp-26f, tau);
+    if (!(tau > 1e-30f && tau <= 1e30f)) {
         if (lead && tid == 0) a.ids[row] = -1, a.logp[row] = a.logq[row] = NAN;
         if (CLUSTER) meet();
         return;
     }
 
-    // ------------------------------------------------------------ chunks' maxima and sums
+    // ------------------------------------------------------------ chunks' maxima and sums, and a sample
+    // two of a lane's tokens, from every chunk or from fewer, so that kSamples hold
+    const int every = (chunks + kSamples / 64 - 1) / (kSamples / 64);
+    const bool sampled = cut_k || cut_p;
     for (int ch = rank * kWarps + warp; ch < chunks; ch += ranks * kWarps) {
         uint4 v[kVec];
 #pragma unroll
@@ -275,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
             R::unpack(v[j], f);
 #pragma unroll
             for (int e = 0; e < E; ++e) m = fmaxf(m, f[e]);
+            if (sampled && j % 2 == 0 && ch % every == 0) L::put(&s.sample[(ch / every) * 64 + j * 16 + lane], f[E / 2]);
         }
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         float z[2] = {0.0f, 0.0f};
@@ -283,152 +392,205 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
             float f[E];
             R::unpack(v[j], f);
 #pragma unroll
-            for (int e = 0; e < E; ++e) z[e % 2] += ex2((f[e] - m) * ex.c);  // NaN and +inf leave NaN
+            for (int e = 0; e < E; ++e) z[e % 2] += fast(ex, f[e] - m);  // NaN and +inf leave NaN
         }
-        float sum = z[0] + z[1];
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        const float sum = warp_sum(z[0] + z[1]);
         if (lane == 0) {
-            if (CLUSTER) {
-                put(remote(&s.chunk_m[ch], 0), __float_as_uint(m));
-                put(remote(&s.chunk_s[ch], 0), __float_as_uint(sum));
-            } else {
-                s.chunk_m[ch] = m, s.chunk_s[ch] = sum;
-            }
+            if (CLUSTER) s_chunk_m[ch] = m;
+            L::put(&s_chunk_m[ch], m);
+            L::put(&s_chunk_s[ch], sum);
         }
     }
     meet();
 
-    // ------------------------------------------------------------ the other CTAs do what the first one asks for
-    const auto count_hist = [&](uint32_t hi, uint32_t lo, int shift, bool weigh) {  // and the last bin's fast mass, or all exact
+    // ------------------------------------------------------------ the sweeps that the first CTA asks for
+    const auto merge_hist = [&]() {
+        if (!CLUSTER) return;
+        __syncthreads();
+        if (!lead)
+            for (int b = tid; b < kBins; b += kThreads) {
+                const uint32_t n = s.hist[b];
+                if (n) L::add(&s.hist[b], n), s.hist[b] = 0;
+                const uint64_t w = s.weight[b];
+                if (w) L::add(&s.weight[b], w), s.weight[b] = 0;
+            }
+    };
+    // histogram of keys in [lo, hi], the last bin with the rest; and the bins' exact masses
+    const auto count_hist = [&](uint32_t hi, uint32_t lo, int shift, bool weigh) {
         uint32_t last = 0;
-        float z = 0.0f;
         uint64_t zs = 0;
         for (int ch = rank * kWarps + warp; ch < chunks; ch += ranks * kWarps) {
+            if (key_of(s_chunk_m[ch]) < lo) continue;
             uint4 v[kVec];
 #pragma unroll
             for (int j = 0; j < kVec; ++j) v[j] = r.load(ch * kChunkVecs + j * 32 + lane);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
                 const int i = ch * kChunkVecs + j * 32 + lane;
-                const bool whole = i * E >= r.off && (i + 1) * E <= r.off + r.n;
+                const bool whole = r.whole(i);
                 float f[E];
                 R::unpack(v[j], f);
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    const uint32_t k = key_of<BF16>(f[e]), bin = (hi - k) >> shift;
-                    if (k <= hi && k >= lo && (whole || r.holds(i, e))) {
-                        if (weigh) {
-                            const uint64_t w = mass(ex, f[e]);
-                            if (w) atomicAdd(reinterpret_cast<unsigned long long *>(&s.weight[min(bin, kBins - 1)]), (unsigned long long)w);
-                        }
+                    const uint32_t key = key_of(f[e]), bin = (hi - key) >> shift;
+                    if (key <= hi && key >= lo && (whole || r.holds(i, e))) {
+                        const uint64_t w = weigh ? mass(ex, f[e]) : 0;
                         if (bin < kBins - 1) {
                             atomicAdd(&s.hist[bin], 1u);
+                            if (w) atomicAdd(reinterpret_cast<unsigned long long *>(&s.weight[bin]), (unsigned long long)w);
                         } else {
                             ++last;
-                            z += ex2((f[e] - ex.top) * ex.c);
+                            zs += w;
                         }
                     }
                 }
             }
-            zs += (uint64_t)__float2ll_rn(z * pow2f(kScale));
-            z = 0.0f;
         }
         last = __reduce_add_sync(0xFFFFFFFFu, last);
-        zs = warp_sum(zs);
-        if (lane == 0) {
-            if (last) atomicAdd(&s.hist[kBins - 1], last);
-            if (CLUSTER) {
-                add64(remote(&s.sum, 0), zs);
-            } else {
-                atomicAdd(reinterpret_cast<unsigned long long *>(&s.sum), (unsigned long long)zs);
-            }
+        if (lane == 0 && last) atomicAdd(&s.hist[kBins - 1], last);
+        if (weigh) {
+            zs = warp_sum(zs);
+            if (lane == 0 && zs) atomicAdd(reinterpret_cast<unsigned long long *>(&s.weight[kBins - 1]), (unsigned long long)zs);
         }
-        if (CLUSTER) {
-            __syncthreads();
-            if (!lead)
-                for (int b = tid; b < kBins; b += kThreads) {
-                    const uint32_t n = s.hist[b];
-                    if (n) add32(remote(&s.hist[b], 0), n), s.hist[b] = 0;
-                    if (weigh) {
-                        const uint64_t w = s.weight[b];
-                        if (w) add64(remote(&s.weight[b], 0), w), s.weight[b] = 0;
-                    }
-                }
-        }
+        merge_hist();
     };
     const auto sum_exact = [&](uint32_t hi, uint32_t lo) {  // masses of keys in [lo, hi]
         uint64_t z = 0;
-        for (int ch = rank * kWarps + warp; ch < chunks; ch += ranks * kWarps)
+        for (int ch = rank * kWarps + warp; ch < chunks; ch += ranks * kWarps) {
+            if (key_of(s_chunk_m[ch]) < lo) continue;
 #pragma unroll 1
             for (int j = 0; j < kVec; ++j) {
                 float f[E];
                 R::unpack(r.load(ch * kChunkVecs + j * 32 + lane), f);
-#pragma unroll 1
-                for (int e = 0; e < E; ++e) {
-                    const uint32_t k = key_of<BF16>(f[e]);
-                    if (k >= lo && k <= hi) z += mass(ex, f[e]);
+                uint32_t in = 0;
+#pragma unroll
+                for (int e = 0; e < E; ++e) in |= (key_of(f[e]) >= lo && key_of(f[e]) <= hi ? 1u : 0u) << e;
+                if (!__any_sync(0xFFFFFFFFu, in)) continue;
+#pragma unroll
+                for (int e = 0; e < E; ++e) {  // without branches, so that the elements' chains overlap
+                    const uint64_t m = mass(ex, f[e]);
+                    z += in >> e & 1 ? m : 0;
                 }
             }
-        z = warp_sum(z);
-        if (lane == 0) {
-            if (CLUSTER) {
-                add64(remote(&s.sum, 0), z);
-            } else {
-                atomicAdd(reinterpret_cast<unsigned long long *>(&s.sum), (unsigned long long)z);
-            }
         }
+        z = warp_sum(z);
+        if (lane == 0) L::add(&s.sum, z);
     };
-    const auto sum_chunks = [&](uint32_t border, bool exact) {  // keys above the border, and how many are at it
+    // Tokens in [low, high] to the list; with `sums` the fast masses above it by chunk, and below it together.  The chunks that
+    // lie below are the first CTA's to add.
+    const auto between = [&](float high, float low, bool sums) {
+        uint64_t zs = 0;
         for (int ch = rank * kWarps + warp; ch < chunks; ch += ranks * kWarps) {
+            if (s_chunk_m[ch] < low) continue;
             uint4 v[kVec];
 #pragma unroll
             for (int j = 0; j < kVec; ++j) v[j] = r.load(ch * kChunkVecs + j * 32 + lane);
-            float z = 0.0f;
-            uint64_t z64 = 0;
-            uint32_t ties = 0;
+            float above = 0.0f, below = 0.0f;
+            uint32_t in = 0;
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
-                const int i = ch * kChunkVecs + j * 32 + lane;
-                const bool whole = i * E >= r.off && (i + 1) * E <= r.off + r.n;
                 float f[E];
                 R::unpack(v[j], f);
-                if (exact) {
-#pragma unroll 1
-                    for (int e = 0; e < E; ++e) {
-                        const float x = r.at(i * E + e - r.off);
-                        if (key_of<BF16>(x) > border) z64 += mass(ex, x);
-                    }
-                }
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    const uint32_t k = key_of<BF16>(f[e]);
-                    if (!exact) z += k > border ? ex2((f[e] - ex.top) * ex.c) : 0.0f;
-                    ties += k == border && (whole || r.holds(i, e));
+                    const bool is_low = f[e] < low, is_high = f[e] > high;
+                    if (sums) {
+                        const float m = fast(ex, f[e] - ex.top);
+                        if (is_low) below += m;
+                        if (is_high) above += m;
+                    }
+                    if (!is_low && !is_high) in |= 1u << (j * E + e);
                 }
             }
-            ties = __reduce_add_sync(0xFFFFFFFFu, ties);
-            if (!exact) {
-                for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
-                z64 = (uint64_t)__double2ll_rn((double)z * (double)(uint64_t(1) << kScale));
-            } else {
-                z64 = warp_sum(z64);
+            if (sums) {
+                above = warp_sum(above);
+                zs += fixed(below);
+                if (lane == 0) L::put(&s_chunk[ch], fixed(above));
+            }
+            if (__any_sync(0xFFFFFFFFu, in)) {
+                const uint32_t n = __popc(in);
+                uint32_t at = n;
+                for (int o = 1; o < 32; o *= 2) {
+                    const uint32_t t = __shfl_up_sync(0xFFFFFFFFu, at, o);
+                    if (lane >= o) at += t;
+                }
+                uint32_t base = 0;
+                if (lane == 31) base = L::add(&s.listed, at);
+                at += __shfl_sync(0xFFFFFFFFu, base, 31) - n;
+                for (; in; in &= in - 1, ++at) {
+                    const int b = __ffs(in) - 1, e = (ch * kChunkVecs + (b / E) * 32 + lane) * E + b % E - r.off;
+                    // outside the row only where low is -inf: the last of all, without mass
+                    if (at < kList) L::put(&s.list[at], r.inside(e) ? place_of(key_of(r.at(e)), (uint32_t)e) : ~uint64_t(0) - 1);
+                }
+            }
+        }
+        if (sums) {
+            zs = warp_sum(zs);
+            if (lane == 0) L::add(&s.sum, zs);
+        }
+    };
+    // By chunk: what is above the border, fast, and how many are at it; or exactly what is kept, `upto` the last index at the border.
+    const auto kept_fast = [&](float border) {
+        for (int ch = rank * kWarps + warp; ch < chunks; ch += ranks * kWarps) {
+            float above = 0.0f;
+            uint32_t ties = 0;
+            if (s_chunk_m[ch] >= border) {
+                uint4 v[kVec];
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) v[j] = r.load(ch * kChunkVecs + j * 32 + lane);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    float f[E];
+                    R::unpack(v[j], f);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        if (f[e] > border) above += fast(ex, f[e] - ex.top);
+                        if (f[e] == border) ++ties;  // nothing outside the row unless the border is -inf, where no mass is at it
+                    }
+                }
+                above = warp_sum(above);
+                ties = __reduce_add_sync(0xFFFFFFFFu, ties);
             }
             if (lane == 0) {
-                if (CLUSTER) {
-                    put64(remote(&s.chunk[ch], 0), z64);
-                    put(remote(&s.ties[ch], 0), ties);
-                } else {
-                    s.chunk[ch] = z64, s.ties[ch] = ties;
-                }
+                L::put(&s_chunk[ch], fixed(above));
+                L::put(&s_ties[ch], ties);
             }
+        }
+    };
+    const auto kept_exact = [&](float border, uint32_t upto) {
+        for (int ch = rank * kWarps + warp; ch < chunks; ch += ranks * kWarps) {
+            uint64_t z = 0;
+            if (s_chunk_m[ch] >= border) {
+#pragma unroll 1
+                for (int j = 0; j < kVec; ++j) {
+                    const int i = ch * kChunkVecs + j * 32 + lane;
+                    float f[E];
+                    R::unpack(r.load(i), f);
+                    uint32_t in = 0;
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        in |= (f[e] > border || (f[e] == border && (uint32_t)max(i * E + e - r.off, 0) <= upto) ? 1u : 0u) << e;
+                    if (!__any_sync(0xFFFFFFFFu, in)) continue;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const uint64_t m = mass(ex, f[e]);
+                        z += in >> e & 1 ? m : 0;
+                    }
+                }
+                z = warp_sum(z);
+            }
+            if (lane == 0) L::put(&s_chunk[ch], z);
         }
     };
     const auto sweep = [&]() {
         ex.top = s.top;
         const int what = s.what;
-        if (what == kHist || what == kWeigh) count_hist(s.hi, s.lo, s.shift, what == kWeigh);
-        if (what == kSum) sum_exact(s.hi, s.lo);
-        if (what == kChunksFast || what == kChunksExact) sum_chunks(s.hi, what == kChunksExact);
+        const uint32_t hi = s.hi, lo = s.lo;
+        if (what == kHist || what == kWeigh) count_hist(hi, lo, s.shift, what == kWeigh);
+        if (what == kSum) sum_exact(hi, lo);
+        if (what == kBetween || what == kBetweenSums) between(__uint_as_float(hi), __uint_as_float(lo), what == kBetweenSums);
+        if (what == kKeptFast) kept_fast(__uint_as_float(hi));
+        if (what == kKeptExact) kept_exact(__uint_as_float(hi), lo);
     };
     if (CLUSTER && !lead) {
         for (;;) {
@@ -446,14 +608,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
             for (int b = tid; b < kBins; b += kThreads) s.hist[b] = 0, s.weight[b] = 0;
         if (tid == 0) {
             s.sum = 0;
+            s.listed = 0;
             s.what = what, s.hi = hi, s.lo = lo, s.shift = shift;
         }
         if (CLUSTER && tid > 0 && tid < ranks) {
-            put(remote(&s.top, tid), __float_as_uint(ex.top));
-            put(remote(&s.hi, tid), hi);
-            put(remote(&s.lo, tid), lo);
-            put(remote(&s.shift, tid), (uint32_t)shift);
-            put(remote(&s.what, tid), (uint32_t)what);
+            L::put(reinterpret_cast<uint32_t *>(&s.top), __float_as_uint(ex.top), tid);
+            L::put(&s.hi, hi, tid);
+            L::put(&s.lo, lo, tid);
+            L::put(reinterpret_cast<uint32_t *>(&s.shift), (uint32_t)shift, tid);
+            L::put(reinterpret_cast<uint32_t *>(&s.what), (uint32_t)what, tid);
         }
         meet();
         if (what == kDone) return;
@@ -464,8 +627,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
     // ------------------------------------------------------------ the row's maximum and sum
     float top = -FLT_MAX, bad = 0.0f;
     for (int i = tid; i < chunks; i += kThreads) {
-        top = fmaxf(top, s.chunk_m[i]);
-        if (isnan(s.chunk_s[i])) bad = 1.0f;
+        top = fmaxf(top, s_chunk_m[i]);
+        if (isnan(s_chunk_s[i])) bad = 1.0f;
     }
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     if (lane == 0) s.wf[warp] = top;
@@ -476,10 +639,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
     ex.top = top;
     uint64_t Z = 0, mine = 0;
     for (int i = tid; i < chunks; i += kThreads) {
-        const float t = s.chunk_s[i];
-        const uint64_t m = any_bad || t == 0.0f ? 0 : (uint64_t)__double2ll_rn((double)t * (double)mass(ex, s.chunk_m[i]));
-        s.chunk[i] = m;
-        s.ties[i] = 0;
+        const float t = s_chunk_s[i];
+        const uint64_t m = any_bad || t == 0.0f ? 0 : (uint64_t)__double2ll_rn((double)t * (double)mass(ex, s_chunk_m[i]));
+        s_chunk[i] = m;
         mine += m;
     }
     block_scan(s, mine, Z);
@@ -488,207 +650,424 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
         ask(kDone, 0, 0, 0);
         return;
     }
+    const uint32_t top_key = key_of(top);
+    uint32_t least = 0;  // the smallest key that min_p keeps
+    if (cut_m) {
+        least = qerl::key_of<false>(__double2float_ru((double)top + (double)tau * log((double)fminf(min_p, 1.0f))));
+        // the first bf16 that is as large: their keys end in 0000 above zero and, before the lower half went, in FFFF below
+        if (BF16) least = (least & 0x80000000u ? least + 0xFFFFu : least) & 0xFFFF0000u;
+    }
 
-    // ------------------------------------------------------------ the border of what is kept
-    int k = a.top_ks ? a.top_ks[row] : a.top_k;
-    float top_p = a.top_ps ? a.top_ps[row] : a.top_p, min_p = a.min_ps ? a.min_ps[row] : a.min_p;
-    if (top_p <= 0.0f) k = 1;
-    const bool cut_k = k > 0 && k < r.n, cut_p = top_p > 0.0f && top_p < 1.0f;
-    const uint32_t top_key = key_of<BF16>(top);
-    uint32_t border = 0;           // keys above it are kept,
-    uint32_t keep = 0xFFFFFFFFu;   // and the first `keep` at it
-    // The weights of this thread's four bins: tokens, or masses.  Bins of single keys need no sweep of masses; what the last one
-    // has then is given.
-    const auto weights = [&](bool by_mass, bool weighed, uint32_t hi, int shift, uint64_t last, uint64_t (&w)[4]) -> uint64_t {
-        uint64_t sum = 0;
+    // ------------------------------------------------------------ the border of what is kept, by a list
+    uint64_t last = ~uint64_t(0);  // the last place that is kept
+    bool found = !sampled && !cut_m, fast = found;  // `fast`: the chunks' masses are
+    const auto wanted = [&](uint64_t z) { return (uint64_t)ceil((double)top_p * (double)z); };
+    if (sampled) {
+        // Thresholds from a histogram in 32nds of an octave below the maximum; the last bin has no mass.  For the first k tokens: of the chunks' maxima, k of
+        // which are k tokens, or, where there are too few chunks, of the sample.  For top_p: of the sample, by what it puts below.
+        const bool by_max = cut_k && 2 * (int64_t)k <= chunks;
+        const int n_sample = by_max ? chunks : (chunks + every - 1) / every * 64;
+        const float step = 32.0f * ex.c, W = by_max ? 1.0f : (float)(kChunk * every) / 64.0f;
+        for (int i = tid; i < n_sample; i += kThreads) {
+            const float x = by_max ? s_chunk_m[i] : s.sample[i], y = (top - x) * step;
+            if (y < kBins - 1.0f)
+                atomicAdd(&s.hist[(int)y], 1u);
+        }
+        if (tid < 4) s.mark[tid] = kBins;
+        __syncthreads();
+        uint64_t cnt = 0, below = 0, all_cnt, all_mass = 0;
+        float squares = 0.0f;
+        uint32_t n[4];
+        uint64_t m[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int b = tid * 4 + j;
-            const uint64_t n = s.hist[b];
-            w[j] = n;
-            if (by_mass && n) w[j] = weighed ? s.weight[b] : b < kBins - 1 ? n * mass(ex, value_of<BF16>(hi - ((uint32_t)b << shift))) : last;
-            sum += w[j];
+            n[j] = s.hist[b];
+            m[j] = 0;
+            if (!cut_k && n[j] && b < kBins - 1) {
+                const float e = ex2((float)(2 * b + 1) * (-1.0f / 64.0f));
+                m[j] = fixed((float)n[j] * e);
+                squares += (float)n[j] * e * e;
+            }
+            cnt += n[j], below += m[j];
         }
-        return sum;
-    };
-    // The first bin where the sum of weights, `before` it included, reaches `want` (kBins where none does), and the sum before it.
-    const auto reach = [&](const uint64_t (&w)[4], uint64_t sum, uint64_t before, uint64_t want, uint64_t &reached) -> uint32_t {
-        uint64_t all, at = block_scan(s, sum, all);
-        at += before - sum;
-        if (tid == 0) s.got32[0] = kBins;
-        __syncthreads();
+        uint64_t at_cnt = block_scan(s, cnt, all_cnt) - cnt, at_mass = 0;
+        if (!cut_k) {
+            at_mass = block_scan(s, below, all_mass) - below;
+            // the sum of squares of the masses from this thread's bins on: the variance of what the sample puts below
+            for (int o = 1; o < 32; o *= 2) {
+                const float t = __shfl_down_sync(0xFFFFFFFFu, squares, o);
+                if (lane + o < 32) squares += t;
+            }
+            if (lane == 0) s.wf[warp] = squares;
+            __syncthreads();
+            for (int w = warp + 1; w < kWarps; ++w) squares += s.wf[w];
+        }
+        const float sigma = W * sqrtf(squares) * pow2f(kScale), rest = (1.0f - top_p) * (float)Z, need = by_max ? (float)k : (float)k + 8.0f * sqrtf(W * (float)k) + 6.0f * W;
+        // of bin b on: enough tokens in the bins up to b; or little enough below them; or surely too much
+        const auto marks = [&](uint64_t c, uint64_t at) -> uint32_t {
+            const float left = W * (float)(all_mass - at), upto = W * (float)c;
+            if (cut_k) return upto >= need ? 2 : 0;
+            // A list of all that is above has to be generous: what stands out is not in the sample.  Where the border lies among
+            // many alike, the sample knows what is below it within its own deviation.
+            return (left + 3.0f * sigma <= 0.25f * rest && upto <= 0.6f * kList ? 1 : 0) | (left + 3.0f * sigma <= 0.99f * rest ? 2 : 0) |
+                   (left - 3.0f * sigma < 1.01f * rest ? 4 : 0) | (upto > 1000.0f ? 8 : 0);
+        };
+        uint64_t c = at_cnt, at = at_mass;
+        uint32_t first[4] = {kBins, kBins, kBins, kBins};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (at < want && at + w[j] >= want) s.got32[0] = tid * 4 + j, s.got64[0] = at;
-            at += w[j];
+            const uint32_t b = tid * 4 + j;
+            c += n[j], at += m[j];
+            const uint32_t now = marks(c, at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (now >> i & 1) first[i] = min(first[i], b);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t b = __reduce_min_sync(0xFFFFFFFFu, first[i]);
+            if (lane == 0 && b < kBins) atomicMin(&s.mark[i], b);
         }
         __syncthreads();
-        const uint32_t bin = s.got32[0];
-        reached = s.got64[0];
+        const bool all_listed = cut_k || s.mark[0] < kBins;
+        // all that is above: down to where there are a thousand, or further
+        const uint32_t b_low = cut_k || !all_listed ? s.mark[1] : max(s.mark[0], min(s.mark[3], kBins - 1u) - 1u), b_high = all_listed ? 0 : s.mark[2] % kBins;
         __syncthreads();
-        return bin;
-    };
-    const auto settle = [&](bool by_mass, uint32_t key, uint64_t n, uint64_t reached, uint64_t want) {
-        const uint64_t one = by_mass ? mass(ex, value_of<BF16>(key)) : 1, more = one ? (want - reached + one - 1) / one : n;
-        border = key;
-        keep = (uint32_t)(more < n ? more : n);
-    };
-    // The place of the k-th token, or of the first where the sum of masses reaches `want`, by histograms of ever finer bins
-    // below the maximum; `first`: the first one is there.  No key below lo counts.
-    constexpr int kFirst = BF16 ? 16 : 14;  // fp32: four octaves below the maximum in 2^-9 of the value
-    const auto find = [&](bool by_mass, uint64_t want, bool first, uint32_t lo) {
-        uint32_t hi = top_key;
-        int shift = kFirst;
-        uint64_t before = 0;
-        for (int turn = 0; turn < 6; ++turn) {  // 2^32 keys, 2^10 bins or more a turn
-            const bool weighed = by_mass && shift != kUnit;
-            if (!(first && turn == 0)) ask(weighed ? kWeigh : kHist, hi, lo, shift);
-            uint64_t w[4], reached;
-            const uint64_t sum = weights(by_mass, weighed, hi, shift, uint64_t(1) << 61, w);  // the last bin reaches it if no other does
-            const uint32_t bin = reach(w, sum, before, want, reached);
-            if (bin >= kBins) return;  // all are kept
-            if (shift == kUnit && bin < kBins - 1) {
-                settle(by_mass, hi - (bin << shift), s.hist[bin], reached, want);
-                return;
-            }
-            before = reached;
-            hi -= bin << shift;
-            if (bin < kBins - 1 && hi - lo >= (1u << shift)) lo = hi - ((1u << shift) - 1u);
-            const int bits = 32 - __clz(hi - lo);
-            shift = max(kUnit, bits < kBinBits ? 0 : bits - kBinBits + 1);  // at most 2^10 bins: no remainder in the last one
+        c = at_cnt;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t b = tid * 4 + j;
+            c += n[j];
+            if (b == min(b_low, kBins - 1u)) s.got64[0] = c;  // the tokens of the bins up to b_low, and before b_high
+            if (b + 1 == b_high) s.got64[1] = c;
         }
-    };
-    if (cut_k) find(false, (uint64_t)k, false, 0);
-    if (cut_p) {
-        uint64_t w[4], all, reached;
-        const auto wanted = [&](uint64_t z) { return (uint64_t)ceil((double)top_p * (double)z); };
-        if (cut_k) {  // the sum of the first k
-            uint64_t above = 0;
-            if (border != top_key) {
-                ask(kSum, 0xFFFFFFFFu, border + (1u << kUnit), 0);
-                above = s.sum;
-            }
-            find(true, wanted(above + keep * mass(ex, value_of<BF16>(border))), false, border);
-        } else if (BF16) {
-            // Single keys but for the last bin, whose mass is fast: would the choice differ at the ends of what it may be?
-            ask(kHist, top_key, 0, kFirst);
-            const uint64_t rest = s.sum, sum = weights(true, false, top_key, kFirst, s.sum, w);
+        __syncthreads();
+        bool try_list = W * (float)(s.got64[0] - (b_high ? s.got64[1] : 0)) <= 0.8f * kList;
+        // fewer than k within 64 octaves: what lies below has no mass
+        float low = top - (float)min(b_low + 1, kBins - 1u) / step, high = b_high ? top - (float)b_high / step : INFINITY;
+        if (r.n <= kThreads || (r.n <= kList && !try_list)) try_list = true, low = -INFINITY, high = INFINITY;
+        if (BF16) low = __bfloat162float(__float2bfloat16_rd(low)), high = __bfloat162float(__float2bfloat16_ru(high));
+        const auto skipped_below = [&](float bound) -> uint64_t {  // fast masses of the chunks that the sweep skips
+            uint64_t sum = 0, all;
+            for (int i = tid; i < chunks; i += kThreads)
+                if (s_chunk_m[i] < bound) sum += s_chunk[i];
             block_scan(s, sum, all);
-            const uint64_t off = rest ? (uint64_t)((double)rest * kEps) + 1 : 0;
-            const uint32_t bin = reach(w, sum, 0, wanted(all - off), reached);
-            bool sure = bin < kBins - 1;
-            if (sure) {
-                const uint32_t key = top_key - (bin << kFirst);
-                settle(true, key, s.hist[bin], reached, wanted(all - off));
-                const uint32_t kept = keep;
-                if (off) sure = reach(w, sum, 0, wanted(all + off), reached) == bin;
-                if (off && sure) {
-                    settle(true, key, s.hist[bin], reached, wanted(all + off));
-                    sure = keep == kept;
+            return all;
+        };
+        if (cut_m && least > key_of(high)) try_list = false;  // min_p's border is the one, as a rule
+        if (try_list) {
+            const bool sums = !cut_k;
+            const uint64_t skipped = sums ? skipped_below(low) : 0;
+            for (int i = tid; i < chunks; i += kThreads) s_chunk[i] = 0;
+            for (int i = tid; i < kBins; i += kThreads) s.weight[i] = 0;
+            uint64_t below = 0, above = 0, held = 0, t;
+            ask(sums ? kBetweenSums : kBetween, __float_as_uint(high), __float_as_uint(low), 0);
+            const uint32_t listed = s.listed;
+            below = skipped + s.sum;
+            if (listed <= kList && listed > 0) {
+                const auto mass_at = [&](uint64_t place) { return mass(ex, value_of(~(uint32_t)(place >> 32))); };
+                // Longer lists than a thread's entry each: in bins of keys, of which those near the border are gathered.
+                const bool binned = listed > kThreads;
+                const uint32_t spread = top_key - key_of(low);
+                const int shift = max(kUnit, 32 - __clz(spread) - kBinBits);
+                const auto bin_of = [&](uint64_t place) { return (top_key - ~(uint32_t)(place >> 32)) >> shift; };
+                if (binned) {
+                    __syncthreads();
+                    for (int b = tid; b < kBins; b += kThreads) s.hist[b] = 0;
+                    __syncthreads();
+                    for (int i = tid; i < (int)listed; i += kThreads) {
+                        const uint64_t place = s.list[i], w = mass_at(place);
+                        atomicAdd(&s.hist[bin_of(place)], 1u);
+                        if (w && shift > kUnit) atomicAdd(reinterpret_cast<unsigned long long *>(&s.weight[bin_of(place)]), (unsigned long long)w);
+                        held += w;
+                    }
+                } else {
+                    uint64_t place = 0;
+                    if (tid < (int)listed) held = mass_at(place = s.list[tid]);
+                    s.small[tid] = place;
+                }
+                t = held;
+                block_scan(s, t, held);
+                // The first entries up to which the tokens, or masses, reach `from` and `to`; with the mass up to the first.
+                int sorted = 0;
+                uint64_t own = 0, mass_before = 0, count_before = 0;
+                const auto pick = [&](bool by_mass, uint64_t from, uint64_t to, uint64_t &place0, uint64_t &place1, uint64_t &upto) -> bool {
+                    if (binned) {
+                        uint64_t w[4], c[4], sum = 0, count = 0, all;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int b = tid * 4 + j;
+                            c[j] = s.hist[b];
+                            w[j] = shift > kUnit ? s.weight[b] : c[j] ? c[j] * mass(ex, value_of(top_key - ((uint32_t)b << shift))) : 0;  // one key a bin
+                            sum += w[j], count += c[j];
+                        }
+                        uint64_t at_m = block_scan(s, sum, all) - sum, at_c = block_scan(s, count, all) - count;
+                        if (tid < 2) s.got32[tid] = kBins;
+                        if (tid == 2) s.listed = 0;
+                        __syncthreads();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint64_t at = by_mass ? at_m : at_c, add = by_mass ? w[j] : c[j];
+                            if (at < from && at + add >= from) s.got32[0] = tid * 4 + j, s.got64[0] = at_m, s.got64[1] = at_c;
+                            if (at < to && at + add >= to) s.got32[1] = tid * 4 + j;
+                            at_m += w[j], at_c += c[j];
+                        }
+                        __syncthreads();
+                        const uint32_t b0 = s.got32[0], b1 = s.got32[1];
+                        mass_before = s.got64[0], count_before = s.got64[1];
+                        if (b0 >= kBins || b1 >= kBins) return false;
+                        for (int i = tid; i < (int)listed; i += kThreads) {
+                            const uint64_t place = s.list[i];
+                            if (bin_of(place) >= b0 && bin_of(place) <= b1) {
+                                const uint32_t to_ = atomicAdd(&s.listed, 1u);
+                                if (to_ < kThreads) s.small[to_] = place;
+                            }
+                        }
+                        __syncthreads();
+                        sorted = 0;
+                        if (s.listed > kThreads) return false;  // as good as equal ones
+                    }
+                    const int n_small = binned ? (int)s.listed : (int)listed;
+                    if (!sorted) {
+                        own = sort_small(s, n_small);
+                        sorted = 1;
+                    }
+                    const uint64_t m = tid < n_small ? mass_at(own) : 0;
+                    uint64_t all, at_m = mass_before + block_scan(s, m, all);
+                    const uint64_t at = by_mass ? at_m : count_before + tid + 1, before = at - (by_mass ? m : 1);
+                    if (tid < 2) s.got64[tid] = 0;
+                    __syncthreads();
+                    if (tid < n_small && before < from && at >= from) s.got64[0] = own, s.sum = at_m;
+                    if (tid < n_small && before < to && at >= to) s.got64[1] = own;
+                    __syncthreads();
+                    place0 = s.got64[0], place1 = s.got64[1], upto = s.sum;
+                    __syncthreads();
+                    return place0 != 0 && place1 != 0;
+                };
+                bool kept = false;
+                uint64_t border = 0, other, upto;
+                if (cut_k) {
+                    const uint64_t few = min((uint32_t)k, listed);
+                    kept = (listed >= (uint32_t)k || b_low >= kBins - 1) && pick(false, few, few, border, other, upto);
+                    if (kept && cut_p) {
+                        const uint64_t want = wanted(upto);  // of the sum of the first k
+                        kept = pick(true, want, want, border, other, upto);
+                    }
+                } else {
+                    uint64_t part = 0;
+                    for (int i = tid; i < chunks; i += kThreads) part += s_chunk[i];
+                    block_scan(s, part, above);
+                    // The border is the first token after which at most 1 - top_p of the sum is left.  The fast sums may move that by
+                    // `off`: is it the same token at either end?
+                    const double leaves = (1.0 - (double)top_p) * (double)(above + held + below);
+                    const double off = ((1.0 - (double)top_p) * (double)(above + below) + (double)below) * kEps + 4.0, in_list = (double)(held + below);
+                    if ((above | below) == 0) {
+                        kept = pick(true, wanted(held), wanted(held), border, other, upto);
+                    } else if (in_list - leaves > off && in_list - leaves + off <= (double)held) {
+                        const uint64_t from = (uint64_t)ceil(in_list - leaves - off), to = (uint64_t)ceil(in_list - leaves + off);
+                        kept = pick(true, from, to, border, other, upto);
+                        if (kept && border != other) {  // exactly: the sums above and below, and what is reached
+                            if (below) {
+                                ask(kSum, key_of(low) - (1u << kUnit), 0, 0);
+                                below = s.sum;
+                            }
+                            if (above) {
+                                ask(kSum, 0xFFFFFFFFu, key_of(high) + (1u << kUnit), 0);
+                                above = s.sum;
+                            }
+                            Z = above + held + below;
+                            const uint64_t want = wanted(Z);
+                            kept = want > above && pick(true, want - above, want - above, border, other, upto);
+                        }
+                    }
+                }
+                if (kept) {
+                    last = border;
+                    if (cut_m) last = min(last, place_of(least, 0xFFFFFFFFu));
+                    // what min_p leaves has to end in the list
+                    found = high == INFINITY || last >= place_of(key_of(high), 0);
+                    fast = high != INFINITY;
+                    __syncthreads();
+                    if (found) {
+                        // What is kept of the list, in halves of 21 bits, so that a chunk's sums fit 32; the chunks' first sums are
+                        // not needed any more.
+                        uint32_t *const s_high = reinterpret_cast<uint32_t *>(s_chunk_s);
+                        for (int i = tid; i < chunks; i += kThreads) s_ties[i] = s_high[i] = 0;
+                        __syncthreads();
+                        for (int i = tid; i < (int)listed; i += kThreads) {
+                            const uint64_t place = s.list[i];
+                            if (place <= last) {
+                                const uint64_t m = mass_at(place);
+                                const int ch = ((int)(uint32_t)place + r.off) / kChunk;
+                                if (m) atomicAdd(&s_ties[ch], (uint32_t)m & 0x1FFFFFu), atomicAdd(&s_high[ch], (uint32_t)(m >> 21));
+                            }
+                        }
+                        __syncthreads();
+                        for (int i = tid; i < chunks; i += kThreads) s_chunk[i] += ((uint64_t)s_high[i] << 21) + s_ties[i];
+                    }
+                    __syncthreads();
                 }
             }
-            if (!sure) {
-                ask(kSum, 0xFFFFFFFFu, 0, 0);
-                Z = s.sum;
-                find(true, wanted(Z), false, 0);
-            }
-        } else {
-            ask(kWeigh, top_key, 0, kFirst);
-            block_scan(s, weights(true, true, top_key, kFirst, 0, w), Z);
-            find(true, wanted(Z), true, 0);
         }
     }
-    if (min_p > 0.0f) {
-        const double t = (double)top + (double)tau * log((double)fminf(min_p, 1.0f));
-        uint32_t least = key_of<false>(__double2float_ru(t));
-        // the first bf16 that is as large: their keys end in 0000 above zero and, before the lower half went, in FFFF below
-        if (BF16) least = (least & 0x80000000u ? least + 0xFFFFu : least) & 0xFFFF0000u;
-        if (least > border) border = least, keep = 0xFFFFFFFFu;
+
+    // ------------------------------------------------------------ or by histograms
+    if (!found) {
+        uint32_t border = key_of(-INFINITY), keep = 0xFFFFFFFFu;  // keys above the border are kept, and the first `keep` at it
+        // The weights of this thread's four bins: tokens, or masses.  Bins of single keys need no sweep of masses; what the last one
+        // has then is given.
+        const auto weights = [&](bool by_mass, bool weighed, uint32_t hi, int shift, uint64_t (&w)[4]) -> uint64_t {
+            uint64_t sum = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int b = tid * 4 + j;
+                const uint64_t n = s.hist[b];
+                w[j] = n;
+                if (by_mass && n) w[j] = weighed ? s.weight[b] : b < kBins - 1 ? n * mass(ex, value_of(hi - ((uint32_t)b << shift))) : uint64_t(1) << 61;
+                sum += w[j];
+            }
+            return sum;
+        };
+        // The place of the k-th token, or of the first where the sum of masses reaches `want`, by histograms of ever finer bins
+        // below the maximum.  No key below lo counts.
+        constexpr int kFirst = BF16 ? 16 : 14;  // fp32: four octaves below the maximum in 2^-9 of the value
+        const auto find = [&](bool by_mass, uint64_t want, uint32_t lo) {
+            uint32_t hi = top_key;
+            int shift = kFirst;
+            uint64_t before = 0;
+            for (int turn = 0; turn < 6; ++turn) {  // 2^32 keys, 2^10 bins or more a turn
+                const bool weighed = by_mass && shift != kUnit;
+                ask(weighed ? kWeigh : kHist, hi, lo, shift);
+                uint64_t w[4], all;
+                const uint64_t sum = weights(by_mass, weighed, hi, shift, w);  // the last bin reaches it if no other does
+                uint64_t at = before + block_scan(s, sum, all) - sum;
+                if (tid == 0) s.got32[0] = kBins;
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (at < want && at + w[j] >= want) s.got32[0] = tid * 4 + j, s.got64[0] = at;
+                    at += w[j];
+                }
+                __syncthreads();
+                const uint32_t bin = s.got32[0];
+                const uint64_t reached = s.got64[0];
+                __syncthreads();
+                if (bin >= kBins) return;  // all are kept
+                if (shift == kUnit && bin < kBins - 1) {
+                    border = hi - (bin << shift);
+                    const uint64_t one = by_mass ? mass(ex, value_of(border)) : 1, n = s.hist[bin];
+                    const uint64_t more = one ? (want - reached + one - 1) / one : n;
+                    keep = (uint32_t)(more < n ? more : n);
+                    return;
+                }
+                before = reached;
+                hi -= bin << shift;
+                if (bin < kBins - 1 && hi - lo >= (1u << shift)) lo = hi - ((1u << shift) - 1u);
+                const int bits = 32 - __clz(hi - lo);
+                shift = max(kUnit, bits < kBinBits ? 0 : bits - kBinBits + 1);  // at most 2^10 bins: no remainder in the last one
+            }
+        };
+        bool by_least = !sampled;
+        if (cut_m && cut_p && !cut_k) {  // does min_p leave less than top_p?
+            ask(kKeptFast, __float_as_uint(value_of(least)), 0, 0);
+            uint64_t sum = 0, all;
+            for (int i = tid; i < chunks; i += kThreads) sum += s_chunk[i] + s_ties[i] * mass(ex, value_of(least));
+            block_scan(s, sum, all);
+            by_least = (double)all * (1.0 + kEps) < (double)top_p * (double)Z * (1.0 - kEps);
+        }
+        if (cut_k && !by_least) find(false, (uint64_t)k, 0);
+        if (cut_p && !by_least) {
+            uint64_t sum = 0;
+            if (cut_k) {  // of the first k
+                if (border != top_key) {
+                    ask(kSum, 0xFFFFFFFFu, border + (1u << kUnit), 0);
+                    sum = s.sum;
+                }
+                sum += keep * mass(ex, value_of(border));
+            } else {
+                ask(kSum, 0xFFFFFFFFu, 0, 0);
+                sum = Z = s.sum;
+            }
+            find(true, wanted(sum), border);
+        }
+        if (cut_m && least > border) border = least, keep = 0xFFFFFFFFu;
+        // what is above it by chunk, and the chunk of the last that is kept at it
+        ask(kKeptFast, __float_as_uint(value_of(border)), 0, 0);
+        const uint64_t tie = mass(ex, value_of(border));
+        const int per = (chunks + kThreads - 1) / kThreads, i0 = min(tid * per, chunks), i1 = min(i0 + per, chunks);
+        uint64_t n = 0, all;
+        for (int i = i0; i < i1; ++i) n += s_ties[i];
+        if (tid == 0) s.got32[0] = 0xFFFFFFFFu;
+        uint64_t at = block_scan(s, n, all) - n;
+        for (int i = i0; i < i1; ++i) {
+            const uint64_t t = s_ties[i], kept = at >= keep ? 0 : (at + t > keep ? keep - at : t);
+            s_chunk[i] += kept * tie;
+            if (at < keep && at + t >= keep) s.got32[0] = i, s.got32[1] = (uint32_t)(keep - at);
+            at += t;
+        }
+        __syncthreads();
+        const int ch = (int)s.got32[0];
+        const uint32_t nth = s.got32[1];
+        uint32_t index = 0xFFFFFFFFu;
+        if (ch >= 0) {  // the index of its nth
+            constexpr int per_thread = kChunk / kThreads;
+            const int e0 = ch * kChunk + tid * per_thread - r.off;
+            uint64_t ties = 0;
+            for (int j = 0; j < per_thread; ++j) ties += r.inside(e0 + j) && r.at(e0 + j) == value_of(border);
+            uint64_t seen = block_scan(s, ties, all) - ties;
+            for (int j = 0; j < per_thread; ++j)
+                if (r.inside(e0 + j) && r.at(e0 + j) == value_of(border) && ++seen == nth) s.got32[0] = (uint32_t)(e0 + j);
+            __syncthreads();
+            index = s.got32[0];
+        }
+        last = place_of(border, index);
+        fast = true;
+        __syncthreads();
     }
-    const bool cut = cut_k || cut_p || min_p > 0.0f;
 
     // ------------------------------------------------------------ the token
-    const float u = fminf(fmaxf(a.u[row], 0.0f), 0.99999994f);  // NaN as 0
-    for (int attempt = cut ? 0 : -1; attempt < 2; ++attempt) {
-        const bool exact = attempt == 1;
-        if (attempt >= 0) {
-            if (attempt == 1 || cut) ask(exact ? kChunksExact : kChunksFast, border, 0, 0);
-        }
-        // ties up to the keep-th; masses up to the target
-        uint64_t total = 0, upto_mass = 0;
-        const uint64_t tie = cut ? mass(ex, value_of<BF16>(border)) : 0;
-        uint64_t seen = 0;
-        if (tid == 0) s.got32[0] = 0xFFFFFFFFu;
-        uint64_t target = 0;
-        // per-thread runs of consecutive chunks
+    const uint32_t u_bits = __float_as_uint(fminf(fmaxf(a.u[row], 0.0f), 0.99999994f));  // NaN as 0
+    const uint64_t u_m = u_bits >> 23 ? (u_bits & 0x7FFFFFu) | 0x800000u : 0;  // below 2^-126 as 0
+    const int u_e = 150 - (int)(u_bits >> 23);  // 24 or more
+    const uint32_t last_key = ~(uint32_t)(last >> 32), last_index = (uint32_t)last;
+    for (;;) {
         const int per = (chunks + kThreads - 1) / kThreads, i0 = min(tid * per, chunks), i1 = min(i0 + per, chunks);
-        uint64_t nt = 0;
-        if (cut || exact) {
-            for (int i = i0; i < i1; ++i) nt += s.ties[i];
-            uint64_t all;
-            seen = block_scan(s, nt, all) - nt;
-        }
-        uint64_t w = 0, at_tie = seen;
+        uint64_t w = 0, total = 0;
+        for (int i = i0; i < i1; ++i) w += s_chunk[i];
+        uint64_t at = block_scan(s, w, total) - w;
+        // floor(u total), u = u_m 2^-u_e
+        const uint64_t high_part = __umul64hi(total, u_m), low_part = total * u_m;
+        const uint64_t target = u_e < 64 ? low_part >> u_e | high_part << (64 - u_e) : u_e < 128 ? high_part >> (u_e - 64) : 0;
         for (int i = i0; i < i1; ++i) {
-            uint64_t m = s.chunk[i];
-            if (cut || exact) {
-                const uint64_t t = s.ties[i], kept = at_tie >= keep ? 0 : (at_tie + t > keep ? keep - at_tie : t);
-                m += kept * (cut ? tie : mass(ex, value_of<BF16>(border)));
-                at_tie += t;
-            }
-            w += m;
-        }
-        upto_mass = block_scan(s, w, total) - w;
-        target = (uint64_t)floor((double)u * (double)total);
-        if (target >= total) target = total - 1;
-        at_tie = seen;
-        uint64_t at = upto_mass;
-        for (int i = i0; i < i1; ++i) {
-            uint64_t m = s.chunk[i];
-            const uint64_t t0 = at_tie;
-            if (cut || exact) {
-                const uint64_t t = s.ties[i], kept = at_tie >= keep ? 0 : (at_tie + t > keep ? keep - at_tie : t);
-                m += kept * (cut ? tie : mass(ex, value_of<BF16>(border)));
-                at_tie += t;
-            }
-            if (at <= target && target < at + m) s.got32[0] = i, s.got64[0] = at, s.got64[1] = t0;
+            const uint64_t m = s_chunk[i];
+            if (at <= target && target < at + m) s.got32[0] = i, s.got64[0] = at;
             at += m;
         }
         __syncthreads();
         const int ch = (int)s.got32[0];
-        const uint64_t before = s.got64[0], ties_before = s.got64[1];
+        const uint64_t before = s.got64[0];
         __syncthreads();
-        if (ch < 0) continue;  // cannot be: total > target
-        // that chunk again, consecutive elements a thread
-        constexpr int per_thread = kChunkVecs * E / kThreads;
+        if (tid == 0) s.got32[0] = 0xFFFFFFFFu;
+        // that chunk again, consecutive tokens a thread
+        constexpr int per_thread = kChunk / kThreads;
         float f[per_thread];
-        uint64_t m[per_thread], t_n = 0;
-        const int e0 = ch * kChunkVecs * E + tid * per_thread - r.off;
+        uint64_t m[per_thread], own = 0, all;
+        const int e0 = ch * kChunk + tid * per_thread - r.off;
 #pragma unroll
         for (int j = 0; j < per_thread; ++j) {
             f[j] = r.at(e0 + j);
-            t_n += cut && e0 + j >= 0 && e0 + j < r.n && key_of<BF16>(f[j]) == border;
-        }
-        uint64_t all, t_at = 0;
-        if (cut) t_at = ties_before + block_scan(s, t_n, all) - t_n;
-        uint64_t own = 0;
-#pragma unroll
-        for (int j = 0; j < per_thread; ++j) {
-            const bool in = e0 + j >= 0 && e0 + j < r.n;
-            const uint32_t key = key_of<BF16>(f[j]);
-            bool kept = in && (!cut || key > border);
-            if (cut && in && key == border) kept = t_at++ < keep;
-            m[j] = kept ? mass(ex, f[j]) : 0;
+            const uint32_t key = key_of(f[j]);
+            const bool kept = key > last_key || (key == last_key && (uint32_t)max(e0 + j, 0) <= last_index);
+            m[j] = kept ? mass(ex, f[j]) : 0;  // 0 outside the row, which reads as -inf
             own += m[j];
         }
         uint64_t cum = before + block_scan(s, own, all) - own;
         // how far the fast sums before this chunk and the target may be off
-        const uint64_t off = exact ? 0 : (uint64_t)((double)total * kEps) + 2;
-        if (tid == 0) s.got32[0] = 0xFFFFFFFFu;
-        __syncthreads();
+        const uint64_t off = fast ? (total >> kOff) + 2 : 0;
 #pragma unroll
         for (int j = 0; j < per_thread; ++j) {
-            if (m[j] && cum + off <= target + (cum == 0 ? off : 0) && target + off < cum + m[j]) {
+            if (m[j] && (cum == 0 || cum + off <= target) && target + off < cum + m[j]) {
                 s.got32[0] = (uint32_t)(e0 + j);
                 s.got32[1] = __float_as_uint(f[j]);
             }
@@ -696,16 +1075,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
         }
         __syncthreads();
         const uint32_t id = s.got32[0];
-        if (id != 0xFFFFFFFFu) {
+        if (id != 0xFFFFFFFFu || !fast) {
             if (tid == 0) {
-                const double y = ((double)__uint_as_float(s.got32[1]) - (double)top) / (double)tau, unit = (double)(uint64_t(1) << kScale);
+                // the sums less the most probable token's, which is 1
+                const float y = (__uint_as_float(s.got32[1]) - top) / tau;
+                const auto log_of = [](uint64_t z) { return log1pf((float)(int64_t)(z - (uint64_t(1) << kScale)) * pow2f(-kScale)); };
                 a.ids[row] = id;
-                a.logp[row] = (float)(y - log((double)Z / unit));
-                a.logq[row] = (float)(y - log((double)total / unit));
+                a.logp[row] = y - log_of(Z);
+                a.logq[row] = y - log_of(total);
             }
             break;
         }
-        if (attempt == -1) attempt = 0;  // without a cut the chunks' exact sums are next
+        fast = false;
+        ask(kKeptExact, last == ~uint64_t(0) ? 0xFF800000u : __float_as_uint(value_of(last_key)), last_index, 0);
     }
     ask(kDone, 0, 0, 0);
 }
@@ -715,12 +1097,12 @@ cudaError_t launch(const Args &a, cudaStream_t stream, bool chain)
 {
     static OncePerDevice once;
     const auto kernel = sample_kernel<BF16, CLUSTER>;
-    cudaError_t e = allow_smem(once, kernel, sizeof(Shared));
+    cudaError_t e = allow_smem(once, kernel, sizeof(Shared) + kMostChunks * Shared::kChunkBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.T * a.cluster));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = sizeof(Shared);
+    cfg.dynamicSmemBytes = sizeof(Shared) + a.chunks * Shared::kChunkBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     int n = 0;
@@ -763,9 +1145,10 @@ extern "C" qerl_status qerl_sample(const void *logits, int dtype, int64_t T, int
     QERL_TRY(check_device());
     if (T == 0) return QERL_OK;
     const bool bf16 = dtype == QERL_DTYPE_BF16, chain = g_chain.load() != 0;
-    Args a = {logits, ld, T, V, u, o->temperature, o->top_p, o->min_p, o->top_k, o->temperatures, o->top_ps, o->min_ps, o->top_ks, ids, logp, logq, 1};
+    Args a = {logits, ld, T, V, u, o->temperature, o->top_p, o->min_p, o->top_k, o->temperatures, o->top_ps, o->min_ps, o->top_ks, ids, logp, logq, 1, 0};
     // Clusters while the rows alone leave SMs idle (two CTAs each), and no more CTAs than give every warp a chunk.
-    const int64_t chunks = (V * (bf16 ? 2 : 4) + kChunkVecs * 16 - 1) / (kChunkVecs * 16);
+    const int64_t chunks = (V * (bf16 ? 2 : 4) + 14 + kChunkVecs * 16 - 1) / (kChunkVecs * 16);
+    a.chunks = (int)chunks + (int)(chunks & 1);
     while (a.cluster < kMaxCluster && T * a.cluster < num_sms() && chunks > (int64_t)a.cluster * kWarps) a.cluster *= 2;
     if (a.cluster > 1) return launched(bf16 ? launch<true, true>(a, as_cuda(stream), chain) : launch<false, true>(a, as_cuda(stream), chain));
     return launched(bf16 ? launch<true, false>(a, as_cuda(stream), chain) : launch<false, false>(a, as_cuda(stream), chain));
