@@ -13,7 +13,6 @@
 #include <math.h>
 
 #include "fp4_round.cuh"
-#include "packed_layout.cuh"
 
 namespace qerl {
 namespace kv4 {
@@ -81,7 +80,7 @@ __global__ void __launch_bounds__(kTok *Tile<D>::B) append_kernel(const Cache c,
         uint32_t sk, sv;
         const uint64_t kc = quantise(k0, k1, c.k_scale, sk, finite);
         s_v[key][blk] = quantise(v0, v1, c.v_scale, sv, finite);
-        *reinterpret_cast<uint2 *>(to + M::k_word(key, 2 * blk)) = make_uint2(pack_code_word((uint32_t)kc), pack_code_word((uint32_t)(kc >> 32)));
+        *reinterpret_cast<uint2 *>(to + M::k_word(key, 2 * blk)) = make_uint2((uint32_t)kc, (uint32_t)(kc >> 32));
         to[M::k_scale(key, blk)] = (uint8_t)sk;
         to[M::v_scale(key, blk)] = (uint8_t)sv;
     }
@@ -138,7 +137,7 @@ __global__ void __launch_bounds__(kTok *Tile<D>::B) read_kernel(const Cache c, c
         const float sv = __fmul_rn(e4m3_to_float(s_tile[M::v_scale(key, blk)]), c.v_scale);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t w = unpack_code_word(*reinterpret_cast<const uint32_t *>(s_tile + M::k_word(key, 2 * blk + h)));
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(s_tile + M::k_word(key, 2 * blk + h));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 ko[4 * h + i] = two(e2m1_to_float(w >> (8 * i) & 15u) * sk, e2m1_to_float(w >> (8 * i + 4) & 15u) * sk);

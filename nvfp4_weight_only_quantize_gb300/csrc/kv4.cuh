@@ -3,8 +3,7 @@
 //
 // A tile holds 32 tokens of one sequence and kv head in 36 D bytes, in one piece,
 // so that one bulk copy brings it to shared memory:
-//   keys' codes    [32 tokens][D / 2]: words of eight dims in the packed code order
-//                  (packed_layout.cuh), which the dequantizer takes as it is;
+//   keys' codes    [32 tokens][D / 2], the even dim of a pair in the low nibble;
 //   values' codes  16 D bytes: a word holds eight tokens of one dim (token 8 q + n
 //                  in nibble n), because the second product sums over tokens;
 //   keys' scales   2 D bytes,  values' scales 2 D bytes.

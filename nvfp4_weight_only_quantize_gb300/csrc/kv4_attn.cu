@@ -7,21 +7,20 @@
 // shared memory, and multiplies them as the m operand of mma.sync, so that the
 // query rows, few in decoding, are the narrow side (8 columns) and nothing is
 // padded to 16:
-//   S^T = K Q^T     K dequantised in registers to bf16 (e2m1 * e4m3 is exact there),
-//                   Q as it is;
+//   S^T = K Q^T     K as fp16, code times scale, which is exact there; Q as fp16 after
+//                   a power of two per row that brings its largest element to [1, 2):
+//                   elements down to 2^-17 of that stay exact, smaller ones are off by
+//                   2^-25 of it, as a sum of FP32 products is anyway;
 //   P = 2^(S c - m) per column, rounded to fp16 and turned (movmatrix);
 //   O^T += V^T (P s)  V's codes converted to fp16 as they are; their scales s, which
 //                   differ by key, multiply P instead (half as many products).  P
 //                   stays at most 2^7, so that P s stays finite (s <= 448).
 // m is raised only when a column's maximum outgrows it by 2^7.
-// K takes the integer pipe (bit fields) and V the conversion pipe, which alone
-// would each bound a tile at about HBM's rate.
 #include "kv4_attn.cuh"
 
 #include <float.h>
 #include <math.h>
 
-#include "dequant.cuh"
 #include "sm100_ptx.cuh"
 
 namespace qerl {
@@ -30,14 +29,14 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kWarps = 4, kStages = 3;
+constexpr int kWarps = 4, kStages = 2, kPerSm = 4;
 constexpr float kHead = 4.0f, kRoom = 7.0f;  // m is set kHead below a maximum, and raised above kRoom
 constexpr uint64_t kLimitNs = 2000000000ull;
 
-template <int D, int NT>
+template <int D>
 struct Smem {
     static constexpr int RING = kWarps * kStages * Tile<D>::BYTES, ROW = D + 4;  // padded: the warps' rows meet without bank conflicts
-    static constexpr int O = RING, ML = O + kWarps * 8 * NT * ROW * 4, TOTAL = ML + kWarps * 8 * NT * 8;
+    static constexpr int O = RING, ML = O + kWarps * kRows * ROW * 4, Q = ML + kWarps * kRows * 8, TOTAL = Q + kRows * D * 2;
 };
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
@@ -45,12 +44,6 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)), "l"(src),
                  "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
-}
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
@@ -93,14 +86,19 @@ __device__ __forceinline__ void scales_f16(uint32_t w, uint32_t &lo, uint32_t &h
 struct Place {
     int seg, unit, T, i0, i1, left, off;  // segment, unit in it, its tiles, the range inside it, steps from i0 to the end, from the CTA's start to i0
 };
-__device__ __forceinline__ bool next_unit(const Side &s, int units, Place &p)
+__device__ __forceinline__ int seg_tiles(const Call &a, int k)
+{
+    return tiles_of(k < a.pre.n ? length(a.pre, k) : length(a.suf, k - a.pre.n));
+}
+__device__ __forceinline__ int seg_units(const Call &a, int k) { return a.Hkv * (k < a.pre.n ? a.pre.row_tiles : a.suf.row_tiles); }
+__device__ __forceinline__ bool next_unit(const Call &a, Place &p)
 {
     p.off += p.i1 - p.i0;
     p.left -= p.i1 - p.i0;
     if (p.left <= 0) return false;
-    if (++p.unit == units) {
+    if (++p.unit == seg_units(a, p.seg)) {
         p.unit = 0;
-        do p.T = tiles_of(length(s, ++p.seg));
+        do p.T = seg_tiles(a, ++p.seg);
         while (p.T == 0);
     }
     p.i0 = 0;
@@ -108,12 +106,12 @@ __device__ __forceinline__ bool next_unit(const Side &s, int units, Place &p)
     return true;
 }
 
-template <int D, int NT, int PER_SM>
-__global__ void __launch_bounds__(kWarps * 32, PER_SM) rows_kernel(const Call a, const Side s, int beside, unsigned int *err)
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32, kPerSm) rows_kernel(const __grid_constant__ Call a, unsigned int *err)
 {
     using M = Tile<D>;
-    using S = Smem<D, NT>;
-    constexpr int MT = D / 16, KW = D / 32, R = 8 * NT;  // row tiles of O^T; key words of a lane; query rows
+    using S = Smem<D>;
+    constexpr int MT = D / 16, KW = D / 32, R = kRows;  // row tiles of O^T; key words of a lane; query rows
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t s_full[kWarps][kStages];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, q = lane % 4;
@@ -121,30 +119,34 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) rows_kernel(const Call a,
         for (int k = 0; k < kWarps * kStages; ++k) mbar_init(&s_full[0][0] + k, 1);
         fence_mbar_init();
     }
-    // Beside the prefixes' kernel, whose CTAs let this one start once all work before both has finished, there is nothing to
-    // wait for; its last CTA waits at its end, so that the join, which waits for this kernel, has both.
-    if (!beside) pdl_wait();
+    pdl_wait();
     pdl_trigger();
     __syncthreads();
 
-    const int units = s.c.Hkv * s.row_tiles;
-    int total = 0;
-    for (int k = lane; k < s.c.n; k += 32) total += tiles_of(length(s, k)) * units;
+    const int segs = a.pre.n + a.suf.n;
+    constexpr int kHeld = 4;  // 32 segments each whose tiles stay in a register
+    int tiles[kHeld], total = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) tiles[i] = i * 32 + lane < segs ? seg_tiles(a, i * 32 + lane) : 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) total += i * 32 + lane < segs ? tiles[i] * seg_units(a, i * 32 + lane) : 0;
+    for (int k = kHeld * 32 + lane; k < segs; k += 32) total += seg_tiles(a, k) * seg_units(a, k);
     total = __reduce_add_sync(0xFFFFFFFFu, total);
-    const int per = max((total + s.grid - 1) / s.grid, kWarps);
+    const int per = max((total + a.grid - 1) / a.grid, 1);
     const int begin = min((int64_t)blockIdx.x * per, (int64_t)total), end = min(begin + per, total);
     Place at = {};
-    for (int k0 = 0, before = 0; k0 < s.c.n; k0 += 32) {
-        const int k = k0 + lane, T = k < s.c.n ? tiles_of(length(s, k)) : 0;
-        int sum = T * units;
+    int before = 0;
+    const auto segments = [&](int k0, int T) {  // 32 of them
+        const int k = k0 + lane, steps = k < segs ? T * seg_units(a, k) : 0;
+        int sum = steps;
         for (int o = 1; o < 32; o *= 2) {
             const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
             if (lane >= o) sum += v;
         }
-        const int from = before + sum - T * units;
+        const int from = before + sum - steps;
         if (blockIdx.x == 0 && warp == 0) {
-            if (k < s.c.n) s.line[1 + k] = from;
-            if (k == 0) s.line[0] = per;
+            if (k < segs) a.line[1 + k] = from;
+            if (k == 0) a.line[0] = per;
         }
         const uint32_t here = __ballot_sync(0xFFFFFFFFu, begin >= from && begin < before + sum);
         if (here) {
@@ -158,7 +160,11 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) rows_kernel(const Call a,
             at.i1 = min(at.T, at.i0 + at.left);
         }
         before += __shfl_sync(0xFFFFFFFFu, sum, 31);
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        if (i * 32 < segs) segments(i * 32, tiles[i]);
+    for (int k0 = kHeld * 32; k0 < segs; k0 += 32) segments(k0, k0 + lane < segs ? seg_tiles(a, k0 + lane) : 0);
     if (begin < end) {
         uint8_t *const ring = smem + warp * kStages * M::BYTES;
         // the first of this warp's tiles from i0 on: every fourth step of the CTA's range
@@ -168,15 +174,17 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) rows_kernel(const Call a,
         bool more = true, dead = false;
         const auto fetch = [&]() {
             while (more && fi >= ahead.i1) {
-                more = next_unit(s, units, ahead);
+                more = next_unit(a, ahead);
                 if (more) fi = first(ahead);
             }
             if (!more || dead) return;
             const int st = fetched % kStages;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&s_full[warp][st], M::BYTES);
-                bulk_load(ring + st * M::BYTES, s.c.data + ahead.seg * s.c.s_n + (ahead.unit / s.row_tiles) * s.c.s_h + fi * s.c.s_t, M::BYTES,
-                          &s_full[warp][st]);
+                const bool pre = ahead.seg < a.pre.n;
+                const Cache &c = pre ? a.pre.c : a.suf.c;
+                const int k = pre ? ahead.seg : ahead.seg - a.pre.n, hk = ahead.unit / (pre ? a.pre.row_tiles : a.suf.row_tiles);
+                bulk_load(ring + st * M::BYTES, c.data + k * c.s_n + hk * c.s_h + fi * c.s_t, M::BYTES, &s_full[warp][st]);
             }
             ++fetched;
             fi += kWarps;
@@ -184,34 +192,59 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) rows_kernel(const Call a,
 #pragma unroll
         for (int k = 0; k < kStages - 1; ++k) fetch();
 
-        for (bool go = true; go; go = next_unit(s, units, at)) {
-            const int len = length(s, at.seg), hk = at.unit / s.row_tiles, tile = at.unit - hk * s.row_tiles;
+        // A unit's query rows come to shared memory while the parts of the unit before it are summed.
+        const auto fetch_q = [&](const Place &p) {
+            const bool pre = p.seg < a.pre.n;
+            const Side &s = pre ? a.pre : a.suf;
+            const int seg = pre ? p.seg : p.seg - a.pre.n, hk = p.unit / s.row_tiles, tile = p.unit - hk * s.row_tiles;
+            for (int i = threadIdx.x; i < R * (D / 8); i += kWarps * 32) {
+                const int n = i / (D / 8), ch = i % (D / 8), rr = tile * R + n;
+                const Row w = row_of(a, pre, seg, hk, min(rr, s.rows - 1));
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem + S::Q + (n * (D / 8) + (ch ^ (n & 7))) * 16)),
+                             "l"(a.q + w.b * a.q_b + w.l * a.q_l + w.h * a.q_h + ch * 8), "r"(rr < s.rows ? 16 : 0)
+                             : "memory");
+            }
+        };
+        fetch_q(at);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+        for (bool go = true; go;) {
+            const bool pre = at.seg < a.pre.n;
+            const Side &s = pre ? a.pre : a.suf;
+            const int seg = pre ? at.seg : at.seg - a.pre.n, len = length(s, seg), hk = at.unit / s.row_tiles, tile = at.unit - hk * s.row_tiles;
             // Q^T: lane (r, q) holds dims D / 4 q .. of row r, four of them a step
-            uint32_t qf[NT][D / 16][2];
-            int limit[NT][2];
+            uint32_t qf[D / 16][2];
+            int limit[2];
+            float scale[2];  // to log2 units
+            uint4 v[D / 32];
+            uint32_t top = 0;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int rr = tile * R + n * 8 + r;
-                const Row w = row_of(a, s, at.seg, hk, rr);
-                const uint4 *from = reinterpret_cast<const uint4 *>(a.q + w.b * a.q_b + w.l * a.q_l + w.h * a.q_h + q * (D / 4));
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    const uint4 v = rr < s.rows ? from[i] : make_uint4(0, 0, 0, 0);
-                    qf[n][2 * i][0] = v.x, qf[n][2 * i][1] = v.y, qf[n][2 * i + 1][0] = v.z, qf[n][2 * i + 1][1] = v.w;
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    limit[n][e] = s.suffix ? len - a.Lq + 1 + row_of(a, s, at.seg, hk, tile * R + n * 8 + 2 * q + e).l : len;
+            for (int i = 0; i < D / 32; ++i) {
+                v[i] = ld_shared_v4(smem_u32(smem + S::Q + (r * (D / 8) + ((q * (D / 32) + i) ^ r)) * 16));
+                const auto mag = [](uint32_t x) { return max(x & 0x7FFFu, x >> 16 & 0x7FFFu); };
+                top = max(max(top, max(mag(v[i].x), mag(v[i].y))), max(mag(v[i].z), mag(v[i].w)));
             }
-            const int all_see = s.suffix ? len - a.Lq + 1 : len;  // keys that every row sees
-            float o[MT][NT][4], m[NT][2], l[NT][2];
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            const int e = min(max((int)(top >> 7) - 127, -126), 126);  // the largest element's exponent; Inf and NaN stay what they are
+            const float down = pow2f(-e);
+            const auto half = [&](uint32_t x) { return f16x2(bf16lo(x) * down, bf16hi(x) * down); };
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                m[n][0] = m[n][1] = kNone;
-                l[n][0] = l[n][1] = 0.0f;
-#pragma unroll
-                for (int t = 0; t < MT; ++t) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.0f;
+            for (int i = 0; i < D / 32; ++i) {
+                qf[2 * i][0] = half(v[i].x), qf[2 * i][1] = half(v[i].y);
+                qf[2 * i + 1][0] = half(v[i].z), qf[2 * i + 1][1] = half(v[i].w);
             }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                limit[k] = pre ? len : len - a.Lq + 1 + row_of(a, pre, seg, hk, tile * R + 2 * q + k).l;
+                scale[k] = s.scale_log2 * pow2f(__shfl_sync(0xFFFFFFFFu, e, (2 * q + k) * 4));
+            }
+            const int all_see = pre ? len : len - a.Lq + 1;  // keys that every row sees
+            float o[MT][4], m[2], l[2];
+            m[0] = m[1] = kNone;
+            l[0] = l[1] = 0.0f;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.0f;
             for (int i = first(at); i < at.i1; i += kWarps) {
                 const int st = used % kStages;
                 if (!dead) {
@@ -241,88 +274,76 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) rows_kernel(const Call a,
                     __syncwarp();
                 }
                 // S^T: column c (16 keys) in turn
-                float x[2][NT][4];
-                uint32_t ks[D / 64];  // the lane's key scales
+                float x[2][4];
+                uint32_t ks[4];  // the lane's key scales, a pair of blocks of token e each (D = 64: of one block, of two tokens)
                 if (D == 128) {
-                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(ks[0]), "=r"(ks[D / 64 - 1]) : "r"(tb + M::KS + lane * 8) : "memory");
+                    uint32_t w0, w1;
+                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(tb + M::KS + lane * 8) : "memory");
+                    scales_f16(w0, ks[0], ks[1]);
+                    scales_f16(w1, ks[2], ks[3]);
                 } else {
-                    ks[0] = ld_shared_u32(tb + M::KS + lane * 4);
+                    scales_f16(ld_shared_u32(tb + M::KS + lane * 4), ks[0], ks[1]);
                 }
-                const float up = pow2f(119);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    uint32_t kw[2][KW], f[2][D / 64];
+                    uint32_t kw[2][KW], f[2][2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t from = tb + M::KC + (8 * (r / 2) + 4 * c + r % 2 + 2 * h) * (D / 2) + q * (D / 8);
                         if (D == 128) {
                             const uint4 v = ld_shared_v4(from);
                             kw[h][0] = v.x, kw[h][1] = v.y, kw[h][KW - 2] = v.z, kw[h][KW - 1] = v.w;
+                            f[h][0] = prmt(ks[2 * c + h], 0, 0x1010), f[h][1] = prmt(ks[2 * c + h], 0, 0x3232);
                         } else {
                             asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(kw[h][0]), "=r"(kw[h][1]) : "r"(from) : "memory");
-                        }
-                        // scales of token e = 2 c + h
-                        if (D == 128) {
-                            const uint32_t w = ks[c * (D / 64 - 1)];
-                            f[h][0] = scale_factor_bf16x2(h ? w << 4 : w << 20, up);
-                            f[h][D / 64 - 1] = scale_factor_bf16x2(h ? w >> 4 : w << 12, up);
-                        } else {
-                            const int sh = 8 * (2 * c + h);
-                            f[h][0] = scale_factor_bf16x2(sh <= 20 ? ks[0] << (20 - sh) : ks[0] >> (sh - 20), up);
+                            f[h][0] = prmt(ks[c], 0, h ? 0x3232 : 0x1010);
                         }
                     }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) x[c][n][0] = x[c][n][1] = x[c][n][2] = x[c][n][3] = 0.0f;
+                    x[c][0] = x[c][1] = x[c][2] = x[c][3] = 0.0f;
 #pragma unroll
                     for (int w = 0; w < KW; ++w) {
                         uint32_t k0w[4], k1w[4];
-                        dequant_word<true>(kw[0][w], f[0][w / 2], k0w);
-                        dequant_word<true>(kw[1][w], f[1][w / 2], k1w);
+                        codes_f16(kw[0][w], k0w);
+                        codes_f16(kw[1][w], k1w);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            mma_bf16(x[c][n], k0w[0], k1w[0], k0w[1], k1w[1], qf[n][2 * w][0], qf[n][2 * w][1]);
-                            mma_bf16(x[c][n], k0w[2], k1w[2], k0w[3], k1w[3], qf[n][2 * w + 1][0], qf[n][2 * w + 1][1]);
-                        }
+                        for (int i = 0; i < 4; ++i) k0w[i] = f16x2_mul(k0w[i], f[0][w / 2]), k1w[i] = f16x2_mul(k1w[i], f[1][w / 2]);
+                        mma_f16(x[c], k0w[0], k1w[0], k0w[1], k1w[1], qf[2 * w][0], qf[2 * w][1]);
+                        mma_f16(x[c], k0w[2], k1w[2], k0w[3], k1w[3], qf[2 * w + 1][0], qf[2 * w + 1][1]);
                     }
                 }
                 if (k0 + kTok > all_see) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (k0 + 8 * (r / 2) + 4 * c + r % 2 + 2 * (e / 2) >= limit[n][e % 2]) x[c][n][e] = -INFINITY;
+                        for (int e = 0; e < 4; ++e)
+                            if (k0 + 8 * (r / 2) + 4 * c + r % 2 + 2 * (e / 2) >= limit[e % 2]) x[c][e] = -INFINITY;
                 }
-                uint32_t p[2][NT][2];
+                uint32_t p[2][2];
+                float top[2];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float top[2];
+                for (int e = 0; e < 2; ++e)
+                    top[e] = fmaxf(fmaxf(fmaxf(x[0][e], x[0][e + 2]), fmaxf(x[1][e], x[1][e + 2])), kNone) * scale[e];
+                if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + kRoom || top[1] > m[1] + kRoom)) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        top[e] = fmaxf(fmaxf(fmaxf(x[0][n][e], x[0][n][e + 2]), fmaxf(x[1][n][e], x[1][n][e + 2])), kNone) * s.scale_log2;
-                    if (__any_sync(0xFFFFFFFFu, top[0] > m[n][0] + kRoom || top[1] > m[n][1] + kRoom)) {
+                    for (int e = 0; e < 2; ++e) {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
+                        for (int k = 4; k < 32; k *= 2) top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], k));
+                        const float to = top[e] > m[e] + kRoom ? top[e] - kHead : m[e], f = ex2(m[e] - to);
+                        m[e] = to;
+                        l[e] *= f;
 #pragma unroll
-                            for (int k = 4; k < 32; k *= 2) top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], k));
-                            const float to = top[e] > m[n][e] + kRoom ? top[e] - kHead : m[n][e], f = ex2(m[n][e] - to);
-                            m[n][e] = to;
-                            l[n][e] *= f;
-#pragma unroll
-                            for (int t = 0; t < MT; ++t) o[t][n][e] *= f, o[t][n][e + 2] *= f;
-                        }
+                        for (int t = 0; t < MT; ++t) o[t][e] *= f, o[t][e + 2] *= f;
                     }
+                }
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            x[c][n][e] = ex2(fmaf(x[c][n][e], s.scale_log2, -m[n][e % 2]));
-                            l[n][e % 2] += x[c][n][e];
-                        }
-                        p[c][n][0] = turned(f16x2(x[c][n][0], x[c][n][1]));
-                        p[c][n][1] = turned(f16x2(x[c][n][2], x[c][n][3]));
+                    for (int e = 0; e < 4; ++e) {
+                        x[c][e] = ex2(fmaf(x[c][e], scale[e % 2], -m[e % 2]));
+                        l[e % 2] += x[c][e];
                     }
+                    p[c][0] = turned(f16x2(x[c][0], x[c][1]));
+                    p[c][1] = turned(f16x2(x[c][2], x[c][3]));
                 }
                 // O^T: lane (r, q) holds keys 8 q .. 8 q + 7 of dims r and r + 8 of a row tile
 #pragma unroll
@@ -337,10 +358,8 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) rows_kernel(const Call a,
                         scales_f16(t ? sc.w : sc.y, s0[1], s1[1]);
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                mma_f16(o[2 * j + t][n], v0[2 * c], v1[2 * c], v0[2 * c + 1], v1[2 * c + 1], f16x2_mul(p[c][n][0], s0[c]),
-                                        f16x2_mul(p[c][n][1], s1[c]));
+                            mma_f16(o[2 * j + t], v0[2 * c], v1[2 * c], v0[2 * c + 1], v1[2 * c + 1], f16x2_mul(p[c][0], s0[c]),
+                                    f16x2_mul(p[c][1], s1[c]));
                     }
                 }
                 __syncwarp();  // the place is free for the copy that the next turn issues
@@ -349,21 +368,21 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) rows_kernel(const Call a,
             float *const so = reinterpret_cast<float *>(smem + S::O);
             float2 *const sml = reinterpret_cast<float2 *>(smem + S::ML);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int e = 0; e < 2; ++e) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int k = 4; k < 32; k *= 2) l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], k);
+                const int row = warp * R + 2 * q + e;
+                if (r == 0) sml[row] = make_float2(m[e], l[e]);
 #pragma unroll
-                    for (int k = 4; k < 32; k *= 2) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], k);
-                    const int row = warp * R + n * 8 + 2 * q + e;
-                    if (r == 0) sml[row] = make_float2(m[n][e], l[n][e]);
-#pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        so[row * S::ROW + t * 16 + r] = o[t][n][e];
-                        so[row * S::ROW + t * 16 + r + 8] = o[t][n][e + 2];
-                    }
+                for (int t = 0; t < MT; ++t) {
+                    so[row * S::ROW + t * 16 + r] = o[t][e];
+                    so[row * S::ROW + t * 16 + r + 8] = o[t][e + 2];
                 }
+            }
             __syncthreads();
-            const int64_t part = (int64_t)at.seg * units + at.unit + blockIdx.x;
+            const int64_t part = (int64_t)(pre ? 0 : a.pre.n * a.Hkv * a.pre.row_tiles) + (int64_t)seg * a.Hkv * s.row_tiles + at.unit + blockIdx.x;
+            go = next_unit(a, at);
+            if (go) fetch_q(at);
             for (int row = warp; row < R; row += kWarps) {
                 float M_ = kNone, L = 0.0f, w[kWarps];
 #pragma unroll
@@ -380,10 +399,11 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) rows_kernel(const Call a,
                         const float4 v = *reinterpret_cast<const float4 *>(so + (k * R + row) * S::ROW + lane * 4);
                         t.x = fmaf(w[k], v.x, t.x), t.y = fmaf(w[k], v.y, t.y), t.z = fmaf(w[k], v.z, t.z), t.w = fmaf(w[k], v.w, t.w);
                     }
-                    *reinterpret_cast<float4 *>(s.part_o + (part * R + row) * D + lane * 4) = t;
+                    *reinterpret_cast<float4 *>(a.part_o + (part * R + row) * D + lane * 4) = t;
                 }
-                if (lane == 0) s.part_ml[part * R + row] = make_float2(M_, L);
+                if (lane == 0) a.part_ml[part * R + row] = make_float2(M_, L);
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
             __syncthreads();
         }
         if (dead) {  // no copy may be in flight when the CTA ends
@@ -394,7 +414,6 @@ __global__ void __launch_bounds__(kWarps * 32, PER_SM) rows_kernel(const Call a,
             __syncwarp();
         }
     }
-    if (beside && blockIdx.x == gridDim.x - 1) pdl_wait();
 }
 
 // ------------------------------------------------------------------ joining a row's parts
@@ -405,39 +424,39 @@ struct Parts {
     int64_t step;  // from part to part, in rows
     float v_scale;
 };
-__device__ __forceinline__ Parts parts_of(const Side &s, int k, int hk, int r, int D)
+__device__ __forceinline__ Parts parts_of(const Call &a, bool pre, int k, int hk, int r, int T, int D)
 {
+    const Side &s = pre ? a.pre : a.suf;
     Parts p = {};
-    const int T = tiles_of(length(s, k));
     if (T == 0) return p;
-    const int per = s.line[0], tile = r / s.tile_rows, u = hk * s.row_tiles + tile, start = s.line[1 + k] + u * T;
+    const int per = a.line[0], tile = r / kRows, u = hk * s.row_tiles + tile, start = a.line[1 + k + (pre ? 0 : a.pre.n)] + u * T;
     const int c0 = start / per;
-    const int64_t row = ((int64_t)k * s.c.Hkv * s.row_tiles + u + c0) * s.tile_rows + r % s.tile_rows;
+    const int64_t row = ((pre ? 0 : (int64_t)a.pre.n * a.Hkv * a.pre.row_tiles) + (int64_t)k * a.Hkv * s.row_tiles + u + c0) * kRows + r % kRows;
     p.n = (start + T - 1) / per - c0 + 1;
-    p.o = s.part_o + row * D;
-    p.ml = s.part_ml + row;
-    p.step = s.tile_rows;
+    p.o = a.part_o + row * D;
+    p.ml = a.part_ml + row;
+    p.step = kRows;
     p.v_scale = s.c.v_scale;
     return p;
 }
 
 // W warps per query row, each takes every W-th part; in a fixed order, so that results repeat.
 template <int D, int W>
-__global__ void __launch_bounds__(128) join_kernel(const Call a, const Side pre, const Side suf)
+__global__ void __launch_bounds__(W > 4 ? 32 * W : 128) join_kernel(const __grid_constant__ Call a)
 {
-    constexpr int E = D / 32, RB = 4 / W, NB = 4;  // columns of a lane; rows of a block; parts in flight
-    __shared__ float s_o[W > 1 ? 4 : 1][W > 1 ? D : 1];
-    __shared__ float2 s_ml[4];
+    constexpr int E = D / 32, RB = W > 4 ? 1 : 4 / W, NB = 4;  // columns of a lane; rows of a block; parts in flight
+    __shared__ float s_o[RB * W][W > 1 ? D : 1];
+    __shared__ float2 s_ml[RB * W];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, share = warp % W;
     const int row = blockIdx.x * RB + warp / W;
     const bool live = row < a.B * a.Lq * a.Hq;
     const int h = row % a.Hq, bl = row / a.Hq, l = bl % a.Lq, b = live ? bl / a.Lq : 0, g = b / a.G;
     const int hk = h / a.gs, hi = h - hk * a.gs;
+    // the kernel before this one lets it start after all work before the call: the lengths are there
+    const int tp = a.pre.n && live ? tiles_of(length(a.pre, g)) : 0, ts = a.suf.n && live ? tiles_of(length(a.suf, b)) : 0;
     pdl_wait();
     pdl_trigger();
-    Parts pp = {}, ps = {};
-    if (live && pre.on) pp = parts_of(pre, g, hk, ((b - g * a.G) * a.Lq + l) * a.gs + hi, D);
-    if (live && suf.on) ps = parts_of(suf, b, hk, l * a.gs + hi, D);
+    const Parts pp = parts_of(a, true, g, hk, ((b - g * a.G) * a.Lq + l) * a.gs + hi, tp, D), ps = parts_of(a, false, b, hk, l * a.gs + hi, ts, D);
     const int n = pp.n + ps.n;
     float M = kNone, L = 0.0f, acc[E] = {};
     for (int k0 = share; k0 < n; k0 += NB * W) {
@@ -512,78 +531,47 @@ __global__ void __launch_bounds__(128) join_kernel(const Call a, const Side pre,
 int ceil_div(int64_t x, int64_t y) { return (int)((x + y - 1) / y); }
 size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 
-constexpr int kPerSm1 = 3, kPerSm2 = 2;  // CTAs per SM with 8 and with 16 rows
+int64_t units_of(const Call &a) { return ((int64_t)a.pre.n * a.pre.row_tiles + (int64_t)a.suf.n * a.suf.row_tiles) * a.Hkv; }
+size_t ml_bytes(const Call &a) { return round256((size_t)(units_of(a) + a.grid) * kRows * sizeof(float2)); }
+size_t line_bytes(const Call &a) { return round256((size_t)(1 + a.pre.n + a.suf.n) * sizeof(int)); }
 
-bool side(Side &s, int64_t n, int64_t T, int64_t Hkv, int64_t rows, bool suffix)
-{
-    const int64_t big = 1 << 30;
-    s.suffix = suffix;
-    s.rows = (int)rows;
-    s.tile_rows = rows <= 8 ? 8 : 16;
-    s.row_tiles = ceil_div(rows, s.tile_rows);
-    const int64_t units = n * Hkv * s.row_tiles, steps = units * ((T + kTok - 1) / kTok);
-    if (units > big || steps > big) return false;
-    const int64_t most = (int64_t)num_sms() * (s.tile_rows == 8 ? kPerSm1 : kPerSm2), want = (steps + kWarps - 1) / kWarps;
-    s.grid = (int)(want < most ? want : most);
-    s.on = true;
-    return true;
-}
-// the part area of a side: m and l, the line, o
-size_t ml_bytes(const Side &s, int64_t units) { return round256((size_t)(units + s.grid) * s.tile_rows * sizeof(float2)); }
-size_t side_bytes(const Side &s, int64_t D)
-{
-    if (!s.on) return 0;
-    const int64_t units = (int64_t)s.c.n * s.c.Hkv * s.row_tiles;
-    return ml_bytes(s, units) + round256((size_t)(1 + s.c.n) * sizeof(int)) + (size_t)(units + s.grid) * s.tile_rows * D * sizeof(float);
-}
-void place(Side &s, char *ws)
-{
-    const int64_t units = (int64_t)s.c.n * s.c.Hkv * s.row_tiles;
-    s.part_ml = reinterpret_cast<float2 *>(ws);
-    s.line = reinterpret_cast<int *>(ws + ml_bytes(s, units));
-    s.part_o = reinterpret_cast<float *>(ws + ml_bytes(s, units) + round256((size_t)(1 + s.c.n) * sizeof(int)));
-}
-
-template <int D, int NT>
-qerl_status launch_rows(const Call &a, const Side &s, int beside, cudaStream_t st, bool chain)
-{
-    constexpr int per_sm = NT == 1 ? kPerSm1 : kPerSm2;
-    static OncePerDevice once;
-    const auto kernel = rows_kernel<D, NT, per_sm>;
-    if (allow_smem(once, kernel, Smem<D, NT>::TOTAL) != cudaSuccess) return QERL_ERR_CUDA;
-    return launched(launch_k(kernel, dim3((unsigned)s.grid), dim3(kWarps * 32), Smem<D, NT>::TOTAL, st, chain, a, s, beside, error_word()));
-}
 template <int D>
-qerl_status run(const Call &a, const Side &pre, const Side &suf, cudaStream_t st)
+qerl_status run(const Call &a, cudaStream_t st)
 {
     const bool chain = g_chain.load() != 0;
-    if (pre.on) QERL_TRY(pre.tile_rows == 8 ? (launch_rows<D, 1>(a, pre, 0, st, chain)) : (launch_rows<D, 2>(a, pre, 0, st, chain)));
-    const int beside = pre.on && chain ? 1 : 0;
-    if (suf.on) QERL_TRY(suf.tile_rows == 8 ? (launch_rows<D, 1>(a, suf, beside, st, chain)) : (launch_rows<D, 2>(a, suf, beside, st, chain)));
-    // a warp per row where the rows fill the SMs or have few parts, else four
-    const int64_t rows = (int64_t)a.B * a.Lq * a.Hq;
-    const auto parts = [](const Side &s) { return s.on ? s.grid / ((int64_t)s.c.n * s.c.Hkv * s.row_tiles) + 2 : 0; };
-    if (parts(pre) + parts(suf) <= 8 || rows > 32 * num_sms())
-        return launched(launch_k(join_kernel<D, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, chain, a, pre, suf));
-    return launched(launch_k(join_kernel<D, 4>, dim3((unsigned)rows), dim3(128), 0, st, chain, a, pre, suf));
+    static OncePerDevice once;
+    if (allow_smem(once, rows_kernel<D>, Smem<D>::TOTAL) != cudaSuccess) return QERL_ERR_CUDA;
+    QERL_TRY(launched(launch_k(rows_kernel<D>, dim3((unsigned)a.grid), dim3(kWarps * 32), Smem<D>::TOTAL, st, chain, a, error_word())));
+    // warps per row: one where the rows fill the SMs or have few parts, sixteen where there are many
+    const int64_t rows = (int64_t)a.B * a.Lq * a.Hq, parts = (a.pre.n != 0) + (a.suf.n != 0) + 2 * a.grid / units_of(a);
+    if (parts <= 8 || rows > 32 * num_sms())
+        return launched(launch_k(join_kernel<D, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, chain, a));
+    if (parts <= 24 || rows > 4 * num_sms()) return launched(launch_k(join_kernel<D, 4>, dim3((unsigned)rows), dim3(128), 0, st, chain, a));
+    return launched(launch_k(join_kernel<D, 16>, dim3((unsigned)rows), dim3(512), 0, st, chain, a));
 }
 
 // The call's sizes and the workspace it needs.
-qerl_status shape(const qerl_kv4_attn_dims *d, const qerl_kv4_cache *prefix, const qerl_kv4_cache *suffix, Call &a, Side &pre, Side &suf,
-                  size_t &bytes)
+qerl_status shape(const qerl_kv4_attn_dims *d, const qerl_kv4_cache *prefix, const qerl_kv4_cache *suffix, Call &a, size_t &bytes)
 {
     if (!d || (!prefix && !suffix)) return QERL_ERR_INVALID_ARG;
-    if (prefix) QERL_TRY(check_cache(prefix, pre.c));
-    if (suffix) QERL_TRY(check_cache(suffix, suf.c));
+    if (prefix) QERL_TRY(check_cache(prefix, a.pre.c));
+    if (suffix) QERL_TRY(check_cache(suffix, a.suf.c));
     const int64_t big = 1 << 30, Hkv = (prefix ? prefix : suffix)->Hkv, D = (prefix ? prefix : suffix)->D;
     if (d->B < 1 || d->Lq < 1 || d->Hq < 1 || d->B > big || d->Lq > big || d->Hq > 65536 || d->Hq % Hkv || d->B * d->Lq > big / d->Hq)
         return QERL_ERR_SHAPE;
     if (prefix && d->B % prefix->n) return QERL_ERR_SHAPE;
     if (suffix && (suffix->n != d->B || suffix->Hkv != Hkv || suffix->D != D)) return QERL_ERR_SHAPE;
     a.B = (int)d->B, a.Lq = (int)d->Lq, a.Hq = (int)d->Hq, a.Hkv = (int)Hkv, a.gs = (int)(d->Hq / Hkv), a.G = prefix ? (int)(d->B / prefix->n) : 1;
-    if (prefix && !side(pre, prefix->n, prefix->T, Hkv, (int64_t)a.G * a.Lq * a.gs, false)) return QERL_ERR_SHAPE;
-    if (suffix && !side(suf, suffix->n, suffix->T, Hkv, (int64_t)a.Lq * a.gs, true)) return QERL_ERR_SHAPE;
-    bytes = round256(side_bytes(pre, D)) + round256(side_bytes(suf, D));
+    a.pre.n = prefix ? (int)prefix->n : 0, a.suf.n = suffix ? a.B : 0;
+    a.pre.rows = a.G * a.Lq * a.gs, a.suf.rows = a.Lq * a.gs;
+    a.pre.row_tiles = ceil_div(a.pre.rows, kRows), a.suf.row_tiles = ceil_div(a.suf.rows, kRows);
+    const int64_t pre = (int64_t)a.pre.n * a.pre.row_tiles * a.Hkv, suf = (int64_t)a.suf.n * a.suf.row_tiles * a.Hkv;
+    if (pre > big || suf > big || pre + suf > big) return QERL_ERR_SHAPE;
+    const int64_t pt = prefix ? (prefix->T + kTok - 1) / kTok : 0, st = suffix ? (suffix->T + kTok - 1) / kTok : 0;
+    if ((pt && pre > big / pt) || (st && suf > big / st) || pre * pt + suf * st > big) return QERL_ERR_SHAPE;
+    const int64_t most = (int64_t)num_sms() * kPerSm, want = pre * pt + suf * st;
+    a.grid = (int)(want < most ? want : most);
+    bytes = ml_bytes(a) + line_bytes(a) + (size_t)(pre + suf + a.grid) * kRows * D * sizeof(float);
     return QERL_OK;
 }
 
@@ -596,9 +584,8 @@ using namespace qerl;
 extern "C" size_t qerl_kv4_attention_ws_bytes(const qerl_kv4_attn_dims *d, const qerl_kv4_cache *prefix, const qerl_kv4_cache *suffix)
 {
     kv4::Call a = {};
-    kv4::Side pre = {}, suf = {};
     size_t bytes = 0;
-    return kv4::shape(d, prefix, suffix, a, pre, suf, bytes) == QERL_OK ? bytes : 0;
+    return kv4::shape(d, prefix, suffix, a, bytes) == QERL_OK ? bytes : 0;
 }
 
 extern "C" qerl_status qerl_kv4_attention(const qerl_kv4_attn_dims *d, const void *q, const qerl_kv4_cache *prefix, const int32_t *prefix_lens,
@@ -607,9 +594,8 @@ extern "C" qerl_status qerl_kv4_attention(const qerl_kv4_attn_dims *d, const voi
 {
     if (!d || !q || !out || !(scale > 0.0f) || !(scale <= FLT_MAX) || (suffix && !suffix_lens)) return QERL_ERR_INVALID_ARG;
     kv4::Call a = {};
-    kv4::Side pre = {}, suf = {};
     size_t need = 0;
-    QERL_TRY(kv4::shape(d, prefix, suffix, a, pre, suf, need));
+    QERL_TRY(kv4::shape(d, prefix, suffix, a, need));
     for (int i = 0; i < 3; ++i) {
         if (d->q_stride[i] < 0 || d->out_stride[i] < 0 || d->q_stride[i] > (int64_t(1) << 40) || d->out_stride[i] > (int64_t(1) << 40))
             return QERL_ERR_SHAPE;
@@ -618,10 +604,9 @@ extern "C" qerl_status qerl_kv4_attention(const qerl_kv4_attn_dims *d, const voi
     if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(prefix_lens) & 3u) ||
         (reinterpret_cast<uintptr_t>(suffix_lens) & 3u))
         return QERL_ERR_ALIGN;
-    // the keys' factor, and the 2^-7 that their products carry
-    for (kv4::Side *s : {&pre, &suf})
-        if (s->on) {
-            const double c = (double)scale * s->c.k_scale * 128.0 * 1.4426950408889634;
+    for (kv4::Side *s : {&a.pre, &a.suf})
+        if (s->n) {
+            const double c = (double)scale * s->c.k_scale * 1.4426950408889634;
             if (!(c >= FLT_MIN && c <= FLT_MAX)) return QERL_ERR_INVALID_ARG;
             s->scale_log2 = (float)c;
         }
@@ -633,8 +618,10 @@ extern "C" qerl_status qerl_kv4_attention(const qerl_kv4_attn_dims *d, const voi
     a.q_b = d->q_stride[0], a.q_l = d->q_stride[1], a.q_h = d->q_stride[2];
     a.o_b = d->out_stride[0], a.o_l = d->out_stride[1], a.o_h = d->out_stride[2];
     const int64_t D = (prefix ? prefix : suffix)->D;
-    pre.lens = prefix_lens, suf.lens = suffix_lens;
-    if (pre.on) kv4::place(pre, static_cast<char *>(ws));
-    if (suf.on) kv4::place(suf, static_cast<char *>(ws) + kv4::round256(kv4::side_bytes(pre, D)));
-    return D == 128 ? kv4::run<128>(a, pre, suf, as_cuda(stream)) : kv4::run<64>(a, pre, suf, as_cuda(stream));
+    a.pre.lens = prefix_lens, a.suf.lens = suffix_lens;
+    char *const to = static_cast<char *>(ws);
+    a.part_ml = reinterpret_cast<float2 *>(to);
+    a.line = reinterpret_cast<int *>(to + kv4::ml_bytes(a));
+    a.part_o = reinterpret_cast<float *>(to + kv4::ml_bytes(a) + kv4::line_bytes(a));
+    return D == 128 ? kv4::run<128>(a, as_cuda(stream)) : kv4::run<64>(a, as_cuda(stream));
 }
