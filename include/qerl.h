@@ -746,7 +746,9 @@ enum {
     QERL_KERNEL_ATTN_ROWS16 = 0,  /* qerl_prefix_attention: tiles of up to 16 rows that share keys */
     QERL_KERNEL_ATTN_ROWS128 = 1, /* and of 128, on tcgen05 */
     QERL_KERNEL_LOSS_ROW = 2,     /* qerl_policy_loss, qerl_token_logp: a cluster per row */
-    QERL_KERNEL_LOSS_RING = 3     /* and clusters that stay, rows through a ring in shared memory */
+    QERL_KERNEL_LOSS_RING = 3,    /* and clusters that stay, rows through a ring in shared memory */
+    QERL_KERNEL_KV4_ROWS8 = 4,    /* qerl_kv4_attention: tiles of up to 8 rows that share keys */
+    QERL_KERNEL_KV4_ROWS128 = 5   /* and of 128, on tcgen05 */
 };
 uint64_t qerl_kernel_launch_count(int kernel);
 

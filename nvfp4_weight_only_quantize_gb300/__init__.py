@@ -32,6 +32,7 @@ DTYPE_F32, DTYPE_BF16 = 0, 1
 ALGO_AUTO, ALGO_SIMT, ALGO_TCGEN05, ALGO_GEMV = 0, 1, 2, 3
 AQN_NOISE_ADD, AQN_NOISE_MUL = 0, 1
 KERNEL_ATTN_ROWS16, KERNEL_ATTN_ROWS128, KERNEL_LOSS_ROW, KERNEL_LOSS_RING = 0, 1, 2, 3
+KERNEL_KV4_ROWS8, KERNEL_KV4_ROWS128 = 4, 5
 
 # Every C symbol include/qerl.h declares (checked by the CPU test suite).
 EXPORTED = ["qerl_nvfp4_quantize", "qerl_nvfp4_dequantize", "qerl_nvfp4_lora_linear_fwd",

@@ -15,7 +15,7 @@ namespace qerl {
 // Host-side count of kernel launches made by the library (qerl_launch_count).
 extern std::atomic<uint64_t> g_launches;
 // The same by QERL_KERNEL_* (qerl_kernel_launch_count).
-constexpr int kCountedKernels = 4;
+constexpr int kCountedKernels = 6;
 extern std::atomic<uint64_t> g_kernel_launches[kCountedKernels];
 
 // QERL_OK when the current device is compute capability 10.3, else

@@ -51,37 +51,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi)
-{
-    uint32_t d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-__device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b)
-{
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
 __device__ __forceinline__ uint32_t turned(uint32_t a)
 {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
-// The four code pairs of a word as fp16 pairs, and the two scale pairs of a word.
-__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&o)[4])
-{
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-        : "r"(w));
-}
-__device__ __forceinline__ void scales_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
-{
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w));
-}
-
 // Where a warp stands on its CTA's range of the line.
 struct Place {
     int seg, unit, T, i0, i1, left, off;  // segment, unit in it, its tiles, the range inside it, steps from i0 to the end, from the CTA's start to i0
@@ -107,7 +82,7 @@ __device__ __forceinline__ bool next_unit(const Call &a, Place &p)
 }
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32, kPerSm) rows_kernel(const __grid_constant__ Call a, unsigned int *err)
+__global__ void __launch_bounds__(kWarps * 32, kPerSm) rows_kernel(const __grid_constant__ Call a, int beside, unsigned int *err)
 {
     using M = Tile<D>;
     using S = Smem<D>;
@@ -119,7 +94,9 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) rows_kernel(const __grid_
         for (int k = 0; k < kWarps * kStages; ++k) mbar_init(&s_full[0][0] + k, 1);
         fence_mbar_init();
     }
-    pdl_wait();
+    // Beside the tcgen05 kernel, whose CTAs let this one start once all work before both has finished, there is nothing to wait
+    // for; its last CTA waits at its end, so that the join, which waits for this kernel, has both.
+    if (!beside) pdl_wait();
     pdl_trigger();
     __syncthreads();
 
@@ -414,6 +391,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) rows_kernel(const __grid_
             __syncwarp();
         }
     }
+    if (beside && blockIdx.x == gridDim.x - 1) pdl_wait();
 }
 
 // ------------------------------------------------------------------ joining a row's parts
@@ -424,25 +402,34 @@ struct Parts {
     int64_t step;  // from part to part, in rows
     float v_scale;
 };
-__device__ __forceinline__ Parts parts_of(const Call &a, bool pre, int k, int hk, int r, int T, int D)
+__device__ __forceinline__ Parts parts_of(const Call &a, const attn::Args &tc, bool pre, int k, int hk, int r, int64_t row, int len, int D)
 {
     const Side &s = pre ? a.pre : a.suf;
     Parts p = {};
+    const int T = tiles_of(len);
     if (T == 0) return p;
+    p.v_scale = s.c.v_scale;
+    if (pre ? tc.p_tc : tc.s_tc) {
+        const int64_t at = row * (tc.n_pp + tc.n_sp) + (pre ? 0 : tc.n_pp);
+        p.n = attn::tc_parts(tc, pre, k + (pre || !tc.p_tc ? 0 : tc.n_prefix), hk, r, len);
+        p.o = tc.part_o + at * D;
+        p.ml = tc.part_ml + at;
+        p.step = 1;
+        return p;
+    }
     const int per = a.line[0], tile = r / kRows, u = hk * s.row_tiles + tile, start = a.line[1 + k + (pre ? 0 : a.pre.n)] + u * T;
     const int c0 = start / per;
-    const int64_t row = ((pre ? 0 : (int64_t)a.pre.n * a.Hkv * a.pre.row_tiles) + (int64_t)k * a.Hkv * s.row_tiles + u + c0) * kRows + r % kRows;
+    const int64_t at = ((pre ? 0 : (int64_t)a.pre.n * a.Hkv * a.pre.row_tiles) + (int64_t)k * a.Hkv * s.row_tiles + u + c0) * kRows + r % kRows;
     p.n = (start + T - 1) / per - c0 + 1;
-    p.o = a.part_o + row * D;
-    p.ml = a.part_ml + row;
+    p.o = a.part_o + at * D;
+    p.ml = a.part_ml + at;
     p.step = kRows;
-    p.v_scale = s.c.v_scale;
     return p;
 }
 
 // W warps per query row, each takes every W-th part; in a fixed order, so that results repeat.
 template <int D, int W>
-__global__ void __launch_bounds__(W > 4 ? 32 * W : 128) join_kernel(const __grid_constant__ Call a)
+__global__ void __launch_bounds__(W > 4 ? 32 * W : 128) join_kernel(const __grid_constant__ Call a, const __grid_constant__ attn::Args tc)
 {
     constexpr int E = D / 32, RB = W > 4 ? 1 : 4 / W, NB = 4;  // columns of a lane; rows of a block; parts in flight
     __shared__ float s_o[RB * W][W > 1 ? D : 1];
@@ -453,10 +440,11 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) join_kernel(const __grid
     const int h = row % a.Hq, bl = row / a.Hq, l = bl % a.Lq, b = live ? bl / a.Lq : 0, g = b / a.G;
     const int hk = h / a.gs, hi = h - hk * a.gs;
     // the kernel before this one lets it start after all work before the call: the lengths are there
-    const int tp = a.pre.n && live ? tiles_of(length(a.pre, g)) : 0, ts = a.suf.n && live ? tiles_of(length(a.suf, b)) : 0;
+    const int tp = live && (a.pre.n || tc.p_tc) ? length(a.pre, g) : 0, ts = live && (a.suf.n || tc.s_tc) ? length(a.suf, b) : 0;
     pdl_wait();
     pdl_trigger();
-    const Parts pp = parts_of(a, true, g, hk, ((b - g * a.G) * a.Lq + l) * a.gs + hi, tp, D), ps = parts_of(a, false, b, hk, l * a.gs + hi, ts, D);
+    const Parts pp = parts_of(a, tc, true, g, hk, ((b - g * a.G) * a.Lq + l) * a.gs + hi, row, tp, D);
+    const Parts ps = parts_of(a, tc, false, b, hk, l * a.gs + hi, row, ts, D);
     const int n = pp.n + ps.n;
     float M = kNone, L = 0.0f, acc[E] = {};
     for (int k0 = share; k0 < n; k0 += NB * W) {
@@ -534,24 +522,36 @@ size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 int64_t units_of(const Call &a) { return ((int64_t)a.pre.n * a.pre.row_tiles + (int64_t)a.suf.n * a.suf.row_tiles) * a.Hkv; }
 size_t ml_bytes(const Call &a) { return round256((size_t)(units_of(a) + a.grid) * kRows * sizeof(float2)); }
 size_t line_bytes(const Call &a) { return round256((size_t)(1 + a.pre.n + a.suf.n) * sizeof(int)); }
+size_t rows_bytes(const Call &a, int64_t D)
+{
+    return a.grid ? ml_bytes(a) + line_bytes(a) + round256((size_t)(units_of(a) + a.grid) * kRows * D * sizeof(float)) : 0;
+}
+size_t tc_rows(const attn::Args &t) { return (size_t)t.B * t.Lq * t.Hq * (t.n_pp + t.n_sp); }
+size_t tc_ml_bytes(const attn::Args &t) { return round256(tc_rows(t) * sizeof(float2)); }
+size_t tc_line_bytes(const attn::Args &t) { return round256((size_t)(1 + t.n_prefix + t.B) * sizeof(int)); }
 
 template <int D>
-qerl_status run(const Call &a, cudaStream_t st)
+qerl_status run(const Call &a, const attn::Args &tc, cudaStream_t st)
 {
-    const bool chain = g_chain.load() != 0;
-    static OncePerDevice once;
-    if (allow_smem(once, rows_kernel<D>, Smem<D>::TOTAL) != cudaSuccess) return QERL_ERR_CUDA;
-    QERL_TRY(launched(launch_k(rows_kernel<D>, dim3((unsigned)a.grid), dim3(kWarps * 32), Smem<D>::TOTAL, st, chain, a, error_word())));
+    const bool chain = g_chain.load() != 0, many = tc.p_tc || tc.s_tc;
+    if (many) QERL_TRY(launched(many_rows(tc, a.pre, a.suf, D, st, chain), QERL_KERNEL_KV4_ROWS128));
+    if (a.grid) {
+        static OncePerDevice once;
+        if (allow_smem(once, rows_kernel<D>, Smem<D>::TOTAL) != cudaSuccess) return QERL_ERR_CUDA;
+        QERL_TRY(launched(launch_k(rows_kernel<D>, dim3((unsigned)a.grid), dim3(kWarps * 32), Smem<D>::TOTAL, st, chain, a, many && chain ? 1 : 0,
+                                   error_word()),
+                          QERL_KERNEL_KV4_ROWS8));
+    }
     // warps per row: one where the rows fill the SMs or have few parts, sixteen where there are many
-    const int64_t rows = (int64_t)a.B * a.Lq * a.Hq, parts = (a.pre.n != 0) + (a.suf.n != 0) + 2 * a.grid / units_of(a);
+    const int64_t rows = (int64_t)a.B * a.Lq * a.Hq, parts = (a.pre.n != 0) + (a.suf.n != 0) + (a.grid ? 2 * a.grid / units_of(a) : 0) + tc.n_pp + tc.n_sp;
     if (parts <= 8 || rows > 32 * num_sms())
-        return launched(launch_k(join_kernel<D, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, chain, a));
-    if (parts <= 24 || rows > 4 * num_sms()) return launched(launch_k(join_kernel<D, 4>, dim3((unsigned)rows), dim3(128), 0, st, chain, a));
-    return launched(launch_k(join_kernel<D, 16>, dim3((unsigned)rows), dim3(512), 0, st, chain, a));
+        return launched(launch_k(join_kernel<D, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, chain, a, tc));
+    if (parts <= 24 || rows > 4 * num_sms()) return launched(launch_k(join_kernel<D, 4>, dim3((unsigned)rows), dim3(128), 0, st, chain, a, tc));
+    return launched(launch_k(join_kernel<D, 16>, dim3((unsigned)rows), dim3(512), 0, st, chain, a, tc));
 }
 
 // The call's sizes and the workspace it needs.
-qerl_status shape(const qerl_kv4_attn_dims *d, const qerl_kv4_cache *prefix, const qerl_kv4_cache *suffix, Call &a, size_t &bytes)
+qerl_status shape(const qerl_kv4_attn_dims *d, const qerl_kv4_cache *prefix, const qerl_kv4_cache *suffix, Call &a, attn::Args &tc, size_t &bytes)
 {
     if (!d || (!prefix && !suffix)) return QERL_ERR_INVALID_ARG;
     if (prefix) QERL_TRY(check_cache(prefix, a.pre.c));
@@ -569,9 +569,40 @@ qerl_status shape(const qerl_kv4_attn_dims *d, const qerl_kv4_cache *prefix, con
     if (pre > big || suf > big || pre + suf > big) return QERL_ERR_SHAPE;
     const int64_t pt = prefix ? (prefix->T + kTok - 1) / kTok : 0, st = suffix ? (suffix->T + kTok - 1) / kTok : 0;
     if ((pt && pre > big / pt) || (st && suf > big / st) || pre * pt + suf * st > big) return QERL_ERR_SHAPE;
-    const int64_t most = (int64_t)num_sms() * kPerSm, want = pre * pt + suf * st;
+    // A kind of segments goes to the tcgen05 kernel where that is quicker: a step of its line (256 rows, 128 keys) takes about 2 us
+    // on a CTA, one of this file's (8 rows, 32 keys) 1 ns over all SMs.
+    const int sms = num_sms();
+    const auto steps_of = [&](int64_t n, int64_t rows, int64_t T) { return n * Hkv * (rows / 256 + 1) * ((T + 127) / 128); };
+    const auto quicker = [&](int64_t n, int64_t rows, int64_t T, int64_t steps8) {
+        const int64_t steps = steps_of(n, rows, T);
+        return n && rows > 16 && T >= 128 && steps + 4 * n * Hkv * (rows / 256 + 1) < big && 8.0 + 2.0 * (double)((steps + sms - 1) / sms) < 1e-3 * (double)steps8;
+    };
+    tc.p_tc = quicker(a.pre.n, a.pre.rows, prefix ? prefix->T : 0, pre * pt);
+    tc.s_tc = quicker(a.suf.n, a.suf.rows, suffix ? suffix->T : 0, suf * st);
+    tc.grid_tc = sms;
+    int free_sms = sms;
+    if (tc.p_tc && !tc.s_tc && suffix) {
+        // The prefixes leave SMs to the own tokens, as many as make the later of the two end soonest; the caches half full, which
+        // they are on average in a rollout (an SM reads some 40 bytes per ns).
+        const double steps = (double)steps_of(a.pre.n, a.pre.rows, prefix->T), bytes8 = 0.5 * (double)(suf * st) * 36.0 * (double)D;
+        double best = 2.0 * ceil(steps / sms) + bytes8 / 6.0e6;
+        for (int n = sms - 4; n >= sms / 2; n -= 4) {
+            const double t = 2.0 * ceil(steps / n), u = bytes8 / ((sms - n) * 40.0e3), later = t > u ? t : u;
+            if (later < best) best = later, tc.grid_tc = n, free_sms = sms - n;
+        }
+    }
+    if (tc.p_tc || tc.s_tc) {
+        tc.B = a.B, tc.Lq = a.Lq, tc.Hq = a.Hq, tc.Hkv = a.Hkv, tc.G = a.G, tc.gs = a.gs, tc.n_prefix = prefix ? a.pre.n : 1;
+        tc.P = prefix ? (int)prefix->T : 0, tc.S = suffix ? (int)suffix->T : 0;
+        tc.n_pp = tc.p_tc ? attn::tc_parts_most(a.pre.rows, prefix->T, Hkv, tc.grid_tc) : 0;
+        tc.n_sp = tc.s_tc ? attn::tc_parts_most(a.suf.rows, suffix->T, Hkv, tc.grid_tc) : 0;
+    }
+    // the rest
+    if (tc.p_tc) a.pre.n = 0;
+    if (tc.s_tc) a.suf.n = 0;
+    const int64_t most = (int64_t)free_sms * kPerSm, want = (a.pre.n ? pre * pt : 0) + (a.suf.n ? suf * st : 0);
     a.grid = (int)(want < most ? want : most);
-    bytes = ml_bytes(a) + line_bytes(a) + (size_t)(pre + suf + a.grid) * kRows * D * sizeof(float);
+    bytes = rows_bytes(a, D) + tc_ml_bytes(tc) + tc_line_bytes(tc) + tc_rows(tc) * D * sizeof(float);
     return QERL_OK;
 }
 
@@ -584,8 +615,9 @@ using namespace qerl;
 extern "C" size_t qerl_kv4_attention_ws_bytes(const qerl_kv4_attn_dims *d, const qerl_kv4_cache *prefix, const qerl_kv4_cache *suffix)
 {
     kv4::Call a = {};
+    attn::Args tc = {};
     size_t bytes = 0;
-    return kv4::shape(d, prefix, suffix, a, bytes) == QERL_OK ? bytes : 0;
+    return kv4::shape(d, prefix, suffix, a, tc, bytes) == QERL_OK ? bytes : 0;
 }
 
 extern "C" qerl_status qerl_kv4_attention(const qerl_kv4_attn_dims *d, const void *q, const qerl_kv4_cache *prefix, const int32_t *prefix_lens,
@@ -594,8 +626,9 @@ extern "C" qerl_status qerl_kv4_attention(const qerl_kv4_attn_dims *d, const voi
 {
     if (!d || !q || !out || !(scale > 0.0f) || !(scale <= FLT_MAX) || (suffix && !suffix_lens)) return QERL_ERR_INVALID_ARG;
     kv4::Call a = {};
+    attn::Args tc = {};
     size_t need = 0;
-    QERL_TRY(kv4::shape(d, prefix, suffix, a, need));
+    QERL_TRY(kv4::shape(d, prefix, suffix, a, tc, need));
     for (int i = 0; i < 3; ++i) {
         if (d->q_stride[i] < 0 || d->out_stride[i] < 0 || d->q_stride[i] > (int64_t(1) << 40) || d->out_stride[i] > (int64_t(1) << 40))
             return QERL_ERR_SHAPE;
@@ -605,7 +638,7 @@ extern "C" qerl_status qerl_kv4_attention(const qerl_kv4_attn_dims *d, const voi
         (reinterpret_cast<uintptr_t>(suffix_lens) & 3u))
         return QERL_ERR_ALIGN;
     for (kv4::Side *s : {&a.pre, &a.suf})
-        if (s->n) {
+        if (s->c.data) {
             const double c = (double)scale * s->c.k_scale * 1.4426950408889634;
             if (!(c >= FLT_MIN && c <= FLT_MAX)) return QERL_ERR_INVALID_ARG;
             s->scale_log2 = (float)c;
@@ -623,5 +656,11 @@ extern "C" qerl_status qerl_kv4_attention(const qerl_kv4_attn_dims *d, const voi
     a.part_ml = reinterpret_cast<float2 *>(to);
     a.line = reinterpret_cast<int *>(to + kv4::ml_bytes(a));
     a.part_o = reinterpret_cast<float *>(to + kv4::ml_bytes(a) + kv4::line_bytes(a));
-    return D == 128 ? kv4::run<128>(a, as_cuda(stream)) : kv4::run<64>(a, as_cuda(stream));
+    char *const tc_to = to + kv4::rows_bytes(a, D);
+    tc.part_ml = reinterpret_cast<float2 *>(tc_to);
+    tc.line = reinterpret_cast<int *>(tc_to + kv4::tc_ml_bytes(tc));
+    tc.part_o = reinterpret_cast<float *>(tc_to + kv4::tc_ml_bytes(tc) + kv4::tc_line_bytes(tc));
+    tc.q = a.q, tc.q_b = a.q_b, tc.q_l = a.q_l, tc.q_h = a.q_h;
+    tc.plen = prefix_lens, tc.slen = suffix_lens;
+    return D == 128 ? kv4::run<128>(a, tc, as_cuda(stream)) : kv4::run<64>(a, tc, as_cuda(stream));
 }

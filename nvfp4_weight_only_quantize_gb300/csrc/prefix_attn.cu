@@ -257,18 +257,6 @@ __global__ void __launch_bounds__(kWarps * 32) rows16_kernel(const Args a, int p
 }
 
 // ------------------------------------------------------------------ joining a row's parts
-// Parts that the tcgen05 kernel left for row r of a segment (the line's k-th) and kv head.
-__device__ __forceinline__ int tc_parts(const Args &a, bool pre, int k, int hk, int r, int len)
-{
-    const int T = key_tiles(len), per_cta = a.line[0], start = a.line[1 + k];
-    if (T == 0) return 0;
-    const Units u((pre ? a.G : 1) * a.Lq * a.gs);
-    const int pair = r / 256;
-    const bool single = pair == u.full;
-    const int first = start + hk * u.steps(T) + pair * (kStart + T) + kStart, n = single ? (T + 1) / 2 : T;
-    return ((first + n - 1) / per_cta - first / per_cta + 1) * (single ? 2 : 1);
-}
-
 // The products of a tile run over keys that some of its rows do not see, with weight 0, and 0 times an Inf or NaN of V is NaN.
 // Over a warp, for a row whose sum is not finite while it has such keys (the new tokens after its own): where one of those
 // values is not finite, the columns that are not are summed again over the keys that the row sees.
@@ -408,17 +396,6 @@ __global__ void __launch_bounds__(128) join_kernel(const Args a)
 }
 
 int ceil_div(int64_t x, int64_t y) { return (int)((x + y - 1) / y); }
-
-// Most parts of a row that the tcgen05 kernel leaves: a unit's steps over a CTA's, which are at least the line's length
-// over the CTAs (its empty steps, which only lengthen it, left out); of a left-over tile two each.
-int tc_parts_most(int64_t rows, int64_t len, int64_t Hkv, int64_t ctas)
-{
-    const int64_t t = (rows + 127) / 128, full = t / 2, T = (len + 127) / 128, half = (T + 1) / 2;
-    const auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
-    const int64_t pairs = full ? least(T, ctas / (Hkv * full) + 3) : 0;
-    const int64_t single = t & 1 ? 2 * least(half, ctas / (Hkv * (full ? full + 1 : 1)) + 3) : 0;
-    return (int)(pairs > single ? pairs : single);
-}
 
 // Kernels, chunk lengths, tiles and parts of a call; false where a size is not covered.
 // A segment of more than 16 rows goes to tcgen05 where that is quicker.  What was measured: a step of its line takes

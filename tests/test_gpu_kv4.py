@@ -230,6 +230,47 @@ def test_attention_over_many_ctas(B, n, Hq, Hkv, P, S, Lq, lo):
     check(rnd(g, B, Lq, Hq, 128) * 1.5, filled(g, n, P, Hkv, 128), filled(g, B, S, Hkv, 128), pl, sl)
 
 
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("n,P,pl,S,sl,Lq,Hq,Hkv", [
+    (1, 3000, [2999], 64, [64, 41, 40, 50, 63, 45, 60, 42], 40, 16, 2),  # the prefix there, the own tokens not
+    (0, 0, None, 1100, [1100, 129, 600, 1001], 129, 16, 2),  # own tokens, causal
+    (2, 1500, [1, 1500], 900, [900, 161, 100, 0], 160, 28, 4),  # both; sequences shorter than their new tokens
+    (3, 2000, [2000, 0, 65], 40, [40, 33, 7, 40, 1, 20, 38, 39, 40], 33, 40, 8),
+])
+def test_attention_of_many_rows(D, n, P, pl, S, sl, Lq, Hq, Hkv):
+    """Sizes that take the tcgen05 kernel."""
+    g = gen(P + S + D)
+    pre = filled(g, n, P, Hkv, D, 0.5, 1.0) if n else None
+    before = q.kernel_launch_count(q.KERNEL_KV4_ROWS128)
+    check(rnd(g, len(sl), Lq, Hq, D) * 1.5, pre, filled(g, len(sl), S, Hkv, D), pl, sl)
+    assert q.kernel_launch_count(q.KERNEL_KV4_ROWS128) == before + 1
+
+
+@pytest.mark.parametrize("fill", [0xFF, 0x7F])
+def test_many_rows_use_nothing_beyond_the_lengths(fill):
+    g = gen(21)
+    B, S, H, D, sl, Lq = 4, 1000, 2, 128, [999, 700, 641, 130], 129
+    k, v = rnd(g, B, S, H, D), rnd(g, B, S, H, D)
+    cache = q.Kv4Cache(B, S, H, D)
+    cache.data.fill_(fill)
+    cache.append(k, v, i32(sl), counts=i32(sl))
+    held = tuple(torch.nan_to_num(x) for x in cache.read(i32([S] * B), S))
+    before = q.kernel_launch_count(q.KERNEL_KV4_ROWS128)
+    qq = rnd(g, B, Lq, 16, D)
+    check(qq, None, (cache, held), None, sl)
+    assert q.kernel_launch_count(q.KERNEL_KV4_ROWS128) == before + 1
+    # a query that is not finite stays in its row; large logits
+    plan = q.Kv4Attention(cache, 16, Lq)
+    clean = plan.run(qq, i32(sl)).clone()
+    bad = qq.clone()
+    bad[1, 7, 3, 5], bad[2, 128, 15, 0] = NAN, float("inf")
+    got = plan.run(bad, i32(sl))
+    same = torch.ones(B, Lq, 16, dtype=torch.bool, device="cuda")
+    same[1, 7, 3] = same[2, 128, 15] = False
+    assert torch.equal(got[same], clean[same]) and bool(torch.isnan(got[~same]).all())
+    check(qq * 60, None, (cache, held), None, sl, plan=plan)
+
+
 def test_prefix_alone_and_scale():
     g = gen(7)
     pre = filled(g, 2, 90, 2, 128)
