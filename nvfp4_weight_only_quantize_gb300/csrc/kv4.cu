@@ -2,14 +2,17 @@
 //
 // Append: a block of 16 values w gets the scale s = the smallest E4M3 number that
 // is at least amax |w| / (6 f), f the cache's factor, and codes nearest(w / (s f)).
-// A CTA takes one tile (32 tokens) of a sequence and head: one thread per token and
-// block quantises 16 keys and 16 values, whose codes then turn through shared
-// memory from one token per thread to eight tokens per word.  Words that hold
-// older tokens too are read and merged; no two threads write to one word.
+// A CTA takes one tile (32 tokens) of a sequence and head, a warp one block of 16
+// dims, a lane one token: eight lanes turn their values' codes by three exchanges
+// (halves, bytes, nibbles of words) from one token per lane to eight tokens per
+// word.  Words that hold older tokens too are read and merged; no two threads write
+// to one word.
 // Bound by HBM for prompts (reads 4 D, writes 9/8 D bytes per token and head), by
 // the launch for single tokens.
 #include "kv4.cuh"
 
+#include <cuda_fp16.h>
+#include <float.h>
 #include <math.h>
 
 #include "fp4_round.cuh"
@@ -25,26 +28,60 @@ struct Tokens {
     int L;
 };
 
-// Sixteen values of a block: their codes (element i in bits 4 i) and the scale's byte.
-__device__ __forceinline__ uint64_t quantise(const uint4 &u0, const uint4 &u1, float factor, uint32_t &scale, bool &finite)
+// Sixteen values of a block: their codes (element i in bits 4 i of two words) and the scale's byte.
+__device__ __forceinline__ uint2 quantise(const uint4 &u0, const uint4 &u1, float factor, uint32_t &scale, bool &finite)
 {
     const uint32_t wd[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
     float w[16], amax = 0.0f;
+    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         w[2 * i] = bf16lo(wd[i]);
         w[2 * i + 1] = bf16hi(wd[i]);
-        finite = finite && (wd[i] & 0x7F80u) != 0x7F80u && (wd[i] & 0x7F800000u) != 0x7F800000u;
+        top = max(top, max(wd[i] & 0x7FFFu, wd[i] >> 16 & 0x7FFFu));
         amax = fmaxf(amax, fmaxf(fabsf(w[2 * i]), fabsf(w[2 * i + 1])));
+    }
+    if (top >= 0x7F80u) {
+        finite = false;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = isnan(w[i]) ? 0.0f : fminf(fmaxf(w[i], -FLT_MAX), FLT_MAX);
     }
     scale = e4m3_ceil(__fdiv_rn(amax, __fmul_rn(6.0f, factor)));
     const float unit = __fmul_rn(e4m3_to_float(scale), factor);
-    uint64_t codes = 0;
-    if (scale != 0u) {
+    // The quotient by a reciprocal and one correction from the exact remainder, which leaves quotients that are borders exact;
+    // the conversion rounds to nearest, ties to the even code, and saturates.
+    const float inv = scale ? __fdiv_rn(1.0f, unit) : 0.0f;
+    uint32_t code[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) codes |= (uint64_t)e2m1_code(__fdiv_rn(w[i], unit)) << (4 * i);
+    for (int i = 0; i < 16; i += 2) {
+        float q[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float q0 = fminf(fmaxf(w[i + e] * inv, -8.0f), 8.0f);  // saturates at 6
+            q[e] = fmaf(fmaf(-q0, unit, w[i + e]), inv, q0);
+        }
+        uint32_t byte;
+        asm("{\n\t.reg .b8 c;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %2, %1;\n\tmov.b32 %0, {c, 0, 0, 0};\n\t}" : "=r"(byte) : "f"(q[0]), "f"(q[1]));
+        code[i / 8] |= byte << (4 * (i % 8));
     }
-    return codes;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // zero has one code
+        const uint32_t c = code[h], some = (c | c >> 1 | c >> 2) & 0x11111111u;
+        code[h] = c & (some * 15u);
+    }
+    return make_uint2(code[0], code[1]);
+}
+
+// Nibble n of lane k's word goes to nibble k of lane n's, among eight lanes.
+__device__ __forceinline__ uint32_t turned(uint32_t w)
+{
+    const int k = threadIdx.x;
+    uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w, 4);
+    w = k & 4 ? (w & 0xFFFF0000u) | o >> 16 : (w & 0x0000FFFFu) | o << 16;
+    o = __shfl_xor_sync(0xFFFFFFFFu, w, 2);
+    w = k & 2 ? (w & 0xFF00FF00u) | (o >> 8 & 0x00FF00FFu) : (w & 0x00FF00FFu) | (o << 8 & 0xFF00FF00u);
+    o = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
+    return k & 1 ? (w & 0xF0F0F0F0u) | (o >> 4 & 0x0F0F0F0Fu) : (w & 0x0F0F0F0Fu) | (o << 4 & 0xF0F0F0F0u);
 }
 
 // Tokens [first, first + count) of sequence b are new: their positions, taken into the cache.
@@ -59,7 +96,6 @@ template <int D>
 __global__ void __launch_bounds__(kTok *Tile<D>::B) append_kernel(const Cache c, const Tokens t, int tiles, unsigned int *err)
 {
     using M = Tile<D>;
-    __shared__ uint64_t s_v[kTok][M::B];
     pdl_wait();
     pdl_trigger();
     const int hk = blockIdx.x % c.Hkv, rest = blockIdx.x / c.Hkv, b = rest / tiles;
@@ -69,37 +105,33 @@ __global__ void __launch_bounds__(kTok *Tile<D>::B) append_kernel(const Cache c,
     const int lo = max(first - base, 0), hi = min(first + count - base, kTok);  // the tile's new tokens
     if (lo >= hi) return;
     uint8_t *const to = c.data + b * c.s_n + hk * c.s_h + tile * c.s_t;
-    const int key = threadIdx.x / M::B, blk = threadIdx.x % M::B;
+    const int key = threadIdx.x % 32, blk = threadIdx.x / 32;
     const bool mine = key >= lo && key < hi;
-    bool finite = true;
+    uint2 vc = make_uint2(0, 0);
     if (mine) {
         const int l = base + key - first;
         const uint4 *ks = reinterpret_cast<const uint4 *>(t.k + b * t.k_b + l * t.k_l + hk * t.k_h + blk * 16);
         const uint4 *vs = reinterpret_cast<const uint4 *>(t.v + b * t.v_b + l * t.v_l + hk * t.v_h + blk * 16);
         const uint4 k0 = ks[0], k1 = ks[1], v0 = vs[0], v1 = vs[1];
         uint32_t sk, sv;
-        const uint64_t kc = quantise(k0, k1, c.k_scale, sk, finite);
-        s_v[key][blk] = quantise(v0, v1, c.v_scale, sv, finite);
-        *reinterpret_cast<uint2 *>(to + M::k_word(key, 2 * blk)) = make_uint2((uint32_t)kc, (uint32_t)(kc >> 32));
+        bool finite = true;
+        *reinterpret_cast<uint2 *>(to + M::k_word(key, 2 * blk)) = quantise(k0, k1, c.k_scale, sk, finite);
+        vc = quantise(v0, v1, c.v_scale, sv, finite);
         to[M::k_scale(key, blk)] = (uint8_t)sk;
         to[M::v_scale(key, blk)] = (uint8_t)sv;
+        if (!finite) latch_error(err, QERL_ERR_NONFINITE);
     }
-    if (!finite) latch_error(err, QERL_ERR_NONFINITE);
-    __syncthreads();
+    __syncwarp();
+    // the lane's words: dims blk 16 + key % 8 and 8 more, the eight tokens of key / 8
+    const uint32_t words[2] = {turned(vc.x), turned(vc.y)};
+    const int from = max(lo - key / 8 * 8, 0), upto = min(hi - key / 8 * 8, 8);
+    if (from < upto) {
+        const uint32_t mask = (upto == 8 ? 0xFFFFFFFFu : (1u << (4 * upto)) - 1u) & ~((1u << (4 * from)) - 1u);
 #pragma unroll
-    for (int j = 0; j < 4 * D / (kTok * M::B); ++j) {
-        const int w = j * kTok * M::B + threadIdx.x, q = (w / 4) % 4, d = (w / 128) * 32 + (w % 4) * 8 + (w / 16) % 8;
-        if (8 * q + 8 <= lo || 8 * q >= hi) continue;
-        uint32_t *const at = reinterpret_cast<uint32_t *>(to + M::VC) + w;
-        uint32_t word = 0;
-        if (8 * q < lo || 8 * q + 8 > hi) word = *at;
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-            if (8 * q + n >= lo && 8 * q + n < hi) {
-                const uint32_t code = (uint32_t)(s_v[8 * q + n][d / 16] >> (4 * (d % 16))) & 15u;
-                word = (word & ~(15u << (4 * n))) | code << (4 * n);
-            }
-        *at = word;
+        for (int h = 0; h < 2; ++h) {
+            uint32_t *const at = reinterpret_cast<uint32_t *>(to + M::v_word(blk * 16 + h * 8 + key % 8, key / 8));
+            *at = mask == 0xFFFFFFFFu ? words[h] : (*at & ~mask) | (words[h] & mask);
+        }
     }
 }
 
@@ -115,7 +147,6 @@ template <int D>
 __global__ void __launch_bounds__(kTok *Tile<D>::B) read_kernel(const Cache c, const Tokens t, int tiles)
 {
     using M = Tile<D>;
-    __shared__ __align__(16) uint8_t s_tile[M::BYTES];
     pdl_wait();
     pdl_trigger();
     const int hk = blockIdx.x % c.Hkv, rest = blockIdx.x / c.Hkv, b = rest / tiles;
@@ -124,30 +155,29 @@ __global__ void __launch_bounds__(kTok *Tile<D>::B) read_kernel(const Cache c, c
     const int base = (first >= 0 ? first / kTok : -((kTok - 1 - first) / kTok)) * kTok + rest % tiles * kTok;
     const int lo = max(first - base, 0), hi = min(first + t.L - base, kTok);
     if (lo >= hi) return;
-    if (base >= 0) {
-        const uint4 *const from = reinterpret_cast<const uint4 *>(c.data + b * c.s_n + hk * c.s_h + (base / kTok) * c.s_t);
-        for (int i = threadIdx.x; i < M::BYTES / 16; i += kTok * M::B) reinterpret_cast<uint4 *>(s_tile)[i] = from[i];
-    }
-    __syncthreads();
-    const int key = threadIdx.x / M::B, blk = threadIdx.x % M::B;
-    if (key < lo || key >= hi) return;
+    const int key = threadIdx.x % 32, blk = threadIdx.x / 32;
     uint32_t ko[8] = {}, vo[8] = {};
     if (base >= 0) {
-        const float sk = __fmul_rn(e4m3_to_float(s_tile[M::k_scale(key, blk)]), c.k_scale);
-        const float sv = __fmul_rn(e4m3_to_float(s_tile[M::v_scale(key, blk)]), c.v_scale);
+        const uint8_t *const from = c.data + b * c.s_n + hk * c.s_h + (base / kTok) * c.s_t;
+        const uint2 kc = *reinterpret_cast<const uint2 *>(from + M::k_word(key, 2 * blk));
+        uint32_t vc[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(s_tile + M::k_word(key, 2 * blk + h));
+        for (int h = 0; h < 2; ++h) vc[h] = turned(*reinterpret_cast<const uint32_t *>(from + M::v_word(blk * 16 + h * 8 + key % 8, key / 8)));
+        const float sk = __fmul_rn(e4m3_to_float(from[M::k_scale(key, blk)]), c.k_scale);
+        const float sv = __fmul_rn(e4m3_to_float(from[M::v_scale(key, blk)]), c.v_scale);
+        const auto values = [](uint32_t w, float f, uint32_t *o) {
+            uint32_t v[4];
+            codes_f16(w, v);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                ko[4 * h + i] = two(e2m1_to_float(w >> (8 * i) & 15u) * sk, e2m1_to_float(w >> (8 * i + 4) & 15u) * sk);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const auto code = [&](int d) { return *reinterpret_cast<const uint32_t *>(s_tile + M::v_word(d, key / 8)) >> (4 * (key % 8)) & 15u; };
-            vo[i] = two(e2m1_to_float(code(blk * 16 + 2 * i)) * sv, e2m1_to_float(code(blk * 16 + 2 * i + 1)) * sv);
-        }
+            for (int i = 0; i < 4; ++i) {
+                const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&v[i]));
+                o[i] = two(x.x * f, x.y * f);
+            }
+        };
+        values(kc.x, sk, ko), values(kc.y, sk, ko + 4);
+        values(vc[0], sv, vo), values(vc[1], sv, vo + 4);
     }
+    if (key < lo || key >= hi) return;
     const int l = base + key - first;
     uint4 *const k = reinterpret_cast<uint4 *>(const_cast<__nv_bfloat16 *>(t.k) + b * t.k_b + l * t.k_l + hk * t.k_h + blk * 16);
     uint4 *const v = reinterpret_cast<uint4 *>(const_cast<__nv_bfloat16 *>(t.v) + b * t.v_b + l * t.v_l + hk * t.v_h + blk * 16);

@@ -47,6 +47,15 @@ struct Tile {
     static __device__ __forceinline__ int v_scale(int t, int b) { return VS + ((t / 8) * B + b) * 8 + t % 8; }
 };
 
+// The four code pairs of a word as fp16 pairs.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&o)[4])
+{
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+        : "r"(w));
+}
+
 // What the entry points share: the cache's description checked and taken over.
 qerl_status check_cache(const qerl_kv4_cache *c, Cache &out);
 

@@ -30,6 +30,7 @@ namespace {
 using namespace ptx;
 
 constexpr int kWarps = 4, kStages = 2, kPerSm = 4;
+constexpr int kStart = 2;  // empty steps before a unit's
 constexpr float kHead = 4.0f, kRoom = 7.0f;  // m is set kHead below a maximum, and raised above kRoom
 constexpr uint64_t kLimitNs = 2000000000ull;
 
@@ -59,25 +60,27 @@ __device__ __forceinline__ uint32_t turned(uint32_t a)
 }
 // Where a warp stands on its CTA's range of the line.
 struct Place {
-    int seg, unit, T, i0, i1, left, off;  // segment, unit in it, its tiles, the range inside it, steps from i0 to the end, from the CTA's start to i0
+    int seg, unit, T, i0, i1, take, left, off;  // segment, unit in it, its tiles, the range of them, its steps and all to the end, tiles before it
 };
 __device__ __forceinline__ int seg_tiles(const Call &a, int k)
 {
     return tiles_of(k < a.pre.n ? length(a.pre, k) : length(a.suf, k - a.pre.n));
 }
 __device__ __forceinline__ int seg_units(const Call &a, int k) { return a.Hkv * (k < a.pre.n ? a.pre.row_tiles : a.suf.row_tiles); }
-__device__ __forceinline__ bool next_unit(const Call &a, Place &p)
+// The next unit of which the CTA has tiles.
+__device__ __forceinline__ bool next_unit(const Call &a, int start, Place &p)
 {
     p.off += p.i1 - p.i0;
-    p.left -= p.i1 - p.i0;
-    if (p.left <= 0) return false;
+    p.left -= p.take;
+    if (p.left <= start) return false;
     if (++p.unit == seg_units(a, p.seg)) {
         p.unit = 0;
         do p.T = seg_tiles(a, ++p.seg);
         while (p.T == 0);
     }
+    p.take = min(p.T + start, p.left);
     p.i0 = 0;
-    p.i1 = min(p.T, p.left);
+    p.i1 = p.take - start;
     return true;
 }
 
@@ -102,19 +105,27 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) rows_kernel(const __grid_
 
     const int segs = a.pre.n + a.suf.n;
     constexpr int kHeld = 4;  // 32 segments each whose tiles stay in a register
-    int tiles[kHeld], total = 0;
+    int tiles[kHeld], total = 0, units = 0;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) tiles[i] = i * 32 + lane < segs ? seg_tiles(a, i * 32 + lane) : 0;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) total += i * 32 + lane < segs ? tiles[i] * seg_units(a, i * 32 + lane) : 0;
-    for (int k = kHeld * 32 + lane; k < segs; k += 32) total += seg_tiles(a, k) * seg_units(a, k);
+    for (int i = 0; i < kHeld; ++i)
+        if (tiles[i]) units += seg_units(a, i * 32 + lane), total += tiles[i] * seg_units(a, i * 32 + lane);
+    for (int k = kHeld * 32 + lane; k < segs; k += 32) {
+        const int T = seg_tiles(a, k);
+        if (T) units += seg_units(a, k), total += T * seg_units(a, k);
+    }
     total = __reduce_add_sync(0xFFFFFFFFu, total);
+    units = __reduce_add_sync(0xFFFFFFFFu, units);
+    // What it costs to begin a unit counts as empty steps before its own, where that matters.
+    const int start = total >= 16 * a.grid ? kStart : 0;
+    total += units * start;
     const int per = max((total + a.grid - 1) / a.grid, 1);
     const int begin = min((int64_t)blockIdx.x * per, (int64_t)total), end = min(begin + per, total);
     Place at = {};
     int before = 0;
     const auto segments = [&](int k0, int T) {  // 32 of them
-        const int k = k0 + lane, steps = k < segs ? T * seg_units(a, k) : 0;
+        const int k = k0 + lane, steps = T ? (T + start) * seg_units(a, k) : 0;
         int sum = steps;
         for (int o = 1; o < 32; o *= 2) {
             const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
@@ -122,8 +133,8 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) rows_kernel(const __grid_
         }
         const int from = before + sum - steps;
         if (blockIdx.x == 0 && warp == 0) {
-            if (k < segs) a.line[1 + k] = from;
-            if (k == 0) a.line[0] = per;
+            if (k < segs) a.line[2 + k] = from;
+            if (k == 0) a.line[0] = per, a.line[1] = start;
         }
         const uint32_t here = __ballot_sync(0xFFFFFFFFu, begin >= from && begin < before + sum);
         if (here) {
@@ -131,10 +142,12 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) rows_kernel(const __grid_
             at.seg = k0 + src;
             at.T = __shfl_sync(0xFFFFFFFFu, T, src);
             const int in = begin - __shfl_sync(0xFFFFFFFFu, from, src);
-            at.unit = in / at.T;
-            at.i0 = in - at.unit * at.T;
+            at.unit = in / (at.T + start);
+            const int into = in - at.unit * (at.T + start);
             at.left = end - begin;
-            at.i1 = min(at.T, at.i0 + at.left);
+            at.take = min(at.T + start - into, at.left);
+            at.i0 = max(into - start, 0);
+            at.i1 = max(into + at.take - start, 0);
         }
         before += __shfl_sync(0xFFFFFFFFu, sum, 31);
     };
@@ -142,7 +155,9 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) rows_kernel(const __grid_
     for (int i = 0; i < kHeld; ++i)
         if (i * 32 < segs) segments(i * 32, tiles[i]);
     for (int k0 = kHeld * 32; k0 < segs; k0 += 32) segments(k0, k0 + lane < segs ? seg_tiles(a, k0 + lane) : 0);
-    if (begin < end) {
+    bool any = begin < end;
+    if (any && at.i1 <= at.i0) any = next_unit(a, start, at);  // the range begins with the last empty steps of a unit
+    if (any) {
         uint8_t *const ring = smem + warp * kStages * M::BYTES;
         // the first of this warp's tiles from i0 on: every fourth step of the CTA's range
         const auto first = [&](const Place &p) { return p.i0 + ((warp - p.off) & (kWarps - 1)); };
@@ -151,7 +166,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) rows_kernel(const __grid_
         bool more = true, dead = false;
         const auto fetch = [&]() {
             while (more && fi >= ahead.i1) {
-                more = next_unit(a, ahead);
+                more = next_unit(a, start, ahead);
                 if (more) fi = first(ahead);
             }
             if (!more || dead) return;
@@ -358,7 +373,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) rows_kernel(const __grid_
             }
             __syncthreads();
             const int64_t part = (int64_t)(pre ? 0 : a.pre.n * a.Hkv * a.pre.row_tiles) + (int64_t)seg * a.Hkv * s.row_tiles + at.unit + blockIdx.x;
-            go = next_unit(a, at);
+            go = next_unit(a, start, at);
             if (go) fetch_q(at);
             for (int row = warp; row < R; row += kWarps) {
                 float M_ = kNone, L = 0.0f, w[kWarps];
@@ -417,7 +432,8 @@ __device__ __forceinline__ Parts parts_of(const Call &a, const attn::Args &tc, b
         p.step = 1;
         return p;
     }
-    const int per = a.line[0], tile = r / kRows, u = hk * s.row_tiles + tile, start = a.line[1 + k + (pre ? 0 : a.pre.n)] + u * T;
+    const int per = a.line[0], empty = a.line[1], tile = r / kRows, u = hk * s.row_tiles + tile;
+    const int start = a.line[2 + k + (pre ? 0 : a.pre.n)] + u * (T + empty) + empty;
     const int c0 = start / per;
     const int64_t at = ((pre ? 0 : (int64_t)a.pre.n * a.Hkv * a.pre.row_tiles) + (int64_t)k * a.Hkv * s.row_tiles + u + c0) * kRows + r % kRows;
     p.n = (start + T - 1) / per - c0 + 1;
@@ -521,7 +537,7 @@ size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
 
 int64_t units_of(const Call &a) { return ((int64_t)a.pre.n * a.pre.row_tiles + (int64_t)a.suf.n * a.suf.row_tiles) * a.Hkv; }
 size_t ml_bytes(const Call &a) { return round256((size_t)(units_of(a) + a.grid) * kRows * sizeof(float2)); }
-size_t line_bytes(const Call &a) { return round256((size_t)(1 + a.pre.n + a.suf.n) * sizeof(int)); }
+size_t line_bytes(const Call &a) { return round256((size_t)(2 + a.pre.n + a.suf.n) * sizeof(int)); }
 size_t rows_bytes(const Call &a, int64_t D)
 {
     return a.grid ? ml_bytes(a) + line_bytes(a) + round256((size_t)(units_of(a) + a.grid) * kRows * D * sizeof(float)) : 0;
@@ -568,7 +584,7 @@ qerl_status shape(const qerl_kv4_attn_dims *d, const qerl_kv4_cache *prefix, con
     const int64_t pre = (int64_t)a.pre.n * a.pre.row_tiles * a.Hkv, suf = (int64_t)a.suf.n * a.suf.row_tiles * a.Hkv;
     if (pre > big || suf > big || pre + suf > big) return QERL_ERR_SHAPE;
     const int64_t pt = prefix ? (prefix->T + kTok - 1) / kTok : 0, st = suffix ? (suffix->T + kTok - 1) / kTok : 0;
-    if ((pt && pre > big / pt) || (st && suf > big / st) || pre * pt + suf * st > big) return QERL_ERR_SHAPE;
+    if ((pt && pre > big / pt) || (st && suf > big / st) || (pre + suf) * kStart + pre * pt + suf * st > big) return QERL_ERR_SHAPE;
     // A kind of segments goes to the tcgen05 kernel where that is quicker: a step of its line (256 rows, 128 keys) takes about 2 us
     // on a CTA, one of this file's (8 rows, 32 keys) 1 ns over all SMs.
     const int sms = num_sms();

@@ -20,7 +20,8 @@ struct Side {
 // One call as the kernels see it.  Strides of q and out in elements.  A query row is (b, l, h): sequence, new token, query head;
 // gs = Hq / Hkv heads share a kv head, G sequences share a prefix.
 // A unit is (segment, kv head, row tile); its steps are the segment's key tiles.  All units' steps form a line, prefixes before
-// suffixes, which the CTAs share in contiguous ranges of line[0] steps; line[1 + k] is where segment k starts.  Each range in a
+// suffixes, which the CTAs share in contiguous ranges of line[0] steps; before a unit's steps come line[1] empty ones, and
+// line[2 + k] is where segment k starts.  Each range in a
 // unit leaves a part: o = sum 2^(a - m) v unnormalised (without the cache's factor), m and l = sum 2^(a - m).  Unit u and CTA c
 // leave part u + c, which no other pair has: along the line, u or c grows from one part to the next.
 struct Call {
@@ -69,14 +70,7 @@ __device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b)
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-// The four code pairs of a word as fp16 pairs, and the two scale pairs of a word.
-__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&o)[4])
-{
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-        : "r"(w));
-}
+// The two scale pairs of a word as fp16 pairs.
 __device__ __forceinline__ void scales_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
 {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w));
