@@ -629,16 +629,21 @@ class Kv4Cache:
         self.data = torch.zeros(shape, dtype=torch.uint8, device=device) if data is None else data
         assert self.data.shape == shape and self.data.dtype == torch.uint8 and self.data.stride(3) == 1
         self.n, self.T, self.Hkv, self.D = n, T, Hkv, D
+        self._rows, self._lens, self._strides = (n, Hkv, D), torch.Size((n,)), None
         self._c = _Kv4Cache(self.data.data_ptr(), n, T, Hkv, D, (C.c_int64 * 3)(*self.data.stride()[:3]), k_scale, v_scale)
         self._ref = C.byref(self._c)
         self._launched_on = {_stream()} if self.data.is_cuda else set()
 
     def _tokens(self, k, v, lens):
-        assert k.dtype == v.dtype == torch.bfloat16 and k.shape == v.shape and k.shape[::2] == (self.n, self.Hkv) and k.shape[3] == self.D
-        assert (k.stride(3) == v.stride(3) == 1) or k.numel() == 0
-        assert lens.dtype == torch.int32 and lens.is_contiguous() and lens.numel() == self.n
-        st = C.c_int64 * 3
-        return (_p(k) or 16, st(*k.stride()[:3]), _p(v) or 16, st(*v.stride()[:3]))  # an empty tensor has no address
+        shape = k.shape
+        assert k.dtype == v.dtype == torch.bfloat16 and shape == v.shape and (shape[0], shape[2], shape[3]) == self._rows
+        assert lens.dtype == torch.int32 and lens.shape == self._lens and lens.is_contiguous()
+        strides = (k.stride(), v.stride())
+        if strides != self._strides:
+            assert (strides[0][3] == strides[1][3] == 1) or k.numel() == 0
+            self._st = [(C.c_int64 * 3)(*t[:3]) for t in strides]
+            self._strides = strides if k.numel() else None
+        return k.data_ptr() or 16, self._st[0], v.data_ptr() or 16, self._st[1]  # an empty tensor has no address
 
     def _launch(self, stream):
         handle = _stream(stream)
@@ -696,8 +701,9 @@ class Kv4Attention:
             out = _new(torch.empty, stream, self._q_shape, dtype=torch.bfloat16, device=q.device)
         assert q.shape == self._q_shape and out.shape == self._q_shape and q.dtype == out.dtype == torch.bfloat16
         assert (suffix is None) == (suffix_lens is None) and (prefix is not None or prefix_lens is None)
-        for t, n in ((suffix_lens, d.B), (prefix_lens, prefix.n if prefix is not None else 0)):
-            assert t is None or (t.dtype == torch.int32 and t.is_contiguous() and t.numel() == n)
+        assert suffix is None or (suffix_lens.dtype == torch.int32 and suffix_lens.shape == suffix._lens and suffix_lens.is_contiguous())
+        if prefix_lens is not None:
+            assert prefix_lens.dtype == torch.int32 and prefix_lens.shape == prefix._lens and prefix_lens.is_contiguous()
         if lse is not None:
             assert lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == self._q_shape[:3]
         strides = (q.stride(), out.stride())

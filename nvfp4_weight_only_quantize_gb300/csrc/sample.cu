@@ -48,6 +48,12 @@ constexpr int kList = 8192, kSamples = 8192;
 // A draw compares a sum with u times the total, which moves by at most kEps 2 u (1 - u) of the total: total >> kOff.
 constexpr double kEps = 6e-7;
 constexpr int kOff = 21;
+// Where that leaves a choice open, sums of the second kind: the exponent's rounding taken back, eight values to an integer.
+// What is left is ex2.approx's error less its average, 5e-8 deviation a value, and three roundings of a sum: below 4e-8 even
+// where a few tokens make the sum, whose borders are far apart.
+constexpr double kEps2 = 4e-8;
+constexpr int kOff2 = 25;
+constexpr double kBias = 5.08e-8;
 
 struct Args {
     const void *x;
@@ -139,6 +145,16 @@ __device__ __forceinline__ uint64_t mass(const Exp &e, float x)
     return some ? all : 0;
 }
 
+// The exponent's rounding taken back: in the units of fast().
+__device__ __forceinline__ float good(const Exp &e, float x)
+{
+    const float d0 = x - e.top;
+    const bool some = d0 > e.low;
+    const float d = some ? d0 : 0.0f, b = d - x, rest = some ? (x - (d - b)) - (e.top + b) : 0.0f;
+    const float y = d * e.c, y_lo = fmaf(d, e.c, -y) + fmaf(d, e.c_lo, rest * e.c), v = ex2(y);
+    return some ? fmaf(v * 0x1.62e430p-1f, y_lo, v) : 0.0f;
+}
+
 // A row as the aligned 16-byte vectors that hold it; elements outside it read as -inf.
 template <bool BF16>
 struct Row {
@@ -212,11 +228,11 @@ struct Shared {
     uint64_t w64[kWarps];
     float wf[kWarps];
     uint64_t got64[2];
-    uint32_t got32[2], mark[4];
+    uint32_t got32[2], mark[6];
     // and behind it, by chunk: the masses of what is kept, the maximum, the sum, the tokens at the border's key
     static constexpr int kChunkBytes = 8 + 4 + 4 + 4;
 };
-enum { kDone, kHist, kWeigh, kSum, kBetween, kBetweenSums, kKeptFast, kKeptExact };
+enum { kDone, kHist, kWeigh, kSumGood, kSum, kBetween, kBetweenSums, kKeptFast, kKeptGood, kKeptExact };
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v)
 {
@@ -454,7 +470,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
         }
         merge_hist();
     };
-    const auto sum_exact = [&](uint32_t hi, uint32_t lo) {  // masses of keys in [lo, hi]
+    // The masses of a vector's elements that are in the mask, without branches, so that the elements' chains overlap.
+    const auto some_of = [&](const float (&f)[E], uint32_t in, bool exact) -> uint64_t {
+        uint64_t z = 0;
+        if (exact) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const uint64_t m = mass(ex, f[e]);
+                z += in >> e & 1 ? m : 0;
+            }
+            return z;
+        }
+        float g[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) g[e] = in >> e & 1 ? good(ex, f[e]) : 0.0f;
+#pragma unroll
+        for (int o = E / 2; o; o /= 2)
+#pragma unroll
+            for (int e = 0; e < o; ++e) g[e] += g[e + o];
+        return fixed(g[0]);
+    };
+    const auto sum_again = [&](uint32_t hi, uint32_t lo, bool exact) {  // masses of keys in [lo, hi], exact or good
         uint64_t z = 0;
         for (int ch = rank * kWarps + warp; ch < chunks; ch += ranks * kWarps) {
             if (key_of(s_chunk_m[ch]) < lo) continue;
@@ -466,11 +502,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
 #pragma unroll
                 for (int e = 0; e < E; ++e) in |= (key_of(f[e]) >= lo && key_of(f[e]) <= hi ? 1u : 0u) << e;
                 if (!__any_sync(0xFFFFFFFFu, in)) continue;
-#pragma unroll
-                for (int e = 0; e < E; ++e) {  // without branches, so that the elements' chains overlap
-                    const uint64_t m = mass(ex, f[e]);
-                    z += in >> e & 1 ? m : 0;
-                }
+                z += some_of(f, in, exact);
             }
         }
         z = warp_sum(z);
@@ -529,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
             if (lane == 0) L::add(&s.sum, zs);
         }
     };
-    // By chunk: what is above the border, fast, and how many are at it; or exactly what is kept, `upto` the last index at the border.
+    // By chunk: what is above the border, fast, and how many are at it; or what is kept, good or exact, `upto` the last index at the border.
     const auto kept_fast = [&](float border) {
         for (int ch = rank * kWarps + warp; ch < chunks; ch += ranks * kWarps) {
             float above = 0.0f;
@@ -557,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
             }
         }
     };
-    const auto kept_exact = [&](float border, uint32_t upto) {
+    const auto kept_again = [&](float border, uint32_t upto, bool exact) {
         for (int ch = rank * kWarps + warp; ch < chunks; ch += ranks * kWarps) {
             uint64_t z = 0;
             if (s_chunk_m[ch] >= border) {
@@ -571,14 +603,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
                     for (int e = 0; e < E; ++e)
                         in |= (f[e] > border || (f[e] == border && (uint32_t)max(i * E + e - r.off, 0) <= upto) ? 1u : 0u) << e;
                     if (!__any_sync(0xFFFFFFFFu, in)) continue;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const uint64_t m = mass(ex, f[e]);
-                        z += in >> e & 1 ? m : 0;
-                    }
+                    z += some_of(f, in, exact);
                 }
                 z = warp_sum(z);
             }
+            if (!exact) z += (uint64_t)((float)z * (float)kBias);
             if (lane == 0) L::put(&s_chunk[ch], z);
         }
     };
@@ -587,10 +616,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
         const int what = s.what;
         const uint32_t hi = s.hi, lo = s.lo;
         if (what == kHist || what == kWeigh) count_hist(hi, lo, s.shift, what == kWeigh);
-        if (what == kSum) sum_exact(hi, lo);
+        if (what == kSum || what == kSumGood) sum_again(hi, lo, what == kSum);
         if (what == kBetween || what == kBetweenSums) between(__uint_as_float(hi), __uint_as_float(lo), what == kBetweenSums);
         if (what == kKeptFast) kept_fast(__uint_as_float(hi));
-        if (what == kKeptExact) kept_exact(__uint_as_float(hi), lo);
+        if (what == kKeptExact || what == kKeptGood) kept_again(__uint_as_float(hi), lo, what == kKeptExact);
     };
     if (CLUSTER && !lead) {
         for (;;) {
@@ -673,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
             if (y < kBins - 1.0f)
                 atomicAdd(&s.hist[(int)y], 1u);
         }
-        if (tid < 4) s.mark[tid] = kBins;
+        if (tid < 6) s.mark[tid] = kBins;
         __syncthreads();
         uint64_t cnt = 0, below = 0, all_cnt, all_mass = 0;
         float squares = 0.0f;
@@ -711,39 +740,50 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
             // A list of all that is above has to be generous: what stands out is not in the sample.  Where the border lies among
             // many alike, the sample knows what is below it within its own deviation.
             return (left + 3.0f * sigma <= 0.25f * rest && upto <= 0.6f * kList ? 1 : 0) | (left + 3.0f * sigma <= 0.99f * rest ? 2 : 0) |
-                   (left - 3.0f * sigma < 1.01f * rest ? 4 : 0) | (upto > 1000.0f ? 8 : 0);
+                   (left - 3.0f * sigma < 1.01f * rest ? 4 : 0) | (upto > 1000.0f ? 8 : 0) | (left + 2.0f * sigma <= 0.997f * rest ? 16 : 0) |
+                   (left - 2.0f * sigma < 1.003f * rest ? 32 : 0);
         };
         uint64_t c = at_cnt, at = at_mass;
-        uint32_t first[4] = {kBins, kBins, kBins, kBins};
+        uint32_t first[6] = {kBins, kBins, kBins, kBins, kBins, kBins};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint32_t b = tid * 4 + j;
             c += n[j], at += m[j];
             const uint32_t now = marks(c, at);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 6; ++i)
                 if (now >> i & 1) first[i] = min(first[i], b);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 6; ++i) {
             const uint32_t b = __reduce_min_sync(0xFFFFFFFFu, first[i]);
             if (lane == 0 && b < kBins) atomicMin(&s.mark[i], b);
         }
         __syncthreads();
         const bool all_listed = cut_k || s.mark[0] < kBins;
         // all that is above: down to where there are a thousand, or further
-        const uint32_t b_low = cut_k || !all_listed ? s.mark[1] : max(s.mark[0], min(s.mark[3], kBins - 1u) - 1u), b_high = all_listed ? 0 : s.mark[2] % kBins;
-        __syncthreads();
-        c = at_cnt;
+        uint32_t b_low = cut_k || !all_listed ? s.mark[1] : max(s.mark[0], min(s.mark[3], kBins - 1u) - 1u), b_high = all_listed ? 0 : s.mark[2] % kBins;
+        const uint32_t narrow[2] = {s.mark[4], s.mark[5] % kBins};
+        const auto tokens_between = [&](uint32_t from, uint32_t to) -> float {  // in the bins up to b_low, less those before b_high
+            __syncthreads();
+            if (tid < 2) s.got64[tid] = 0;
+            __syncthreads();
+            uint64_t c = at_cnt;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t b = tid * 4 + j;
-            c += n[j];
-            if (b == min(b_low, kBins - 1u)) s.got64[0] = c;  // the tokens of the bins up to b_low, and before b_high
-            if (b + 1 == b_high) s.got64[1] = c;
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t b = tid * 4 + j;
+                c += n[j];
+                if (b == min(to, kBins - 1u)) s.got64[0] = c;
+                if (b + 1 == from) s.got64[1] = c;
+            }
+            __syncthreads();
+            return W * (float)(s.got64[0] - s.got64[1]);
+        };
+        bool try_list = tokens_between(b_high, b_low) <= 0.8f * kList;
+        if (!try_list && !all_listed) {  // nearer thresholds, which miss the border more often
+            b_low = narrow[0], b_high = narrow[1];
+            try_list = tokens_between(b_high, b_low) <= 0.8f * kList;
         }
-        __syncthreads();
-        bool try_list = W * (float)(s.got64[0] - (b_high ? s.got64[1] : 0)) <= 0.8f * kList;
         // fewer than k within 64 octaves: what lies below has no mass
         float low = top - (float)min(b_low + 1, kBins - 1u) / step, high = b_high ? top - (float)b_high / step : INFINITY;
         if (r.n <= kThreads || (r.n <= kList && !try_list)) try_list = true, low = -INFINITY, high = INFINITY;
@@ -860,23 +900,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
                     block_scan(s, part, above);
                     // The border is the first token after which at most 1 - top_p of the sum is left.  The fast sums may move that by
                     // `off`: is it the same token at either end?
-                    const double leaves = (1.0 - (double)top_p) * (double)(above + held + below);
-                    const double off = ((1.0 - (double)top_p) * (double)(above + below) + (double)below) * kEps + 4.0, in_list = (double)(held + below);
+                    const auto again = [&](bool exact) {
+                        const auto sum = [&](uint64_t &v, uint32_t hi, uint32_t lo) {
+                            if (!v) return;
+                            ask(exact ? kSum : kSumGood, hi, lo, 0);
+                            v = exact ? s.sum : s.sum + (uint64_t)((double)s.sum * kBias);
+                        };
+                        sum(below, key_of(low) - (1u << kUnit), 0);
+                        sum(above, 0xFFFFFFFFu, key_of(high) + (1u << kUnit));
+                        Z = above + held + below;
+                    };
+                    const auto choose = [&](double eps) -> bool {
+                        const double in_list = (double)(held + below), leaves = (1.0 - (double)top_p) * (double)(above + held + below);
+                        const double off = ((1.0 - (double)top_p) * (double)(above + below) + (double)below) * eps + 1024.0;
+                        if (!(in_list - leaves > off && in_list - leaves + off <= (double)held)) return false;
+                        return pick(true, (uint64_t)ceil(in_list - leaves - off), (uint64_t)ceil(in_list - leaves + off), border, other, upto);
+                    };
                     if ((above | below) == 0) {
                         kept = pick(true, wanted(held), wanted(held), border, other, upto);
-                    } else if (in_list - leaves > off && in_list - leaves + off <= (double)held) {
-                        const uint64_t from = (uint64_t)ceil(in_list - leaves - off), to = (uint64_t)ceil(in_list - leaves + off);
-                        kept = pick(true, from, to, border, other, upto);
-                        if (kept && border != other) {  // exactly: the sums above and below, and what is reached
-                            if (below) {
-                                ask(kSum, key_of(low) - (1u << kUnit), 0, 0);
-                                below = s.sum;
-                            }
-                            if (above) {
-                                ask(kSum, 0xFFFFFFFFu, key_of(high) + (1u << kUnit), 0);
-                                above = s.sum;
-                            }
-                            Z = above + held + below;
+                    } else {
+                        kept = choose(kEps);
+                        if (kept && border != other) {
+                            again(false);
+                            kept = choose(kEps2);
+                        }
+                        if (kept && border != other) {  // by what is reached
+                            again(true);
                             const uint64_t want = wanted(Z);
                             kept = want > above && pick(true, want - above, want - above, border, other, upto);
                         }
@@ -1031,7 +1080,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
     const uint64_t u_m = u_bits >> 23 ? (u_bits & 0x7FFFFFu) | 0x800000u : 0;  // below 2^-126 as 0
     const int u_e = 150 - (int)(u_bits >> 23);  // 24 or more
     const uint32_t last_key = ~(uint32_t)(last >> 32), last_index = (uint32_t)last;
-    for (;;) {
+    for (int level = fast ? 0 : 2;;) {  // of the chunks' sums
         const int per = (chunks + kThreads - 1) / kThreads, i0 = min(tid * per, chunks), i1 = min(i0 + per, chunks);
         uint64_t w = 0, total = 0;
         for (int i = i0; i < i1; ++i) w += s_chunk[i];
@@ -1064,7 +1113,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
         }
         uint64_t cum = before + block_scan(s, own, all) - own;
         // how far the fast sums before this chunk and the target may be off
-        const uint64_t off = fast ? (total >> kOff) + 2 : 0;
+        const uint64_t off = level == 0 ? (total >> kOff) + 1024 : level == 1 ? (total >> kOff2) + 1024 : 0;
 #pragma unroll
         for (int j = 0; j < per_thread; ++j) {
             if (m[j] && (cum == 0 || cum + off <= target) && target + off < cum + m[j]) {
@@ -1075,7 +1124,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
         }
         __syncthreads();
         const uint32_t id = s.got32[0];
-        if (id != 0xFFFFFFFFu || !fast) {
+        if (id != 0xFFFFFFFFu || level == 2) {
             if (tid == 0) {
                 // the sums less the most probable token's, which is 1
                 const float y = (__uint_as_float(s.got32[1]) - top) / tau;
@@ -1086,8 +1135,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
             }
             break;
         }
-        fast = false;
-        ask(kKeptExact, last == ~uint64_t(0) ? 0xFF800000u : __float_as_uint(value_of(last_key)), last_index, 0);
+        ++level;
+        ask(level == 1 ? kKeptGood : kKeptExact, last == ~uint64_t(0) ? 0xFF800000u : __float_as_uint(value_of(last_key)), last_index, 0);
     }
     ask(kDone, 0, 0, 0);
 }
