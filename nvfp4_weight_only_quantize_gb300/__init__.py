@@ -179,6 +179,13 @@ def workspace(op: int, M: int, N: int, K: int, r: int, device="cuda") -> torch.T
     return torch.empty(max(workspace_bytes(op, M, N, K, r), 1), dtype=torch.uint8, device=device)
 
 
+def _here(*tensors):
+    """All of them on the current device, whose stream the call is launched on."""
+    device = torch._C._cuda_getDevice()
+    for t in tensors:
+        assert t is None or t.get_device() == device
+
+
 def _new(make, stream, *args, **kw):
     """make(*args, **kw), a tensor of a call's own.  With `stream` it comes from that stream's memory, so that nothing still
     queued elsewhere for its last owner meets the call; the caller goes on with it on the current stream."""
@@ -656,6 +663,7 @@ class Kv4Cache:
         (int32 [n]): how many of the L each sequence has, all if None."""
         args = self._tokens(k, v, lens)
         assert counts is None or (counts.dtype == torch.int32 and counts.is_contiguous() and counts.numel() == self.n)
+        _here(self.data, k, v, lens, counts)
         _check(lib().qerl_kv4_append(self._ref, k.shape[1], *args, lens.data_ptr(), _p(counts), self._launch(stream)), "qerl_kv4_append")
 
     def read(self, lens, L: int, k=None, v=None, stream=None):
@@ -664,6 +672,7 @@ class Kv4Cache:
         v = _new(torch.empty, stream, self.n, L, self.Hkv, self.D, dtype=torch.bfloat16, device=self.data.device) if v is None else v
         kp, ks, vp, vs = self._tokens(k, v, lens)
         assert k.shape[1] == L
+        _here(self.data, k, v, lens)
         _check(lib().qerl_kv4_read(self._ref, L, lens.data_ptr(), kp, ks, vp, vs, self._launch(stream)), "qerl_kv4_read")
         return k, v
 
@@ -717,6 +726,7 @@ class Kv4Attention:
         for c in self._caches:
             if c is not None and handle not in c._launched_on:
                 c._launch(stream)
+        _here(self.ws, q, out, suffix_lens, prefix_lens, lse)
         _check(lib().qerl_kv4_attention(self._ref, q.data_ptr(), self._pref, _p(prefix_lens), self._suf, _p(suffix_lens), self._scale,
                                         out.data_ptr(), _p(lse), self._ws[0], self._ws[1], handle), "qerl_kv4_attention")
         return out
@@ -804,6 +814,7 @@ def qerl_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, ids=N
             setattr(o, name + "s", v.data_ptr())
         else:
             setattr(o, name, v)
+    _here(logits, u, ids, logp, logq, *(v for v in (temperature, top_k, top_p, min_p) if isinstance(v, torch.Tensor)))
     _check(lib().qerl_sample(logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld if T > 1 else V, u.data_ptr(), C.byref(o), ids.data_ptr(),
                              logp.data_ptr(), logq.data_ptr(), _stream(stream)), "qerl_sample")
     return ids, logp, logq

@@ -38,7 +38,7 @@ constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCluster = 8;
 constexpr int kVec = 4, kChunkVecs = 32 * kVec;  // 16-byte vectors of a lane and of a chunk
 constexpr int kBins = 2048, kBinBits = 11;
 constexpr int64_t kMaxV = 1 << 20;  // 2^42 times that fits 62 bits
-constexpr int kMostChunks = kMaxV * 4 / (kChunkVecs * 16) + 1;
+constexpr int kMostChunks = kMaxV * 4 / (kChunkVecs * 16) + 2;  // a row may start inside a vector; an even number
 constexpr int kScale = 42;
 constexpr int kList = 8192, kSamples = 8192;
 // What a fast sum is taken to be off by, relative to it.  ex2.approx is off by -5e-8 on average over an octave (measured, the
@@ -119,7 +119,7 @@ __device__ __forceinline__ float fast(const Exp &e, float d)
     asm("max.NaN.f32 %0, %0, %1;" : "+f"(d) : "f"(e.low));  // no -inf times a c_lo below 0
     return ex2(fmaf(d, e.c, d * e.c_lo));
 }
-__device__ __forceinline__ uint64_t mass(const Exp &e, float x)
+__device__ __forceinline__ uint64_t mass_in_line(const Exp &e, float x)
 {
     const float d0 = x - e.top;
     const bool some = d0 * e.c > -60.0f;  // false for NaN
@@ -145,6 +145,9 @@ __device__ __forceinline__ uint64_t mass(const Exp &e, float x)
     return some ? all : 0;
 }
 
+// The same as a call, where it is not in a sweep.
+__device__ __noinline__ uint64_t mass_call(float x, float top, float c, float c_lo);  // below: the table lies in shared memory
+__device__ __forceinline__ uint64_t mass(const Exp &e, float x) { return mass_call(x, e.top, e.c, e.c_lo); }
 // The exponent's rounding taken back: in the units of fast().
 __device__ __forceinline__ float good(const Exp &e, float x)
 {
@@ -161,11 +164,10 @@ struct Row {
     static constexpr int E = BF16 ? 8 : 4, S = 16 / E;
     const char *x;
     int off, n, nvec;
-    __device__ __forceinline__ Row(const Args &a, int64_t row)
+    __device__ __forceinline__ Row(const char *row, int off_, int n_) : x(row), off(off_), n(n_), nvec((off_ + n_ + E - 1) / E) {}
+    __device__ __forceinline__ Row(const Args &a, int64_t row) : Row(static_cast<const char *>(a.x) + row * a.ld * S, 0, (int)a.V)
     {
-        x = static_cast<const char *>(a.x) + row * a.ld * S;
         off = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / S);
-        n = (int)a.V;
         nvec = (off + n + E - 1) / E;
     }
     __device__ __forceinline__ float at(int e) const
@@ -232,6 +234,8 @@ struct Shared {
     // and behind it, by chunk: the masses of what is kept, the maximum, the sum, the tokens at the border's key
     static constexpr int kChunkBytes = 8 + 4 + 4 + 4;
 };
+extern __shared__ __align__(16) uint8_t smem[];
+
 enum { kDone, kHist, kWeigh, kSumGood, kSum, kBetween, kBetweenSums, kKeptFast, kKeptGood, kKeptExact };
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v)
@@ -244,9 +248,17 @@ __device__ __forceinline__ float warp_sum(float v)
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
-// Inclusive sums over the block's threads; `all` is the total.
-__device__ __forceinline__ uint64_t block_scan(Shared &s, uint64_t v, uint64_t &all)
+__device__ __noinline__ uint64_t mass_call(float x, float top, float c, float c_lo)
 {
+    return mass_in_line(Exp{top, c, c_lo, 0.0f, reinterpret_cast<Shared *>(smem)->roots}, x);
+}
+
+struct Scan {
+    uint64_t upto, all;
+};
+__device__ __noinline__ Scan scan_call(uint64_t v)
+{
+    Shared &s = *reinterpret_cast<Shared *>(smem);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     for (int o = 1; o < 32; o *= 2) {
         const uint64_t t = __shfl_up_sync(0xFFFFFFFFu, v, o);
@@ -262,8 +274,14 @@ __device__ __forceinline__ uint64_t block_scan(Shared &s, uint64_t v, uint64_t &
         total += t;
     }
     __syncthreads();
-    all = total;
-    return before + v;
+    return Scan{before + v, total};
+}
+// Inclusive sums over the block's threads; `all` is the total.
+__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t &all)
+{
+    const Scan r = scan_call(v);
+    all = r.all;
+    return r.upto;
 }
 __device__ __forceinline__ uint64_t fixed(float v) { return (uint64_t)__float2ll_rn(v * pow2f(kScale)); }  // 2^20 tokens at most
 
@@ -310,8 +328,9 @@ struct Lead {
 };
 
 // The first n <= kThreads entries of s.small in order; returns this thread's.
-__device__ __forceinline__ uint64_t sort_small(Shared &s, int n)
+__device__ __noinline__ uint64_t sort_small(int n)
 {
+    Shared &s = *reinterpret_cast<Shared *>(smem);
     const int tid = threadIdx.x;
     uint64_t v = tid < n ? s.small[tid] : ~uint64_t(0);
     for (int k = 2; k < 2 * n; k *= 2)
@@ -332,94 +351,22 @@ __device__ __forceinline__ uint64_t sort_small(Shared &s, int n)
     return v;
 }
 
+// What the first CTA of a row asks all of them for (s.what): one place in the code, with what it needs by value.
 template <bool BF16, bool CLUSTER>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
+__device__ __noinline__ void sweep(const char *x, int off, int n, int chunks, int most_chunks, float c, float c_lo, float low_, int rank, int ranks)
 {
-    extern __shared__ __align__(16) uint8_t smem[];
     Shared &s = *reinterpret_cast<Shared *>(smem);
     using R = Row<BF16>;
     using L = Lead<CLUSTER>;
-    constexpr int E = R::E, kUnit = BF16 ? 16 : 0;  // a key's low bits that say nothing
-    constexpr int kChunk = kChunkVecs * E;          // tokens of a chunk
-    const auto key_of = [](float x) { return qerl::key_of<BF16>(x); };
-    const auto value_of = [](uint32_t k) { return qerl::value_of<BF16>(k); };
+    constexpr int E = R::E;
+    const auto key_of = [](float v) { return qerl::key_of<BF16>(v); };
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    int rank = 0, ranks = 1;
-    if (CLUSTER) {
-        asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-        ranks = a.cluster;
-    }
     const bool lead = rank == 0;
-    const auto meet = [&]() {
-        if (CLUSTER) {
-            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        } else {
-            __syncthreads();
-        }
-    };
-    if (tid < 64) s.roots[tid] = kRoots[tid];
-    for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0, s.weight[i] = 0;
-    if (CLUSTER) meet();  // every CTA of the cluster runs: the first one's memory may be written
-    pdl_wait();
-    pdl_trigger();
-
-    const int64_t row = blockIdx.x / ranks;
-    const R r(a, row);
-    const float tau = a.taus ? a.taus[row] : a.tau;
-    int k = a.top_ks ? a.top_ks[row] : a.top_k;
-    const float top_p = a.top_ps ? a.top_ps[row] : a.top_p, min_p = a.min_ps ? a.min_ps[row] : a.min_p;
-    if (top_p <= 0.0f) k = 1;
-    const bool cut_k = k > 0 && k < r.n, cut_p = top_p > 0.0f && top_p < 1.0f, cut_m = min_p > 0.0f;
-    const int chunks = (r.nvec + kChunkVecs - 1) / kChunkVecs;
+    const R r(x, off, n);
+    const Exp ex = {s.top, c, c_lo, low_, s.roots};
     uint64_t *const s_chunk = reinterpret_cast<uint64_t *>(smem + sizeof(Shared));
-    float *const s_chunk_m = reinterpret_cast<float *>(s_chunk + a.chunks), *const s_chunk_s = s_chunk_m + a.chunks;
-    uint32_t *const s_ties = reinterpret_cast<uint32_t *>(s_chunk_s + a.chunks);
-    // log2(e) / tau in two numbers; log2(e) = 0x1.715476p+0 + 0x1.4ae0cp-26
-    Exp ex = {0.0f, __fdiv_rn(0x1.715476p+0f, tau), 0.0f, -138.0f * tau, s.roots};
-    ex.c_lo = __fdiv_rn(fmaf(-ex.c, tau, 0x1.715476p+0f) + 0x1.4ae0cp-26f, tau);
-    if (!(tau > 1e-30f && tau <= 1e30f)) {
-        if (lead && tid == 0) a.ids[row] = -1, a.logp[row] = a.logq[row] = NAN;
-        if (CLUSTER) meet();
-        return;
-    }
-
-    // ------------------------------------------------------------ chunks' maxima and sums, and a sample
-    // two of a lane's tokens, from every chunk or from fewer, so that kSamples hold
-    const int every = (chunks + kSamples / 64 - 1) / (kSamples / 64);
-    const bool sampled = cut_k || cut_p;
-    for (int ch = rank * kWarps + warp; ch < chunks; ch += ranks * kWarps) {
-        uint4 v[kVec];
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) v[j] = r.load(ch * kChunkVecs + j * 32 + lane);
-        float m = -FLT_MAX;
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            float f[E];
-            R::unpack(v[j], f);
-#pragma unroll
-            for (int e = 0; e < E; ++e) m = fmaxf(m, f[e]);
-            if (sampled && j % 2 == 0 && ch % every == 0) L::put(&s.sample[(ch / every) * 64 + j * 16 + lane], f[E / 2]);
-        }
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        float z[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            float f[E];
-            R::unpack(v[j], f);
-#pragma unroll
-            for (int e = 0; e < E; ++e) z[e % 2] += fast(ex, f[e] - m);  // NaN and +inf leave NaN
-        }
-        const float sum = warp_sum(z[0] + z[1]);
-        if (lane == 0) {
-            if (CLUSTER) s_chunk_m[ch] = m;
-            L::put(&s_chunk_m[ch], m);
-            L::put(&s_chunk_s[ch], sum);
-        }
-    }
-    meet();
-
-    // ------------------------------------------------------------ the sweeps that the first CTA asks for
+    const float *const s_chunk_m = reinterpret_cast<const float *>(s_chunk + most_chunks);
+    uint32_t *const s_ties = reinterpret_cast<uint32_t *>(s_chunk + 2 * most_chunks);
     const auto merge_hist = [&]() {
         if (!CLUSTER) return;
         __syncthreads();
@@ -476,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
         if (exact) {
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const uint64_t m = mass(ex, f[e]);
+                const uint64_t m = mass_in_line(ex, f[e]);
                 z += in >> e & 1 ? m : 0;
             }
             return z;
@@ -611,21 +558,107 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
             if (lane == 0) L::put(&s_chunk[ch], z);
         }
     };
-    const auto sweep = [&]() {
-        ex.top = s.top;
-        const int what = s.what;
-        const uint32_t hi = s.hi, lo = s.lo;
-        if (what == kHist || what == kWeigh) count_hist(hi, lo, s.shift, what == kWeigh);
-        if (what == kSum || what == kSumGood) sum_again(hi, lo, what == kSum);
-        if (what == kBetween || what == kBetweenSums) between(__uint_as_float(hi), __uint_as_float(lo), what == kBetweenSums);
-        if (what == kKeptFast) kept_fast(__uint_as_float(hi));
-        if (what == kKeptExact || what == kKeptGood) kept_again(__uint_as_float(hi), lo, what == kKeptExact);
+    const int what = s.what;
+    const uint32_t hi = s.hi, lo = s.lo;
+    if (what == kHist || what == kWeigh) count_hist(hi, lo, s.shift, what == kWeigh);
+    if (what == kSum || what == kSumGood) sum_again(hi, lo, what == kSum);
+    if (what == kBetween || what == kBetweenSums) between(__uint_as_float(hi), __uint_as_float(lo), what == kBetweenSums);
+    if (what == kKeptFast) kept_fast(__uint_as_float(hi));
+    if (what == kKeptExact || what == kKeptGood) kept_again(__uint_as_float(hi), lo, what == kKeptExact);
+}
+
+template <bool BF16, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
+{
+    Shared &s = *reinterpret_cast<Shared *>(smem);
+    using R = Row<BF16>;
+    using L = Lead<CLUSTER>;
+    constexpr int E = R::E, kUnit = BF16 ? 16 : 0;  // a key's low bits that say nothing
+    constexpr int kChunk = kChunkVecs * E;          // tokens of a chunk
+    const auto key_of = [](float x) { return qerl::key_of<BF16>(x); };
+    const auto value_of = [](uint32_t k) { return qerl::value_of<BF16>(k); };
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    int rank = 0, ranks = 1;
+    if (CLUSTER) {
+        asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+        ranks = a.cluster;
+    }
+    const bool lead = rank == 0;
+    const auto meet = [&]() {
+        if (CLUSTER) {
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        } else {
+            __syncthreads();
+        }
     };
+    if (tid < 64) s.roots[tid] = kRoots[tid];
+    for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0, s.weight[i] = 0;
+    if (CLUSTER) meet();  // every CTA of the cluster runs: the first one's memory may be written
+    pdl_wait();
+    pdl_trigger();
+
+    const int64_t row = blockIdx.x / ranks;
+    const R r(a, row);
+    const float tau = a.taus ? a.taus[row] : a.tau;
+    int k = a.top_ks ? a.top_ks[row] : a.top_k;
+    const float top_p = a.top_ps ? a.top_ps[row] : a.top_p, min_p = a.min_ps ? a.min_ps[row] : a.min_p;
+    if (top_p <= 0.0f) k = 1;
+    const bool cut_k = k > 0 && k < r.n, cut_p = top_p > 0.0f && top_p < 1.0f, cut_m = min_p > 0.0f;
+    const int chunks = (r.nvec + kChunkVecs - 1) / kChunkVecs;
+    uint64_t *const s_chunk = reinterpret_cast<uint64_t *>(smem + sizeof(Shared));
+    float *const s_chunk_m = reinterpret_cast<float *>(s_chunk + a.chunks), *const s_chunk_s = s_chunk_m + a.chunks;
+    uint32_t *const s_ties = reinterpret_cast<uint32_t *>(s_chunk_s + a.chunks);
+    // log2(e) / tau in two numbers; log2(e) = 0x1.715476p+0 + 0x1.4ae0cp-26
+    Exp ex = {0.0f, __fdiv_rn(0x1.715476p+0f, tau), 0.0f, -138.0f * tau, s.roots};
+    ex.c_lo = __fdiv_rn(fmaf(-ex.c, tau, 0x1.715476p+0f) + 0x1.4ae0cp-26f, tau);
+    if (!(tau > 1e-30f && tau <= 1e30f)) {
+        if (lead && tid == 0) a.ids[row] = -1, a.logp[row] = a.logq[row] = NAN;
+        if (CLUSTER) meet();
+        return;
+    }
+
+    // ------------------------------------------------------------ chunks' maxima and sums, and a sample
+    // two of a lane's tokens, from every chunk or from fewer, so that kSamples hold
+    const int every = (chunks + kSamples / 64 - 1) / (kSamples / 64);
+    const bool sampled = cut_k || cut_p;
+    for (int ch = rank * kWarps + warp; ch < chunks; ch += ranks * kWarps) {
+        uint4 v[kVec];
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) v[j] = r.load(ch * kChunkVecs + j * 32 + lane);
+        float m = -FLT_MAX;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            float f[E];
+            R::unpack(v[j], f);
+#pragma unroll
+            for (int e = 0; e < E; ++e) m = fmaxf(m, f[e]);
+            if (sampled && j % 2 == 0 && ch % every == 0) L::put(&s.sample[(ch / every) * 64 + j * 16 + lane], f[E / 2]);
+        }
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        float z[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            float f[E];
+            R::unpack(v[j], f);
+#pragma unroll
+            for (int e = 0; e < E; ++e) z[e % 2] += fast(ex, f[e] - m);  // NaN and +inf leave NaN
+        }
+        const float sum = warp_sum(z[0] + z[1]);
+        if (lane == 0) {
+            if (CLUSTER) s_chunk_m[ch] = m;
+            L::put(&s_chunk_m[ch], m);
+            L::put(&s_chunk_s[ch], sum);
+        }
+    }
+    meet();
+
+    const auto run_sweep = [&]() { sweep<BF16, CLUSTER>(r.x, r.off, r.n, chunks, a.chunks, ex.c, ex.c_lo, ex.low, rank, ranks); };
     if (CLUSTER && !lead) {
         for (;;) {
             meet();  // the order is there
             if (s.what == kDone) break;
-            sweep();
+            run_sweep();
             meet();  // and done
         }
         return;
@@ -649,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
         }
         meet();
         if (what == kDone) return;
-        sweep();
+        run_sweep();
         meet();
     };
 
@@ -673,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
         s_chunk[i] = m;
         mine += m;
     }
-    block_scan(s, mine, Z);
+    block_scan(mine, Z);
     if (any_bad || Z == 0) {  // NaN or +inf among the logits, or nothing but -inf
         if (tid == 0) a.ids[row] = -1, a.logp[row] = a.logq[row] = any_bad ? NAN : -INFINITY;
         ask(kDone, 0, 0, 0);
@@ -720,9 +753,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
             }
             cnt += n[j], below += m[j];
         }
-        uint64_t at_cnt = block_scan(s, cnt, all_cnt) - cnt, at_mass = 0;
+        uint64_t at_cnt = block_scan(cnt, all_cnt) - cnt, at_mass = 0;
         if (!cut_k) {
-            at_mass = block_scan(s, below, all_mass) - below;
+            at_mass = block_scan(below, all_mass) - below;
             // the sum of squares of the masses from this thread's bins on: the variance of what the sample puts below
             for (int o = 1; o < 32; o *= 2) {
                 const float t = __shfl_down_sync(0xFFFFFFFFu, squares, o);
@@ -792,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
             uint64_t sum = 0, all;
             for (int i = tid; i < chunks; i += kThreads)
                 if (s_chunk_m[i] < bound) sum += s_chunk[i];
-            block_scan(s, sum, all);
+            block_scan(sum, all);
             return all;
         };
         if (cut_m && least > key_of(high)) try_list = false;  // min_p's border is the one, as a rule
@@ -828,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
                     s.small[tid] = place;
                 }
                 t = held;
-                block_scan(s, t, held);
+                block_scan(t, held);
                 // The first entries up to which the tokens, or masses, reach `from` and `to`; with the mass up to the first.
                 int sorted = 0;
                 uint64_t own = 0, mass_before = 0, count_before = 0;
@@ -842,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
                             w[j] = shift > kUnit ? s.weight[b] : c[j] ? c[j] * mass(ex, value_of(top_key - ((uint32_t)b << shift))) : 0;  // one key a bin
                             sum += w[j], count += c[j];
                         }
-                        uint64_t at_m = block_scan(s, sum, all) - sum, at_c = block_scan(s, count, all) - count;
+                        uint64_t at_m = block_scan(sum, all) - sum, at_c = block_scan(count, all) - count;
                         if (tid < 2) s.got32[tid] = kBins;
                         if (tid == 2) s.listed = 0;
                         __syncthreads();
@@ -870,11 +903,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
                     }
                     const int n_small = binned ? (int)s.listed : (int)listed;
                     if (!sorted) {
-                        own = sort_small(s, n_small);
+                        own = sort_small(n_small);
                         sorted = 1;
                     }
                     const uint64_t m = tid < n_small ? mass_at(own) : 0;
-                    uint64_t all, at_m = mass_before + block_scan(s, m, all);
+                    uint64_t all, at_m = mass_before + block_scan(m, all);
                     const uint64_t at = by_mass ? at_m : count_before + tid + 1, before = at - (by_mass ? m : 1);
                     if (tid < 2) s.got64[tid] = 0;
                     __syncthreads();
@@ -897,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
                 } else {
                     uint64_t part = 0;
                     for (int i = tid; i < chunks; i += kThreads) part += s_chunk[i];
-                    block_scan(s, part, above);
+                    block_scan(part, above);
                     // The border is the first token after which at most 1 - top_p of the sum is left.  The fast sums may move that by
                     // `off`: is it the same token at either end?
                     const auto again = [&](bool exact) {
@@ -990,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
                 ask(weighed ? kWeigh : kHist, hi, lo, shift);
                 uint64_t w[4], all;
                 const uint64_t sum = weights(by_mass, weighed, hi, shift, w);  // the last bin reaches it if no other does
-                uint64_t at = before + block_scan(s, sum, all) - sum;
+                uint64_t at = before + block_scan(sum, all) - sum;
                 if (tid == 0) s.got32[0] = kBins;
                 __syncthreads();
 #pragma unroll
@@ -1022,7 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
             ask(kKeptFast, __float_as_uint(value_of(least)), 0, 0);
             uint64_t sum = 0, all;
             for (int i = tid; i < chunks; i += kThreads) sum += s_chunk[i] + s_ties[i] * mass(ex, value_of(least));
-            block_scan(s, sum, all);
+            block_scan(sum, all);
             by_least = (double)all * (1.0 + kEps) < (double)top_p * (double)Z * (1.0 - kEps);
         }
         if (cut_k && !by_least) find(false, (uint64_t)k, 0);
@@ -1048,7 +1081,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
         uint64_t n = 0, all;
         for (int i = i0; i < i1; ++i) n += s_ties[i];
         if (tid == 0) s.got32[0] = 0xFFFFFFFFu;
-        uint64_t at = block_scan(s, n, all) - n;
+        uint64_t at = block_scan(n, all) - n;
         for (int i = i0; i < i1; ++i) {
             const uint64_t t = s_ties[i], kept = at >= keep ? 0 : (at + t > keep ? keep - at : t);
             s_chunk[i] += kept * tie;
@@ -1064,7 +1097,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
             const int e0 = ch * kChunk + tid * per_thread - r.off;
             uint64_t ties = 0;
             for (int j = 0; j < per_thread; ++j) ties += r.inside(e0 + j) && r.at(e0 + j) == value_of(border);
-            uint64_t seen = block_scan(s, ties, all) - ties;
+            uint64_t seen = block_scan(ties, all) - ties;
             for (int j = 0; j < per_thread; ++j)
                 if (r.inside(e0 + j) && r.at(e0 + j) == value_of(border) && ++seen == nth) s.got32[0] = (uint32_t)(e0 + j);
             __syncthreads();
@@ -1084,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
         const int per = (chunks + kThreads - 1) / kThreads, i0 = min(tid * per, chunks), i1 = min(i0 + per, chunks);
         uint64_t w = 0, total = 0;
         for (int i = i0; i < i1; ++i) w += s_chunk[i];
-        uint64_t at = block_scan(s, w, total) - w;
+        uint64_t at = block_scan(w, total) - w;
         // floor(u total), u = u_m 2^-u_e
         const uint64_t high_part = __umul64hi(total, u_m), low_part = total * u_m;
         const uint64_t target = u_e < 64 ? low_part >> u_e | high_part << (64 - u_e) : u_e < 128 ? high_part >> (u_e - 64) : 0;
@@ -1111,7 +1144,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
             m[j] = kept ? mass(ex, f[j]) : 0;  // 0 outside the row, which reads as -inf
             own += m[j];
         }
-        uint64_t cum = before + block_scan(s, own, all) - own;
+        uint64_t cum = before + block_scan(own, all) - own;
         // how far the fast sums before this chunk and the target may be off
         const uint64_t off = level == 0 ? (total >> kOff) + 1024 : level == 1 ? (total >> kOff2) + 1024 : 0;
 #pragma unroll

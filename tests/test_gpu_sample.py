@@ -111,6 +111,23 @@ def test_many_rows_of_a_full_vocabulary():
     check(x[:100].float() + torch.randn(100, 100003, generator=gen(7), device="cuda") * 0.01, u[:100], top_p=0.95)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [300007, 1 << 20])
+def test_the_largest_vocabularies(dtype, V):
+    u = torch.rand(3, generator=gen(20), device="cuda")
+    x = logits_of(3, V, dtype, 21)
+    for cut in (dict(), dict(top_k=100, top_p=0.9), dict(top_p=0.7), dict(top_k=300000), dict(min_p=0.3)):
+        check(x, u, **cut)
+    check(torch.zeros(2, V, dtype=dtype, device="cuda"), torch.tensor([0.3, 0.999], device="cuda"), top_k=77777)
+
+
+def test_tensors_of_another_device_are_refused():
+    x, u = logits_of(2, 100, torch.float32, 22), torch.rand(2, device="cuda")
+    for args in ((x.cpu(), u), (x, u.cpu())):
+        with pytest.raises(AssertionError):
+            q.qerl_sample(*args)
+
+
 def test_ends_of_u():
     x = logits_of(6, 3000, torch.float32, 8)
     u = torch.tensor([0.0, 1.0, 5.0, -1.0, math.nan, 2.0 ** -149], device="cuda")
