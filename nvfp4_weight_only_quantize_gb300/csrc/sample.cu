@@ -114,11 +114,7 @@ struct Exp {
     const float2 *roots;
 };
 // The same in FP32 for a difference d <= 0, 1 for d = 0; NaN stays.
-__device__ __forceinline__ float fast(const Exp &e, float d)
-{
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(d) : "f"(e.low));  // no -inf times a c_lo below 0
-    return ex2(fmaf(d, e.c, d * e.c_lo));
-}
+__device__ __forceinline__ float fast(const Exp &e, float d) { return ex2(fmaf(d, e.c, d * e.c_lo)); }
 __device__ __forceinline__ uint64_t mass_in_line(const Exp &e, float x)
 {
     const float d0 = x - e.top;
@@ -611,7 +607,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
     uint32_t *const s_ties = reinterpret_cast<uint32_t *>(s_chunk_s + a.chunks);
     // log2(e) / tau in two numbers; log2(e) = 0x1.715476p+0 + 0x1.4ae0cp-26
     Exp ex = {0.0f, __fdiv_rn(0x1.715476p+0f, tau), 0.0f, -138.0f * tau, s.roots};
-    ex.c_lo = __fdiv_rn(fmaf(-ex.c, tau, 0x1.715476p+0f) + 0x1.4ae0cp-26f, tau);
+    const auto rest_of = [&](float c) { return __fdiv_rn(fmaf(-c, tau, 0x1.715476p+0f) + 0x1.4ae0cp-26f, tau); };
+    ex.c_lo = rest_of(ex.c);
+    if (!(ex.c_lo > 0.0f)) ex.c = __uint_as_float(__float_as_uint(ex.c) - 1u), ex.c_lo = rest_of(ex.c);  // so that -inf c_lo is -inf
     if (!(tau > 1e-30f && tau <= 1e30f)) {
         if (lead && tid == 0) a.ids[row] = -1, a.logp[row] = a.logq[row] = NAN;
         if (CLUSTER) meet();
