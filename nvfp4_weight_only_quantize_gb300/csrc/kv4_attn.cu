@@ -16,6 +16,19 @@
 //                   differ by key, multiply P instead (half as many products).  P
 //                   stays at most 2^7, so that P s stays finite (s <= 448).
 // m is raised only when a column's maximum outgrows it by 2^7.
+//
+// The work is one line of steps (kv4_attn.cuh) that 608 CTAs of four warps share, four
+// on an SM, so that long and short sequences fill the SMs alike.  Rows are tiled by
+// eight whatever their number: tiles of 16 in one warp took three times as long as
+// two of eight (213 registers, half the warps).
+// Bound by HBM in long caches (two sequences of 2 M tokens: 6.2 TB/s, 93 % of the copy
+// rate) and by its start, the join and uneven CTAs in shorter ones: some 4 us before
+// the first tile and 4 us after the last.  28 / 4 heads, D = 128: two sequences of
+// 131072 and 81007 tokens 31 us (122 MB); one sequence over 513 keys 7.4 us in a
+// graph; 64 of up to 4096 tokens, 40 / 8 heads, with prefixes of 512: 52 us.
+// Issue slots 57 % used, tensor pipe 19 %.  Keys in bf16 by bit fields took 703
+// instructions a tile instead of some 560, and a long cache 5.35 TB/s.
+// Rows of a segment beyond 16 go to kv4_attn_tc.cu where that is quicker.
 #include "kv4_attn.cuh"
 
 #include <float.h>

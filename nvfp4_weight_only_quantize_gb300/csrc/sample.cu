@@ -7,11 +7,13 @@
 //
 // Which token that is must not depend on rounding, on the number of CTAs or on
 // the order of sums: masses e^((x - max) / tau) are held as 64-bit integers (2^42
-// for the most probable token), whose sums are exact.  Two ways lead to them:
+// for the most probable token), whose sums are exact.  Ways that lead to them:
 //   fast   ex2 in FP32, summed over a chunk of 2 KB of the row and then turned to an
 //          integer; such sums are off by at most kEps of their value (below);
+//   good   the same with the exponent's rounding taken back, eight values at a time (kEps2);
 //   exact  the exponential in pairs of FP32 numbers, good to 2^-40.
-// A choice that kEps could change is made again with exact sums.
+// A choice that kEps could change is made again with good sums, and with exact ones
+// where kEps2 could.
 //
 // A row is swept by one CTA, or by a cluster of up to eight where there are few
 // rows.  The first sweep takes it from HBM: the maximum and the fast sum of each
@@ -25,6 +27,14 @@
 // sum: with top_p near 1 the fast part of that is small.  Where the sample misled,
 // or more tokens than the list holds are as good as equal, histograms of the keys
 // find the border.
+//
+// One row of 131072 bf16 (top-k and top-p) 20 us, cluster barriers and dependent steps;
+// 64 rows uncut 27 us, or 44 where a row needs the exact sums (its CTAs then work
+// alone); 1024 rows with top-p 0.95, half of whose mass is a bulk of tens of thousands
+// of alike tokens: 400 us, bound by issue (70 % of the slots; a row's first sweep is
+// 13 us of its some 60, the list 20, border and draw 15); 257 x 100003 FP32 with every
+// cut 113 us, the slowest rows' latency.  With histograms of every row's keys in
+// shared memory instead of the list: 500 us and 2700 us, atomics on few addresses.
 #include <float.h>
 #include <math.h>
 
