@@ -852,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
                 const bool binned = listed > kThreads;
                 const uint32_t spread = top_key - key_of(low);
                 const int shift = max(kUnit, 32 - __clz(spread) - kBinBits);
-                const auto bin_of = [&](uint64_t place) { return (top_key - ~(uint32_t)(place >> 32)) >> shift; };
+                const auto bin_of = [&](uint64_t place) { return min((top_key - ~(uint32_t)(place >> 32)) >> shift, kBins - 1u); };
                 if (binned) {
                     __syncthreads();
                     for (int b = tid; b < kBins; b += kThreads) s.hist[b] = 0;

@@ -200,6 +200,19 @@ def test_the_split_does_not_matter():
             assert torch.equal(again[0], ids) and torch.equal(again[1], lp) and torch.equal(again[2], lq)
 
 
+def test_lists_of_a_whole_row():
+    """Rows that are listed whole, from every alignment, with tokens of no mass among them and the maximum below zero."""
+    for dtype in (torch.bfloat16, torch.float32):
+        wide = (-1.9921875 - 0.3 * logits_of(3, 8200, torch.float32, 23).abs()).to(dtype)
+        wide[1, 100:7000] = -math.inf
+        wide[2] = wide[2] * 1e-3 - 7
+        u = torch.tensor([0.11, 0.73, 0.998], device="cuda")
+        for first in (0, 1, 3, 6):
+            for V in (600, 8000, 8185):
+                for cut in (dict(top_p=0.9999), dict(top_k=V - 1), dict(top_k=V // 2, top_p=0.99), dict(top_p=0.3, min_p=0.2)):
+                    check(wide[:, first:first + V], u, **cut)
+
+
 def test_strides_graph_and_stream():
     wide = logits_of(7, 3001, torch.bfloat16, 16)
     x, u = wide[:, 5:2998], torch.rand(7, generator=gen(17), device="cuda")
