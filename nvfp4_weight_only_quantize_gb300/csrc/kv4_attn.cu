@@ -26,8 +26,8 @@
 // the first tile and 4 us after the last.  28 / 4 heads, D = 128: two sequences of
 // 131072 and 81007 tokens 31 us (122 MB); one sequence over 513 keys 7.4 us in a
 // graph; 64 of up to 4096 tokens, 40 / 8 heads, with prefixes of 512: 52 us.
-// Issue slots 57 % used, tensor pipe 19 %.  Keys in bf16 by bit fields took 703
-// instructions a tile instead of some 560, and a long cache 5.35 TB/s.
+// Issue slots 57 % used, tensor pipe 19 %.  With the keys in bf16 by bit fields, three
+// CTAs an SM, a tile took 703 instructions and a long cache read at 5.35 TB/s.
 // Rows of a segment beyond 16 go to kv4_attn_tc.cu where that is quicker.
 #include "kv4_attn.cuh"
 
