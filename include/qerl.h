@@ -575,8 +575,8 @@ qerl_status qerl_kv4_read(const qerl_kv4_cache *cache, int64_t L, const int32_t 
  *   may overlap need a workspace each.
  * Keys and values are multiplied as fp16, which holds them exactly; q as fp16 after a
  * power of two per row: elements below 2^-17 of the row's largest are off by at most
- * 2^-25 of it.  Probabilities are rounded to fp16, for few rows their product with a
- * value's scale again; sums are FP32.  Results are the same on every run.
+ * 2^-25 of it.  Probabilities are rounded to fp16, those below 2^-22 of the row's largest
+ * by up to 2^-33 of that; sums are FP32.  Results are the same on every run.
  */
 typedef struct {
     int64_t B, Lq, Hq;

@@ -11,11 +11,13 @@
 //                   a power of two per row that brings its largest element to [1, 2):
 //                   elements down to 2^-17 of that stay exact, smaller ones are off by
 //                   2^-25 of it, as a sum of FP32 products is anyway;
-//   P = 2^(S c - m) per column, rounded to fp16 and turned (movmatrix);
-//   O^T += V^T (P s)  V's codes converted to fp16 as they are; their scales s, which
-//                   differ by key, multiply P instead (half as many products).  P
-//                   stays at most 2^7, so that P s stays finite (s <= 448).
-// m is raised only when a column's maximum outgrows it by 2^7.
+//   P = 2^(S c - m) per column, rounded to fp16 and turned (movmatrix): between 2^8 and
+//                   2^15 for the largest, so that keys of up to 15 nats less keep all of
+//                   fp16's digits;
+//   O^T += V^T P    V as fp16, code times scale, exact.  (Scales that multiply P instead,
+//                   half as many products, leave fp16's smallest numbers where values are
+//                   small against the cache's factor: 11 % off under a key 14 nats above.)
+// m is raised only when a column's maximum outgrows it by 2^15.
 //
 // The work is one line of steps (kv4_attn.cuh) that 608 CTAs of four warps share, four
 // on an SM, so that long and short sequences fill the SMs alike.  Rows are tiled by
@@ -44,7 +46,7 @@ using namespace ptx;
 
 constexpr int kWarps = 4, kStages = 2, kPerSm = 4;
 constexpr int kStart = 2;  // empty steps before a unit's
-constexpr float kHead = 4.0f, kRoom = 7.0f;  // m is set kHead below a maximum, and raised above kRoom
+constexpr float kHead = 8.0f, kRoom = 15.0f;  // m is set kHead below a maximum, and raised above kRoom
 constexpr uint64_t kLimitNs = 2000000000ull;
 
 template <int D>
@@ -356,15 +358,15 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) rows_kernel(const __grid_
                     const uint4 w = ld_shared_v4(tb + M::VC + (j * 32 + lane) * 16), sc = ld_shared_v4(tb + M::VS + (q * MT + 2 * j) * 8);
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        uint32_t v0[4], v1[4], s0[2], s1[2];
+                        uint32_t v0[4], v1[4], f[4];  // a pair of keys each
                         codes_f16(t ? w.z : w.x, v0);
                         codes_f16(t ? w.w : w.y, v1);
-                        scales_f16(t ? sc.z : sc.x, s0[0], s1[0]);
-                        scales_f16(t ? sc.w : sc.y, s0[1], s1[1]);
+                        scales_f16(t ? sc.z : sc.x, f[0], f[1]);
+                        scales_f16(t ? sc.w : sc.y, f[2], f[3]);
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            mma_f16(o[2 * j + t], v0[2 * c], v1[2 * c], v0[2 * c + 1], v1[2 * c + 1], f16x2_mul(p[c][0], s0[c]),
-                                    f16x2_mul(p[c][1], s1[c]));
+                        for (int i = 0; i < 4; ++i) v0[i] = f16x2_mul(v0[i], f[i]), v1[i] = f16x2_mul(v1[i], f[i]);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) mma_f16(o[2 * j + t], v0[2 * c], v1[2 * c], v0[2 * c + 1], v1[2 * c + 1], p[c][0], p[c][1]);
                     }
                 }
                 __syncwarp();  // the place is free for the copy that the next turn issues

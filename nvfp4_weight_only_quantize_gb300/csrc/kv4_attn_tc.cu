@@ -10,7 +10,7 @@
 //         before the last one's are written;
 //   V     K-major, its transpose as the cache holds it: eight tokens of a dim are a
 //         16-byte piece of a row of the swizzled tile;
-//   P     fp16, at most 2^8.
+//   P     fp16, between 2^8 and 2^15 for a row's largest, so that keys of up to 15 nats less keep all of fp16's digits.
 // 129 tokens of eight sequences, 16 heads, over a prefix of 4001 keys and their own: 72 us
 // with the join (the tiles of eight rows: 405 us); 28 heads of 64 sequences over 16384
 // keys, the own tokens beside it, 50 us (126 us).  Tensor pipe 22 % over the run, issue
@@ -39,6 +39,7 @@ using attn::Units;
 
 constexpr int kThreads = 448, kProducer = 8, kMmaWarp = 12;  // the MMA warps are two
 constexpr int kStages = 4;  // tiles of 64 keys: K and V each
+constexpr float kHead = 8.0f, kRoom = 15.0f;  // m is set kHead below a maximum, and raised above kRoom
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r)
 {
@@ -474,8 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
                 }
                 top = fmaxf(top, top1);
                 top = top == attn::kNone ? attn::kNone : top * scale;
-                const bool raise = top > m + 8.0f;
-                const float to = raise ? top : m, f = raise ? attn::ex2(m - top) : 1.0f;
+                const bool raise = top > m + kRoom;
+                const float to = raise ? top - kHead : m, f = raise ? attn::ex2(m - to) : 1.0f;
                 if (j > 0 && __any_sync(0xFFFFFFFFu, raise)) {
                     if (!(ok = wait(&b_o[h], sn - 1))) break;  // O is still
                     tc_fence_after();
