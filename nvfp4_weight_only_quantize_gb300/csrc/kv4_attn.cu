@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) rows_kernel(const __grid_
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 limit[k] = pre ? len : len - a.Lq + 1 + row_of(a, pre, seg, hk, tile * R + 2 * q + k).l;
-                scale[k] = s.scale_log2 * pow2f(__shfl_sync(0xFFFFFFFFu, e, (2 * q + k) * 4));
+                scale[k] = row_scale(s.scale_log2, __shfl_sync(0xFFFFFFFFu, e, (2 * q + k) * 4));
             }
             const int all_see = pre ? len : len - a.Lq + 1;  // keys that every row sees
             float o[MT][4], m[2], l[2];

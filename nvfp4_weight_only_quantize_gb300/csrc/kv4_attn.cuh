@@ -76,6 +76,14 @@ __device__ __forceinline__ void scales_f16(uint32_t w, uint32_t &lo, uint32_t &h
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w));
 }
 
+// From the products' sum to log2 units where the row was divided by 2^e.  Not 0, which a masked score of -inf would make NaN (a
+// row of zeros has the smallest e), and not inf, which a score of 0 would.  Sums are below 2^20: with the smallest scale
+// all scores are 0 within 2^-106.
+__device__ __forceinline__ float row_scale(float scale_log2, int e)
+{
+    return fminf(fmaxf(scale_log2 * pow2f(e), 1.17549435e-38f), 3.402823466e+38f);
+}
+
 // The tcgen05 kernel's launch over the sides that `a` gives it.
 cudaError_t many_rows(const attn::Args &a, const Side &pre, const Side &suf, int64_t D, cudaStream_t s, bool chain);
 

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
     __shared__ uint64_t b_q[2], b_kfull[kStages], b_kempty[kStages], b_vfull[kStages], b_vempty[kStages], b_s[2][2], b_p[2][2], b_o[2], b_done[2], b_end;
     __shared__ uint32_t s_tmem;
     __shared__ int s_stop;
-    __shared__ float s_up[2][128];  // what a row of Q was divided by
+    __shared__ int s_up[2][128];  // the power of two that a row of Q was divided by
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (tid == 0) {
         for (int k = 0; k < kStages; ++k) {
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
                     const float down = pow2f(-e);
                     const auto pair = [&](uint32_t x) { return f16x2(bf16lo(x) * down, bf16hi(x) * down); };
                     st_shared_v4(qs + (c / 8) * 16384 + r * 128 + (((c % 8) ^ (r & 7)) << 4), pair(v[i].x), pair(v[i].y), pair(v[i].z), pair(v[i].w));
-                    if (c == 0) s_up[h][r] = pow2f(e);
+                    if (c == 0) s_up[h][r] = e;
                 }
                 __syncwarp();
             }
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
             mbar_arrive(&b_q[h]);
 
             const int limit = s.pre ? s.len : s.len - a.Lq + 1 + l;
-            const float scale = (s.pre ? pre_scale : suf_scale) * s_up[h][t];
+            const float scale = row_scale(s.pre ? pre_scale : suf_scale, s_up[h][t]);
             const float2 scale2 = make_float2(scale, scale);
             float m = attn::kNone, sum = 0.0f;
             for (int j = 0; j < n; ++j, ++sn) {
