@@ -477,6 +477,9 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) join_kernel(const __grid
     const Parts pp = parts_of(a, tc, true, g, hk, ((b - g * a.G) * a.Lq + l) * a.gs + hi, row, tp, D);
     const Parts ps = parts_of(a, tc, false, b, hk, l * a.gs + hi, row, ts, D);
     const int n = pp.n + ps.n;
+    // Sums of values without the factor are below 2^57 (2^30 keys); so that they stay finite with one of up to 2^100, 2^40 comes last.
+    const bool large = fmaxf(pp.v_scale, ps.v_scale) >= 1.0f;
+    const float down = large ? 0x1p-40f : 1.0f, up = large ? 0x1p40f : 1.0f, p_scale = pp.v_scale * down, s_scale = ps.v_scale * down;
     float M = kNone, L = 0.0f, acc[E] = {};
     for (int k0 = share; k0 < n; k0 += NB * W) {
         float2 ml[NB];
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) join_kernel(const __grid
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             const bool none = ml[j].x == kNone && ml[j].y == 0.0f;
-            const float w = none ? 0.0f : ex2(ml[j].x - M), wv = w * (k0 + j * W < pp.n ? pp.v_scale : ps.v_scale);
+            const float w = none ? 0.0f : ex2(ml[j].x - M), wv = w * (k0 + j * W < pp.n ? p_scale : s_scale);
             L = fmaf(w, ml[j].y, L);
 #pragma unroll
             for (int e = 0; e < E; ++e) acc[e] = fmaf(wv, none ? 0.0f : v[j][e], acc[e]);
@@ -540,7 +543,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) join_kernel(const __grid
     uint32_t *out = reinterpret_cast<uint32_t *>(a.out + b * a.o_b + l * a.o_l + h * a.o_h + lane * E);
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
-        const __nv_bfloat162 t = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+        const __nv_bfloat162 t = __floats2bfloat162_rn(acc[e] * inv * up, acc[e + 1] * inv * up);
         out[e / 2] = *reinterpret_cast<const uint32_t *>(&t);
     }
     if (lane == 0 && a.lse) a.lse[row] = L == 0.0f ? -INFINITY : (float)((double)M * 0.6931471805599453 + (double)logf(L));

@@ -43,3 +43,29 @@ def test_queries_of_zeros(D, k_scale, Lq, S, lens, kernel):
     before = q.kernel_launch_count(kernel)
     check_means(cache, cache.read(i32([S] * B), S)[1].double(), 16, Lq, lens)
     assert q.kernel_launch_count(kernel) == before + 1
+
+
+@pytest.mark.parametrize("S,Lq,lens", [(30001, 1, [30001]), (30001, 33, [30000])])
+def test_values_near_the_top_of_the_largest_factor(S, Lq, lens):
+    g = gen(2)
+    cache, unit = q.Kv4Cache(1, S, 1, 64, 1.0, 1e30), q.Kv4Cache(1, S, 1, 64)
+    k, v = rnd(g, 1, S, 1, 64), (torch.rand(1, S, 1, 64, generator=g, device="cuda") * 1000 + 1500).to(torch.bfloat16)
+    cache.append(k, (v.float() * 1e30).to(torch.bfloat16), i32([S]))
+    # the codes and scales alone: the same bytes read with a factor of one
+    unit.data.copy_(cache.data)
+    held = unit.read(i32([S]), S)[1].double() * float(torch.tensor(1e30, dtype=torch.float32))
+    check_means(cache, held, 8, Lq, lens)
+
+
+def test_prefix_and_own_tokens_with_factors_far_apart():
+    """Values of a factor of 1e-30 beside values of 1e30: the small ones count in the weights alone."""
+    g = gen(3)
+    pre, own = q.Kv4Cache(1, 64, 1, 64, 1.0, 1e-30), q.Kv4Cache(2, 64, 1, 64, 1.0, 1e30)
+    k, v = rnd(g, 1, 64, 1, 64), rnd(g, 1, 64, 1, 64)
+    pre.append(k, (v.float() * 1e-30).to(torch.bfloat16), i32([64]))
+    k, v = rnd(g, 2, 64, 1, 64), (torch.rand(2, 64, 1, 64, generator=g, device="cuda") * 1000 + 1500).to(torch.bfloat16)
+    own.append(k, (v.float() * 1e30).to(torch.bfloat16), i32([64, 64]))
+    held = own.read(i32([64, 64]), 64)[1].double()
+    out = q.Kv4Attention(own, 4, prefix=pre).run(torch.zeros(2, 1, 4, 64, dtype=torch.bfloat16, device="cuda"), i32([64, 64]))
+    ref = held.sum(1) / 128  # [2, 1, 64]; read's rounding of the values: 2^-8 of each, of one sign all
+    assert bool(((out[:, 0].double() - ref).abs() <= 1.02 * (2 * 2.0 ** -8 + SUMS) * ref).all())
