@@ -202,7 +202,7 @@ qerl_status tokens(const qerl_kv4_cache *c, int64_t L, const void *k, const int6
     t = Tokens{static_cast<const __nv_bfloat16 *>(k), static_cast<const __nv_bfloat16 *>(v), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
                lens, counts, (int)L};
     tiles = (L + kTok - 2) / kTok + 1;  // L tokens from any place in a tile on
-    if (tiles * c->n * c->Hkv > 0x7FFFFFFF) return QERL_ERR_SHAPE;
+    if (tiles * c->n > 0x7FFFFFFF / c->Hkv) return QERL_ERR_SHAPE;  // 2^55 at most, times Hkv it may pass 64 bits
     return QERL_OK;
 }
 
