@@ -688,12 +688,15 @@ class Kv4Attention:
         one = suffix if suffix is not None else prefix
         B = suffix.n if suffix is not None else batch
         self._caches = (prefix, suffix)
+        device = one.data.device  # of q and the rest too, which run() checks
+        assert prefix is None or prefix.data.device == device
+        assert ws is None or ws.device == device
         self._pref, self._suf = (None if c is None else c._ref for c in self._caches)
         self._d = _Kv4AttnDims(B, q_len, q_heads)
         nbytes = lib().qerl_kv4_attention_ws_bytes(C.byref(self._d), self._pref, self._suf)
         if nbytes == 0:
             raise QerlError(2, "qerl_kv4_attention_ws_bytes")
-        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=one.data.device) if ws is None else ws
+        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if ws is None else ws
         self._ws = (self.ws.data_ptr(), self.ws.numel())
         self._launched_on = {_stream()}
         self._q_shape = torch.Size((B, q_len, q_heads, one.D))

@@ -1,6 +1,10 @@
-"""What the 4-bit cache's calls refuse on the host (CPU only): sizes whose products pass 64 bits."""
-import pytest
+"""What the 4-bit cache's calls refuse on the host (CPU only): sizes whose products pass 64 bits, caches of different devices."""
+import types
 
+import pytest
+import torch
+
+import nvfp4_weight_only_quantize_gb300 as q
 from test_kv4_abi import L, cache, tokens  # noqa: F401
 
 
@@ -9,3 +13,23 @@ from test_kv4_abi import L, cache, tokens  # noqa: F401
                                        (1 << 30, 65535, 1 << 30), (1 << 26, 32768, 1)])
 def test_grids_beyond_any_launch(L, call, n, Hkv, new):  # noqa: F811
     assert tokens(L, cache(n=n, Hkv=Hkv, T=1 << 30), n=new, call=call) == 2
+
+
+def test_attention_takes_caches_and_workspace_of_one_device(monkeypatch):
+    """Caches whose tensors say that they lie on two made-up devices."""
+    q.build()
+    monkeypatch.setattr(q, "_stream", lambda stream=None: 0)
+    prefix, suffix = q.Kv4Cache(2, 40, 2, 64, device="cpu"), q.Kv4Cache(4, 40, 2, 64, device="cpu")
+    q.Kv4Attention(suffix, 4, prefix=prefix)
+    ws = torch.empty(1 << 20, dtype=torch.uint8)
+    q.Kv4Attention(suffix, 4, prefix=prefix, ws=ws)
+    elsewhere = types.SimpleNamespace(device=torch.device("cuda", 1), numel=ws.numel, data_ptr=ws.data_ptr)
+    with pytest.raises(AssertionError):
+        q.Kv4Attention(suffix, 4, prefix=prefix, ws=elsewhere)
+    prefix.data = types.SimpleNamespace(device=torch.device("cuda", 1))
+    with pytest.raises(AssertionError):
+        q.Kv4Attention(suffix, 4, prefix=prefix)
+    with pytest.raises(AssertionError):
+        q.Kv4Attention(suffix, 4, prefix=prefix, ws=ws)
+    with pytest.raises(AssertionError):
+        q.Kv4Attention(None, 4, prefix=prefix, batch=4, ws=ws)
