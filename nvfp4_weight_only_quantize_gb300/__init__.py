@@ -816,7 +816,7 @@ def qerl_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, ids=N
             assert v.dtype is dt and v.shape == vec and v.is_contiguous()
             setattr(o, name + "s", v.data_ptr())
         else:
-            setattr(o, name, v)
+            setattr(o, name, v if dt is f32 else max(-1, min(v, 0x7FFFFFFF)))  # 32 bits: more would be cut off without a word
     _here(logits, u, ids, logp, logq, *(v for v in (temperature, top_k, top_p, min_p) if isinstance(v, torch.Tensor)))
     _check(lib().qerl_sample(logits.data_ptr(), _DTYPES[logits.dtype], T, V, ld if T > 1 else V, u.data_ptr(), C.byref(o), ids.data_ptr(),
                              logp.data_ptr(), logq.data_ptr(), _stream(stream)), "qerl_sample")
