@@ -615,9 +615,13 @@ qerl_status qerl_token_logp(const void *logits, int dtype, int64_t T, int64_t V,
  *   Each setting holds for all rows, or is a device array [T] where its pointer is
  *   not NULL: there top_k < 0 counts as 0, top_p <= 0 keeps one token, top_p that is
  *   not below 1 all, min_p is taken into [0, 1] (NaN as 0).
- * The token is that of the definition: sums are exact integers, and it does not
- * depend on how the work is split.  A row with NaN or +inf, or with a temperature
- * outside (1e-30, 1e30], gets id -1 and NaN; one of nothing but -inf id -1 and -inf.
+ * p is counted in units of 2^-42 of the row's largest, off by at most one unit and 2^-40
+ * of itself (below half a unit it is nothing), and the sums of those are exact; single
+ * precision decides only where its error bound leaves no choice.  So the token is that
+ * of the definition unless top_p or u puts a border within V 2^-42 of the largest p and
+ * 2^-40 of the sum of where the next token begins; even then it does not depend on how
+ * the work is split.  A row with NaN or +inf, or with a temperature outside (1e-30, 1e30],
+ * gets id -1 and NaN; one of nothing but -inf id -1 and -inf.
  */
 typedef struct {
     float temperature, top_p, min_p;

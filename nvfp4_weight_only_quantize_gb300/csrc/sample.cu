@@ -9,11 +9,12 @@
 // the order of sums: masses e^((x - max) / tau) are held as 64-bit integers (2^42
 // for the most probable token), whose sums are exact.  Ways that lead to them:
 //   fast   ex2 in FP32, summed over a chunk of 2 KB of the row and then turned to an
-//          integer; such sums are off by at most kEps of their value (below);
-//   good   the same with the exponent's rounding taken back, eight values at a time (kEps2);
-//   exact  the exponential in pairs of FP32 numbers, good to 2^-40.
-// A choice that kEps could change is made again with good sums, and with exact ones
-// where kEps2 could.
+//          integer;
+//   good   the same with the exponent's rounding taken back, summed as integers;
+//   exact  the exponential in pairs of FP32 numbers, good to 2^-40 and one unit.
+// The first two are off by at most what is said below, whatever the row holds (equal
+// logits are all off the same way).  A choice that this could change is made again with
+// good sums, and then with exact ones.
 //
 // A row is swept by one CTA, or by a cluster of up to eight where there are few
 // rows.  The first sweep takes it from HBM: the maximum and the fast sum of each
@@ -51,19 +52,16 @@ constexpr int64_t kMaxV = 1 << 20;  // 2^42 times that fits 62 bits
 constexpr int kMostChunks = kMaxV * 4 / (kChunkVecs * 16) + 2;  // a row may start inside a vector; an even number
 constexpr int kScale = 42;
 constexpr int kList = 8192, kSamples = 8192;
-// What a fast sum is taken to be off by, relative to it.  ex2.approx is off by -5e-8 on average over an octave (measured, the
-// same in all of them) and 1.4e-7 at most; the exponent y by up to 2 * 2^-24 |y| and the sum by some 20 roundings, neither of
-// one sign.  Weighted by the masses the mean of |y| is at most log2 N where N tokens count, so that six deviations of those
-// two, which shrink with the root of N, stay below 3e-7 and 2.5e-7.
-// A draw compares a sum with u times the total, which moves by at most kEps 2 u (1 - u) of the total: total >> kOff.
-constexpr double kEps = 6e-7;
-constexpr int kOff = 21;
-// Where that leaves a choice open, sums of the second kind: the exponent's rounding taken back, eight values to an integer.
-// What is left is ex2.approx's error less its average, 5e-8 deviation a value, and three roundings of a sum: below 4e-8 even
-// where a few tokens make the sum, whose borders are far apart.
-constexpr double kEps2 = 4e-8;
-constexpr int kOff2 = 25;
-constexpr double kBias = 5.08e-8;
+// What a fast sum may be off by, relative to it.  The exponent y has two roundings of 2^-24 |y| each, 2^-23 ln 2 a value and
+// octave.  Weighted by the masses the mean of |y| over n tokens is at most log2 n less the logarithm of their sum (the entropy of
+// their shares is at most log2 n).  ex2.approx is off by -1.44e-7 to 1.05e-7 (measured, every float down to -64), and the
+// sum of a chunk by seven roundings, as the trees of additions below have them.  These are bounds, not deviations: a row of few
+// distinct logits has errors of one sign.
+constexpr float kOctave = 8.3e-8f, kFast = 5.7e-7f;
+constexpr double kMost = 2.6e-6;  // both over 2^20 tokens
+// Of a good sum, with kBias added, ex2.approx's error is what is left; values and the exponent's rounding are summed apart.
+constexpr float kGood = 1.3e-7f;
+constexpr double kBias = 2e-8;
 
 struct Args {
     const void *x;
@@ -154,14 +152,24 @@ __device__ __forceinline__ uint64_t mass_in_line(const Exp &e, float x)
 // The same as a call, where it is not in a sweep.
 __device__ __noinline__ uint64_t mass_call(float x, float top, float c, float c_lo);  // below: the table lies in shared memory
 __device__ __forceinline__ uint64_t mass(const Exp &e, float x) { return mass_call(x, e.top, e.c, e.c_lo); }
-// The exponent's rounding taken back: in the units of fast().
-__device__ __forceinline__ float good(const Exp &e, float x)
+// The same as fast() of the difference to the maximum, and what the exponent's rounding took from it.
+__device__ __forceinline__ float2 good(const Exp &e, float x, bool in)
 {
     const float d0 = x - e.top;
-    const bool some = d0 > e.low;
+    const bool some = in && d0 > e.low;
     const float d = some ? d0 : 0.0f, b = d - x, rest = some ? (x - (d - b)) - (e.top + b) : 0.0f;
-    const float y = d * e.c, y_lo = fmaf(d, e.c, -y) + fmaf(d, e.c_lo, rest * e.c), v = ex2(y);
-    return some ? fmaf(v * 0x1.62e430p-1f, y_lo, v) : 0.0f;
+    const float y = d * e.c, y_lo = fmaf(d, e.c, -y) + fmaf(d, e.c_lo, rest * e.c), v = some ? ex2(y) : 0.0f;
+    return make_float2(v, v * 0x1.62e430p-1f * y_lo);
+}
+// Sums as trees: log2 E roundings.
+template <int E>
+__device__ __forceinline__ float tree(float (&g)[E])
+{
+#pragma unroll
+    for (int o = E / 2; o; o /= 2)
+#pragma unroll
+        for (int e = 0; e < o; ++e) g[e] += g[e + o];
+    return g[0];
 }
 
 // A row as the aligned 16-byte vectors that hold it; elements outside it read as -inf.
@@ -249,14 +257,17 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v)
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
-__device__ __forceinline__ float warp_sum(float v)
-{
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
-}
 __device__ __noinline__ uint64_t mass_call(float x, float top, float c, float c_lo)
 {
     return mass_in_line(Exp{top, c, c_lo, 0.0f, reinterpret_cast<Shared *>(smem)->roots}, x);
+}
+
+// The sum over a warp of numbers up to 32, in units of 2^-42, each rounded to one: in steps of 2^-21 and of a unit.
+__device__ __forceinline__ uint64_t warp_fixed(float v)
+{
+    const uint32_t coarse = __float2uint_rn(v * 0x1p21f);
+    const int fine = __float2int_rn(fmaf((float)coarse, -0x1p-21f, v) * 0x1p42f);
+    return ((uint64_t)__reduce_add_sync(0xFFFFFFFFu, coarse) << 21) + (int64_t)__reduce_add_sync(0xFFFFFFFFu, fine);
 }
 
 struct Scan {
@@ -434,14 +445,19 @@ __device__ __noinline__ void sweep(const char *x, int off, int n, int chunks, in
             }
             return z;
         }
-        float g[E];
+        // values as integers of 2^-21, what that leaves as integers of 2^-42, both by adding 3 * 2^22; the exponents' part beside them
+        const float magic = 12582912.0f;
+        uint32_t coarse = 0u - E * 0x4B400000u, fine = coarse;
+        float rest[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) g[e] = in >> e & 1 ? good(ex, f[e]) : 0.0f;
-#pragma unroll
-        for (int o = E / 2; o; o /= 2)
-#pragma unroll
-            for (int e = 0; e < o; ++e) g[e] += g[e + o];
-        return fixed(g[0]);
+        for (int e = 0; e < E; ++e) {
+            const float2 v = good(ex, f[e], in >> e & 1);
+            const float c = fmaf(v.x, 0x1p21f, magic);
+            coarse += __float_as_uint(c);
+            fine += __float_as_uint(fmaf(fmaf(c - magic, -0x1p-21f, v.x), 0x1p42f, magic));
+            rest[e] = v.y;
+        }
+        return ((uint64_t)coarse << 21) + (int64_t)(int)fine + (int64_t)__float2int_rn(tree(rest) * 0x1p42f);
     };
     const auto sum_again = [&](uint32_t hi, uint32_t lo, bool exact) {  // masses of keys in [lo, hi], exact or good
         uint64_t z = 0;
@@ -470,7 +486,7 @@ __device__ __noinline__ void sweep(const char *x, int off, int n, int chunks, in
             uint4 v[kVec];
 #pragma unroll
             for (int j = 0; j < kVec; ++j) v[j] = r.load(ch * kChunkVecs + j * 32 + lane);
-            float above = 0.0f, below = 0.0f;
+            float above[E] = {}, below[E] = {};
             uint32_t in = 0;
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
@@ -481,16 +497,16 @@ __device__ __noinline__ void sweep(const char *x, int off, int n, int chunks, in
                     const bool is_low = f[e] < low, is_high = f[e] > high;
                     if (sums) {
                         const float m = fast(ex, f[e] - ex.top);
-                        if (is_low) below += m;
-                        if (is_high) above += m;
+                        if (is_low) below[e] += m;
+                        if (is_high) above[e] += m;
                     }
                     if (!is_low && !is_high) in |= 1u << (j * E + e);
                 }
             }
             if (sums) {
-                above = warp_sum(above);
-                zs += fixed(below);
-                if (lane == 0) L::put(&s_chunk[ch], fixed(above));
+                const uint64_t sum = warp_fixed(tree(above));
+                zs += fixed(tree(below));
+                if (lane == 0) L::put(&s_chunk[ch], sum);
             }
             if (__any_sync(0xFFFFFFFFu, in)) {
                 const uint32_t n = __popc(in);
@@ -517,10 +533,11 @@ __device__ __noinline__ void sweep(const char *x, int off, int n, int chunks, in
     // By chunk: what is above the border, fast, and how many are at it; or what is kept, good or exact, `upto` the last index at the border.
     const auto kept_fast = [&](float border) {
         for (int ch = rank * kWarps + warp; ch < chunks; ch += ranks * kWarps) {
-            float above = 0.0f;
+            uint64_t sum = 0;
             uint32_t ties = 0;
             if (s_chunk_m[ch] >= border) {
                 uint4 v[kVec];
+                float above[E] = {};
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) v[j] = r.load(ch * kChunkVecs + j * 32 + lane);
 #pragma unroll
@@ -529,15 +546,15 @@ __device__ __noinline__ void sweep(const char *x, int off, int n, int chunks, in
                     R::unpack(v[j], f);
 #pragma unroll
                     for (int e = 0; e < E; ++e) {
-                        if (f[e] > border) above += fast(ex, f[e] - ex.top);
+                        if (f[e] > border) above[e] += fast(ex, f[e] - ex.top);
                         if (f[e] == border) ++ties;  // nothing outside the row unless the border is -inf, where no mass is at it
                     }
                 }
-                above = warp_sum(above);
+                sum = warp_fixed(tree(above));
                 ties = __reduce_add_sync(0xFFFFFFFFu, ties);
             }
             if (lane == 0) {
-                L::put(&s_chunk[ch], fixed(above));
+                L::put(&s_chunk[ch], sum);
                 L::put(&s_ties[ch], ties);
             }
         }
@@ -644,15 +661,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
             if (sampled && j % 2 == 0 && ch % every == 0) L::put(&s.sample[(ch / every) * 64 + j * 16 + lane], f[E / 2]);
         }
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        float z[2] = {0.0f, 0.0f};
+        float z[E] = {};
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
             float f[E];
             R::unpack(v[j], f);
 #pragma unroll
-            for (int e = 0; e < E; ++e) z[e % 2] += fast(ex, f[e] - m);  // NaN and +inf leave NaN
+            for (int e = 0; e < E; ++e) z[e] += fast(ex, f[e] - m);  // NaN and +inf leave NaN
         }
-        const float sum = warp_sum(z[0] + z[1]);
+        const float own = tree(z), sum = __any_sync(0xFFFFFFFFu, isnan(own)) ? NAN : (float)warp_fixed(own) * 0x1p-42f;
         if (lane == 0) {
             if (CLUSTER) s_chunk_m[ch] = m;
             L::put(&s_chunk_m[ch], m);
@@ -728,13 +745,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
         if (BF16) least = (least & 0x80000000u ? least + 0xFFFFu : least) & 0xFFFF0000u;
     }
 
+    // What a fast sum of the row's may be off by: |y| counts from the row's maximum, in the first sweep from the chunk's.
+    const auto off_fast = [&](uint64_t z) -> float {
+        const float octaves = __log2f((float)r.n) + (float)kScale - __log2f((float)z), most = sampled || cut_m ? 64.0f : __log2f((float)kChunk);
+        return z ? (float)z * fmaf(kOctave, fminf(fmaxf(octaves, 0.0f), most), kFast) : 0.0f;
+    };
+    const uint64_t units = (uint64_t)chunks * kChunk + 1024;  // and every sum for roundings to units, less than one a token
+
     // ------------------------------------------------------------ the border of what is kept, by a list
     uint64_t last = ~uint64_t(0);  // the last place that is kept
     bool found = !sampled && !cut_m, fast = found;  // `fast`: the chunks' masses are
     const auto wanted = [&](uint64_t z) { return (uint64_t)ceil((double)top_p * (double)z); };
     if (sampled) {
-        // Thresholds from a histogram in 32nds of an octave below the maximum; the last bin has no mass.  For the first k tokens: of the chunks' maxima, k of
-        // which are k tokens, or, where there are too few chunks, of the sample.  For top_p: of the sample, by what it puts below.
+        // Thresholds from a histogram in 32nds of an octave below the maximum; the last bin has no mass.  For the first k tokens: of
+        // the chunks' maxima, k of which are k tokens, or, where there are too few chunks, of the sample.  For top_p: of the
+        // sample, by what it puts below.
         const bool by_max = cut_k && 2 * (int64_t)k <= chunks;
         const int n_sample = by_max ? chunks : (chunks + every - 1) / every * 64;
         const float step = 32.0f * ex.c, W = by_max ? 1.0f : (float)(kChunk * every) / 64.0f;
@@ -951,19 +976,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
                         sum(above, 0xFFFFFFFFu, key_of(high) + (1u << kUnit));
                         Z = above + held + below;
                     };
-                    const auto choose = [&](double eps) -> bool {
+                    const auto choose = [&](bool good) -> bool {
                         const double in_list = (double)(held + below), leaves = (1.0 - (double)top_p) * (double)(above + held + below);
-                        const double off = ((1.0 - (double)top_p) * (double)(above + below) + (double)below) * eps + 1024.0;
+                        const double off = (double)((1.0f - top_p) * (good ? kGood * (float)above : off_fast(above)) +
+                                                    top_p * (good ? kGood * (float)below : off_fast(below))) + (double)units;
                         if (!(in_list - leaves > off && in_list - leaves + off <= (double)held)) return false;
                         return pick(true, (uint64_t)ceil(in_list - leaves - off), (uint64_t)ceil(in_list - leaves + off), border, other, upto);
                     };
                     if ((above | below) == 0) {
                         kept = pick(true, wanted(held), wanted(held), border, other, upto);
                     } else {
-                        kept = choose(kEps);
+                        kept = choose(false);
                         if (kept && border != other) {
                             again(false);
-                            kept = choose(kEps2);
+                            kept = choose(true);
                         }
                         if (kept && border != other) {  // by what is reached
                             again(true);
@@ -1064,7 +1090,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
             uint64_t sum = 0, all;
             for (int i = tid; i < chunks; i += kThreads) sum += s_chunk[i] + s_ties[i] * mass(ex, value_of(least));
             block_scan(sum, all);
-            by_least = (double)all * (1.0 + kEps) < (double)top_p * (double)Z * (1.0 - kEps);
+            by_least = (double)all * (1.0 + kMost) < (double)top_p * (double)Z * (1.0 - kMost);
         }
         if (cut_k && !by_least) find(false, (uint64_t)k, 0);
         if (cut_p && !by_least) {
@@ -1117,7 +1143,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
     }
 
     // ------------------------------------------------------------ the token
-    const uint32_t u_bits = __float_as_uint(fminf(fmaxf(a.u[row], 0.0f), 0.99999994f));  // NaN as 0
+    const float u = fminf(fmaxf(a.u[row], 0.0f), 0.99999994f);  // NaN as 0
+    const uint32_t u_bits = __float_as_uint(u);
     const uint64_t u_m = u_bits >> 23 ? (u_bits & 0x7FFFFFu) | 0x800000u : 0;  // below 2^-126 as 0
     const int u_e = 150 - (int)(u_bits >> 23);  // 24 or more
     const uint32_t last_key = ~(uint32_t)(last >> 32), last_index = (uint32_t)last;
@@ -1153,8 +1180,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
             own += m[j];
         }
         uint64_t cum = before + block_scan(own, all) - own;
-        // how far the fast sums before this chunk and the target may be off
-        const uint64_t off = level == 0 ? (total >> kOff) + 1024 : level == 1 ? (total >> kOff2) + 1024 : 0;
+        // how far the sum before this chunk less the target, u times it and the sum from here on, may be off
+        const auto off_of = [&](uint64_t z) -> float { return level ? kGood * (float)z : off_fast(z); };
+        const uint64_t off = level < 2 ? (uint64_t)((1.0f - u) * off_of(before) + u * off_of(total - before)) + units : 0;
 #pragma unroll
         for (int j = 0; j < per_thread; ++j) {
             if (m[j] && (cum == 0 || cum + off <= target) && target + off < cum + m[j]) {
