@@ -636,7 +636,8 @@ class Kv4Cache:
         self.data = torch.zeros(shape, dtype=torch.uint8, device=device) if data is None else data
         assert self.data.shape == shape and self.data.dtype == torch.uint8 and self.data.stride(3) == 1
         self.n, self.T, self.Hkv, self.D = n, T, Hkv, D
-        self._rows, self._lens, self._strides = (n, Hkv, D), torch.Size((n,)), None
+        self._rows, self._lens = (n, Hkv, D), torch.Size((n,))
+        self._last = (None, None, None)  # the last tokens' strides, and as the library takes them; exchanged whole, for calls by several threads
         self._c = _Kv4Cache(self.data.data_ptr(), n, T, Hkv, D, (C.c_int64 * 3)(*self.data.stride()[:3]), k_scale, v_scale)
         self._ref = C.byref(self._c)
         self._launched_on = {_stream()} if self.data.is_cuda else set()
@@ -645,12 +646,13 @@ class Kv4Cache:
         shape = k.shape
         assert k.dtype == v.dtype == torch.bfloat16 and shape == v.shape and (shape[0], shape[2], shape[3]) == self._rows
         assert lens.dtype == torch.int32 and lens.shape == self._lens and lens.is_contiguous()
-        strides = (k.stride(), v.stride())
-        if strides != self._strides:
+        strides, last = (k.stride(), v.stride()), self._last
+        if strides != last[0]:
             assert (strides[0][3] == strides[1][3] == 1) or k.numel() == 0
-            self._st = [(C.c_int64 * 3)(*t[:3]) for t in strides]
-            self._strides = strides if k.numel() else None
-        return k.data_ptr() or 16, self._st[0], v.data_ptr() or 16, self._st[1]  # an empty tensor has no address
+            last = (strides, *((C.c_int64 * 3)(*t[:3]) for t in strides))
+            if k.numel():
+                self._last = last
+        return k.data_ptr() or 16, last[1], v.data_ptr() or 16, last[2]  # an empty tensor has no address
 
     def _launch(self, stream):
         handle = _stream(stream)
@@ -692,8 +694,7 @@ class Kv4Attention:
         assert prefix is None or prefix.data.device == device
         assert ws is None or ws.device == device
         self._pref, self._suf = (None if c is None else c._ref for c in self._caches)
-        self._d = _Kv4AttnDims(B, q_len, q_heads)
-        nbytes = lib().qerl_kv4_attention_ws_bytes(C.byref(self._d), self._pref, self._suf)
+        nbytes = lib().qerl_kv4_attention_ws_bytes(C.byref(_Kv4AttnDims(B, q_len, q_heads)), self._pref, self._suf)
         if nbytes == 0:
             raise QerlError(2, "qerl_kv4_attention_ws_bytes")
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if ws is None else ws
@@ -701,13 +702,11 @@ class Kv4Attention:
         self._launched_on = {_stream()}
         self._q_shape = torch.Size((B, q_len, q_heads, one.D))
         self._scale = one.D ** -0.5 if scale is None else float(scale)
-        self._strides = None  # of the last q and out
-        self._ref = C.byref(self._d)
+        self._last = (None, None)  # strides of the last q and out, and the call's sizes with them; exchanged whole
 
     def run(self, q, suffix_lens=None, prefix_lens=None, out=None, lse=None, stream=None):
         """q bf16 [B, Lq, Hq, D], suffix_lens int32 [B] (new tokens included), prefix_lens int32 [n_prefix] or None
         (full) -> out bf16 like q; lse f32 [B, Lq, Hq] is filled if given."""
-        d = self._d
         prefix, suffix = self._caches
         if out is None:
             out = _new(torch.empty, stream, self._q_shape, dtype=torch.bfloat16, device=q.device)
@@ -718,11 +717,11 @@ class Kv4Attention:
             assert prefix_lens.dtype == torch.int32 and prefix_lens.shape == prefix._lens and prefix_lens.is_contiguous()
         if lse is not None:
             assert lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == self._q_shape[:3]
-        strides = (q.stride(), out.stride())
-        if strides != self._strides:
+        strides, last = (q.stride(), out.stride()), self._last
+        if strides != last[0]:
             assert strides[0][3] == strides[1][3] == 1
-            d.q_stride[:], d.out_stride[:] = strides[0][:3], strides[1][:3]
-            self._strides = strides
+            dims = _Kv4AttnDims(*self._q_shape[:3], *((C.c_int64 * 3)(*t[:3]) for t in strides))
+            last = self._last = (strides, C.byref(dims))
         handle = _stream(stream)
         if handle not in self._launched_on:
             _hold(stream, handle, self._launched_on, (self.ws,))
@@ -730,7 +729,7 @@ class Kv4Attention:
             if c is not None and handle not in c._launched_on:
                 c._launch(stream)
         _here(self.ws, q, out, suffix_lens, prefix_lens, lse)
-        _check(lib().qerl_kv4_attention(self._ref, q.data_ptr(), self._pref, _p(prefix_lens), self._suf, _p(suffix_lens), self._scale,
+        _check(lib().qerl_kv4_attention(last[1], q.data_ptr(), self._pref, _p(prefix_lens), self._suf, _p(suffix_lens), self._scale,
                                         out.data_ptr(), _p(lse), self._ws[0], self._ws[1], handle), "qerl_kv4_attention")
         return out
 
