@@ -170,9 +170,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) rows_kernel(const __grid_
     for (int i = 0; i < kHeld; ++i)
         if (i * 32 < segs) segments(i * 32, tiles[i]);
     for (int k0 = kHeld * 32; k0 < segs; k0 += 32) segments(k0, k0 + lane < segs ? seg_tiles(a, k0 + lane) : 0);
-    bool any = begin < end;
-    if (any && at.i1 <= at.i0) any = next_unit(a, start, at);  // the range begins with the last empty steps of a unit
-    if (any) {
+    if (begin < end && at.i0 < at.i1) {  // a range of empty steps alone has no tile
         uint8_t *const ring = smem + warp * kStages * M::BYTES;
         // the first of this warp's tiles from i0 on: every fourth step of the CTA's range
         const auto first = [&](const Place &p) { return p.i0 + ((warp - p.off) & (kWarps - 1)); };
