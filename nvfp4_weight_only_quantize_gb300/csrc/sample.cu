@@ -233,7 +233,7 @@ struct Shared {
     uint64_t small[kThreads];  // those near the border
     uint32_t hist[kBins];    // tokens of a bin
     uint64_t weight[kBins];  // and their masses, where they are asked for
-    uint64_t sum;            // of a sweep
+    uint64_t sum, sum_above;  // of a sweep
     uint32_t listed;
     float top;  // the row's maximum
     // the next sweep
@@ -250,7 +250,7 @@ struct Shared {
 };
 extern __shared__ __align__(16) uint8_t smem[];
 
-enum { kDone, kHist, kWeigh, kSumGood, kSum, kBetween, kBetweenSums, kKeptFast, kKeptGood, kKeptExact };
+enum { kDone, kHist, kWeigh, kSum, kSumOutside, kBetween, kBetweenSums, kKeptFast, kKeptGood, kKeptExact };
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v)
 {
@@ -434,32 +434,33 @@ __device__ __noinline__ void sweep(const char *x, int off, int n, int chunks, in
         }
         merge_hist();
     };
-    // The masses of a vector's elements that are in the mask, without branches, so that the elements' chains overlap.
-    const auto some_of = [&](const float (&f)[E], uint32_t in, bool exact) -> uint64_t {
-        uint64_t z = 0;
-        if (exact) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const uint64_t m = mass_in_line(ex, f[e]);
-                z += in >> e & 1 ? m : 0;
-            }
-            return z;
-        }
-        // values as integers of 2^-21, what that leaves as integers of 2^-42, both by adding 3 * 2^22; the exponents' part beside them
+    // The good masses of a vector's elements that are in the mask, to z, and of those that are in `also`, to z_also as well; without
+    // branches, so that the elements' chains overlap.  Values as integers of 2^-21, what that leaves as integers of 2^-42, both
+    // by adding 3 * 2^22; the exponents' part, some 2^-20 of them, beside them.
+    const auto add_good = [&](const float (&f)[E], uint32_t in, uint32_t also, uint64_t &z, uint64_t &z_also) {
         const float magic = 12582912.0f;
-        uint32_t coarse = 0u - E * 0x4B400000u, fine = coarse;
-        float rest[E];
+        uint32_t coarse[2] = {0u - E * 0x4B400000u, 0u - __popc(also) * 0x4B400000u}, fine[2] = {coarse[0], coarse[1]};
+        float rest[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const float2 v = good(ex, f[e], in >> e & 1);
-            const float c = fmaf(v.x, 0x1p21f, magic);
-            coarse += __float_as_uint(c);
-            fine += __float_as_uint(fmaf(fmaf(c - magic, -0x1p-21f, v.x), 0x1p42f, magic));
-            rest[e] = v.y;
+            const float c = fmaf(v.x, 0x1p21f, magic), d = fmaf(fmaf(c - magic, -0x1p-21f, v.x), 0x1p42f, magic);
+            coarse[0] += __float_as_uint(c), fine[0] += __float_as_uint(d), rest[0] += v.y;
+            if (also >> e & 1) coarse[1] += __float_as_uint(c), fine[1] += __float_as_uint(d), rest[1] += v.y;
         }
-        return ((uint64_t)coarse << 21) + (int64_t)(int)fine + (int64_t)__float2int_rn(tree(rest) * 0x1p42f);
+        const auto all = [&](int i) { return ((uint64_t)coarse[i] << 21) + (int64_t)(int)fine[i] + (int64_t)__float2int_rn(rest[i] * 0x1p42f); };
+        z += all(0);
+        if (also) z_also += all(1);
     };
-    const auto sum_again = [&](uint32_t hi, uint32_t lo, bool exact) {  // masses of keys in [lo, hi], exact or good
+    // exact
+    const auto add_exact = [&](const float (&f)[E], uint32_t in, uint64_t &z) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const uint64_t m = mass_in_line(ex, f[e]);
+            z += in >> e & 1 ? m : 0;
+        }
+    };
+    const auto sum_again = [&](uint32_t hi, uint32_t lo) {  // exact masses of keys in [lo, hi]
         uint64_t z = 0;
         for (int ch = rank * kWarps + warp; ch < chunks; ch += ranks * kWarps) {
             if (key_of(s_chunk_m[ch]) < lo) continue;
@@ -471,11 +472,26 @@ __device__ __noinline__ void sweep(const char *x, int off, int n, int chunks, in
 #pragma unroll
                 for (int e = 0; e < E; ++e) in |= (key_of(f[e]) >= lo && key_of(f[e]) <= hi ? 1u : 0u) << e;
                 if (!__any_sync(0xFFFFFFFFu, in)) continue;
-                z += some_of(f, in, exact);
+                add_exact(f, in, z);
             }
         }
         z = warp_sum(z);
         if (lane == 0) L::add(&s.sum, z);
+    };
+    const auto sum_outside = [&](float high, float low) {  // good masses outside [low, high], and of those the ones above
+        uint64_t z = 0, z_above = 0;
+        for (int ch = rank * kWarps + warp; ch < chunks; ch += ranks * kWarps)
+#pragma unroll 1
+            for (int j = 0; j < kVec; ++j) {
+                float f[E];
+                R::unpack(r.load(ch * kChunkVecs + j * 32 + lane), f);
+                uint32_t below = 0, above = 0;
+#pragma unroll
+                for (int e = 0; e < E; ++e) below |= (f[e] < low ? 1u : 0u) << e, above |= (f[e] > high ? 1u : 0u) << e;
+                if (__any_sync(0xFFFFFFFFu, below | above)) add_good(f, below | above, above, z, z_above);
+            }
+        z = warp_sum(z), z_above = warp_sum(z_above);
+        if (lane == 0) L::add(&s.sum, z), L::add(&s.sum_above, z_above);
     };
     // Tokens in [low, high] to the list; with `sums` the fast masses above it by chunk, and below it together.  The chunks that
     // lie below are the first CTA's to add.
@@ -573,7 +589,10 @@ __device__ __noinline__ void sweep(const char *x, int off, int n, int chunks, in
                     for (int e = 0; e < E; ++e)
                         in |= (f[e] > border || (f[e] == border && (uint32_t)max(i * E + e - r.off, 0) <= upto) ? 1u : 0u) << e;
                     if (!__any_sync(0xFFFFFFFFu, in)) continue;
-                    z += some_of(f, in, exact);
+                    if (exact)
+                        add_exact(f, in, z);
+                    else
+                        add_good(f, in, 0, z, z);
                 }
                 z = warp_sum(z);
             }
@@ -584,7 +603,8 @@ __device__ __noinline__ void sweep(const char *x, int off, int n, int chunks, in
     const int what = s.what;
     const uint32_t hi = s.hi, lo = s.lo;
     if (what == kHist || what == kWeigh) count_hist(hi, lo, s.shift, what == kWeigh);
-    if (what == kSum || what == kSumGood) sum_again(hi, lo, what == kSum);
+    if (what == kSum) sum_again(hi, lo);
+    if (what == kSumOutside) sum_outside(__uint_as_float(hi), __uint_as_float(lo));
     if (what == kBetween || what == kBetweenSums) between(__uint_as_float(hi), __uint_as_float(lo), what == kBetweenSums);
     if (what == kKeptFast) kept_fast(__uint_as_float(hi));
     if (what == kKeptExact || what == kKeptGood) kept_again(__uint_as_float(hi), lo, what == kKeptExact);
@@ -694,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
         if (what == kHist || what == kWeigh)
             for (int b = tid; b < kBins; b += kThreads) s.hist[b] = 0, s.weight[b] = 0;
         if (tid == 0) {
-            s.sum = 0;
+            s.sum = s.sum_above = 0;
             s.listed = 0;
             s.what = what, s.hi = hi, s.lo = lo, s.shift = shift;
         }
@@ -967,13 +987,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a)
                     // The border is the first token after which at most 1 - top_p of the sum is left.  The fast sums may move that by
                     // `off`: is it the same token at either end?
                     const auto again = [&](bool exact) {
-                        const auto sum = [&](uint64_t &v, uint32_t hi, uint32_t lo) {
-                            if (!v) return;
-                            ask(exact ? kSum : kSumGood, hi, lo, 0);
-                            v = exact ? s.sum : s.sum + (uint64_t)((double)s.sum * kBias);
-                        };
-                        sum(below, key_of(low) - (1u << kUnit), 0);
-                        sum(above, 0xFFFFFFFFu, key_of(high) + (1u << kUnit));
+                        if (exact) {
+                            const auto sum = [&](uint64_t &v, uint32_t hi, uint32_t lo) {
+                                if (!v) return;
+                                ask(kSum, hi, lo, 0);
+                                v = s.sum;
+                            };
+                            sum(below, key_of(low) - (1u << kUnit), 0);
+                            sum(above, 0xFFFFFFFFu, key_of(high) + (1u << kUnit));
+                        } else {
+                            ask(kSumOutside, __float_as_uint(high), __float_as_uint(low), 0);
+                            above = s.sum_above, below = s.sum - above;
+                            above += (uint64_t)((float)above * (float)kBias), below += (uint64_t)((float)below * (float)kBias);
+                        }
                         Z = above + held + below;
                     };
                     const auto choose = [&](bool good) -> bool {
