@@ -637,7 +637,7 @@ class Kv4Cache:
         assert self.data.shape == shape and self.data.dtype == torch.uint8 and self.data.stride(3) == 1
         self.n, self.T, self.Hkv, self.D = n, T, Hkv, D
         self._rows, self._lens = (n, Hkv, D), torch.Size((n,))
-        self._last = (None, None, None)  # the last tokens' strides, and as the library takes them; exchanged whole, for calls by several threads
+        self._last = (None, None, None)  # the last tokens' strides, and as the library takes them: one tuple, for threads' sake
         self._c = _Kv4Cache(self.data.data_ptr(), n, T, Hkv, D, (C.c_int64 * 3)(*self.data.stride()[:3]), k_scale, v_scale)
         self._ref = C.byref(self._c)
         self._launched_on = {_stream()} if self.data.is_cuda else set()

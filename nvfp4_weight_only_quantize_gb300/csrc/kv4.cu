@@ -7,10 +7,11 @@
 // (halves, bytes, nibbles of words) from one token per lane to eight tokens per
 // word.  Words that hold older tokens too are read and merged; no two threads write
 // to one word.
-// Eight prompts of up to 4001 tokens, 8 heads, D = 128: 59 us (131 MB read, 37 MB
-// written, 2.5 TB/s), bound by issue (72 % of the slots, ALU 65 %); reading them back
-// 42 us.  A token of each of 64 sequences: 5 us in a graph, the launch and three
-// dependent memory accesses.
+// Eight prompts of up to 4001 tokens, 8 heads, D = 128: 58 us (131 MB read, 37 MB
+// written, 2.9 TB/s), bound by issue (72 % of the slots, ALU 65 %); reading them back
+// 44 us (3.8 TB/s), bound by the queue of shuffles, scales' bytes and stores (its stall is
+// the longest, issue 42 %).  D = 64: 27 and 22 us.  A token of each of 64 sequences: 5.8
+// and 3.3 us in a graph, the launch and three dependent memory accesses.
 #include "kv4.cuh"
 
 #include <cuda_fp16.h>

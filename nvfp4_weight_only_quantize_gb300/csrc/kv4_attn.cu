@@ -23,13 +23,15 @@
 // on an SM, so that long and short sequences fill the SMs alike.  Rows are tiled by
 // eight whatever their number: tiles of 16 in one warp took three times as long as
 // two of eight (213 registers, half the warps).
-// Bound by HBM in long caches (two sequences of 2 M tokens: 6.2 TB/s, 93 % of the copy
-// rate) and by its start, the join and uneven CTAs in shorter ones: some 4 us before
-// the first tile and 4 us after the last.  28 / 4 heads, D = 128: two sequences of
-// 131072 and 81007 tokens 31 us (122 MB); one sequence over 513 keys 7.4 us in a
-// graph; 64 of up to 4096 tokens, 40 / 8 heads, with prefixes of 512: 52 us.
-// Issue slots 57 % used, tensor pipe 19 %.  With the keys in bf16 by bit fields, three
-// CTAs an SM, a tile took 703 instructions and a long cache read at 5.35 TB/s.
+// Bound by HBM in long caches (two sequences of 2 M tokens: 395 us, 6.1 TB/s, 92 % of
+// the copy rate) and by its start, the join and uneven CTAs in shorter ones: some 4 us
+// before the first tile and 4 us after the last.  In a graph, 28 / 4 heads, D = 128: two
+// sequences of 131072 and 81007 tokens 31 us (122 MB); one sequence over 513 keys 7.8
+// us; 64 of up to 4096 tokens, 40 / 8 heads, with prefixes of 512: 52 to 59 us over three
+// orders of their lengths (51 to 59 with scales on P); the same at D = 64 without
+// prefixes, all of 4096: 44 us, 3.4 TB/s.  Issue slots 58 % used, tensor pipe 19 %.  With
+// the keys in bf16 by bit fields, three CTAs an SM, a tile took 703 instructions and a long
+// cache read at 5.35 TB/s.
 // Rows of a segment beyond 16 go to kv4_attn_tc.cu where that is quicker.
 #include "kv4_attn.cuh"
 

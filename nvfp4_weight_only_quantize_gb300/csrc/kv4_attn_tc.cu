@@ -13,9 +13,11 @@
 //   P     fp16, between 2^8 and 2^15 for a row's largest, so that keys of up to 15 nats less keep all of fp16's digits.
 // 129 tokens of eight sequences, 16 heads, over a prefix of 4001 keys and their own: 72 us
 // with the join (the tiles of eight rows: 405 us); 28 heads of 64 sequences over 16384
-// keys, the own tokens beside it, 50 us (126 us).  Tensor pipe 22 % over the run, issue
+// keys, the own tokens beside it, 51 to 56 us (126 us).  Tensor pipe 22 % over the run, issue
 // 34 %: a step's softmax, products and the arrival of its operands follow one another as
-// in the bf16 kernel; HBM is idle (6 MB).
+// in the bf16 kernel; HBM is idle (6 MB).  As many new tokens as keys: eight sequences of
+// 1000, 16 heads, 178 us (140 at D = 64), one of 4000, 28 heads, 318 us; every key tile runs
+// for every row tile, twice what the rows see.
 #include <cuda.h>
 
 #include "kv4_attn.cuh"

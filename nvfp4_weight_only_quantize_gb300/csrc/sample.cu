@@ -29,13 +29,14 @@
 // or more tokens than the list holds are as good as equal, histograms of the keys
 // find the border.
 //
-// One row of 131072 bf16 (top-k and top-p) 20 us, cluster barriers and dependent steps;
-// 64 rows uncut 27 us, or 44 where a row needs the exact sums (its CTAs then work
-// alone); 1024 rows with top-p 0.95, half of whose mass is a bulk of tens of thousands
-// of alike tokens: 400 us, bound by issue (70 % of the slots; a row's first sweep is
-// 13 us of its some 60, the list 20, border and draw 15); 257 x 100003 FP32 with every
-// cut 113 us, the slowest rows' latency.  With histograms of every row's keys in
-// shared memory instead of the list: 500 us and 2700 us, atomics on few addresses.
+// In a graph, over ten inputs each: one row of 131072 bf16 (top-k and top-p) 21 us,
+// cluster barriers and dependent steps; 64 rows uncut 14 to 48 us, by how many rows
+// need the better sums (their CTAs then work alone); 1024 rows with top-p 0.95, half of
+// whose mass is a bulk of tens of thousands of alike tokens: 382 to 484 us, bound by
+// issue (70 % of the slots); 257 x 100003 FP32 with every cut 79 to 221 us, the slowest
+// rows' latency.  Margins that took errors for independent: 371 to 490 us for the 1024
+// rows, and tokens beside the border's.  With histograms of every row's keys in shared
+// memory instead of the list: 500 us and 2700 us, atomics on few addresses.
 #include <float.h>
 #include <math.h>
 
