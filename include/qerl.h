@@ -549,12 +549,14 @@ typedef struct {
  * Quantises L new tokens of every sequence into the cache, and reads back what it
  * holds of the last L tokens.
  *   k, v (device) bf16 [n, L, Hkv, D], strides of n, L, Hkv in elements (multiples
- *   of 8, >= 0), 16-byte aligned.  lens (device) int32 [n]: tokens of each sequence,
+ *   of 8, >= 0; for read's, which must not overlap, > 0 along more than one), 16-byte
+ *   aligned.  lens (device) int32 [n]: tokens of each sequence,
  *   the new ones among them, taken into [0, T].  counts (device) int32 [n] or NULL
  *   (L): how many of the L are tokens; the rest is not read.  New token l gets
  *   position len - count + l; one before position 0 is left out.
  *   Per block of 16 along D: scale byte s = smallest E4M3 >= amax / (6 factor),
- *   code = nearest E2M1 of w / (s factor), ties to the even code.  Inf or NaN latches
+ *   code = nearest E2M1 of w / (s factor), ties to the even code (in single precision,
+ *   exact where the factor is a power of two).  Inf or NaN latches
  *   QERL_ERR_NONFINITE; Inf is stored as the largest value, NaN as 0.
  * Read returns e2m1 * e4m3 * factor rounded to bf16 (exact where the factor is a
  * power of two), and zeros for positions before 0.
@@ -568,7 +570,8 @@ qerl_status qerl_kv4_read(const qerl_kv4_cache *cache, int64_t L, const int32_t 
  * qerl_prefix_attention over 4-bit caches: sequence b of B sees all keys of prefix
  * b / (B / prefix->n) and, token l of its Lq new ones, the own keys 0 .. len_b - Lq + l.
  *   q, out (device) bf16 [B, Lq, Hq, D], lse (device) optional float [B, Lq, Hq],
- *   lengths, strides, alignment and empty rows as there.  prefix (n divides B) or
+ *   lengths, strides (out's > 0 along more than one), alignment and empty rows as there.
+ *   prefix (n divides B) or
  *   suffix (n = B) may be NULL; both have the same Hkv and D; prefix_lens NULL means
  *   full.  What lies beyond the lengths is never used, whatever it holds.
  *   ws (device) >= qerl_kv4_attention_ws_bytes, contents on entry ignored; calls that

@@ -252,6 +252,7 @@ extern "C" qerl_status qerl_kv4_read(const qerl_kv4_cache *cache, int64_t L, con
     kv4::Tokens t;
     int64_t tiles;
     QERL_TRY(kv4::tokens(cache, L, k, k_stride, v, v_stride, lens, nullptr, c, t, tiles));
+    if (kv4::repeated(c.n, L, c.Hkv, k_stride) || kv4::repeated(c.n, L, c.Hkv, v_stride)) return QERL_ERR_SHAPE;
     QERL_TRY(check_device());
     if (L == 0) return QERL_OK;
     const dim3 grid((unsigned)(tiles * c.n * c.Hkv));

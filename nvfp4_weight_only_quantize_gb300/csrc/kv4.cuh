@@ -58,6 +58,11 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&o)[4])
 
 // What the entry points share: the cache's description checked and taken over.
 qerl_status check_cache(const qerl_kv4_cache *c, Cache &out);
+// Whether an output of sizes a, b, c along its strides has elements at one address.
+inline bool repeated(int64_t a, int64_t b, int64_t c, const int64_t *stride)
+{
+    return (a > 1 && stride[0] == 0) || (b > 1 && stride[1] == 0) || (c > 1 && stride[2] == 0);
+}
 
 }  // namespace kv4
 }  // namespace qerl

@@ -668,6 +668,7 @@ extern "C" qerl_status qerl_kv4_attention(const qerl_kv4_attn_dims *d, const voi
             return QERL_ERR_SHAPE;
         if (d->q_stride[i] % 8 || d->out_stride[i] % 8) return QERL_ERR_ALIGN;
     }
+    if (kv4::repeated(d->B, d->Lq, d->Hq, d->out_stride)) return QERL_ERR_SHAPE;
     if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(prefix_lens) & 3u) ||
         (reinterpret_cast<uintptr_t>(suffix_lens) & 3u))
         return QERL_ERR_ALIGN;

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import nvfp4_weight_only_quantize_gb300 as q
-from test_kv4_abi import L, cache, tokens  # noqa: F401
+from test_kv4_abi import L, attn, cache, tokens  # noqa: F401
 
 
 @pytest.mark.parametrize("call", ["append", "read"])
@@ -33,3 +33,15 @@ def test_attention_takes_caches_and_workspace_of_one_device(monkeypatch):
         q.Kv4Attention(suffix, 4, prefix=prefix, ws=ws)
     with pytest.raises(AssertionError):
         q.Kv4Attention(None, 4, prefix=prefix, batch=4, ws=ws)
+
+
+def test_outputs_whose_elements_share_an_address(L):  # noqa: F811
+    """A stride of 0 repeats an input; what is written needs an address each."""
+    for strides in ((0, 512, 128), (1024, 0, 128), (1024, 512, 0)):
+        assert tokens(L, cache(), call="read", ks=strides) == 2 and tokens(L, cache(), call="read", vs=strides) == 2
+        assert attn(L, Lq=2, os_=strides)[0] == 2
+        # nothing is repeated along a dimension of one; inputs may be.  The workspace and the lengths, looked at later, are what is wrong here
+        assert attn(L, Lq=2, qs=strides, ws=None)[0] == 8
+        assert tokens(L, cache(), ks=strides, lens=1 << 20 | 2) == 3
+    assert tokens(L, cache(n=1), n=1, call="read", ks=(0, 0, 128), lens=1 << 20 | 2) == 3
+    assert attn(L, B=1, pre=None, suf=cache(n=1), os_=(0, 0, 128), ws=None)[0] == 8
